@@ -277,6 +277,132 @@ la_status la_decode_step_proj(const void* x, const void* W, float* S, float* Z, 
                               int H, int d_model, int D, int M, la_dtype dtype, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The layer with a data-dependent decay: a short causal convolution and the
+ * selective scan behind it, and the kernelized cross attention to an encoder.
+ * Row-strided inputs (x, dt, Bm, Cm below) are token-major: row n of batch
+ * entry b starts ld elements after row n - 1, and batch entry b starts N ld
+ * elements after b - 1, so slices of one wider row (a projection's, or the
+ * convolution's [x | B | C]) are read in place.  Strides are in elements.
+ * lengths: device int32 [B] of valid rows (clamped to [0, N]), or NULL for all:
+ * rows at or past a sequence's length are not read, their outputs and gradients
+ * are zeros.  Every other tensor is dense and 16-byte aligned, as above.
+ */
+
+/*
+ * Short causal depthwise convolution: with the K - 1 rows before row 0 taken
+ * from `state` (oldest first) or zero where state is NULL,
+ *   pre[n][c] = bias[c] + sum_j w[c][j] x[n - K + 1 + j][c],
+ *   y = pre sigmoid(pre) with silu != 0, else pre.
+ * x [B][N][C] (row stride ldx >= C; aligned to its elements), w [C][K], bias [C]
+ * or NULL, y [B][N][C], state [B][K-1][C] of the same dtype, replaced by the last
+ * K - 1 inputs of each sequence (of its valid rows).  K = 2, 3 or 4, else
+ * LA_ERR_UNSUPPORTED; 1 <= B <= 65535, 1 <= N <= 2^24, 1 <= C <= 65536.
+ * Sums are fp32.  One launch, no workspace.
+ */
+la_status la_short_conv_fwd(const void* x, const void* w, const void* bias, const int* lengths,
+                            void* state, void* y, int B, int N, int C, int K, int ldx, int silu,
+                            la_dtype dtype, void* stream);
+
+/*
+ * Its gradients from dy [B][N][C], for a history of zeros: dx [B][N][C], dw [C][K]
+ * and db [C] (NULL with a NULL bias).  Two launches; deterministic.  workspace:
+ * la_short_conv_workspace_bytes(...) bytes.
+ */
+la_status la_short_conv_bwd(const void* x, const void* w, const void* bias, const int* lengths,
+                            const void* dy, void* dx, void* dw, void* db, void* workspace,
+                            size_t workspace_bytes, int B, int N, int C, int K, int ldx, int silu,
+                            la_dtype dtype, void* stream);
+size_t la_short_conv_workspace_bytes(int B, int N, int C, int K, la_dtype dtype);
+
+/*
+ * One row for each of B streams: x [B][C] (row stride ldx), y [B][C]; state
+ * [B][K-1][C] is shifted in place.  1 <= B <= 2^20.
+ */
+la_status la_short_conv_step(const void* x, const void* w, const void* bias, void* state, void* y,
+                             int B, int C, int K, int ldx, int silu, la_dtype dtype, void* stream);
+
+/*
+ * Selective scan: the decayed causal recurrence with a decay and an input gate
+ * of every row's own.  Per batch entry and head h of group g = h / (H / G),
+ *   delta_n = softplus(dt[n][h] + dt_bias[h]),  a_n = exp(delta_n A[h]),
+ *   S_n = a_n S_{n-1} + Bm[n][g] (delta_n x[n][h])^T,
+ *   y[n][h] = S_n^T Cm[n][g] + skip[h] x[n][h].
+ * x [B][N][H][M] (row stride ldx >= H M), dt [B][N][H] (lddt >= H; aligned to its
+ * elements), Bm and Cm [B][N][G][D] (ldb, ldc >= G D); ldx, ldb and ldc are
+ * multiples of 16 bytes.  A, skip (may be NULL) and dt_bias (may be NULL) are [H]
+ * of the call's dtype; A <= 0 keeps the recurrence stable and is not checked.
+ * y [B][N][H][M] dense.  S [B][H][D][M] float, read as the state before row 0
+ * and replaced by the state after each sequence's last valid row, or NULL (from
+ * zero, not returned).  G divides H; D and M in {16, 32, 64}; 1 <= B H <= 65535.
+ * workspace: la_scan_workspace_bytes(0, ...) bytes.
+ */
+la_status la_scan_fwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm,
+                      const void* skip, const void* dt_bias, const int* lengths, float* S, void* y,
+                      void* workspace, size_t workspace_bytes, int B, int H, int G, int N, int D,
+                      int M, int ldx, int lddt, int ldb, int ldc, la_dtype dtype, void* stream);
+
+/*
+ * Its gradients from dy [B][N][H][M], for a zero state before row 0 and a final
+ * state nothing reads: dx [B][N][H][M], ddt [B][N][H], dA [H], dB and dC
+ * [B][N][G][D] (summed over a group's heads), dskip and ddt_bias [H] (NULL with
+ * their parameters).  Nothing of the forward pass is kept: the chunks' states
+ * are formed again.  Deterministic.  workspace: la_scan_workspace_bytes(1, ...).
+ */
+la_status la_scan_bwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm,
+                      const void* skip, const void* dt_bias, const int* lengths, const void* dy,
+                      void* dx, void* ddt, void* dA, void* dB, void* dC, void* dskip,
+                      void* ddt_bias, void* workspace, size_t workspace_bytes, int B, int H, int G,
+                      int N, int D, int M, int ldx, int lddt, int ldb, int ldc, la_dtype dtype,
+                      void* stream);
+size_t la_scan_workspace_bytes(int bwd, int B, int H, int G, int N, int D, int M, la_dtype dtype);
+
+/*
+ * One row for each of B streams: x [B][H][M], dt [B][H], Bm and Cm [B][G][D]
+ * (rows ldx, lddt, ldb, ldc apart; all aligned to their elements only); S is
+ * updated in place, y [B][H][M].  1 <= B H <= 2^20.  No workspace.
+ */
+la_status la_scan_step(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm,
+                       const void* skip, const void* dt_bias, float* S, void* y, int B, int H,
+                       int G, int D, int M, int ldx, int lddt, int ldb, int ldc, la_dtype dtype,
+                       void* stream);
+
+/*
+ * Kernelized cross attention: queries q [B][H][Nq][D] against an encoder's keys
+ * and values k [B][Hk][Nk][D], v [B][Hk][Nk][M] of another length, H / Hk query
+ * heads to a key head (Hk divides H):
+ *   S = sum_{j<L_b} phi(k_j) v_j^T,  Z = sum_{j<L_b} phi(k_j)   ([B][Hk][D][M], [B][Hk][D]),
+ *   out_i = phi(q_i)^T S / den_i,  den_i = phi(q_i)^T Z; zeros where L_b = 0.
+ * lengths are the encoder's.  Outputs out [B][H][Nq][M], den [B][H][Nq], S and Z
+ * (all required).  workspace: la_cross_workspace_bytes(0, ...) bytes.
+ */
+la_status la_cross_fwd(const void* q, const void* k, const void* v, const int* lengths, void* out,
+                       float* den, float* S, float* Z, void* workspace, size_t workspace_bytes,
+                       int B, int H, int Hk, int Nq, int Nk, int D, int M, la_dtype dtype,
+                       void* stream);
+
+/*
+ * Its gradients: dq as q, dk as k and dv as v (rows past a sequence's length
+ * zero; summed over the query heads of a key head).  out, den, S and Z are
+ * la_cross_fwd's.  workspace: la_cross_workspace_bytes(1, ...) bytes.
+ */
+la_status la_cross_bwd(const void* q, const void* k, const void* v, const int* lengths,
+                       const void* out, const float* den, const float* S, const float* Z,
+                       const void* dout, void* dq, void* dk, void* dv, void* workspace,
+                       size_t workspace_bytes, int B, int H, int Hk, int Nq, int Nk, int D, int M,
+                       la_dtype dtype, void* stream);
+size_t la_cross_workspace_bytes(int bwd, int B, int H, int Hk, int Nq, int Nk, int D, int M,
+                                la_dtype dtype);
+
+/*
+ * One token for each of B streams, read from the kept S and Z alone:
+ * y [B][H][M] = phi(q)^T S / phi(q)^T Z (zeros where Z = 0), q [B][H][D].
+ * 1 <= B H <= 2^20.  No workspace.
+ */
+la_status la_cross_step(const void* q, const float* S, const float* Z, void* y, int B, int H,
+                        int Hk, int D, int M, la_dtype dtype, void* stream);
+
+/*
  * Reads the status word of the current GPU after all work queued on
  * `stream` so far (the call synchronises `stream`; other streams' work is
  * covered once it has finished).  Returns LA_OK when no bounded wait has

@@ -12,11 +12,15 @@ place of pointers): ``la_causal_fwd``, ``la_causal_bwd``, ``la_causal_prefill``,
 ``la_noncausal_fwd``, ``la_noncausal_bwd``, ``la_decode_step``, the decayed
 ``la_causal_fwd_decay``, ``la_causal_bwd_decay``, ``la_decode_step_decay``, the projected
 ``la_decode_step_proj``, the degree-2 polynomial ``la_causal_fwd_poly``,
-``la_causal_bwd_poly``, ``la_workspace_bytes``, ``la_device_status``.
+``la_causal_bwd_poly``, the short convolution's ``la_short_conv_fwd``, ``la_short_conv_bwd``,
+``la_short_conv_step``, the selective scan's ``la_scan_fwd``, ``la_scan_bwd``, ``la_scan_step``, the cross
+attention's ``la_cross_fwd``, ``la_cross_bwd``, ``la_cross_step``, ``la_workspace_bytes``, ``la_device_status``.
 Convenience wrappers that allocate outputs with torch: ``causal_fwd``,
 ``causal_bwd``, ``causal_prefill``, ``noncausal_fwd``, ``noncausal_bwd``, ``decode_step``, ``decode_step_proj``,
-``causal_fwd_poly``, ``causal_bwd_poly`` and the
-autograd functions ``causal_linear_attention`` / ``noncausal_linear_attention``.
+``causal_fwd_poly``, ``causal_bwd_poly``, ``short_conv_fwd``, ``short_conv_bwd``, ``short_conv_step``,
+``scan_fwd``, ``scan_bwd``, ``scan_step``, ``cross_fwd``, ``cross_bwd``, ``cross_step`` and the
+autograd functions ``causal_linear_attention`` / ``noncausal_linear_attention`` /
+``short_conv`` / ``selective_scan`` / ``cross_linear_attention``.
 
 The method is Katharopoulos et al., "Transformers are RNNs" (part 2/3):
 eq. 7 (phi), §3.3 eq. 9-12, §3.3.1 eq. 13-15, §3.4 eq. 16-20.
@@ -58,6 +62,18 @@ _SIGS = {
     "la_causal_fwd_poly": ("p p p p p p z i i i i i i p", ctypes.c_int),
     "la_causal_bwd_poly": ("p p p p p p p p p p z i i i i i i p", ctypes.c_int),
     "la_causal_fwd_noalloc": ("p p p p p i i i i i i p", ctypes.c_int),
+    "la_short_conv_workspace_bytes": ("i i i i i", ctypes.c_size_t),
+    "la_short_conv_fwd": ("p p p p p p i i i i i i i p", ctypes.c_int),
+    "la_short_conv_bwd": ("p p p p p p p p p z i i i i i i i p", ctypes.c_int),
+    "la_short_conv_step": ("p p p p p i i i i i i p", ctypes.c_int),
+    "la_scan_workspace_bytes": ("i i i i i i i i", ctypes.c_size_t),
+    "la_scan_fwd": ("p p p p p p p p p p p z i i i i i i i i i i i p", ctypes.c_int),
+    "la_scan_bwd": ("p p p p p p p p p p p p p p p p p z i i i i i i i i i i i p", ctypes.c_int),
+    "la_scan_step": ("p p p p p p p p p i i i i i i i i i i p", ctypes.c_int),
+    "la_cross_workspace_bytes": ("i i i i i i i i i", ctypes.c_size_t),
+    "la_cross_fwd": ("p p p p p p p p p z i i i i i i i i p", ctypes.c_int),
+    "la_cross_bwd": ("p p p p p p p p p p p p p z i i i i i i i i p", ctypes.c_int),
+    "la_cross_step": ("p p p p i i i i i i p", ctypes.c_int),
     "la_device_status": ("p i p", ctypes.c_int),
     "la_selftest_wait": ("p u", ctypes.c_int),
 }
@@ -120,6 +136,15 @@ def _p(t):
     if not t.is_contiguous():
         raise ValueError("tensors must be contiguous")
     return t.data_ptr()
+
+
+def _pv(t):
+    """A device address without the contiguity check (row-strided inputs)."""
+    if isinstance(t, torch.Tensor):
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
+        return t.data_ptr()
+    return t
 
 
 def _stream(stream):
@@ -230,6 +255,76 @@ def la_causal_fwd_noalloc(q, k, v, out, den, B, H, N, D, M, dtype, stream=None):
     (for callers that may not allocate device memory)."""
     _check(lib().la_causal_fwd_noalloc(_p(q), _p(k), _p(v), _p(out), _p(den), B, H, N, D, M,
                                        dtype, _stream(stream)), "la_causal_fwd_noalloc")
+
+
+def la_short_conv_workspace_bytes(B, N, C, K, dtype) -> int:
+    return int(lib().la_short_conv_workspace_bytes(B, N, C, K, dtype))
+
+
+def la_short_conv_fwd(x, w, bias, lengths, state, y, B, N, C, K, ldx, silu, dtype, stream=None):
+    _check(lib().la_short_conv_fwd(_pv(x), _p(w), _p(bias), _p(lengths), _p(state), _p(y), B, N, C,
+                                   K, ldx, int(silu), dtype, _stream(stream)), "la_short_conv_fwd")
+
+
+def la_short_conv_bwd(x, w, bias, lengths, dy, dx, dw, db, workspace, B, N, C, K, ldx, silu, dtype,
+                      stream=None):
+    _check(lib().la_short_conv_bwd(_pv(x), _p(w), _p(bias), _p(lengths), _p(dy), _p(dx), _p(dw),
+                                   _p(db), _p(workspace), _nbytes(workspace), B, N, C, K, ldx,
+                                   int(silu), dtype, _stream(stream)), "la_short_conv_bwd")
+
+
+def la_short_conv_step(x, w, bias, state, y, B, C, K, ldx, silu, dtype, stream=None):
+    _check(lib().la_short_conv_step(_pv(x), _p(w), _p(bias), _p(state), _p(y), B, C, K, ldx,
+                                    int(silu), dtype, _stream(stream)), "la_short_conv_step")
+
+
+def la_scan_workspace_bytes(bwd, B, H, G, N, D, M, dtype) -> int:
+    return int(lib().la_scan_workspace_bytes(int(bwd), B, H, G, N, D, M, dtype))
+
+
+def la_scan_fwd(x, dt, A, Bm, Cm, skip, dt_bias, lengths, S, y, workspace, B, H, G, N, D, M, ldx,
+                lddt, ldb, ldc, dtype, stream=None):
+    _check(lib().la_scan_fwd(_pv(x), _pv(dt), _p(A), _pv(Bm), _pv(Cm), _p(skip), _p(dt_bias),
+                             _p(lengths), _p(S), _p(y), _p(workspace), _nbytes(workspace), B, H, G,
+                             N, D, M, ldx, lddt, ldb, ldc, dtype, _stream(stream)), "la_scan_fwd")
+
+
+def la_scan_bwd(x, dt, A, Bm, Cm, skip, dt_bias, lengths, dy, dx, ddt, dA, dB, dC, dskip, ddt_bias,
+                workspace, B, H, G, N, D, M, ldx, lddt, ldb, ldc, dtype, stream=None):
+    _check(lib().la_scan_bwd(_pv(x), _pv(dt), _p(A), _pv(Bm), _pv(Cm), _p(skip), _p(dt_bias),
+                             _p(lengths), _p(dy), _p(dx), _p(ddt), _p(dA), _p(dB), _p(dC),
+                             _p(dskip), _p(ddt_bias), _p(workspace), _nbytes(workspace), B, H, G, N,
+                             D, M, ldx, lddt, ldb, ldc, dtype, _stream(stream)), "la_scan_bwd")
+
+
+def la_scan_step(x, dt, A, Bm, Cm, skip, dt_bias, S, y, B, H, G, D, M, ldx, lddt, ldb, ldc, dtype,
+                 stream=None):
+    _check(lib().la_scan_step(_pv(x), _pv(dt), _p(A), _pv(Bm), _pv(Cm), _p(skip), _p(dt_bias), _p(S),
+                              _p(y), B, H, G, D, M, ldx, lddt, ldb, ldc, dtype, _stream(stream)),
+           "la_scan_step")
+
+
+def la_cross_workspace_bytes(bwd, B, H, Hk, Nq, Nk, D, M, dtype) -> int:
+    return int(lib().la_cross_workspace_bytes(int(bwd), B, H, Hk, Nq, Nk, D, M, dtype))
+
+
+def la_cross_fwd(q, k, v, lengths, out, den, S, Z, workspace, B, H, Hk, Nq, Nk, D, M, dtype,
+                 stream=None):
+    _check(lib().la_cross_fwd(_p(q), _p(k), _p(v), _p(lengths), _p(out), _p(den), _p(S), _p(Z),
+                              _p(workspace), _nbytes(workspace), B, H, Hk, Nq, Nk, D, M, dtype,
+                              _stream(stream)), "la_cross_fwd")
+
+
+def la_cross_bwd(q, k, v, lengths, out, den, S, Z, dout, dq, dk, dv, workspace, B, H, Hk, Nq, Nk, D,
+                 M, dtype, stream=None):
+    _check(lib().la_cross_bwd(_p(q), _p(k), _p(v), _p(lengths), _p(out), _p(den), _p(S), _p(Z),
+                              _p(dout), _p(dq), _p(dk), _p(dv), _p(workspace), _nbytes(workspace), B,
+                              H, Hk, Nq, Nk, D, M, dtype, _stream(stream)), "la_cross_bwd")
+
+
+def la_cross_step(q, S, Z, y, B, H, Hk, D, M, dtype, stream=None):
+    _check(lib().la_cross_step(_p(q), _p(S), _p(Z), _p(y), B, H, Hk, D, M, dtype, _stream(stream)),
+           "la_cross_step")
 
 
 def la_device_status(clear=True, stream=None):
@@ -408,6 +503,232 @@ def decode_step_proj(x, W, S, Z, H, D, M, stream=None):
     return y
 
 
+# ------------------------- the layer with a data-dependent decay, and its encoder
+#
+# These wrappers check shapes, types and devices, allocate on the inputs' device and run on that
+# device's current stream (``with torch.cuda.stream(s):`` for another one).
+
+def _like(t, name, shape, dtype, device, optional=False):
+    """t has the shape, type and device that the call needs."""
+    if t is None and optional:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: a tensor is needed")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the call is on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, the call needs {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
+
+
+def _row_stride(t, name, lead):
+    """The row stride of a token-major view whose first `lead` dimensions are batch (and row): rows
+    dense, and all rows of all batch entries evenly spaced."""
+    want = 1
+    for n, st in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
+        if n != 1 and st != want:
+            raise ValueError(f"{name}: every row must be dense")
+        want *= n
+    if lead == 1:
+        return t.stride(0) if t.shape[0] > 1 else want
+    B, N = t.shape[:2]
+    sb, sn = t.stride()[:2]
+    ld = sn if N > 1 else (sb if B > 1 else want)
+    if B > 1 and sb != N * ld:
+        raise ValueError(f"{name}: batch entries must be N rows apart")
+    return ld
+
+
+class _On:
+    """The device of the call's tensors as the current one, where it is not already."""
+
+    def __init__(self, device):
+        if device.type != "cuda":
+            raise ValueError("tensors must be on a CUDA device")
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *a):
+        if self.guard is not None:
+            self.guard.__exit__(*a)
+
+
+def _scratch(n, device):
+    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _conv_args(x, w, bias, lengths, lead):
+    C, dt, dev = x.shape[-1], _dtype_code(x), x.device
+    if x.dim() != lead + 1 or w.dim() != 2:
+        raise ValueError(f"x: {lead + 1} dimensions, w: [C, K]")
+    K = w.shape[1]
+    _like(w, "w", (C, K), x.dtype, dev)
+    _like(bias, "bias", (C,), x.dtype, dev, True)
+    _like(lengths, "lengths", (x.shape[0],), torch.int32, dev, True)
+    return C, K, dt, dev, _row_stride(x, "x", lead)
+
+
+def short_conv_fwd(x, w, bias=None, state=None, lengths=None, silu=True):
+    """y [B,N,C] of the short causal depthwise convolution: x [B,N,C] (rows may be slices of wider
+    ones), w [C,K], K = 2..4, bias [C]; state [B,K-1,C] holds the inputs before row 0 (zeros if None)
+    and is updated in place; lengths: int32 [B] of valid rows."""
+    C, K, dt, dev, ld = _conv_args(x, w, bias, lengths, 2)
+    B, N = x.shape[:2]
+    _like(state, "state", (B, K - 1, C), x.dtype, dev, True)
+    with _On(dev):
+        y = torch.empty(B, N, C, dtype=x.dtype, device=dev)
+        la_short_conv_fwd(x, w, bias, lengths, state, y, B, N, C, K, ld, silu, dt)
+    return y
+
+
+def short_conv_bwd(x, w, bias, dy, lengths=None, silu=True):
+    """(dx, dw, db) of sum(dy * y) for a history of zeros; db is None without a bias."""
+    C, K, dt, dev, ld = _conv_args(x, w, bias, lengths, 2)
+    B, N = x.shape[:2]
+    _like(dy, "dy", (B, N, C), x.dtype, dev)
+    with _On(dev):
+        dx, dw = torch.empty(B, N, C, dtype=x.dtype, device=dev), torch.empty_like(w)
+        db = None if bias is None else torch.empty_like(bias)
+        ws = _scratch(la_short_conv_workspace_bytes(B, N, C, K, dt), dev)
+        la_short_conv_bwd(x, w, bias, lengths, dy, dx, dw, db, ws, B, N, C, K, ld, silu, dt)
+    return dx, dw, db
+
+
+def short_conv_step(x, w, bias, state, silu=True):
+    """y [B,C] for one row x [B,C] of each stream; state [B,K-1,C] is shifted in place."""
+    C, K, dt, dev, ld = _conv_args(x, w, bias, None, 1)
+    B = x.shape[0]
+    _like(state, "state", (B, K - 1, C), x.dtype, dev)
+    with _On(dev):
+        y = torch.empty(B, C, dtype=x.dtype, device=dev)
+        la_short_conv_step(x, w, bias, state, y, B, C, K, ld, silu, dt)
+    return y
+
+
+def _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, lengths, lead):
+    if x.dim() != lead + 2 or Bm.dim() != lead + 2:
+        raise ValueError(f"x, Bm and Cm: {lead + 2} dimensions")
+    rows, (H, M), (G, D) = tuple(x.shape[:lead]), x.shape[lead:], Bm.shape[lead:]
+    t, dev = x.dtype, x.device
+    code = _dtype_code(x)
+    _like(dt, "dt", rows + (H,), t, dev)
+    for v, n in ((Bm, "Bm"), (Cm, "Cm")):
+        _like(v, n, rows + (G, D), t, dev)
+    _like(A, "A", (H,), t, dev)
+    _like(skip, "skip", (H,), t, dev, True)
+    _like(dt_bias, "dt_bias", (H,), t, dev, True)
+    _like(lengths, "lengths", rows[:1], torch.int32, dev, True)
+    strides = [_row_stride(v, n, lead) for v, n in ((x, "x"), (dt, "dt"), (Bm, "Bm"), (Cm, "Cm"))]
+    return (H, G, D, M), strides, code, dev
+
+
+def scan_fwd(x, dt, A, Bm, Cm, skip=None, dt_bias=None, S=None, lengths=None):
+    """y [B,N,H,M] of the selective scan S_n = exp(delta_n A) S_{n-1} + B_n (delta_n x_n)^T,
+    y_n = S_n^T C_n + skip x_n, delta = softplus(dt + dt_bias).  x [B,N,H,M], dt [B,N,H], Bm and Cm
+    [B,N,G,D] (G divides H; rows may be slices of wider ones), A, skip, dt_bias [H].  S [B,H,D,M]
+    (float32) is the state before row 0 (zeros if None), updated in place to the state after each
+    sequence's last valid row; scan_step continues from it."""
+    (H, G, D, M), ld, code, dev = _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, lengths, 2)
+    B, N = x.shape[:2]
+    _like(S, "S", (B, H, D, M), torch.float32, dev, True)
+    with _On(dev):
+        y = torch.empty(B, N, H, M, dtype=x.dtype, device=dev)
+        ws = _scratch(la_scan_workspace_bytes(0, B, H, G, N, D, M, code), dev)
+        la_scan_fwd(x, dt, A, Bm, Cm, skip, dt_bias, lengths, S, y, ws, B, H, G, N, D, M, *ld, code)
+    return y
+
+
+def scan_bwd(x, dt, A, Bm, Cm, skip, dt_bias, dy, lengths=None):
+    """(dx, ddt, dA, dBm, dCm, dskip, ddt_bias) of sum(dy * y) for a zero state before row 0; dskip
+    and ddt_bias are None without their parameters."""
+    (H, G, D, M), ld, code, dev = _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, lengths, 2)
+    B, N = x.shape[:2]
+    _like(dy, "dy", (B, N, H, M), x.dtype, dev)
+    with _On(dev):
+        new = lambda *shape: torch.empty(shape, dtype=x.dtype, device=dev)  # noqa: E731
+        dx, ddt, dA, dB, dC = new(B, N, H, M), new(B, N, H), new(H), new(B, N, G, D), new(B, N, G, D)
+        dskip, dbias = None if skip is None else new(H), None if dt_bias is None else new(H)
+        ws = _scratch(la_scan_workspace_bytes(1, B, H, G, N, D, M, code), dev)
+        la_scan_bwd(x, dt, A, Bm, Cm, skip, dt_bias, lengths, dy, dx, ddt, dA, dB, dC, dskip, dbias, ws,
+                    B, H, G, N, D, M, *ld, code)
+    return dx, ddt, dA, dB, dC, dskip, dbias
+
+
+def scan_step(x, dt, A, Bm, Cm, skip, dt_bias, S):
+    """y [B,H,M] for one row of each stream: x [B,H,M], dt [B,H], Bm and Cm [B,G,D]; S [B,H,D,M]
+    (float32) is updated in place."""
+    (H, G, D, M), ld, code, dev = _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, None, 1)
+    B = x.shape[0]
+    _like(S, "S", (B, H, D, M), torch.float32, dev)
+    with _On(dev):
+        y = torch.empty(B, H, M, dtype=x.dtype, device=dev)
+        la_scan_step(x, dt, A, Bm, Cm, skip, dt_bias, S, y, B, H, G, D, M, *ld, code)
+    return y
+
+
+def _cross_args(q, k, v, lengths):
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError("q, k and v: 4 dimensions")
+    B, H, Nq, D = q.shape
+    Hk, Nk, M = k.shape[1], k.shape[2], v.shape[3]
+    code = _dtype_code(q)
+    _like(k, "k", (B, Hk, Nk, D), q.dtype, q.device)
+    _like(v, "v", (B, Hk, Nk, M), q.dtype, q.device)
+    _like(lengths, "lengths", (B,), torch.int32, q.device, True)
+    return (B, H, Hk, Nq, Nk, D, M), code, q.device
+
+
+def cross_fwd(q, k, v, lengths=None):
+    """(out, den, S, Z) of the kernelized cross attention of q [B,H,Nq,D] to an encoder's k [B,Hk,Nk,D]
+    and v [B,Hk,Nk,M] (Hk divides H); lengths: int32 [B] of valid encoder states.  S [B,Hk,D,M] and
+    Z [B,Hk,D] (float32) are all that cross_step needs of the encoder."""
+    size, code, dev = _cross_args(q, k, v, lengths)
+    B, H, Hk, Nq, Nk, D, M = size
+    with _On(dev):
+        out = torch.empty(B, H, Nq, M, dtype=q.dtype, device=dev)
+        den = torch.empty(B, H, Nq, dtype=torch.float32, device=dev)
+        S = torch.empty(B, Hk, D, M, dtype=torch.float32, device=dev)
+        Z = torch.empty(B, Hk, D, dtype=torch.float32, device=dev)
+        ws = _scratch(la_cross_workspace_bytes(0, *size, code), dev)
+        la_cross_fwd(q, k, v, lengths, out, den, S, Z, ws, *size, code)
+    return out, den, S, Z
+
+
+def cross_bwd(q, k, v, lengths, out, den, S, Z, dout):
+    """(dq, dk, dv) of sum(dout * out); out, den, S, Z from cross_fwd."""
+    size, code, dev = _cross_args(q, k, v, lengths)
+    B, H, Hk, Nq, Nk, D, M = size
+    for t, n in ((out, "out"), (dout, "dout")):
+        _like(t, n, (B, H, Nq, M), q.dtype, dev)
+    _like(den, "den", (B, H, Nq), torch.float32, dev)
+    _like(S, "S", (B, Hk, D, M), torch.float32, dev)
+    _like(Z, "Z", (B, Hk, D), torch.float32, dev)
+    with _On(dev):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        ws = _scratch(la_cross_workspace_bytes(1, *size, code), dev)
+        la_cross_bwd(q, k, v, lengths, out, den, S, Z, dout, dq, dk, dv, ws, *size, code)
+    return dq, dk, dv
+
+
+def cross_step(q, S, Z):
+    """y [B,H,M] for one token q [B,H,D] of each stream, from the kept S [B,Hk,D,M] and Z [B,Hk,D]."""
+    if q.dim() != 3 or S.dim() != 4:
+        raise ValueError("q: 3 dimensions, S: 4")
+    B, H, D = q.shape
+    Hk, M = S.shape[1], S.shape[3]
+    code = _dtype_code(q)
+    _like(S, "S", (B, Hk, D, M), torch.float32, q.device)
+    _like(Z, "Z", (B, Hk, D), torch.float32, q.device)
+    with _On(q.device):
+        y = torch.empty(B, H, M, dtype=q.dtype, device=q.device)
+        la_cross_step(q, S, Z, y, B, H, Hk, D, M, code)
+    return y
+
+
 class _Causal(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v):
@@ -446,3 +767,58 @@ def causal_linear_attention(q, k, v):
 def noncausal_linear_attention(q, k, v, lengths=None):
     """Non-causal elu+1 linear attention (shared S, Z per sequence)."""
     return _NonCausal.apply(q, k, v, lengths)
+
+
+class _ShortConv(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, bias, lengths, silu):
+        ctx.save_for_backward(x, w, bias, lengths)
+        ctx.silu = silu
+        return short_conv_fwd(x, w, bias, None, lengths, silu)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, bias, lengths = ctx.saved_tensors
+        return *short_conv_bwd(x, w, bias, dy.contiguous(), lengths, ctx.silu), None, None
+
+
+class _Scan(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, dt, A, Bm, Cm, skip, dt_bias, lengths):
+        ctx.save_for_backward(x, dt, A, Bm, Cm, skip, dt_bias, lengths)
+        return scan_fwd(x, dt, A, Bm, Cm, skip, dt_bias, None, lengths)
+
+    @staticmethod
+    def backward(ctx, dy):
+        *inputs, lengths = ctx.saved_tensors
+        return *scan_bwd(*inputs, dy.contiguous(), lengths), None
+
+
+class _Cross(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, lengths):
+        q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
+        out, den, S, Z = cross_fwd(q, k, v, lengths)
+        ctx.save_for_backward(q, k, v, lengths, out, den, S, Z)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, lengths, out, den, S, Z = ctx.saved_tensors
+        return *cross_bwd(q, k, v, lengths, out, den, S, Z, dout.contiguous()), None
+
+
+def short_conv(x, w, bias=None, lengths=None, silu=True):
+    """short_conv_fwd with its gradients (history zero)."""
+    return _ShortConv.apply(x, w, bias, lengths, silu)
+
+
+def selective_scan(x, dt, A, Bm, Cm, skip=None, dt_bias=None, lengths=None):
+    """scan_fwd with its gradients (zero state before row 0; nothing of the forward pass is kept but
+    its inputs)."""
+    return _Scan.apply(x, dt, A, Bm, Cm, skip, dt_bias, lengths)
+
+
+def cross_linear_attention(q, k, v, lengths=None):
+    """Kernelized cross attention to an encoder's states (cross_fwd) with its gradients."""
+    return _Cross.apply(q, k, v, lengths)

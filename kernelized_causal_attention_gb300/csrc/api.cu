@@ -100,6 +100,46 @@ int check_proj(int B, int H, int dm, int D, int M, int dtype) {
   return LA_OK;
 }
 
+// The convolution, the scan and the cross attention: aligned to `to` bytes, or
+// (opt) null.
+int check_to(const void* p, size_t to, bool opt = false) {
+  if (p == nullptr) return opt ? LA_OK : LA_ERR_INVALID_ARG;
+  return reinterpret_cast<uintptr_t>(p) % to == 0 ? LA_OK : LA_ERR_INVALID_ARG;
+}
+
+size_t elem(int dtype) { return dtype == LA_F32 ? 4 : 2; }
+
+int check_conv(int B, int N, int C, int K, int ldx, int dtype, int max_b) {
+  if (B < 1 || N < 1 || C < 1 || K < 1 || ldx < C) return LA_ERR_INVALID_ARG;
+  if (B > max_b || N > (1 << 24) || C > 65536) return LA_ERR_INVALID_ARG;
+  if (dtype != LA_F32 && dtype != LA_BF16) return LA_ERR_INVALID_ARG;
+  return K < 2 || K > 4 ? LA_ERR_UNSUPPORTED : LA_OK;
+}
+
+int check_scan(const la::ScanShape& s, long long max_bh) {
+  if (s.G < 1 || s.H < 1 || s.H % s.G != 0) return LA_ERR_INVALID_ARG;
+  return check_shape(s.B, s.H, s.N, s.D, s.M, s.dtype, max_bh);
+}
+
+// Row strides: `unit` elements is what the kernels load at once.
+int check_strides(const la::ScanShape& s, int unit) {
+  if (s.ldx < (long)s.H * s.M || s.ldb < (long)s.G * s.D || s.ldc < (long)s.G * s.D || s.lddt < s.H) return LA_ERR_INVALID_ARG;
+  return s.ldx % unit || s.ldb % unit || s.ldc % unit ? LA_ERR_INVALID_ARG : LA_OK;
+}
+
+int check_cross(const la::CrossShape& s, long long max_bh) {
+  if (s.Hk < 1 || s.H < 1 || s.H % s.Hk != 0 || s.Nk < 1 || s.Nk > (1 << 24)) return LA_ERR_INVALID_ARG;
+  return check_shape(s.B, s.H, s.Nq, s.D, s.M, s.dtype, max_bh);
+}
+
+int check_room(const void* ws, size_t bytes, size_t need) {
+  if (need == 0) return LA_OK;
+  if (ws == nullptr || bytes < need) return LA_ERR_WORKSPACE;
+  return aligned16(ws) ? LA_OK : LA_ERR_INVALID_ARG;
+}
+
+size_t scan_ws(const la::ScanShape& s, bool bwd) { return la::scan_cc_ws_bytes(s, bwd); }
+
 }  // namespace
 
 namespace la {
@@ -325,6 +365,138 @@ int la_decode_step(const void* q, const void* k, const void* v, float* S, float*
   LA_TRY(check_ptrs({q, k, v, S, Z, y}));
   const Shape s{B, H, 1, D, M, dtype};
   return from_cuda(la::decode_step(q, k, v, S, Z, y, s, static_cast<cudaStream_t>(stream)));
+}
+
+size_t la_short_conv_workspace_bytes(int B, int N, int C, int K, int dtype) {
+  if (check_conv(B, N, C, K, C, dtype, 65535) != LA_OK) return 0;
+  return la::short_conv_bwd_ws_bytes(la::ConvShape{B, N, C, K, C, 0, dtype});
+}
+
+int la_short_conv_fwd(const void* x, const void* w, const void* bias, const int* lengths, void* state, void* y, int B, int N,
+                      int C, int K, int ldx, int silu, int dtype, void* stream) {
+  LA_TRY(check_conv(B, N, C, K, ldx, dtype, 65535));
+  LA_TRY(check_to(x, elem(dtype)));
+  LA_TRY(check_ptrs({w, y}));
+  LA_TRY(check_opt_ptr(bias));
+  LA_TRY(check_opt_ptr(state));
+  LA_TRY(check_to(lengths, 4, true));
+  return from_cuda(la::short_conv_fwd(x, w, bias, lengths, state, y, la::ConvShape{B, N, C, K, ldx, silu, dtype},
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+int la_short_conv_bwd(const void* x, const void* w, const void* bias, const int* lengths, const void* dy, void* dx, void* dw,
+                      void* db, void* workspace, size_t workspace_bytes, int B, int N, int C, int K, int ldx, int silu,
+                      int dtype, void* stream) {
+  LA_TRY(check_conv(B, N, C, K, ldx, dtype, 65535));
+  LA_TRY(check_to(x, elem(dtype)));
+  LA_TRY(check_ptrs({w, dy, dx, dw}));
+  LA_TRY(check_opt_ptr(bias));
+  LA_TRY(check_opt_ptr(db));
+  if (bias != nullptr && db == nullptr) return LA_ERR_INVALID_ARG;
+  LA_TRY(check_to(lengths, 4, true));
+  const la::ConvShape s{B, N, C, K, ldx, silu, dtype};
+  LA_TRY(check_room(workspace, workspace_bytes, la::short_conv_bwd_ws_bytes(s)));
+  return from_cuda(la::short_conv_bwd(x, w, bias, lengths, dy, dx, dw, db, static_cast<float*>(workspace), s,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+int la_short_conv_step(const void* x, const void* w, const void* bias, void* state, void* y, int B, int C, int K, int ldx,
+                       int silu, int dtype, void* stream) {
+  LA_TRY(check_conv(B, 1, C, K, ldx, dtype, 1 << 20));
+  LA_TRY(check_to(x, elem(dtype)));
+  LA_TRY(check_ptrs({w, state, y}));
+  LA_TRY(check_opt_ptr(bias));
+  return from_cuda(la::short_conv_step(x, w, bias, state, y, la::ConvShape{B, 1, C, K, ldx, silu, dtype},
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+size_t la_scan_workspace_bytes(int bwd, int B, int H, int G, int N, int D, int M, int dtype) {
+  const la::ScanShape s{B, H, G, N, D, M, (long)H * M, H, (long)G * D, (long)G * D, dtype};
+  return check_scan(s, 65535) == LA_OK ? scan_ws(s, bwd != 0) : 0;
+}
+
+int la_scan_fwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* skip,
+                const void* dt_bias, const int* lengths, float* S, void* y, void* workspace, size_t workspace_bytes, int B,
+                int H, int G, int N, int D, int M, int ldx, int lddt, int ldb, int ldc, int dtype, void* stream) {
+  const la::ScanShape s{B, H, G, N, D, M, ldx, lddt, ldb, ldc, dtype};
+  LA_TRY(check_scan(s, 65535));
+  LA_TRY(check_strides(s, static_cast<int>(16 / elem(dtype))));
+  LA_TRY(check_ptrs({x, A, Bm, Cm, y}));
+  LA_TRY(check_to(dt, elem(dtype)));
+  for (const void* p : {skip, dt_bias, static_cast<const void*>(S)}) LA_TRY(check_opt_ptr(p));
+  LA_TRY(check_to(lengths, 4, true));
+  LA_TRY(check_room(workspace, workspace_bytes, scan_ws(s, false)));
+  const la::ScanIn a{x, dt, A, Bm, Cm, skip, dt_bias, lengths};
+  return from_cuda(la::scan_fwd_cc(a, S, y, workspace, s, static_cast<cudaStream_t>(stream)));
+}
+
+int la_scan_bwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* skip,
+                const void* dt_bias, const int* lengths, const void* dy, void* dx, void* ddt, void* dA, void* dB, void* dC,
+                void* dskip, void* ddt_bias, void* workspace, size_t workspace_bytes, int B, int H, int G, int N, int D,
+                int M, int ldx, int lddt, int ldb, int ldc, int dtype, void* stream) {
+  const la::ScanShape s{B, H, G, N, D, M, ldx, lddt, ldb, ldc, dtype};
+  LA_TRY(check_scan(s, 65535));
+  LA_TRY(check_strides(s, static_cast<int>(16 / elem(dtype))));
+  LA_TRY(check_ptrs({x, A, Bm, Cm, dy, dx, ddt, dA, dB, dC}));
+  LA_TRY(check_to(dt, elem(dtype)));
+  for (const void* p : {skip, dt_bias, static_cast<const void*>(dskip), static_cast<const void*>(ddt_bias)})
+    LA_TRY(check_opt_ptr(p));
+  if ((skip != nullptr && dskip == nullptr) || (dt_bias != nullptr && ddt_bias == nullptr)) return LA_ERR_INVALID_ARG;
+  LA_TRY(check_to(lengths, 4, true));
+  LA_TRY(check_room(workspace, workspace_bytes, scan_ws(s, true)));
+  const la::ScanIn a{x, dt, A, Bm, Cm, skip, dt_bias, lengths};
+  const la::ScanGrads d{dx, ddt, dA, dB, dC, dskip, ddt_bias};
+  return from_cuda(la::scan_bwd_cc(a, dy, d, workspace, s, static_cast<cudaStream_t>(stream)));
+}
+
+int la_scan_step(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* skip,
+                 const void* dt_bias, float* S, void* y, int B, int H, int G, int D, int M, int ldx, int lddt, int ldb,
+                 int ldc, int dtype, void* stream) {
+  const la::ScanShape s{B, H, G, 1, D, M, ldx, lddt, ldb, ldc, dtype};
+  LA_TRY(check_scan(s, 1ll << 20));
+  LA_TRY(check_strides(s, 1));
+  for (const void* p : {x, dt, Bm, Cm}) LA_TRY(check_to(p, elem(dtype)));
+  LA_TRY(check_ptrs({A, S, y}));
+  for (const void* p : {skip, dt_bias}) LA_TRY(check_opt_ptr(p));
+  const la::ScanIn a{x, dt, A, Bm, Cm, skip, dt_bias, nullptr};
+  return from_cuda(la::scan_step(a, S, y, s, static_cast<cudaStream_t>(stream)));
+}
+
+size_t la_cross_workspace_bytes(int bwd, int B, int H, int Hk, int Nq, int Nk, int D, int M, int dtype) {
+  const la::CrossShape s{B, H, Hk, Nq, Nk, D, M, dtype};
+  return check_cross(s, 65535) == LA_OK ? la::cross_ws_bytes(s, bwd != 0) : 0;
+}
+
+int la_cross_fwd(const void* q, const void* k, const void* v, const int* lengths, void* out, float* den, float* S, float* Z,
+                 void* workspace, size_t workspace_bytes, int B, int H, int Hk, int Nq, int Nk, int D, int M, int dtype,
+                 void* stream) {
+  const la::CrossShape s{B, H, Hk, Nq, Nk, D, M, dtype};
+  LA_TRY(check_cross(s, 65535));
+  LA_TRY(check_ptrs({q, k, v, out, den, S, Z}));
+  LA_TRY(check_to(lengths, 4, true));
+  LA_TRY(check_room(workspace, workspace_bytes, la::cross_ws_bytes(s, false)));
+  return from_cuda(la::cross_fwd(q, k, v, lengths, out, den, S, Z, static_cast<float*>(workspace), s,
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+int la_cross_bwd(const void* q, const void* k, const void* v, const int* lengths, const void* out, const float* den,
+                 const float* S, const float* Z, const void* dout, void* dq, void* dk, void* dv, void* workspace,
+                 size_t workspace_bytes, int B, int H, int Hk, int Nq, int Nk, int D, int M, int dtype, void* stream) {
+  const la::CrossShape s{B, H, Hk, Nq, Nk, D, M, dtype};
+  LA_TRY(check_cross(s, 65535));
+  LA_TRY(check_ptrs({q, k, v, out, den, S, Z, dout, dq, dk, dv}));
+  LA_TRY(check_to(lengths, 4, true));
+  LA_TRY(check_room(workspace, workspace_bytes, la::cross_ws_bytes(s, true)));
+  return from_cuda(la::cross_bwd(q, k, v, lengths, out, den, S, Z, dout, dq, dk, dv, static_cast<float*>(workspace), s,
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+int la_cross_step(const void* q, const float* S, const float* Z, void* y, int B, int H, int Hk, int D, int M, int dtype,
+                  void* stream) {
+  const la::CrossShape s{B, H, Hk, 1, 1, D, M, dtype};
+  LA_TRY(check_cross(s, 1ll << 20));
+  LA_TRY(check_ptrs({q, S, Z, y}));
+  return from_cuda(la::cross_step(q, S, Z, y, s, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

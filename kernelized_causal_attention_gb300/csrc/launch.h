@@ -154,19 +154,65 @@ struct ProjPlan {
 ProjPlan decode_proj_plan(int B, int H);
 int decode_proj_block(int B, int H);
 
+// The short causal convolution (short_conv.cu): x rows ldx elements apart.
+struct ConvShape {
+  int B, N, C, K;
+  long ldx;
+  int silu;
+  int dtype;
+};
+size_t short_conv_bwd_ws_bytes(const ConvShape& s);
+cudaError_t short_conv_fwd(const void* x, const void* w, const void* bias, const int* lengths, void* state, void* y,
+                           const ConvShape& s, cudaStream_t st);
+cudaError_t short_conv_bwd(const void* x, const void* w, const void* bias, const int* lengths, const void* dy, void* dx,
+                           void* dw, void* db, float* ws, const ConvShape& s, cudaStream_t st);
+cudaError_t short_conv_step(const void* x, const void* w, const void* bias, void* state, void* y, const ConvShape& s,
+                            cudaStream_t st);
+
+// The selective scan (scan.cu): token-major inputs, row strides in elements.
+struct ScanShape {
+  int B, H, G, N, D, M;
+  long ldx, lddt, ldb, ldc;
+  int dtype;
+};
+struct ScanIn {
+  const void *x, *dt, *A, *B, *C, *skip, *dt_bias;  // skip and dt_bias may be null
+  const int* lengths;                               // null: every row
+};
+struct ScanGrads {
+  void *x, *dt, *A, *B, *C, *skip, *dt_bias;  // skip and dt_bias may be null
+};
+size_t scan_cc_ws_bytes(const ScanShape& s, bool bwd);
+cudaError_t scan_fwd_cc(const ScanIn& a, float* S, void* y, void* ws, const ScanShape& s, cudaStream_t st);
+cudaError_t scan_bwd_cc(const ScanIn& a, const void* dy, const ScanGrads& d, void* ws, const ScanShape& s, cudaStream_t st);
+cudaError_t scan_step(const ScanIn& a, float* S, void* y, const ScanShape& s, cudaStream_t st);
+
+// The kernelized cross attention (cross.cu).
+struct CrossShape {
+  int B, H, Hk, Nq, Nk, D, M;
+  int dtype;
+};
+size_t cross_ws_bytes(const CrossShape& s, bool bwd);
+cudaError_t cross_fwd(const void* q, const void* k, const void* v, const int* lengths, void* out, float* den, float* S,
+                      float* Z, float* ws, const CrossShape& s, cudaStream_t st);
+cudaError_t cross_bwd(const void* q, const void* k, const void* v, const int* lengths, const void* out, const float* den,
+                      const float* S, const float* Z, const void* dout, void* dq, void* dk, void* dv, float* ws,
+                      const CrossShape& s, cudaStream_t st);
+cudaError_t cross_step(const void* q, const float* S, const float* Z, void* y, const CrossShape& s, cudaStream_t st);
+
 }  // namespace la
 
-// Expands BODY once per supported (D, M) pair with constexpr D_ and M_ in scope.
-#define LA_DISPATCH_DM(Dv, Mv, BODY)                         \
+// Expands the body once per supported (D, M) pair with constexpr D_ and M_ in scope.
+#define LA_DISPATCH_DM(Dv, Mv, ...)                          \
   switch ((Dv) * 1000 + (Mv)) {                              \
-    case 16016: { constexpr int D_ = 16, M_ = 16; BODY; } break; \
-    case 16032: { constexpr int D_ = 16, M_ = 32; BODY; } break; \
-    case 16064: { constexpr int D_ = 16, M_ = 64; BODY; } break; \
-    case 32016: { constexpr int D_ = 32, M_ = 16; BODY; } break; \
-    case 32032: { constexpr int D_ = 32, M_ = 32; BODY; } break; \
-    case 32064: { constexpr int D_ = 32, M_ = 64; BODY; } break; \
-    case 64016: { constexpr int D_ = 64, M_ = 16; BODY; } break; \
-    case 64032: { constexpr int D_ = 64, M_ = 32; BODY; } break; \
-    case 64064: { constexpr int D_ = 64, M_ = 64; BODY; } break; \
+    case 16016: { constexpr int D_ = 16, M_ = 16; __VA_ARGS__; } break; \
+    case 16032: { constexpr int D_ = 16, M_ = 32; __VA_ARGS__; } break; \
+    case 16064: { constexpr int D_ = 16, M_ = 64; __VA_ARGS__; } break; \
+    case 32016: { constexpr int D_ = 32, M_ = 16; __VA_ARGS__; } break; \
+    case 32032: { constexpr int D_ = 32, M_ = 32; __VA_ARGS__; } break; \
+    case 32064: { constexpr int D_ = 32, M_ = 64; __VA_ARGS__; } break; \
+    case 64016: { constexpr int D_ = 64, M_ = 16; __VA_ARGS__; } break; \
+    case 64032: { constexpr int D_ = 64, M_ = 32; __VA_ARGS__; } break; \
+    case 64064: { constexpr int D_ = 64, M_ = 64; __VA_ARGS__; } break; \
     default: return cudaErrorInvalidValue;                   \
   }

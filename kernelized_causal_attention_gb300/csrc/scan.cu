@@ -1,0 +1,601 @@
+// Selective state space scan (the data-dependent form of the decayed causal
+// recurrence): per batch entry and head, with the state S [D][M],
+//   delta_t = softplus(dt_t + dt_bias),  a_t = exp(delta_t A),
+//   S_t = a_t S_{t-1} + B_t (delta_t x_t)^T,   y_t = S_t^T C_t + skip x_t,
+// B and C shared by the H / G heads of a group.
+//
+// Chunk form.  With cum_i the sum of delta A over a chunk's rows up to i and
+// W_ij = exp(cum_i - cum_j) for j <= i, else 0 (u = delta x),
+//   y_i = sum_j W_ij (C_i . B_j) u_j + exp(cum_i) S_prev^T C_i + skip x_i,
+//   S_next = exp(cum_end) S_prev + sum_j exp(cum_end - cum_j) B_j u_j^T,
+// so every chunk's own sum is formed first, the states are carried over the
+// chunks, and then every chunk is independent.  Gradients, with R the gradient
+// of the state after the chunk (carried from the last chunk to the first):
+//   du_j = sum_i W_ij (C_i . B_j) dy_i + exp(cum_end - cum_j) R^T B_j
+//   dB_j = sum_i W_ij (dy_i . u_j) C_i + exp(cum_end - cum_j) R u_j
+//   dC_i = sum_j W_ij (dy_i . u_j) B_j + exp(cum_i) S_prev dy_i
+//   R_prev = exp(cum_end) R + sum_i exp(cum_i) C_i dy_i^T
+// and the gradient of log a_t, which every pair, carry-in and carry-out that
+// spans row t feels (G_ij = W_ij (C_i . B_j)(dy_i . u_j)):
+//   dl_t = sum_{i>=t, j<t} G_ij + sum_{i>=t} C_i . carry part of dC_i
+//        + sum_{j<t} B_j . carry part of dB_j + exp(cum_end) <S_prev, R>.
+//
+// This file: the fp32 kernels (chunks of 64 rows, FFMA), the carry and the
+// reductions both paths use, and the single-row step.  The fp32 chunk kernels
+// are bound by the FFMA rate (about 16 D M-sized products a row).
+#include "ffma.cuh"
+#include "scan.cuh"
+
+namespace la {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+// delta, cum and the raw gate's argument of a chunk's 64 rows (rows at or past
+// `rows`: delta 0, cum carried on).  Threads 0 .. 63; all must call.
+template <typename T>
+__device__ __forceinline__ void gates(const T* dt, long lddt, int rows, float bias, float A, float* delta, float* cum, float* z) {
+  const int t = threadIdx.x;
+  float d = 0.f, c = 0.f;
+  if (t < 64) {
+    if (t < rows) {
+      const float x = to_f(dt[t * lddt]) + bias;
+      if (z != nullptr) z[t] = x;
+      d = softplus(x);
+    } else if (z != nullptr) {
+      z[t] = 0.f;
+    }
+    delta[t] = d;
+    c = warp_prefix(d * A);
+    cum[t] = c;
+  }
+  __syncthreads();
+  if (t >= 32 && t < 64) cum[t] = c + cum[31];
+  __syncthreads();
+}
+
+// A chunk's own sums: F[d][m] = sum_j exp(cum_end - cum_j) delta_j B_j x_j^T
+// (fwd) and, where rev is given, E[d][m] = sum_i exp(cum_i) C_i dy_i^T, and the
+// chunk's log decay.  Grid (nch, BH).
+template <int D, int M, typename T>
+__global__ void __launch_bounds__(256)
+    k_scan_sums(const T* __restrict__ x, const T* __restrict__ dt, const T* __restrict__ A, const T* __restrict__ Bm,
+                const T* __restrict__ Cm, const T* __restrict__ bias, const int* __restrict__ lengths,
+                const T* __restrict__ dy, float* __restrict__ fwd, float* __restrict__ rev, float* __restrict__ tot,
+                ScanShape s) {
+  extern __shared__ float sm[];
+  float* tb = sm;                  // [64][D + 4]
+  float* tx = tb + 64 * (D + 4);   // [64][M + 4]
+  __shared__ float delta[64], cum[64];
+  const int c = blockIdx.x, bh = blockIdx.y, b = bh / s.H, h = bh % s.H, g = h / (s.H / s.G);
+  const int n0 = c * FT, nch = gridDim.x;
+  const int rows = max(0, min(FT, valid_rows(lengths, b, s.N) - n0));
+  const long r0 = (long)b * s.N + n0;
+  gates(dt + r0 * s.lddt + h, s.lddt, rows, par(bias, h), par(A, h), delta, cum, (float*)nullptr);
+  const float end = cum[63];
+  if (threadIdx.x == 0) tot[(long)bh * nch + c] = end;
+  const int tx0 = (threadIdx.x & 15) * (M / 16), ty0 = (threadIdx.x >> 4) * (D / 16);
+  for (int dir = 0; dir < (rev == nullptr ? 1 : 2); ++dir) {
+    stage<T, D>((dir ? Cm + r0 * s.ldc : Bm + r0 * s.ldb) + g * D, dir ? s.ldc : s.ldb, rows, tb, D + 4, nullptr);
+    stage<T, M>(dir ? dy + (r0 * s.H + h) * M : x + r0 * s.ldx + h * M, dir ? (long)s.H * M : s.ldx, rows, tx, M + 4, nullptr);
+    __syncthreads();
+    for (int e = threadIdx.x; e < FT * M; e += 256) {
+      const int r = e / M;
+      tx[r * (M + 4) + e % M] *= dir ? expf(cum[r]) : delta[r] * expf(end - cum[r]);
+    }
+    __syncthreads();
+    float acc[D / 16][M / 16];
+    zero_acc(acc);
+    ffma_mm(acc, tb, D + 4, tx, M + 4, FT);
+    float* o = (dir ? rev : fwd) + ((long)bh * nch + c) * D * M;
+#pragma unroll
+    for (int r = 0; r < D / 16; ++r)
+#pragma unroll
+      for (int q = 0; q < M / 16; ++q) o[(ty0 + r) * M + tx0 + q] = acc[r][q];
+    __syncthreads();
+  }
+}
+
+// In place, four values a thread: fwd[c] becomes the state before chunk c, rev[c] the state
+// gradient after it.  The chunk walk is a chain of one fused multiply-add; the
+// loads run eight chunks ahead of it.
+template <bool REV>
+__device__ __forceinline__ void carry_walk(float4* p, const float* tot, long step, int nch, float4& run) {
+  constexpr int U = 8;
+  for (int c0 = 0; c0 < nch; c0 += U) {
+    float4 v[U];
+    float e[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int k = c0 + i, c = REV ? nch - 1 - k : k;
+      if (k < nch) {
+        v[i] = p[c * step];
+        e[i] = expf(tot[c]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int k = c0 + i, c = REV ? nch - 1 - k : k;
+      if (k < nch) {
+        p[c * step] = run;
+        run.x = fmaf(e[i], run.x, v[i].x);
+        run.y = fmaf(e[i], run.y, v[i].y);
+        run.z = fmaf(e[i], run.z, v[i].z);
+        run.w = fmaf(e[i], run.w, v[i].w);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(128)
+    k_scan_carry(float* __restrict__ fwd, float* __restrict__ rev, const float* __restrict__ tot, float* __restrict__ S,
+                 int nch, int DM) {
+  const int e = (blockIdx.x * 128 + threadIdx.x) * 4;
+  const long bh = blockIdx.y;
+  if (e >= DM) return;
+  const float* tt = tot + bh * nch;
+  float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (blockIdx.z == 0) {
+    if (S != nullptr) run = *reinterpret_cast<const float4*>(S + bh * DM + e);
+    carry_walk<false>(reinterpret_cast<float4*>(fwd + bh * nch * DM + e), tt, DM / 4, nch, run);
+    if (S != nullptr) *reinterpret_cast<float4*>(S + bh * DM + e) = run;
+  } else {
+    carry_walk<true>(reinterpret_cast<float4*>(rev + bh * nch * DM + e), tt, DM / 4, nch, run);
+  }
+}
+
+// y of one chunk and head.
+template <int D, int M, typename T>
+__global__ void __launch_bounds__(256)
+    k_scan_out(const T* __restrict__ x, const T* __restrict__ dt, const T* __restrict__ A, const T* __restrict__ Bm,
+               const T* __restrict__ Cm, const T* __restrict__ skip, const T* __restrict__ bias,
+               const int* __restrict__ lengths, const float* __restrict__ prev, T* __restrict__ y, ScanShape s) {
+  extern __shared__ float sm[];
+  float* ct = sm;                   // C^T [D][FLD]
+  float* bt = ct + D * FLD;         // B^T [D][FLD]
+  float* xs = bt + D * FLD;         // x   [64][M + 4]
+  float* ss = xs + 64 * (M + 4);    // S_prev [D][M + 4]
+  float* pt = ss + D * (M + 4);     // P^T [64][FLD]
+  __shared__ float delta[64], cum[64];
+  const int c = blockIdx.x, bh = blockIdx.y, b = bh / s.H, h = bh % s.H, g = h / (s.H / s.G);
+  const int n0 = c * FT, nch = gridDim.x;
+  const int rows = max(0, min(FT, valid_rows(lengths, b, s.N) - n0));
+  const long r0 = (long)b * s.N + n0;
+  stage<T, D>(Cm + r0 * s.ldc + g * D, s.ldc, rows, nullptr, 0, ct);
+  stage<T, D>(Bm + r0 * s.ldb + g * D, s.ldb, rows, nullptr, 0, bt);
+  stage<T, M>(x + r0 * s.ldx + h * M, s.ldx, rows, xs, M + 4, nullptr);
+  if (prev != nullptr) stage_state<D, M>(prev + ((long)bh * nch + c) * D * M, ss, nullptr);
+  gates(dt + r0 * s.lddt + h, s.lddt, rows, par(bias, h), par(A, h), delta, cum, (float*)nullptr);
+  const int i0 = (threadIdx.x >> 4) * 4, j0 = (threadIdx.x & 15) * 4, m0 = (threadIdx.x & 15) * (M / 16);
+  {
+    float a[4][4];
+    zero_acc(a);
+    ffma_mm(a, ct, FLD, bt, FLD, D);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int i = i0 + r, j = j0 + q;
+        pt[j * FLD + i] = j <= i ? a[r][q] * delta[j] * expf(cum[i] - cum[j]) : 0.f;
+      }
+  }
+  __syncthreads();
+  float acc[4][M / 16];
+  zero_acc(acc);
+  if (prev != nullptr) {
+    ffma_mm(acc, ct, FLD, ss, M + 4, D);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int q = 0; q < M / 16; ++q) acc[r][q] *= expf(cum[i0 + r]);
+  }
+  ffma_mm(acc, pt, FLD, xs, M + 4, FT);
+  const float sk = par(skip, h);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int i = i0 + r;
+    if (n0 + i >= s.N) break;
+#pragma unroll
+    for (int q = 0; q < M / 16; ++q) acc[r][q] = i < rows ? fmaf(sk, xs[i * (M + 4) + m0 + q], acc[r][q]) : 0.f;
+    store_cols(y + ((r0 + i) * s.H + h) * M + m0, acc[r]);
+  }
+}
+
+// Gradients of one chunk and head: dx, ddt, this head's dB and dC (fp32, one
+// partial a head) and the chunk's parameter sums.
+template <int D, int M, typename T>
+__global__ void __launch_bounds__(256)
+    k_scan_grad(const T* __restrict__ x, const T* __restrict__ dt, const T* __restrict__ A, const T* __restrict__ Bm,
+                const T* __restrict__ Cm, const T* __restrict__ skip, const T* __restrict__ bias,
+                const int* __restrict__ lengths, const T* __restrict__ dy, const float* __restrict__ prev,
+                const float* __restrict__ next, T* __restrict__ dx, T* __restrict__ ddt, float* __restrict__ pB,
+                float* __restrict__ pC, float* __restrict__ pp, ScanShape s) {
+  extern __shared__ float sm[];
+  constexpr int TS = 64 * FLD;  // one tile of up to 64 x 64
+  float* ct = sm;               // C^T, then Q^T
+  float* bt = sm + TS;          // B^T
+  float* cn = sm + 2 * TS;      // C
+  float* bn = sm + 3 * TS;      // B
+  float* xt = sm + 4 * TS;      // x^T
+  float* gt = sm + 5 * TS;      // dy^T
+  float* gn = sm + 6 * TS;      // dy
+  float* pn = sm + 7 * TS;      // P
+  float* qn = sm + 8 * TS;      // Q
+  float* rn = sm + 9 * TS;      // R
+  float* rt = sm + 10 * TS;     // R^T
+  float* st = sm + 11 * TS;     // S_prev^T
+  __shared__ float delta[64], cum[64], z[64], rowg[64], v[64], w[64], xdu[64], colg[16][64], red[8];
+  const int c = blockIdx.x, bh = blockIdx.y, b = bh / s.H, h = bh % s.H, g = h / (s.H / s.G);
+  const int n0 = c * FT, nch = gridDim.x;
+  const int rows = max(0, min(FT, valid_rows(lengths, b, s.N) - n0));
+  const long r0 = (long)b * s.N + n0;
+  stage<T, D>(Cm + r0 * s.ldc + g * D, s.ldc, rows, cn, D + 4, ct);
+  stage<T, D>(Bm + r0 * s.ldb + g * D, s.ldb, rows, bn, D + 4, bt);
+  stage<T, M>(x + r0 * s.ldx + h * M, s.ldx, rows, nullptr, 0, xt);
+  stage<T, M>(dy + (r0 * s.H + h) * M, (long)s.H * M, rows, gn, M + 4, gt);
+  const float* Sp = prev + ((long)bh * nch + c) * D * M;
+  const float* Rp = next + ((long)bh * nch + c) * D * M;
+  stage_state<D, M>(Sp, nullptr, st);
+  stage_state<D, M>(Rp, rn, rt);
+  float sr = 0.f;
+  for (int e = threadIdx.x; e < D * M; e += 256) sr = fmaf(Sp[e], Rp[e], sr);
+  const float Ah = par(A, h), sk = par(skip, h);
+  gates(dt + r0 * s.lddt + h, s.lddt, rows, par(bias, h), Ah, delta, cum, z);
+  const float end = cum[63];
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15, i0 = ty * 4, j0 = tx * 4;
+  {
+    float a[4][4], e[4][4];
+    zero_acc(a);
+    zero_acc(e);
+    ffma_mm(a, ct, FLD, bt, FLD, D);
+    ffma_mm(e, gt, FLD, xt, FLD, M);
+    __syncthreads();  // C^T has been read: Q^T takes its place
+    float rs[4] = {0.f, 0.f, 0.f, 0.f}, cs[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + r, j = j0 + q;
+        const float wt = j <= i ? expf(cum[i] - cum[j]) : 0.f;
+        const float p = wt * a[r][q], qq = wt * delta[j] * e[r][q];
+        pn[i * FLD + j] = p;
+        qn[i * FLD + j] = qq;
+        ct[j * FLD + i] = qq;
+        if (j < i) {  // a pair with itself feels no decay
+          const float gg = qq * a[r][q];
+          rs[r] += gg;
+          cs[q] += gg;
+        }
+      }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float t = row_sum(rs[r]);
+      if (tx == 0) rowg[i0 + r] = t;
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) colg[ty][j0 + q] = cs[q];
+  }
+  __syncthreads();
+  const long prow = (r0 * s.H + h) * D;  // this head's partial of row n0
+  {
+    // dC
+    constexpr int CC = D / 16;
+    const int d0 = tx * CC;
+    float acc[4][CC];
+    zero_acc(acc);
+    ffma_mm(acc, gt, FLD, st, D + 4, M);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float f = expf(cum[i0 + r]);
+      float t = 0.f;
+#pragma unroll
+      for (int q = 0; q < CC; ++q) {
+        acc[r][q] *= f;
+        t = fmaf(acc[r][q], cn[(i0 + r) * (D + 4) + d0 + q], t);
+      }
+      t = row_sum(t);
+      if (tx == 0) v[i0 + r] = t;
+    }
+    ffma_mm(acc, ct, FLD, bn, D + 4, FT);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n0 + i0 + r < s.N) store_cols(pC + prow + (long)(i0 + r) * s.H * D + d0, acc[r]);
+    // dB
+    zero_acc(acc);
+    ffma_mm(acc, xt, FLD, rt, D + 4, M);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float f = delta[i0 + r] * expf(end - cum[i0 + r]);
+      float t = 0.f;
+#pragma unroll
+      for (int q = 0; q < CC; ++q) {
+        acc[r][q] *= f;
+        t = fmaf(acc[r][q], bn[(i0 + r) * (D + 4) + d0 + q], t);
+      }
+      t = row_sum(t);
+      if (tx == 0) w[i0 + r] = t;
+    }
+    ffma_mm(acc, qn, FLD, cn, D + 4, FT);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (n0 + i0 + r < s.N) store_cols(pB + prow + (long)(i0 + r) * s.H * D + d0, acc[r]);
+  }
+  float dskip = 0.f;
+  {
+    // dx
+    constexpr int CC = M / 16;
+    const int m0 = tx * CC;
+    float acc[4][CC];
+    zero_acc(acc);
+    ffma_mm(acc, bt, FLD, rn, M + 4, D);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int q = 0; q < CC; ++q) acc[r][q] *= expf(end - cum[i0 + r]);
+    ffma_mm(acc, pn, FLD, gn, M + 4, FT);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int j = i0 + r;
+      float t = 0.f;
+#pragma unroll
+      for (int q = 0; q < CC; ++q) {
+        const float xv = xt[(m0 + q) * FLD + j], gv = gn[j * (M + 4) + m0 + q];
+        t = fmaf(acc[r][q], xv, t);
+        dskip = fmaf(gv, xv, dskip);
+        acc[r][q] = fmaf(acc[r][q], delta[j], sk * gv);
+      }
+      t = row_sum(t);
+      if (tx == 0) xdu[j] = t;
+      if (n0 + j < s.N) store_cols(dx + ((r0 + j) * s.H + h) * M + m0, acc[r]);
+    }
+  }
+  sr = block_sum(sr, red);
+  dskip = block_sum(dskip, red);
+  __syncthreads();
+  float dA = 0.f, db = 0.f;
+  const int t = threadIdx.x;
+  if (t < 64) {
+    float dl = expf(end) * sr;
+    for (int i = t; i < 64; ++i) {
+      float cg = 0.f;
+#pragma unroll
+      for (int q = 0; q < 16; ++q) cg += colg[q][i];
+      dl += rowg[i] - cg + v[i];
+    }
+    for (int j = 0; j < t; ++j) dl += w[j];
+    const float dd = xdu[t] + Ah * dl;
+    const float dz = t < rows ? dd / (1.f + expf(-z[t])) : 0.f;
+    if (n0 + t < s.N) ddt[(r0 + t) * s.H + h] = from_f<T>(dz);
+    dA = delta[t] * dl;
+    db = dz;
+  }
+  dA = block_sum(dA, red);
+  db = block_sum(db, red);
+  if (t == 0) {
+    float* o = pp + ((long)bh * nch + c) * 3;
+    o[0] = dA, o[1] = dskip, o[2] = db;
+  }
+}
+
+// One head's parameter gradients: a block sums its B x nch chunks in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_scan_params(const float* __restrict__ pp, T* dA, T* dskip, T* dbias, int B, int H, int nch) {
+  __shared__ float red[8];
+  const int h = blockIdx.x;
+  float a[3] = {0.f, 0.f, 0.f};
+  for (long i = threadIdx.x; i < (long)B * nch; i += 256) {
+    const float* p = pp + ((i / nch * H + h) * nch + i % nch) * 3;
+    a[0] += p[0], a[1] += p[1], a[2] += p[2];
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const float t = block_sum(a[k], red);
+    if (threadIdx.x == 0) {
+      T* o = k == 0 ? dA : (k == 1 ? dskip : dbias);
+      if (o != nullptr) o[h] = from_f<T>(t);
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+    k_scan_groups(const float* __restrict__ pB, const float* __restrict__ pC, T* __restrict__ dB, T* __restrict__ dC, long n,
+                  int pg, int D4) {
+  const long e = (long)blockIdx.x * 256 + threadIdx.x;
+  if (e >= n) return;
+  const long row = e / D4;  // (b, n, g)
+  const int d = (int)(e % D4);
+  const float4* p = reinterpret_cast<const float4*>(blockIdx.y ? pC : pB) + row * pg * D4 + d;
+  float4 s = p[0];
+  for (int i = 1; i < pg; ++i) {
+    const float4 u = p[(long)i * D4];
+    s.x += u.x, s.y += u.y, s.z += u.z, s.w += u.w;
+  }
+  const float f[4] = {s.x, s.y, s.z, s.w};
+  store_cols((blockIdx.y ? dC : dB) + e * 4, f);
+}
+
+// One row for each stream: the state is read and written once (the traffic
+// that bounds the step), the read-out folded into the same pass.  Every thread
+// holds float4 columns of rows rg, rg + RG, ... .
+template <int D, int M, typename T>
+__global__ void __launch_bounds__(256)
+    k_scan_step(const T* __restrict__ x, const T* __restrict__ dt, const T* __restrict__ A, const T* __restrict__ Bm,
+                const T* __restrict__ Cm, const T* __restrict__ skip, const T* __restrict__ bias, float* __restrict__ S,
+                T* __restrict__ y, ScanShape s) {
+  constexpr int M4 = M / 4, RG = 256 / M4, RPT = (D + RG - 1) / RG;
+  __shared__ float sb[D], sc[D], su[M];
+  __shared__ float4 red[RG < D ? RG : D][M4];
+  const long bh = blockIdx.x;
+  const int b = (int)(bh / s.H), h = (int)(bh % s.H), g = h / (s.H / s.G), t = threadIdx.x;
+  const int c4 = t % M4, rg = t / M4;
+  float4* Sh = reinterpret_cast<float4*>(S + bh * D * M);
+  float4 r[RPT];
+#pragma unroll
+  for (int k = 0; k < RPT; ++k)
+    if (rg + k * RG < D) r[k] = Sh[(rg + k * RG) * M4 + c4];
+  const float delta = softplus(to_f(dt[(long)b * s.lddt + h]) + par(bias, h));
+  const float a = expf(delta * par(A, h));
+  if (t < D) {
+    sb[t] = to_f(Bm[(long)b * s.ldb + g * D + t]);
+    sc[t] = to_f(Cm[(long)b * s.ldc + g * D + t]);
+  }
+  if (t < M) su[t] = to_f(x[(long)b * s.ldx + h * M + t]);
+  __syncthreads();
+  float u[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = delta * su[4 * c4 + i];
+#pragma unroll
+  for (int k = 0; k < RPT; ++k) {
+    const int d = rg + k * RG;
+    if (d < D) {
+      const float bd = sb[d], cd = sc[d];
+      r[k].x = fmaf(a, r[k].x, bd * u[0]);
+      r[k].y = fmaf(a, r[k].y, bd * u[1]);
+      r[k].z = fmaf(a, r[k].z, bd * u[2]);
+      r[k].w = fmaf(a, r[k].w, bd * u[3]);
+      Sh[d * M4 + c4] = r[k];
+      acc[0] = fmaf(cd, r[k].x, acc[0]);
+      acc[1] = fmaf(cd, r[k].y, acc[1]);
+      acc[2] = fmaf(cd, r[k].z, acc[2]);
+      acc[3] = fmaf(cd, r[k].w, acc[3]);
+    }
+  }
+  if (rg < D) red[rg][c4] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  __syncthreads();
+  if (t < M) {
+    float o = par(skip, h) * su[t];
+    for (int k = 0; k < (RG < D ? RG : D); ++k) o += reinterpret_cast<const float*>(red[k])[t];
+    y[bh * M + t] = from_f<T>(o);
+  }
+}
+
+template <typename K>
+cudaError_t smem(K* k, size_t bytes) {
+  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+size_t align16(size_t n) { return (n + 15) / 16 * 16; }
+
+// The workspace of the fp32 path (bytes from its start).
+struct WsCC {
+  size_t tot, fwd, rev, pB, pC, pp, end;
+  WsCC(const ScanShape& s, bool bwd) {
+    const size_t BH = (size_t)s.B * s.H, nch = (s.N + FT - 1) / FT, st = BH * nch * s.D * s.M * 4;
+    tot = 0;
+    fwd = align16(BH * nch * 4);
+    rev = fwd + st;
+    end = rev;
+    if (bwd) {
+      const size_t part = (size_t)s.B * s.N * s.H * s.D * 4;
+      pB = rev + st;
+      pC = pB + part;
+      pp = pC + part;
+      end = pp + align16(BH * nch * 12);
+    }
+  }
+};
+
+}  // namespace
+
+#define LA_TRY_CUDA(x)                     \
+  do {                                     \
+    const cudaError_t e_ = (x);            \
+    if (e_ != cudaSuccess) return e_;      \
+  } while (0)
+
+size_t scan_cc_ws_bytes(const ScanShape& s, bool bwd) { return WsCC(s, bwd).end; }
+
+cudaError_t scan_carry(float* fwd, float* rev, const float* tot, float* S, int BH, int nch, int DM, cudaStream_t st) {
+  const dim3 grid((DM / 4 + 127) / 128, BH, rev == nullptr ? 1 : 2);
+  k_scan_carry<<<grid, 128, 0, st>>>(fwd, rev, tot, S, nch, DM);
+  return cudaGetLastError();
+}
+
+cudaError_t scan_params(const float* pp, void* dA, void* dskip, void* dbias, const ScanShape& s, int nch, cudaStream_t st) {
+  if (s.dtype == 0)
+    k_scan_params<float><<<s.H, 256, 0, st>>>(pp, (float*)dA, (float*)dskip, (float*)dbias, s.B, s.H, nch);
+  else
+    k_scan_params<bf16><<<s.H, 256, 0, st>>>(pp, (bf16*)dA, (bf16*)dskip, (bf16*)dbias, s.B, s.H, nch);
+  return cudaGetLastError();
+}
+
+cudaError_t scan_groups(const float* pB, const float* pC, void* dB, void* dC, const ScanShape& s, int pg, cudaStream_t st) {
+  const long n = (long)s.B * s.N * s.G * (s.D / 4);
+  const dim3 grid((unsigned)((n + 255) / 256), 2);
+  if (s.dtype == 0)
+    k_scan_groups<float><<<grid, 256, 0, st>>>(pB, pC, (float*)dB, (float*)dC, n, pg, s.D / 4);
+  else
+    k_scan_groups<bf16><<<grid, 256, 0, st>>>(pB, pC, (bf16*)dB, (bf16*)dC, n, pg, s.D / 4);
+  return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t fwd_cc(const ScanIn& a, float* S, void* y, char* ws, const ScanShape& s, cudaStream_t st) {
+  const WsCC w(s, false);
+  const int nch = (s.N + FT - 1) / FT, BH = s.B * s.H;
+  float *tot = (float*)(ws + w.tot), *fwd = (float*)(ws + w.fwd);
+  const bool states = nch > 1 || S != nullptr;
+  const dim3 grid(nch, BH);
+  const T *x = (const T*)a.x, *dt = (const T*)a.dt, *A = (const T*)a.A, *Bm = (const T*)a.B, *Cm = (const T*)a.C,
+          *skip = (const T*)a.skip, *bias = (const T*)a.dt_bias;
+  LA_DISPATCH_DM(s.D, s.M, {
+    if (states) {
+      constexpr size_t b1 = 64 * (D_ + M_ + 8) * 4;
+      k_scan_sums<D_, M_, T><<<grid, 256, b1, st>>>(x, dt, A, Bm, Cm, bias, a.lengths, nullptr, fwd, nullptr, tot, s);
+      LA_TRY_CUDA(cudaGetLastError());
+      LA_TRY_CUDA(scan_carry(fwd, nullptr, tot, S, BH, nch, D_ * M_, st));
+    }
+    constexpr size_t b2 = (2 * D_ * FLD + 64 * (M_ + 4) + D_ * (M_ + 4) + 64 * FLD) * 4;
+    LA_TRY_CUDA(smem(&k_scan_out<D_, M_, T>, b2));
+    k_scan_out<D_, M_, T><<<grid, 256, b2, st>>>(x, dt, A, Bm, Cm, skip, bias, a.lengths, states ? fwd : nullptr, (T*)y, s);
+  });
+  return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t bwd_cc(const ScanIn& a, const void* dy, const ScanGrads& d, char* ws, const ScanShape& s, cudaStream_t st) {
+  const WsCC w(s, true);
+  const int nch = (s.N + FT - 1) / FT, BH = s.B * s.H;
+  float *tot = (float*)(ws + w.tot), *fwd = (float*)(ws + w.fwd), *rev = (float*)(ws + w.rev), *pB = (float*)(ws + w.pB),
+        *pC = (float*)(ws + w.pC), *pp = (float*)(ws + w.pp);
+  const dim3 grid(nch, BH);
+  const T *x = (const T*)a.x, *dt = (const T*)a.dt, *A = (const T*)a.A, *Bm = (const T*)a.B, *Cm = (const T*)a.C,
+          *skip = (const T*)a.skip, *bias = (const T*)a.dt_bias;
+  LA_DISPATCH_DM(s.D, s.M, {
+    constexpr size_t b1 = 64 * (D_ + M_ + 8) * 4;
+    k_scan_sums<D_, M_, T><<<grid, 256, b1, st>>>(x, dt, A, Bm, Cm, bias, a.lengths, (const T*)dy, fwd, rev, tot, s);
+    LA_TRY_CUDA(cudaGetLastError());
+    LA_TRY_CUDA(scan_carry(fwd, rev, tot, nullptr, BH, nch, D_ * M_, st));
+    constexpr size_t b2 = 12 * 64 * FLD * 4;
+    LA_TRY_CUDA(smem(&k_scan_grad<D_, M_, T>, b2));
+    k_scan_grad<D_, M_, T><<<grid, 256, b2, st>>>(x, dt, A, Bm, Cm, skip, bias, a.lengths, (const T*)dy, fwd, rev, (T*)d.x,
+                                                 (T*)d.dt, pB, pC, pp, s);
+  });
+  LA_TRY_CUDA(cudaGetLastError());
+  LA_TRY_CUDA(scan_groups(pB, pC, d.B, d.C, s, s.H / s.G, st));
+  return scan_params(pp, d.A, d.skip, d.dt_bias, s, nch, st);
+}
+
+cudaError_t scan_fwd_cc(const ScanIn& a, float* S, void* y, void* ws, const ScanShape& s, cudaStream_t st) {
+  return s.dtype == 0 ? fwd_cc<float>(a, S, y, (char*)ws, s, st) : fwd_cc<bf16>(a, S, y, (char*)ws, s, st);
+}
+
+cudaError_t scan_bwd_cc(const ScanIn& a, const void* dy, const ScanGrads& d, void* ws, const ScanShape& s, cudaStream_t st) {
+  return s.dtype == 0 ? bwd_cc<float>(a, dy, d, (char*)ws, s, st) : bwd_cc<bf16>(a, dy, d, (char*)ws, s, st);
+}
+
+template <typename T>
+static cudaError_t step(const ScanIn& a, float* S, void* y, const ScanShape& s, cudaStream_t st) {
+  LA_DISPATCH_DM(s.D, s.M, (k_scan_step<D_, M_, T><<<s.B * s.H, 256, 0, st>>>((const T*)a.x, (const T*)a.dt, (const T*)a.A,
+                                                                             (const T*)a.B, (const T*)a.C, (const T*)a.skip,
+                                                                             (const T*)a.dt_bias, S, (T*)y, s)));
+  return cudaGetLastError();
+}
+
+cudaError_t scan_step(const ScanIn& a, float* S, void* y, const ScanShape& s, cudaStream_t st) {
+  return s.dtype == 0 ? step<float>(a, S, y, s, st) : step<bf16>(a, S, y, s, st);
+}
+
+}  // namespace la

@@ -1,0 +1,46 @@
+// Shared by the selective scan's CUDA-core (scan.cu) and tensor-core
+// (scan_tc.cu) kernels: the call's sizes and pointers, and the gate.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace la {
+
+// softplus(x) = log(1 + exp(x)), written so that neither branch overflows.
+__device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+
+__device__ __forceinline__ int valid_rows(const int* lengths, int b, int N) {
+  return lengths == nullptr ? N : min(max(lengths[b], 0), N);
+}
+
+// Element h of a per-head parameter vector that may be absent.
+template <typename T>
+__device__ __forceinline__ float par(const T* p, int h) { return p == nullptr ? 0.f : to_f(p[h]); }
+
+// Inclusive prefix sum over a warp.
+__device__ __forceinline__ float warp_prefix(float v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// The chunks' states: ws holds [BH][nch][D M] partial sums on entry of the
+// carry, the state before (fwd) or the state gradient after (rev) each chunk on
+// return; tot holds [BH][nch] log decays of whole chunks.  T_ = what the carried
+// states are stored as (over the fp32 partial sums' own place, or bf16 in `out`).
+cudaError_t scan_carry(float* fwd, float* rev, const float* tot, float* S, int BH, int nch, int DM, cudaStream_t st);
+
+// Sums the per-chunk parameter gradients pp[BH][nch][3] (A, skip, dt_bias) over
+// the batch and the chunks, in a fixed order.
+cudaError_t scan_params(const float* pp, void* dA, void* dskip, void* dbias, const ScanShape& s, int nch, cudaStream_t st);
+
+// dB and dC from fp32 partial sums [B N][parts][D] each (parts per group
+// neighbouring, parts = G pg): pg partials a value, summed in order.
+cudaError_t scan_groups(const float* pB, const float* pC, void* dB, void* dC, const ScanShape& s, int pg, cudaStream_t st);
+
+}  // namespace la

@@ -1,0 +1,378 @@
+// Short causal depthwise convolution over token-major rows, the layer in front
+// of the selective scan:
+//   pre[t][c] = bias[c] + sum_j w[c][j] x[t - K + 1 + j][c],   y = silu(pre) or pre,
+// with K = 2, 3 or 4 taps and rows before the first one taken from a history
+// (the last K - 1 inputs, oldest first) or zero.  Gradients, with g = dy silu'(pre):
+//   dx[t] = sum_j w[j] g[t + K - 1 - j],  dw[j] = sum_t g[t] x[t - K + 1 + j],  db = sum_t g[t].
+//
+// All three directions are bound by HBM traffic (about 2 K flops an element).
+// A thread owns V neighbouring channels and walks a run of rows with the last K
+// inputs (and, backward, the last K values of g) in registers, so every row is
+// read once plus the K - 1 rows (backward 2 (K - 1)) before a run.  Sums and
+// SiLU are fp32; y, dx and the parameters' gradients are rounded once.
+#include "common.cuh"
+#include "launch.h"
+
+namespace la {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+// V neighbouring channels, loaded as one vector where V > 1 (the caller has
+// checked the alignment) and kept as fp32.
+template <typename T, int V>
+struct Pack {
+  static_assert(sizeof(T) * V <= 16, "one load");
+  __device__ __forceinline__ static void ld(const T* p, float (&f)[V]) {
+    if constexpr (V == 1) {
+      f[0] = to_f(*p);
+    } else if constexpr (sizeof(T) == 4) {
+      const float4 u = *reinterpret_cast<const float4*>(p);
+      f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      f[0] = __uint_as_float(u.x << 16), f[1] = __uint_as_float(u.x & 0xffff0000u);
+      f[2] = __uint_as_float(u.y << 16), f[3] = __uint_as_float(u.y & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ static void st(T* p, const float (&f)[V]) {
+    if constexpr (V == 1) {
+      *p = from_f<T>(f[0]);
+    } else if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+      *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+  }
+};
+
+template <int V>
+__device__ __forceinline__ void zero(float (&f)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] = 0.f;
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+
+__device__ __forceinline__ int rows_of(const int* lengths, int b, int N) {
+  return lengths == nullptr ? N : min(max(lengths[b], 0), N);
+}
+
+constexpr int FWD_RUN = 16;   // rows a thread walks (forward)
+constexpr int BWD_RUN = 32;   // rows a thread walks (backward)
+constexpr int CG = 32;        // channel groups a block spans
+constexpr int RG = 8;         // row runs a block spans
+constexpr int BWD_ROWS = BWD_RUN * RG;
+
+// y, and the history in place.  Rows at or past the sequence's length are
+// written as zeros and not read.  The block of the first row group alone reads
+// the history and, after a barrier, writes the new one.
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(CG * RG)
+    k_conv_fwd(const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const int* __restrict__ lengths,
+               T* state, T* __restrict__ y, int N, int C, long ldx, int silu) {
+  const int c = (blockIdx.x * CG + threadIdx.x) * V;
+  const int b = blockIdx.z;
+  const bool live = c < C;
+  const int L = rows_of(lengths, b, N);
+  const T* xb = x + (long)b * N * ldx + c;
+  T* sb = state == nullptr ? nullptr : state + (long)b * (K - 1) * C + c;
+  // grid.y is capped: a block walks row groups at the grid's stride
+  for (int rg = blockIdx.y; (long)rg * RG * FWD_RUN < N; rg += gridDim.y) {
+    const int t0 = (rg * RG + threadIdx.y) * FWD_RUN;
+    if (live && t0 < N) {
+      float wk[K][V], bs[V], h[K][V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        bs[i] = bias == nullptr ? 0.f : to_f(bias[c + i]);
+#pragma unroll
+        for (int j = 0; j < K; ++j) wk[j][i] = to_f(w[(long)(c + i) * K + j]);
+      }
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) {  // the K - 1 rows before the run
+        const int t = t0 - (K - 1) + j;
+        if (t >= 0 && t < L)
+          Pack<T, V>::ld(xb + t * ldx, h[j + 1]);
+        else if (t < 0 && sb != nullptr)
+          Pack<T, V>::ld(sb + (long)(t + K - 1) * C, h[j + 1]);
+        else
+          zero(h[j + 1]);
+      }
+      T* yb = y + ((long)b * N + t0) * C + c;
+#pragma unroll 4
+      for (int r = 0; r < FWD_RUN; ++r) {
+        const int t = t0 + r;
+        if (t >= N) break;
+        float o[V];
+        if (t < L) {
+#pragma unroll
+          for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i];
+          Pack<T, V>::ld(xb + t * ldx, h[K - 1]);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float p = bs[i];
+#pragma unroll
+            for (int j = 0; j < K; ++j) p = fmaf(wk[j][i], h[j][i], p);
+            o[i] = silu ? p * sigmoid(p) : p;
+          }
+        } else {
+          zero(o);
+        }
+        Pack<T, V>::st(yb + (long)r * C, o);
+      }
+    }
+    if (rg == 0 && state != nullptr) {
+      __syncthreads();  // the history's readers are this block's first rows
+      if (live && threadIdx.y == 0) {
+        float n[K - 1][V];
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) {
+          const int t = L - (K - 1) + j;
+          if (t >= 0)
+            Pack<T, V>::ld(xb + t * ldx, n[j]);
+          else
+            Pack<T, V>::ld(sb + (long)(t + K - 1) * C, n[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j) Pack<T, V>::st(sb + (long)j * C, n[j]);
+      }
+    }
+  }
+}
+
+// dx, and each block's sums of g x and g over its BWD_ROWS rows into
+// part[group][K + 1][C] (fp32; the last plane is the bias's).  History zero.
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(CG * RG)
+    k_conv_bwd(const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const int* __restrict__ lengths,
+               const T* __restrict__ dy, T* __restrict__ dx, float* __restrict__ part, int N, int C, long ldx, int silu,
+               int groups) {
+  __shared__ float red[RG][CG * V];
+  const int c = (blockIdx.x * CG + threadIdx.x) * V;
+  const bool live = c < C;
+  const int b = blockIdx.z;
+  const int L = rows_of(lengths, b, N);
+  const T* xb = x + (long)b * N * ldx + c;
+  const T* gb = dy + (long)b * N * C + c;
+  T* ob = dx + (long)b * N * C + c;
+  float wk[K][V], bs[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    bs[i] = live && bias != nullptr ? to_f(bias[c + i]) : 0.f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) wk[j][i] = live ? to_f(w[(long)(c + i) * K + j]) : 0.f;
+  }
+  for (int rg = blockIdx.y; rg < groups; rg += gridDim.y) {
+    float sums[K + 1][V];
+#pragma unroll
+    for (int j = 0; j <= K; ++j) zero(sums[j]);
+    const int t0 = rg * BWD_ROWS + threadIdx.y * BWD_RUN;
+    if (live && t0 < N) {
+      // h: x rows t - K + 1 .. t;  g: rows t - K + 1 .. t of dy silu'(pre).
+      // Row t's g completes dx of row t - K + 1, so the run looks K - 1 rows ahead.
+      float h[K][V], g[K][V];
+#pragma unroll
+      for (int j = 0; j < K; ++j) zero(g[j]);
+#pragma unroll
+      for (int j = 0; j < K - 1; ++j) {
+        const int t = t0 - (K - 1) + j;
+        if (t >= 0 && t < L)
+          Pack<T, V>::ld(xb + t * ldx, h[j + 1]);
+        else
+          zero(h[j + 1]);
+      }
+#pragma unroll 2
+      for (int r = 0; r < BWD_RUN + K - 1; ++r) {
+        const int t = t0 + r;
+#pragma unroll
+        for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+          for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i], g[j][i] = g[j + 1][i];
+        if (t < L) {
+          float d[V];
+          Pack<T, V>::ld(xb + t * ldx, h[K - 1]);
+          Pack<T, V>::ld(gb + (long)t * C, d);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            if (silu) {
+              float p = bs[i];
+#pragma unroll
+              for (int j = 0; j < K; ++j) p = fmaf(wk[j][i], h[j][i], p);
+              const float s = sigmoid(p);
+              d[i] *= s * (1.f + p * (1.f - s));
+            }
+            g[K - 1][i] = d[i];
+            if (r < BWD_RUN) {
+              sums[K][i] += d[i];
+#pragma unroll
+              for (int j = 0; j < K; ++j) sums[j][i] = fmaf(d[i], h[j][i], sums[j][i]);
+            }
+          }
+        } else {
+          zero(h[K - 1]);
+          zero(g[K - 1]);
+        }
+        const int to = t - (K - 1);  // the row that is complete
+        if (r >= K - 1 && to < N) {
+          float o[V];
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float s = 0.f;
+#pragma unroll
+            for (int j = 0; j < K; ++j) s = fmaf(wk[K - 1 - j][i], g[j][i], s);
+            o[i] = to < L ? s : 0.f;
+          }
+          Pack<T, V>::st(ob + (long)to * C, o);
+        }
+      }
+    }
+    float* pb = part + ((long)b * groups + rg) * (K + 1) * C;
+#pragma unroll
+    for (int j = 0; j <= K; ++j) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < V; ++i) red[threadIdx.y][threadIdx.x * V + i] = sums[j][i];
+      __syncthreads();
+      for (int e = threadIdx.y * CG + threadIdx.x; e < CG * V; e += CG * RG) {
+        const int ch = blockIdx.x * CG * V + e;
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < RG; ++q) s += red[q][e];
+        if (ch < C) pb[(long)j * C + ch] = s;
+      }
+    }
+  }
+}
+
+// dw[c][j] and db[c] from the P blocks' sums, in a fixed order: RS threads a
+// value, each a strided share, joined in shared memory.
+constexpr int RS = 8;
+template <typename T>
+__global__ void __launch_bounds__(32 * RS)
+    k_conv_sum(const float* __restrict__ part, T* __restrict__ dw, T* __restrict__ db, int P, int C, int K) {
+  __shared__ float red[RS][32];
+  const int c = blockIdx.x * 32 + threadIdx.x, j = blockIdx.y;
+  float s = 0.f;
+  if (c < C) {
+    const float* p = part + (long)j * C + c;
+    const long stride = (long)(K + 1) * C;
+#pragma unroll 4
+    for (int i = threadIdx.y; i < P; i += RS) s += p[i * stride];
+  }
+  red[threadIdx.y][threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.y == 0 && c < C) {
+    for (int q = 1; q < RS; ++q) s += red[q][threadIdx.x];
+    if (j < K)
+      dw[(long)c * K + j] = from_f<T>(s);
+    else if (db != nullptr)
+      db[c] = from_f<T>(s);
+  }
+}
+
+// One row for each of B streams: y, and the history shifted in place.
+template <typename T, int V, int K>
+__global__ void __launch_bounds__(128)
+    k_conv_step(const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, T* __restrict__ state,
+                T* __restrict__ y, int B, int C, long ldx, int silu) {
+  const int per = C / V;
+  const long e = (long)blockIdx.x * 128 + threadIdx.x;
+  if (e >= (long)B * per) return;
+  const int b = (int)(e / per), c = (int)(e % per) * V;
+  float h[K][V], o[V];
+  T* sb = state + (long)b * (K - 1) * C + c;
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) Pack<T, V>::ld(sb + (long)j * C, h[j]);
+  Pack<T, V>::ld(x + b * ldx + c, h[K - 1]);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float p = bias == nullptr ? 0.f : to_f(bias[c + i]);
+#pragma unroll
+    for (int j = 0; j < K; ++j) p = fmaf(to_f(w[(long)(c + i) * K + j]), h[j][i], p);
+    o[i] = silu ? p * sigmoid(p) : p;
+  }
+  Pack<T, V>::st(y + (long)b * C + c, o);
+#pragma unroll
+  for (int j = 0; j < K - 1; ++j) Pack<T, V>::st(sb + (long)j * C, h[j + 1]);
+}
+
+int bwd_groups(int N) { return (N + BWD_ROWS - 1) / BWD_ROWS; }
+
+// Vectors of four channels where every row starts on a vector: C and the row
+// stride multiples of four and every base aligned to four elements (all but x
+// are 16-byte aligned by the interface).  Measured against one channel a
+// thread: see the sizes in the tests; the scalar form takes the rest.
+bool by_four(const void* x, int C, long ldx, size_t elem) {
+  return C % 4 == 0 && ldx % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * elem) == 0;
+}
+
+#define LA_CONV_CASE(T, V, Kv, BODY) \
+  { using T_ = T; constexpr int V_ = V, K_ = Kv; BODY; }
+#define LA_CONV_K(T, V, K, BODY)             \
+  do {                                       \
+    if ((K) == 2) LA_CONV_CASE(T, V, 2, BODY) \
+    else if ((K) == 3) LA_CONV_CASE(T, V, 3, BODY) \
+    else LA_CONV_CASE(T, V, 4, BODY)          \
+  } while (0)
+#define LA_CONV_DISPATCH(dtype, four, K, BODY)        \
+  do {                                                \
+    if ((dtype) == 0) {                               \
+      if (four) LA_CONV_K(float, 4, K, BODY);         \
+      else LA_CONV_K(float, 1, K, BODY);              \
+    } else {                                          \
+      if (four) LA_CONV_K(bf16, 4, K, BODY);          \
+      else LA_CONV_K(bf16, 1, K, BODY);               \
+    }                                                 \
+  } while (0)
+
+}  // namespace
+
+size_t short_conv_bwd_ws_bytes(const ConvShape& s) {
+  return sizeof(float) * s.B * (size_t)bwd_groups(s.N) * (s.K + 1) * s.C;
+}
+
+cudaError_t short_conv_fwd(const void* x, const void* w, const void* bias, const int* lengths, void* state, void* y,
+                           const ConvShape& s, cudaStream_t st) {
+  const bool four = by_four(x, s.C, s.ldx, s.dtype == 0 ? 4 : 2);
+  const int per = CG * (four ? 4 : 1);
+  const int rg = (s.N + RG * FWD_RUN - 1) / (RG * FWD_RUN);
+  const dim3 grid((s.C + per - 1) / per, rg < 65535 ? rg : 65535, s.B), block(CG, RG);
+  LA_CONV_DISPATCH(s.dtype, four, s.K,
+                   (k_conv_fwd<T_, V_, K_><<<grid, block, 0, st>>>((const T_*)x, (const T_*)w, (const T_*)bias, lengths,
+                                                                   (T_*)state, (T_*)y, s.N, s.C, s.ldx, s.silu)));
+  return cudaGetLastError();
+}
+
+cudaError_t short_conv_bwd(const void* x, const void* w, const void* bias, const int* lengths, const void* dy, void* dx,
+                           void* dw, void* db, float* ws, const ConvShape& s, cudaStream_t st) {
+  const bool four = by_four(x, s.C, s.ldx, s.dtype == 0 ? 4 : 2);
+  const int per = CG * (four ? 4 : 1), groups = bwd_groups(s.N);
+  const dim3 grid((s.C + per - 1) / per, groups < 65535 ? groups : 65535, s.B), block(CG, RG);
+  LA_CONV_DISPATCH(s.dtype, four, s.K,
+                   (k_conv_bwd<T_, V_, K_><<<grid, block, 0, st>>>((const T_*)x, (const T_*)w, (const T_*)bias, lengths,
+                                                                   (const T_*)dy, (T_*)dx, ws, s.N, s.C, s.ldx, s.silu,
+                                                                   groups)));
+  const dim3 sgrid((s.C + 31) / 32, s.K + 1), sblock(32, RS);
+  const int P = s.B * groups;
+  if (s.dtype == 0)
+    k_conv_sum<float><<<sgrid, sblock, 0, st>>>(ws, (float*)dw, (float*)db, P, s.C, s.K);
+  else
+    k_conv_sum<bf16><<<sgrid, sblock, 0, st>>>(ws, (bf16*)dw, (bf16*)db, P, s.C, s.K);
+  return cudaGetLastError();
+}
+
+cudaError_t short_conv_step(const void* x, const void* w, const void* bias, void* state, void* y, const ConvShape& s,
+                            cudaStream_t st) {
+  const bool four = by_four(x, s.C, s.ldx, s.dtype == 0 ? 4 : 2);
+  const long n = (long)s.B * (s.C / (four ? 4 : 1));
+  const unsigned grid = (unsigned)((n + 127) / 128);
+  LA_CONV_DISPATCH(s.dtype, four, s.K,
+                   (k_conv_step<T_, V_, K_><<<grid, 128, 0, st>>>((const T_*)x, (const T_*)w, (const T_*)bias, (T_*)state,
+                                                                  (T_*)y, s.B, s.C, s.ldx, s.silu)));
+  return cudaGetLastError();
+}
+
+}  // namespace la
