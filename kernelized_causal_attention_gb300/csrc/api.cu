@@ -138,7 +138,9 @@ int check_room(const void* ws, size_t bytes, size_t need) {
   return aligned16(ws) ? LA_OK : LA_ERR_INVALID_ARG;
 }
 
-size_t scan_ws(const la::ScanShape& s, bool bwd) { return la::scan_cc_ws_bytes(s, bwd); }
+size_t scan_ws(const la::ScanShape& s, bool bwd) {
+  return s.dtype == LA_BF16 && !bwd ? la::scan_tc_ws_bytes(s) : la::scan_cc_ws_bytes(s, bwd);
+}
 
 }  // namespace
 
@@ -427,7 +429,8 @@ int la_scan_fwd(const void* x, const void* dt, const void* A, const void* Bm, co
   LA_TRY(check_to(lengths, 4, true));
   LA_TRY(check_room(workspace, workspace_bytes, scan_ws(s, false)));
   const la::ScanIn a{x, dt, A, Bm, Cm, skip, dt_bias, lengths};
-  return from_cuda(la::scan_fwd_cc(a, S, y, workspace, s, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return from_cuda(dtype == LA_BF16 ? la::scan_fwd_tc(a, S, y, workspace, s, st) : la::scan_fwd_cc(a, S, y, workspace, s, st));
 }
 
 int la_scan_bwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* skip,

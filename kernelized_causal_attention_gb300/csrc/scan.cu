@@ -96,11 +96,18 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// In place, four values a thread: fwd[c] becomes the state before chunk c, rev[c] the state
-// gradient after it.  The chunk walk is a chain of one fused multiply-add; the
-// loads run eight chunks ahead of it.
-template <bool REV>
-__device__ __forceinline__ void carry_walk(float4* p, const float* tot, long step, int nch, float4& run) {
+__device__ __forceinline__ void put4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void put4(bf16* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// Four values a thread: out[c] becomes the state before chunk c (REV: the state
+// gradient after it) from the chunks' own sums p, which may be the same memory.
+// The chunk walk is a chain of one fused multiply-add; the loads run eight
+// chunks ahead of it.
+template <bool REV, typename O>
+__device__ __forceinline__ void carry_walk(const float* p, O* out, const float* tot, long step, int nch, float4& run) {
   constexpr int U = 8;
   for (int c0 = 0; c0 < nch; c0 += U) {
     float4 v[U];
@@ -109,7 +116,7 @@ __device__ __forceinline__ void carry_walk(float4* p, const float* tot, long ste
     for (int i = 0; i < U; ++i) {
       const int k = c0 + i, c = REV ? nch - 1 - k : k;
       if (k < nch) {
-        v[i] = p[c * step];
+        v[i] = *reinterpret_cast<const float4*>(p + c * step);
         e[i] = expf(tot[c]);
       }
     }
@@ -117,7 +124,7 @@ __device__ __forceinline__ void carry_walk(float4* p, const float* tot, long ste
     for (int i = 0; i < U; ++i) {
       const int k = c0 + i, c = REV ? nch - 1 - k : k;
       if (k < nch) {
-        p[c * step] = run;
+        put4(out + c * step, run);
         run.x = fmaf(e[i], run.x, v[i].x);
         run.y = fmaf(e[i], run.y, v[i].y);
         run.z = fmaf(e[i], run.z, v[i].z);
@@ -127,20 +134,22 @@ __device__ __forceinline__ void carry_walk(float4* p, const float* tot, long ste
   }
 }
 
+template <typename O>
 __global__ void __launch_bounds__(128)
-    k_scan_carry(float* __restrict__ fwd, float* __restrict__ rev, const float* __restrict__ tot, float* __restrict__ S,
+    k_scan_carry(const float* fwd, const float* rev, O* fs, O* rs, const float* __restrict__ tot, float* __restrict__ S,
                  int nch, int DM) {
   const int e = (blockIdx.x * 128 + threadIdx.x) * 4;
   const long bh = blockIdx.y;
   if (e >= DM) return;
   const float* tt = tot + bh * nch;
+  const long at = bh * nch * DM + e;
   float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
   if (blockIdx.z == 0) {
     if (S != nullptr) run = *reinterpret_cast<const float4*>(S + bh * DM + e);
-    carry_walk<false>(reinterpret_cast<float4*>(fwd + bh * nch * DM + e), tt, DM / 4, nch, run);
+    carry_walk<false>(fwd + at, fs + at, tt, DM, nch, run);
     if (S != nullptr) *reinterpret_cast<float4*>(S + bh * DM + e) = run;
   } else {
-    carry_walk<true>(reinterpret_cast<float4*>(rev + bh * nch * DM + e), tt, DM / 4, nch, run);
+    carry_walk<true>(rev + at, rs + at, tt, DM, nch, run);
   }
 }
 
@@ -507,10 +516,21 @@ struct WsCC {
 
 size_t scan_cc_ws_bytes(const ScanShape& s, bool bwd) { return WsCC(s, bwd).end; }
 
-cudaError_t scan_carry(float* fwd, float* rev, const float* tot, float* S, int BH, int nch, int DM, cudaStream_t st) {
+template <typename O>
+static cudaError_t carry(const float* fwd, const float* rev, O* fs, O* rs, const float* tot, float* S, int BH, int nch, int DM,
+                         cudaStream_t st) {
   const dim3 grid((DM / 4 + 127) / 128, BH, rev == nullptr ? 1 : 2);
-  k_scan_carry<<<grid, 128, 0, st>>>(fwd, rev, tot, S, nch, DM);
+  k_scan_carry<<<grid, 128, 0, st>>>(fwd, rev, fs, rs, tot, S, nch, DM);
   return cudaGetLastError();
+}
+
+cudaError_t scan_carry(float* fwd, float* rev, const float* tot, float* S, int BH, int nch, int DM, cudaStream_t st) {
+  return carry(fwd, rev, fwd, rev, tot, S, BH, nch, DM, st);
+}
+
+cudaError_t scan_carry_bf16(const float* fwd, const float* rev, void* fs, void* rs, const float* tot, float* S, int BH,
+                            int nch, int DM, cudaStream_t st) {
+  return carry(fwd, rev, (bf16*)fs, (bf16*)rs, tot, S, BH, nch, DM, st);
 }
 
 cudaError_t scan_params(const float* pp, void* dA, void* dskip, void* dbias, const ScanShape& s, int nch, cudaStream_t st) {

@@ -29,11 +29,14 @@ __device__ __forceinline__ float warp_prefix(float v) {
   return v;
 }
 
-// The chunks' states: ws holds [BH][nch][D M] partial sums on entry of the
-// carry, the state before (fwd) or the state gradient after (rev) each chunk on
-// return; tot holds [BH][nch] log decays of whole chunks.  T_ = what the carried
-// states are stored as (over the fp32 partial sums' own place, or bf16 in `out`).
+// The carry over the chunks: fwd (and rev) hold [BH][nch][D M] chunk sums, tot
+// [BH][nch] the chunks' log decays.  On return fwd[c] holds the state before
+// chunk c and rev[c] the state gradient after it; S, if given, is the state to
+// start from and becomes the last one.
 cudaError_t scan_carry(float* fwd, float* rev, const float* tot, float* S, int BH, int nch, int DM, cudaStream_t st);
+// The same, with the carried states rounded to bf16 into fs (and rs).
+cudaError_t scan_carry_bf16(const float* fwd, const float* rev, void* fs, void* rs, const float* tot, float* S, int BH,
+                            int nch, int DM, cudaStream_t st);
 
 // Sums the per-chunk parameter gradients pp[BH][nch][3] (A, skip, dt_bias) over
 // the batch and the chunks, in a fixed order.
