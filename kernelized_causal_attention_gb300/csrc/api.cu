@@ -139,7 +139,7 @@ int check_room(const void* ws, size_t bytes, size_t need) {
 }
 
 size_t scan_ws(const la::ScanShape& s, bool bwd) {
-  return s.dtype == LA_BF16 && !bwd ? la::scan_tc_ws_bytes(s) : la::scan_cc_ws_bytes(s, bwd);
+  return s.dtype == LA_BF16 ? la::scan_tc_ws_bytes(s, bwd) : la::scan_cc_ws_bytes(s, bwd);
 }
 
 }  // namespace
@@ -449,7 +449,8 @@ int la_scan_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   LA_TRY(check_room(workspace, workspace_bytes, scan_ws(s, true)));
   const la::ScanIn a{x, dt, A, Bm, Cm, skip, dt_bias, lengths};
   const la::ScanGrads d{dx, ddt, dA, dB, dC, dskip, ddt_bias};
-  return from_cuda(la::scan_bwd_cc(a, dy, d, workspace, s, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return from_cuda(dtype == LA_BF16 ? la::scan_bwd_tc(a, dy, d, workspace, s, st) : la::scan_bwd_cc(a, dy, d, workspace, s, st));
 }
 
 int la_scan_step(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm, const void* skip,

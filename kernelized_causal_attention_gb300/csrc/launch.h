@@ -185,7 +185,8 @@ struct ScanGrads {
 size_t scan_cc_ws_bytes(const ScanShape& s, bool bwd);
 cudaError_t scan_fwd_cc(const ScanIn& a, float* S, void* y, void* ws, const ScanShape& s, cudaStream_t st);
 cudaError_t scan_bwd_cc(const ScanIn& a, const void* dy, const ScanGrads& d, void* ws, const ScanShape& s, cudaStream_t st);
-size_t scan_tc_ws_bytes(const ScanShape& s);  // bf16, on the tensor cores (scan_tc.cu)
+size_t scan_tc_ws_bytes(const ScanShape& s, bool bwd);  // bf16, on the tensor cores (scan_tc.cu)
+cudaError_t scan_bwd_tc(const ScanIn& a, const void* dy, const ScanGrads& d, void* ws, const ScanShape& s, cudaStream_t st);
 cudaError_t scan_fwd_tc(const ScanIn& a, float* S, void* y, void* ws, const ScanShape& s, cudaStream_t st);
 cudaError_t scan_step(const ScanIn& a, float* S, void* y, const ScanShape& s, cudaStream_t st);
 
