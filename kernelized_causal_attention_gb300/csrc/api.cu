@@ -491,7 +491,7 @@ int la_cross_bwd(const void* q, const void* k, const void* v, const int* lengths
   LA_TRY(check_ptrs({q, k, v, out, den, S, Z, dout, dq, dk, dv}));
   LA_TRY(check_to(lengths, 4, true));
   LA_TRY(check_room(workspace, workspace_bytes, la::cross_ws_bytes(s, true)));
-  return from_cuda(la::cross_bwd(q, k, v, lengths, out, den, S, Z, dout, dq, dk, dv, static_cast<float*>(workspace), s,
+  return from_cuda(la::cross_bwd(q, k, v, lengths, den, S, Z, dout, dq, dk, dv, static_cast<float*>(workspace), s,
                                  static_cast<cudaStream_t>(stream)));
 }
 

@@ -5,13 +5,13 @@
 // and for each of the H / Hk query heads that share it
 //   out_i = S^T phi(q_i) / den_i,  den_i = phi(q_i) . Z;  L_b = 0 gives zeros.
 // Gradients, with e_i = 1 / den_i and gamma_i = -e_i (dout_i . out_i):
-//   dphi(q_i) = e_i S dout_i + gamma_i Z
+//   dphi(q_i) = e_i S dout_i + gamma_i Z,   dout_i . out_i = e_i phi(q_i) . (S dout_i)
 //   R = sum_i e_i phi(q_i) dout_i^T,  r = sum_i gamma_i phi(q_i)   (over the query heads too)
 //   dphi(k_j) = R v_j + r,   dv_j = R^T phi(k_j),   j < L_b.
 // S and Z are what a decoder keeps of its encoder: a single token then reads
 // them alone (k_cross_step), whatever the encoder's length.
 //
-// This file: the fp32 kernels (64-row tiles, FFMA), the sums over partial
+// This file (bf16 prompts and training: cross_tc.cu): the fp32 kernels (64-row tiles, FFMA), the sums over partial
 // records, and the single-token read.  The fp32 tile kernels are bound by the
 // FFMA rate and their shared-memory operands.
 #include "ffma.cuh"
@@ -124,8 +124,8 @@ __global__ void __launch_bounds__(256)
 // dq of a segment of query tiles, and the segment's partial R and r.
 template <int D, int M, typename T>
 __global__ void __launch_bounds__(256)
-    k_cross_grad_q(const T* __restrict__ q, const T* __restrict__ out, const float* __restrict__ den,
-                   const T* __restrict__ dout, const float* __restrict__ S, const float* __restrict__ Z, T* __restrict__ dq,
+    k_cross_grad_q(const T* __restrict__ q, const float* __restrict__ den, const T* __restrict__ dout,
+                   const float* __restrict__ S, const float* __restrict__ Z, T* __restrict__ dq,
                    float* __restrict__ rec, int H, int Hk, int N, int per) {
   extern __shared__ float sm[];
   float* qn = sm;                   // q, then e phi(q) [64][D + 4]
@@ -151,11 +151,7 @@ __global__ void __launch_bounds__(256)
     if (threadIdx.x < 64) {
       const int i = threadIdx.x;
       const float d = i < rows ? den[r0 + i] : 0.f;
-      float s = 0.f;
-      if (i < rows)
-        for (int m = 0; m < M; ++m) s = fmaf(gn[i * (M + 4) + m], to_f(out[(r0 + i) * M + m]), s);
       es[i] = d != 0.f ? 1.f / d : 0.f;
-      gs[i] = d != 0.f ? -s / d : 0.f;
     }
     __syncthreads();
     float acc[4][CC];
@@ -164,13 +160,21 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int i = ty * 4 + r;
-      const float e = es[i], g = gs[i];
+      const float e = es[i];
+      // dout_i . out_i = e phi(q_i) . (S dout_i): out itself, rounded, is not read
+      float x[CC], f[CC], t = 0.f;
 #pragma unroll
       for (int k = 0; k < CC; ++k) {
-        float& qv = qn[i * (D + 4) + tx * CC + k];
-        const float x = qv, f = phi(x);
-        acc[r][k] = fmaf(e, acc[r][k], g * zs[tx * CC + k]) * (x > 0.f ? 1.f : f);
-        qv = i < rows ? f : 0.f;
+        x[k] = qn[i * (D + 4) + tx * CC + k];
+        f[k] = i < rows ? phi(x[k]) : 0.f;
+        t = fmaf(f[k], acc[r][k], t);
+      }
+      const float g = -e * e * row_sum(t);
+      if (tx == 0) gs[i] = g;
+#pragma unroll
+      for (int k = 0; k < CC; ++k) {
+        acc[r][k] = fmaf(e, acc[r][k], g * zs[tx * CC + k]) * (x[k] > 0.f ? 1.f : f[k]);
+        qn[i * (D + 4) + tx * CC + k] = f[k];
       }
       if (i < rows) store_cols(dq + (r0 + i) * D + tx * CC, acc[r]);
     }
@@ -323,29 +327,31 @@ size_t rec_bytes(const CrossShape& s) { return (size_t)(s.D * s.M + s.D) * 4; }
     if (e_ != cudaSuccess) return e_;      \
   } while (0)
 
-cudaError_t join(const float* rec, float* S, float* Z, int heads, int nrec, const CrossShape& s, cudaStream_t st) {
+}  // namespace
+
+cudaError_t cross_join(const float* rec, float* S, float* Z, int heads, int nrec, const CrossShape& s, cudaStream_t st) {
   const int DM = s.D * s.M;
   k_cross_join<<<dim3(((DM + s.D) / 4 + 255) / 256, heads), 256, 0, st>>>(rec, S, Z, nrec, DM, s.D);
   return cudaGetLastError();
 }
 
-template <typename T>
+namespace {
+
 cudaError_t fwd(const void* q, const void* k, const void* v, const int* lengths, void* out, float* den, float* S, float* Z,
                 float* ws, const CrossShape& s, cudaStream_t st) {
   const Split p(s.B * s.Hk, s.Nk, FT);
   LA_DISPATCH_DM(s.D, s.M, {
     constexpr size_t b1 = 64 * (D_ + M_ + 8) * 4;
-    k_cross_sums<D_, M_, T><<<dim3(p.nseg, s.B * s.Hk), 256, b1, st>>>((const T*)k, (const T*)v, lengths, ws, s.Hk, s.Nk, p.per);
+    k_cross_sums<D_, M_, float><<<dim3(p.nseg, s.B * s.Hk), 256, b1, st>>>((const float*)k, (const float*)v, lengths, ws, s.Hk, s.Nk, p.per);
     LA_TRY_CUDA(cudaGetLastError());
-    LA_TRY_CUDA(join(ws, S, Z, s.B * s.Hk, p.nseg, s, st));
+    LA_TRY_CUDA(cross_join(ws, S, Z, s.B * s.Hk, p.nseg, s, st));
     constexpr size_t b2 = (D_ * FLD + D_ * (M_ + 4)) * 4;
-    k_cross_read<D_, M_, T><<<dim3((s.Nq + FT - 1) / FT, s.B * s.H), 256, b2, st>>>((const T*)q, S, Z, (T*)out, den, s.H, s.Hk, s.Nq);
+    k_cross_read<D_, M_, float><<<dim3((s.Nq + FT - 1) / FT, s.B * s.H), 256, b2, st>>>((const float*)q, S, Z, (float*)out, den, s.H, s.Hk, s.Nq);
   });
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t bwd(const void* q, const void* k, const void* v, const int* lengths, const void* out, const float* den,
+cudaError_t bwd(const void* q, const void* k, const void* v, const int* lengths, const float* den,
                 const float* S, const float* Z, const void* dout, void* dq, void* dk, void* dv, float* ws,
                 const CrossShape& s, cudaStream_t st) {
   const Split p(s.B * s.H, s.Nq, FT);
@@ -353,15 +359,15 @@ cudaError_t bwd(const void* q, const void* k, const void* v, const int* lengths,
   float* r = R + (size_t)s.B * s.Hk * s.D * s.M;
   LA_DISPATCH_DM(s.D, s.M, {
     constexpr size_t b1 = (64 * (D_ + 4) + M_ * FLD + 64 * (M_ + 4) + M_ * (D_ + 4)) * 4;
-    LA_TRY_CUDA(smem(&k_cross_grad_q<D_, M_, T>, b1));
-    k_cross_grad_q<D_, M_, T><<<dim3(p.nseg, s.B * s.H), 256, b1, st>>>((const T*)q, (const T*)out, den, (const T*)dout, S, Z,
-                                                                       (T*)dq, ws, s.H, s.Hk, s.Nq, p.per);
+    LA_TRY_CUDA(smem(&k_cross_grad_q<D_, M_, float>, b1));
+    k_cross_grad_q<D_, M_, float><<<dim3(p.nseg, s.B * s.H), 256, b1, st>>>((const float*)q, den, (const float*)dout, S, Z, (float*)dq,
+                                                                       ws, s.H, s.Hk, s.Nq, p.per);
     LA_TRY_CUDA(cudaGetLastError());
-    LA_TRY_CUDA(join(ws, R, r, s.B * s.Hk, p.nseg * (s.H / s.Hk), s, st));
+    LA_TRY_CUDA(cross_join(ws, R, r, s.B * s.Hk, p.nseg * (s.H / s.Hk), s, st));
     constexpr size_t b2 = (D_ * FLD + M_ * FLD + D_ * (M_ + 4) + M_ * (D_ + 4)) * 4;
-    LA_TRY_CUDA(smem(&k_cross_grad_k<D_, M_, T>, b2));
-    k_cross_grad_k<D_, M_, T><<<dim3((s.Nk + FT - 1) / FT, s.B * s.Hk), 256, b2, st>>>((const T*)k, (const T*)v, lengths, R, r,
-                                                                                       (T*)dk, (T*)dv, s.Hk, s.Nk);
+    LA_TRY_CUDA(smem(&k_cross_grad_k<D_, M_, float>, b2));
+    k_cross_grad_k<D_, M_, float><<<dim3((s.Nk + FT - 1) / FT, s.B * s.Hk), 256, b2, st>>>((const float*)k, (const float*)v, lengths, R, r,
+                                                                                       (float*)dk, (float*)dv, s.Hk, s.Nk);
   });
   return cudaGetLastError();
 }
@@ -375,21 +381,22 @@ cudaError_t step(const void* q, const float* S, const float* Z, void* y, const C
 }  // namespace
 
 size_t cross_ws_bytes(const CrossShape& s, bool bwd) {
+  if (s.dtype != 0) return cross_tc_ws_bytes(s, bwd);
   if (!bwd) return (size_t)s.B * s.Hk * Split(s.B * s.Hk, s.Nk, FT).nseg * rec_bytes(s);
   return ((size_t)s.B * s.H * Split(s.B * s.H, s.Nq, FT).nseg + (size_t)s.B * s.Hk) * rec_bytes(s);
 }
 
 cudaError_t cross_fwd(const void* q, const void* k, const void* v, const int* lengths, void* out, float* den, float* S,
                       float* Z, float* ws, const CrossShape& s, cudaStream_t st) {
-  return s.dtype == 0 ? fwd<float>(q, k, v, lengths, out, den, S, Z, ws, s, st)
-                      : fwd<bf16>(q, k, v, lengths, out, den, S, Z, ws, s, st);
+  return s.dtype == 0 ? fwd(q, k, v, lengths, out, den, S, Z, ws, s, st)
+                      : cross_fwd_tc(q, k, v, lengths, out, den, S, Z, ws, s, st);
 }
 
-cudaError_t cross_bwd(const void* q, const void* k, const void* v, const int* lengths, const void* out, const float* den,
-                      const float* S, const float* Z, const void* dout, void* dq, void* dk, void* dv, float* ws,
-                      const CrossShape& s, cudaStream_t st) {
-  return s.dtype == 0 ? bwd<float>(q, k, v, lengths, out, den, S, Z, dout, dq, dk, dv, ws, s, st)
-                      : bwd<bf16>(q, k, v, lengths, out, den, S, Z, dout, dq, dk, dv, ws, s, st);
+cudaError_t cross_bwd(const void* q, const void* k, const void* v, const int* lengths, const float* den, const float* S,
+                      const float* Z, const void* dout, void* dq, void* dk, void* dv, float* ws, const CrossShape& s,
+                      cudaStream_t st) {
+  return s.dtype == 0 ? bwd(q, k, v, lengths, den, S, Z, dout, dq, dk, dv, ws, s, st)
+                      : cross_bwd_tc(q, k, v, lengths, den, S, Z, dout, dq, dk, dv, ws, s, st);
 }
 
 cudaError_t cross_step(const void* q, const float* S, const float* Z, void* y, const CrossShape& s, cudaStream_t st) {

@@ -198,9 +198,18 @@ struct CrossShape {
 size_t cross_ws_bytes(const CrossShape& s, bool bwd);
 cudaError_t cross_fwd(const void* q, const void* k, const void* v, const int* lengths, void* out, float* den, float* S,
                       float* Z, float* ws, const CrossShape& s, cudaStream_t st);
-cudaError_t cross_bwd(const void* q, const void* k, const void* v, const int* lengths, const void* out, const float* den,
-                      const float* S, const float* Z, const void* dout, void* dq, void* dk, void* dv, float* ws,
-                      const CrossShape& s, cudaStream_t st);
+cudaError_t cross_bwd(const void* q, const void* k, const void* v, const int* lengths, const float* den, const float* S,
+                      const float* Z, const void* dout, void* dq, void* dk, void* dv, float* ws, const CrossShape& s,
+                      cudaStream_t st);
+// (S, Z) of every key head: the sum of its nrec neighbouring records of D M + D floats.
+cudaError_t cross_join(const float* rec, float* S, float* Z, int heads, int nrec, const CrossShape& s, cudaStream_t st);
+// bf16, on the tensor cores (cross_tc.cu).
+size_t cross_tc_ws_bytes(const CrossShape& s, bool bwd);
+cudaError_t cross_fwd_tc(const void* q, const void* k, const void* v, const int* lengths, void* out, float* den, float* S,
+                         float* Z, float* ws, const CrossShape& s, cudaStream_t st);
+cudaError_t cross_bwd_tc(const void* q, const void* k, const void* v, const int* lengths, const float* den, const float* S,
+                         const float* Z, const void* dout, void* dq, void* dk, void* dv, float* ws, const CrossShape& s,
+                         cudaStream_t st);
 cudaError_t cross_step(const void* q, const float* S, const float* Z, void* y, const CrossShape& s, cudaStream_t st);
 
 }  // namespace la

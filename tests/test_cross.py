@@ -4,7 +4,8 @@ Bounds, element by element, on the sizes of ``plain64.cross(size=True)``: in
 fp32 a sum over n rows rounds by less than n + 64 half steps of its size (both
 sequences' rows are summed, one after the other, in a gradient).  With bf16
 inputs phi of one side and the summed states are rounded to bf16 once before a
-product and the result once; den, S and Z stay fp32-accurate (two bf16 terms).
+product and the result once; S is fp32-accurate to two bf16 terms (2^-16), den and
+Z are fp32 sums.
 """
 import pytest
 import torch
