@@ -21,7 +21,7 @@
 //
 // Roundings: P and the carried states to bf16 before their products (half a
 // step, 2^-8, each on its own part of y), y once.  The chunk sums take w_j x_j
-// as two bf16 terms (2^-16), since the final state is an fp32 output.
+// as three bf16 terms (2^-24), since the final state is an fp32 output.
 #include <cudaTypedefs.h>
 
 #include "rows_map.cuh"
@@ -41,22 +41,25 @@ constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr int STILE = 64 * 64 * 2;  // one [64][64] bf16 state tile
 
 // One chunk's gates of one head.  wp: prefix sums of log2 decays within each
-// 32-row block; tot: the blocks' totals; del: delta; cf: delta exp(block end - cum).
-struct Gates {
-  float wp[128], del[128], cf[128], tot[4];
+// 32-row block; tot: the blocks' totals; del: delta; cf: delta exp(block end -
+// cum); ew: exp(cum - block start).
+struct __align__(16) Gates {
+  float wp[128], del[128], cf[128], ew[128], tot[4];
   __device__ __forceinline__ float off(int q) const {  // log2 decay of the blocks before q
-    float s = 0.f;
-    for (int p = 0; p < q; ++p) s += tot[p];
-    return s;
+    return (q > 0 ? tot[0] : 0.f) + (q > 1 ? tot[1] : 0.f) + (q > 2 ? tot[2] : 0.f) + (q > 3 ? tot[3] : 0.f);
   }
   __device__ __forceinline__ float past(int q) const {  // of the blocks after q
-    float s = 0.f;
-    for (int p = 3; p > q; --p) s += tot[p];
-    return s;
+    return (q < 3 ? tot[3] : 0.f) + (q < 2 ? tot[2] : 0.f) + (q < 1 ? tot[1] : 0.f);
   }
 };
 
-// By warps 0 .. 3, row = 32 warp + lane.
+// A head's parameters, for all heads of a block.
+constexpr int MAXH = 16;
+struct Params {
+  float A, skip, bias;
+};
+
+// By four warps, row = 32 (warp mod 4) + lane.
 __device__ __forceinline__ void put_gates(Gates& g, float z, bool live, float A, int row) {
   const float d = live ? softplus(z) : 0.f;
   const float wp = warp_prefix(d * A * LOG2E);
@@ -64,6 +67,7 @@ __device__ __forceinline__ void put_gates(Gates& g, float z, bool live, float A,
   g.wp[row] = wp;
   g.del[row] = d;
   g.cf[row] = d * exp2f(tot - wp);
+  g.ew[row] = exp2f(wp);
   if ((row & 31) == 31) g.tot[row >> 5] = tot;
 }
 
@@ -83,11 +87,16 @@ struct Share {
     h0 = g * hg + p * hs;
     nh = min(hs, hg - p * hs);
   }
+  // The heads' parameters into shared memory, by threads 0 .. nh - 1 (before a block barrier).
+  __device__ void params(Params* to, const bf16* A, const bf16* skip, const bf16* bias) const {
+    const int i = threadIdx.x;
+    if (i < nh) to[i] = Params{to_f(A[h0 + i]), par(skip, h0 + i), par(bias, h0 + i)};
+  }
 };
 
-// Rows [rows, 128) of a swizzled [128][64] tile become zeros (256 threads).
-__device__ __forceinline__ void clear_rows(uint8_t* tile, int rows) {
-  for (int v = rows * 8 + threadIdx.x; v < TILE / 16; v += 256) sts128(tile + v * 16, make_uint4(0u, 0u, 0u, 0u));
+// Rows [rows, 128) of a swizzled [128][64] tile become zeros, by n threads.
+__device__ __forceinline__ void clear_rows(uint8_t* tile, int rows, int n = 256) {
+  for (int v = rows * 8 + threadIdx.x; v < TILE / 16; v += n) sts128(tile + v * 16, make_uint4(0u, 0u, 0u, 0u));
 }
 
 #define LA_SCAN_WAITS()                                                     \
@@ -109,8 +118,10 @@ struct Maps {
 };
 
 // ------------------------------------------------------------- chunk sums
-// TERMS bf16 terms of the scaled operand.  blockIdx.y = part, or parts + part
-// for the reverse sums E = sum_i exp(cum_i) C_i dy_i^T.
+// TERMS bf16 terms of the scaled operand, side by side along the product's N
+// (three for the forward pass, whose final state is an fp32 output: 2^-24; one
+// for the gradients, which are bf16).  blockIdx.y = part, or parts + part for
+// the reverse sums E = sum_i exp(cum_i) C_i dy_i^T.
 constexpr int S_A = 0, S_X = TILE, S_T = 3 * TILE;  // B or C; two x stages; the terms
 constexpr int S_SMEM(int terms) { return (3 + terms) * TILE + 1024; }
 
@@ -123,8 +134,10 @@ __global__ void __launch_bounds__(NT, 2)
   uint8_t* sm = align1024(smraw);
   __shared__ uint64_t bar_a, bar_x[2], bar_t, bar_m, bar_fin;
   __shared__ Gates gates[2];
+  __shared__ Params par_[MAXH];
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
+  constexpr int COLS = TERMS > 1 ? 256 : 64;
   const int parts = s.G * pg;
   const bool back = blockIdx.y >= parts;
   const Share w(s, lengths, back ? blockIdx.y - parts : blockIdx.y, pg, hs);
@@ -138,7 +151,7 @@ __global__ void __launch_bounds__(NT, 2)
     }
     return;
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == NT - 1) {
     mbar_init(&bar_a, 1);
     mbar_init(&bar_x[0], 1);
     mbar_init(&bar_x[1], 1);
@@ -148,7 +161,8 @@ __global__ void __launch_bounds__(NT, 2)
     fence_barrier_init();
     s_abort = 0;
   }
-  if (warp == W_ISSUE) tmem_alloc(&tmem_base, 128);
+  w.params(par_, A, nullptr, bias);
+  if (warp == W_ISSUE) tmem_alloc(&tmem_base, COLS);
   LA_SCAN_WAITS()
   tc_fence_before();
   __syncthreads();
@@ -158,8 +172,6 @@ __global__ void __launch_bounds__(NT, 2)
   if (warp == W_ISSUE) {
     if (lane == 0) {
       const CUtensorMap* mx = back ? &maps.g : &maps.x;
-      mbar_arrive_expect_tx(&bar_a, TILE);
-      tma_load_4d(sm + S_A, back ? &maps.C : &maps.B, &bar_a, 0, w.g, w.n0, w.b);
       int issued = 0;
       auto load = [&](int i) {
         mbar_arrive_expect_tx(&bar_x[i & 1], TILE);
@@ -167,21 +179,18 @@ __global__ void __launch_bounds__(NT, 2)
         ++issued;
       };
       load(0);
+      mbar_arrive_expect_tx(&bar_a, TILE);
+      tma_load_4d(sm + S_A, back ? &maps.C : &maps.B, &bar_a, 0, w.g, w.n0, w.b);
       if (w.nh > 1) load(1);
-      constexpr uint32_t ID = idesc_bf16(64, 64, true, true);
-      const uint64_t da = sdesc(smem_u32(sm + S_A), 16, 1024);
+      constexpr uint32_t ID = idesc_bf16(64, 64 * TERMS, true, true);
+      const uint64_t da = sdesc(smem_u32(sm + S_A), 16, 1024), db = sdesc(smem_u32(sm + S_T), TILE, 1024);
       const bool in = wt(&bar_a, 0, 66);
       for (int i = 0; in && i < w.nh; ++i) {
         if (!wt(&bar_t, i & 1, 61)) break;
         tc_fence_after();
         if (i + 2 < w.nh) load(i + 2);  // head i's stage has been read
 #pragma unroll
-        for (int k = 0; k < TERMS; ++k) {
-          const uint64_t db = sdesc(smem_u32(sm + S_T + k * TILE), 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_bf16(tm + (i & 1) * 64, dadd(da, kk * 2048), dadd(db, kk * 2048), ID, k > 0 || kk > 0);
-        }
+        for (int kk = 0; kk < 8; ++kk) mma_bf16(tm, dadd(da, kk * 2048), dadd(db, kk * 2048), ID, kk > 0);
         mma_commit(&bar_m);
       }
       // nothing in flight at exit: the products' last commit, the loads
@@ -198,62 +207,80 @@ __global__ void __launch_bounds__(NT, 2)
     auto drain = [&](int i, bool done) {  // head i's sums, its products done
       if (done) {
         tc_fence_after();
-        float f[32];
-        tmem_ldn<2>(tm + (i & 1) * 64 + lq + 32 * half, f);
-        if (lane < 16 && srow < s.D) {
-          float* o = out + (long)i * nch * DM + srow * s.M + 32 * half;
 #pragma unroll
-          for (int c = 0; c < 32; c += 4)
-            if (32 * half + c < s.M) *reinterpret_cast<float4*>(o + c) = make_float4(f[c], f[c + 1], f[c + 2], f[c + 3]);
+        for (int j = 0; j < 2; ++j) {
+          float f[TERMS][16];
+#pragma unroll
+          for (int k = 0; k < TERMS; ++k) tmem_ld16(tm + lq + 64 * k + 32 * half + 16 * j, f[k]);
+          tmem_ld_wait();
+          if (TERMS > 1) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) f[0][c] += f[1][c] + f[TERMS - 1][c];
+          }
+          const int c0 = 32 * half + 16 * j;
+          if (lane < 16 && srow < s.D && c0 < s.M) {
+            float* o = out + (long)i * nch * DM + srow * s.M + c0;
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4*>(o + c) = make_float4(f[0][c], f[0][c + 1], f[0][c + 2], f[0][c + 3]);
+          }
         }
       }
       tc_fence_before();
     };
-    float z = half == 0 ? raw(0) : 0.f;
+    float z = 0.f;
+    if (half == 0) {
+      put_gates(gates[0], raw(0) + par_[0].bias, row < w.rows, par_[0].A, row);
+      z = raw(1);
+    }
     if (w.rows < min(TC_C, s.N - w.n0)) {  // rows past the sequence's length: not to be multiplied
       if (wtu(&bar_a, 0, 63)) clear_rows(sm + S_A, w.rows);
     }
+    sync_compute();
     for (int i = 0; i < w.nh; ++i) {
-      Gates& g = gates[i & 1];
-      const int h = w.h0 + i;
-      if (half == 0) {
-        put_gates(g, z + par(bias, h), row < w.rows, to_f(A[h]), row);
-        z = raw(i + 1);
-      }
-      sync_compute();
-      if (threadIdx.x == 0 && !back) tot[((long)w.b * s.H + h) * nch + blockIdx.x] = (g.off(4)) * LN2;
+      const Gates& g = gates[i & 1];
+      if (threadIdx.x == 0 && !back) tot[((long)w.b * s.H + w.h0 + i) * nch + blockIdx.x] = g.off(4) * LN2;
       const float f = row >= w.rows ? 0.f : (back ? exp2f(g.wp[row] + g.off(q)) : g.cf[row] * exp2f(g.past(q)));
       const bool in = wtu(&bar_x[i & 1], (i >> 1) & 1, 64);
-      const bool clear = i == 0 || wtu(&bar_m, (i - 1) & 1, 65);  // the terms' tiles have been read
-      if (in && clear) {
-        const uint8_t* xt = sm + S_X + (i & 1) * TILE;
+      uint4 u[4];
+      const uint8_t* xt = sm + S_X + (i & 1) * TILE;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) u[c] = lds128(xt + row * 128 + (((4 * half + c) ^ (row & 7)) << 4));
+      // the products that read the terms' tiles are done; their sums leave the accumulator
+      if (i > 0) drain(i - 1, wtu(&bar_m, (i - 1) & 1, 65));
+      if (in) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int o = row * 128 + (((4 * half + c) ^ (row & 7)) << 4);
-          const uint4 u = lds128(xt + o);
-          const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-          uint32_t hi[4], lo[4];
+          const uint32_t v[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+          uint32_t t[3][4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const float a = f != 0.f ? __uint_as_float(v[k] << 16) * f : 0.f;
-            const float b = f != 0.f ? __uint_as_float(v[k] & 0xffff0000u) * f : 0.f;
-            hi[k] = pack_bf16(a, b);
-            if (TERMS > 1) lo[k] = pack_bf16(a - __uint_as_float(hi[k] << 16), b - __uint_as_float(hi[k] & 0xffff0000u));
+            float a = f != 0.f ? __uint_as_float(v[k] << 16) * f : 0.f;
+            float b = f != 0.f ? __uint_as_float(v[k] & 0xffff0000u) * f : 0.f;
+#pragma unroll
+            for (int j = 0; j < TERMS; ++j) {
+              t[j][k] = pack_bf16(a, b);
+              a -= __uint_as_float(t[j][k] << 16);
+              b -= __uint_as_float(t[j][k] & 0xffff0000u);
+            }
           }
-          sts128(sm + S_T + o, make_uint4(hi[0], hi[1], hi[2], hi[3]));
-          if (TERMS > 1) sts128(sm + S_T + TILE + o, make_uint4(lo[0], lo[1], lo[2], lo[3]));
+#pragma unroll
+          for (int j = 0; j < TERMS; ++j) sts128(sm + S_T + j * TILE + o, make_uint4(t[j][0], t[j][1], t[j][2], t[j][3]));
         }
       }
       fence_proxy_async();
-      tc_fence_before();
       mbar_arrive(&bar_t);
-      if (i > 0) drain(i - 1, clear);  // (the next head's products may already be done)
+      if (half == 0 && i + 1 < w.nh) {  // the next head's gates, beside this one's products
+        put_gates(gates[(i + 1) & 1], z + par_[i + 1].bias, row < w.rows, par_[i + 1].A, row);
+        z = raw(i + 2);
+      }
+      sync_compute();
     }
     drain(w.nh - 1, wtu(&bar_m, (w.nh - 1) & 1, 62));
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == W_ISSUE) tmem_dealloc(tm, 128);
+  if (warp == W_ISSUE) tmem_dealloc(tm, COLS);
 }
 
 // ------------------------------------------------------------------ outputs
@@ -269,6 +296,7 @@ __global__ void __launch_bounds__(NT, 2)
   uint8_t* sm = align1024(smraw);
   __shared__ uint64_t bar_cb, bar_x[2], bar_a, bar_p, bar_o, bar_free;
   __shared__ Gates gates[2];
+  __shared__ Params par_[MAXH];
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   const Share w(s, lengths, blockIdx.y, pg, hs);
@@ -280,7 +308,7 @@ __global__ void __launch_bounds__(NT, 2)
       *reinterpret_cast<uint4*>(y + ((r0 + e / per) * s.H + w.h0) * s.M + e % per * 8) = make_uint4(0u, 0u, 0u, 0u);
     return;
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == NT - 1) {
     mbar_init(&bar_cb, 1);
     mbar_init(&bar_x[0], 1);
     mbar_init(&bar_x[1], 1);
@@ -291,6 +319,7 @@ __global__ void __launch_bounds__(NT, 2)
     fence_barrier_init();
     s_abort = 0;
   }
+  w.params(par_, A, skip, bias);
   if (warp == W_ISSUE) tmem_alloc(&tmem_base, 256);
   LA_SCAN_WAITS()
   tc_fence_before();
@@ -315,24 +344,30 @@ __global__ void __launch_bounds__(NT, 2)
       if (w.nh > 1) load(1);
       constexpr uint32_t ID_A = idesc_bf16(128, 128, false, false), ID_O = idesc_bf16(128, 64, false, true);
       const uint64_t dC = sdesc(smem_u32(sm + O_C), 16, 1024), dB = sdesc(smem_u32(sm + O_B), 16, 1024);
-      bool ok = wt(&bar_cb, 0, 71);
-      for (int i = 0; ok && i < w.nh; ++i) {
-        const int k = i & 1;
-        const uint64_t dX = sdesc(smem_u32(sm + O_X + k * TILE), 16, 1024), dS = sdesc(smem_u32(sm + O_S + k * STILE), 16, 1024);
-        if (!(ok = wt(&bar_x[k], (i >> 1) & 1, 72))) break;
+      // The scores of head i + 1 go out as soon as P of head i has been read, beside
+      // the outputs' read-out; bar_o's commit covers C S as well.
+      auto scores = [&](int i) {
+        if (!wt(&bar_x[i & 1], (i >> 1) & 1, 72)) return false;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) mma_bf16(tm + T_A, dadd(dC, 32 * kk), dadd(dB, 32 * kk), ID_A, kk > 0);
+        mma_commit(&bar_a);
+        return true;
+      };
+      bool ok = wt(&bar_cb, 0, 71) && scores(0);
+      for (int i = 0; ok && i < w.nh; ++i) {
+        const int k = i & 1;
+        const uint64_t dX = sdesc(smem_u32(sm + O_X + k * TILE), 16, 1024), dS = sdesc(smem_u32(sm + O_S + k * STILE), 16, 1024);
         if (states)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) mma_bf16(tm + T_CS, dadd(dC, 32 * kk), dadd(dS, kk * 2048), ID_O, kk > 0);
-        mma_commit(&bar_a);
         if (!(ok = wt(&bar_p, k, 73))) break;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
           mma_bf16_ts(tm + T_O, tm + T_A + (kk < 4 ? 8 * kk : 32 + 8 * kk), dadd(dX, kk * 2048), ID_O, kk > 0);
         mma_commit(&bar_o);
+        if (i + 1 < w.nh && !(ok = wt(&bar_o, k, 79) && scores(i + 1))) break;
         if (!(ok = wt(&bar_free, k, 74))) break;
         tc_fence_after();
         tma_store_4d(&maps.o, sm + O_X + k * TILE, 0, w.h0 + i, w.n0, w.b);  // y has taken x's place
@@ -352,17 +387,17 @@ __global__ void __launch_bounds__(NT, 2)
     const int qd = warp & 3, wg = warp >> 2, row = 32 * qd + lane;
     const uint32_t lq = static_cast<uint32_t>(32 * qd) << 16;
     auto raw = [&](int i) { return i < w.nh && row < w.rows ? to_f(dt[(r0 + row) * s.lddt + w.h0 + i]) : 0.f; };
-    float z = wg == 0 ? raw(0) : 0.f;
+    float z = 0.f;
+    if (wg == 0) {
+      put_gates(gates[0], raw(0) + par_[0].bias, row < w.rows, par_[0].A, row);
+      z = raw(1);
+    }
+    sync_compute();
     const bool cut = w.rows < min(TC_C, s.N - w.n0);
     for (int i = 0; i < w.nh; ++i) {
-      const int k = i & 1, h = w.h0 + i;
-      Gates& g = gates[k];
+      const int k = i & 1;
+      const Gates& g = gates[k];
       uint8_t* xt = sm + O_X + k * TILE;
-      if (wg == 0) {
-        put_gates(g, z + par(bias, h), row < w.rows, to_f(A[h]), row);
-        z = raw(i + 1);
-      }
-      sync_compute();
       const float wp = g.wp[row], here = g.off(qd);
       if (cut && wtu(&bar_x[k], (i >> 1) & 1, 75)) clear_rows(xt, w.rows);
       if (wtu(&bar_a, k, 76)) {
@@ -381,12 +416,20 @@ __global__ void __launch_bounds__(NT, 2)
             if (J < qd) {
               const float f = exp2f(wp + here - g.off(J + 1));
 #pragma unroll
-              for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(a[2 * c] * (f * g.cf[32 * J + 2 * c]), a[2 * c + 1] * (f * g.cf[32 * J + 2 * c + 1]));
+              for (int c = 0; c < 32; c += 4) {
+                const float4 u = *reinterpret_cast<const float4*>(&g.cf[32 * J + c]);
+                pk[c / 2] = pack_bf16(a[c] * (f * u.x), a[c + 1] * (f * u.y));
+                pk[c / 2 + 1] = pack_bf16(a[c + 2] * (f * u.z), a[c + 3] * (f * u.w));
+              }
             } else {
 #pragma unroll
-              for (int c = 0; c < 32; ++c) a[c] = c <= lane ? a[c] * (exp2f(wp - g.wp[32 * J + c]) * g.del[32 * J + c]) : 0.f;
-#pragma unroll
-              for (int c = 0; c < 16; ++c) pk[c] = pack_bf16(a[2 * c], a[2 * c + 1]);
+              for (int c = 0; c < 32; c += 4) {
+                const float4 u = *reinterpret_cast<const float4*>(&g.wp[32 * J + c]), d = *reinterpret_cast<const float4*>(&g.del[32 * J + c]);
+                const float p0 = c <= lane ? a[c] * (exp2f(wp - u.x) * d.x) : 0.f, p1 = c + 1 <= lane ? a[c + 1] * (exp2f(wp - u.y) * d.y) : 0.f;
+                const float p2 = c + 2 <= lane ? a[c + 2] * (exp2f(wp - u.z) * d.z) : 0.f, p3 = c + 3 <= lane ? a[c + 3] * (exp2f(wp - u.w) * d.w) : 0.f;
+                pk[c / 2] = pack_bf16(p0, p1);
+                pk[c / 2 + 1] = pack_bf16(p2, p3);
+              }
             }
           }
           tmem_st16u(ta + 16 * j, pk);  // over columns this warp has read
@@ -396,25 +439,34 @@ __global__ void __launch_bounds__(NT, 2)
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive(&bar_p);
-      const bool x_in = wtu(&bar_x[k], (i >> 1) & 1, 77);
+      if (wg == 0 && i + 1 < w.nh) {  // the next head's gates, beside this one's products
+        put_gates(gates[k ^ 1], z + par_[i + 1].bias, row < w.rows, par_[i + 1].A, row);
+        z = raw(i + 2);
+      }
+      const float e = exp2f(wp + here), sk = par_[i].skip;
+      const bool x_in = wtu(&bar_x[k], (i >> 1) & 1, 77), live = row < w.rows;
       if (wtu(&bar_o, k, 78) && x_in) {
         tc_fence_after();
-        float o[32], cs[32], x[32];
-        tmem_ldn<2>(tm + T_O + 32 * wg + lq, o);
-        if (states) tmem_ldn<2>(tm + T_CS + 32 * wg + lq, cs);
-        tile_row_cols<32>(xt, row, 32 * wg, x);
-        const float e = exp2f(wp + here), sk = par(skip, h);
-        const bool live = row < w.rows;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float v = fmaf(sk, x[c], states ? fmaf(e, cs[c], o[c]) : o[c]);
-          o[c] = live ? v : 0.f;
+        for (int j = 0; j < 2; ++j) {
+          const int c0 = 32 * wg + 16 * j;
+          float o[16], cs[16], x[16];
+          tmem_ld16(tm + T_O + c0 + lq, o);
+          if (states) tmem_ld16(tm + T_CS + c0 + lq, cs);
+          tile_row_cols<16>(xt, row, c0, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const float v = fmaf(sk, x[c], states ? fmaf(e, cs[c], o[c]) : o[c]);
+            o[c] = live ? v : 0.f;
+          }
+          tile_put_cols<16>(xt, row, c0, o);
         }
-        tile_put_cols<32>(xt, row, 32 * wg, o);
       }
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive(&bar_free);
+      sync_compute();  // the next head's gates are in place
     }
   }
   __syncthreads();
@@ -432,19 +484,25 @@ __global__ void __launch_bounds__(NT, 2)
 // blocks leave fp32 partial sums that scan_groups adds up (one block: the
 // gradients themselves).  The gate's gradient takes its pair sums G_ij =
 // Q_ij A_ij from the fp32 scores in registers: the column sums of a 32 x 32 block
-// cost 31 shuffles a warp.
+// cost 32 shuffles a warp.
 //
-// Bound by the chain score products -> weights -> gradient products of one head
-// at a time on one block an SM (all 512 tensor-memory columns, 166 KB of shared
-// memory); the carried states' products and their read-out run beside it.
+// Sixteen compute warps, one 32 x 32 score block each (warp mod 4 is the lane
+// quarter it can reach, warp / 4 the block's column), on one block an SM (all
+// 512 tensor-memory columns, 161 KB of tiles).  The next head's gates and the
+// last head's gate gradient are formed beside the products, the latter by the
+// warps that the masked triangle leaves idle.  Bound by the per-head chain and by
+// instruction issue, not by a unit's rate.
+constexpr int GT = 512, NTG = GT + 32, WG_ISSUE = GT / 32;
 constexpr int G_C = 0, G_B = TILE, G_X = 2 * TILE, G_Y = 4 * TILE, G_S = 6 * TILE, G_R = G_S + 2 * STILE, G_Q = G_R + 2 * STILE;
 constexpr int G_SMEM = G_Q + 2 * TILE + 1024;
 constexpr uint32_t TG_A = 0, TG_E = 128, TG_U = 256, TG_BR = 320, TG_B = 384, TG_C = 448;
 
-// Sum over the warp's lanes of g[c] for each column c, to lane c.
-__device__ __forceinline__ float column_sums(float (&g)[32], int lane) {
+__device__ __forceinline__ void sync_grad() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+
+// Sum over the warp's lanes of g[c] for each of 16 columns c, to lanes c and c + 16.
+__device__ __forceinline__ float column_sums(float (&g)[16], int lane) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = 8; o > 0; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int c = 0; c < o; ++c) {
@@ -452,7 +510,7 @@ __device__ __forceinline__ float column_sums(float (&g)[32], int lane) {
       g[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
   }
-  return g[0];
+  return g[0] + __shfl_xor_sync(0xffffffffu, g[0], 16);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -471,7 +529,13 @@ __device__ __forceinline__ float warp_suffix(float v) {  // inclusive, from the 
   return v;
 }
 
-__global__ void __launch_bounds__(NT, 1)
+// What the gate's gradient of a head is summed from, by row (and by the column
+// group that formed it).
+struct GateSums {
+  float row[4][128], col[4][128], v[4][128], w[4][128], u[4][128], red[16][2];
+};
+
+__global__ void __launch_bounds__(NTG, 1)
     k_grad(const __grid_constant__ Maps maps, const bf16* __restrict__ dt, const bf16* __restrict__ A,
            const bf16* __restrict__ skip, const bf16* __restrict__ bias, const int* __restrict__ lengths,
            bf16* __restrict__ dx, bf16* __restrict__ ddt, void* dB, void* dC, float* __restrict__ pp, ScanShape s, int pg,
@@ -480,7 +544,9 @@ __global__ void __launch_bounds__(NT, 1)
   uint8_t* sm = align1024(smraw);
   __shared__ uint64_t bar_cb, bar_in[2], bar_clear, bar_1, bar_2, bar_3, bar_4, bar_p, bar_c, bar_x, bar_free;
   __shared__ Gates gates[2];
-  __shared__ float s_row[4][128], s_col[2][128], s_v[2][128], s_w[2][128], s_u[2][128], s_red[8][2], s_tot[4][2], s_out[4][2];
+  __shared__ Params par_[MAXH];
+  __shared__ GateSums sums[2];
+  __shared__ float s_tot[4][2], s_out[4][2];
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   const Share w(s, lengths, blockIdx.y, pg, hs);
@@ -491,10 +557,10 @@ __global__ void __launch_bounds__(NT, 1)
   const int parts = s.G * pg;
   if (w.rows == 0) {  // nothing but rows past the sequence's length
     const int per = w.nh * s.M / 8;
-    for (int e = threadIdx.x; e < in_n * per; e += NT)
+    for (int e = threadIdx.x; e < in_n * per; e += NTG)
       *reinterpret_cast<uint4*>(dx + ((r0 + e / per) * s.H + w.h0) * s.M + e % per * 8) = make_uint4(0u, 0u, 0u, 0u);
-    for (int e = threadIdx.x; e < in_n * w.nh; e += NT) ddt[(r0 + e / w.nh) * s.H + w.h0 + e % w.nh] = from_f<bf16>(0.f);
-    for (int e = threadIdx.x; e < in_n * s.D; e += NT) {
+    for (int e = threadIdx.x; e < in_n * w.nh; e += NTG) ddt[(r0 + e / w.nh) * s.H + w.h0 + e % w.nh] = from_f<bf16>(0.f);
+    for (int e = threadIdx.x; e < in_n * s.D; e += NTG) {
       const long o = ((r0 + e / s.D) * parts + w.part) * s.D + e % s.D;
       if (direct) {
         static_cast<bf16*>(dB)[o] = from_f<bf16>(0.f);
@@ -504,16 +570,17 @@ __global__ void __launch_bounds__(NT, 1)
         static_cast<float*>(dC)[o] = 0.f;
       }
     }
-    for (int e = threadIdx.x; e < w.nh * 3; e += NT) pp[(((long)w.b * s.H + w.h0 + e / 3) * nch + blockIdx.x) * 3 + e % 3] = 0.f;
+    for (int e = threadIdx.x; e < w.nh * 3; e += NTG) pp[(((long)w.b * s.H + w.h0 + e / 3) * nch + blockIdx.x) * 3 + e % 3] = 0.f;
     return;
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == GT) {
     for (uint64_t* b : {&bar_cb, &bar_in[0], &bar_in[1], &bar_1, &bar_2, &bar_3, &bar_4}) mbar_init(b, 1);
-    for (uint64_t* b : {&bar_clear, &bar_p, &bar_c, &bar_x, &bar_free}) mbar_init(b, 256);
+    for (uint64_t* b : {&bar_clear, &bar_p, &bar_c, &bar_x, &bar_free}) mbar_init(b, GT);
     fence_barrier_init();
     s_abort = 0;
   }
-  if (warp == W_ISSUE) tmem_alloc(&tmem_base, 512);
+  w.params(par_, A, skip, bias);
+  if (warp == WG_ISSUE) tmem_alloc(&tmem_base, 512);
   LA_SCAN_WAITS()
   tc_fence_before();
   __syncthreads();
@@ -521,7 +588,7 @@ __global__ void __launch_bounds__(NT, 1)
   const uint32_t tm = tmem_base;
   const bool cut = w.rows < in_n;
 
-  if (warp == W_ISSUE) {
+  if (warp == WG_ISSUE) {
     if (lane == 0) {
       mbar_arrive_expect_tx(&bar_cb, 2 * TILE);
       tma_load_4d(sm + G_C, &maps.C, &bar_cb, 0, w.g, w.n0, w.b);
@@ -567,13 +634,13 @@ __global__ void __launch_bounds__(NT, 1)
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)  // P^T dy
-          mma_bf16_ts(tm + TG_U, tm + TG_A + (kk < 4 ? 8 * kk : 32 + 8 * kk), dadd(dY, kk * 2048), ID_KM, kk > 0);
+          mma_bf16_ts(tm + TG_U, tm + TG_A + 32 * (kk >> 1) + 8 * (kk & 1), dadd(dY, kk * 2048), ID_KM, kk > 0);
         mma_commit(&bar_3);
         if (!(ok = wt(&bar_c, k, 86))) break;  // x R^T and dy S^T have been read
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)  // Q^T C
-          mma_bf16_ts(tm + TG_B, tm + TG_E + (kk < 4 ? 8 * kk : 32 + 8 * kk), dadd(dCt, kk * 2048), ID_KM, kk > 0);
+          mma_bf16_ts(tm + TG_B, tm + TG_E + 32 * (kk >> 1) + 8 * (kk & 1), dadd(dCt, kk * 2048), ID_KM, kk > 0);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)  // Q B
           mma_bf16(tm + TG_C, dadd(dQ, kk * 2048), dadd(dBt, kk * 2048), ID_MM, kk > 0);
@@ -593,87 +660,97 @@ __global__ void __launch_bounds__(NT, 1)
       bulk_wait_all();
     }
   } else {
-    const int qd = warp & 3, wg = warp >> 2, row = 32 * qd + lane;
+    const int qd = warp & 3, I = warp >> 2, row = 32 * qd + lane, c0 = 16 * I;
     const uint32_t lq = static_cast<uint32_t>(32 * qd) << 16;
     const bool live = row < w.rows;
     auto raw = [&](int i) { return i < w.nh && live ? to_f(dt[(r0 + row) * s.lddt + w.h0 + i]) : 0.f; };
-    float z = wg == 0 ? raw(0) : 0.f;
-    float aB[32], aC[32];
+    float z = 0.f;
+    if (I == 1) {
+      put_gates(gates[0], raw(0) + par_[0].bias, live, par_[0].A, row);
+      z = raw(1);
+    }
+    float aB[16], aC[16];  // dB and dC of this row, columns c0 .. c0 + 15, over the heads
 #pragma unroll
-    for (int c = 0; c < 32; ++c) aB[c] = aC[c] = 0.f;
+    for (int c = 0; c < 16; ++c) aB[c] = aC[c] = 0.f;
     const bool cb = wtu(&bar_cb, 0, 89);
+    sync_grad();
     for (int i = 0; i < w.nh; ++i) {
       const int k = i & 1, h = w.h0 + i;
-      Gates& g = gates[k];
+      const Gates& g = gates[k];
+      GateSums& gs = sums[k];
       uint8_t *xt = sm + G_X + k * TILE, *yt = sm + G_Y + k * TILE;
-      const float zi = z + par(bias, h), Ah = to_f(A[h]);
-      if (wg == 0) {
-        put_gates(g, zi, live, Ah, row);
-        z = raw(i + 1);
-      }
-      sync_compute();
       const bool in = wtu(&bar_in[k], (i >> 1) & 1, 90) && cb;
       if (cut) {
         if (in) {
           if (i == 0) {
-            clear_rows(sm + G_C, w.rows);
-            clear_rows(sm + G_B, w.rows);
+            clear_rows(sm + G_C, w.rows, GT);
+            clear_rows(sm + G_B, w.rows, GT);
           }
-          clear_rows(xt, w.rows);
-          clear_rows(yt, w.rows);
+          clear_rows(xt, w.rows, GT);
+          clear_rows(yt, w.rows, GT);
         }
         fence_proxy_async();
         mbar_arrive(&bar_clear);
       }
-      const float wp = g.wp[row], here = g.off(qd), del = g.del[row];
+      const float wp = g.wp[row], del = g.del[row];
       const float tail = exp2f(g.tot[qd] - wp);     // from this row to its block's end
       const float fend = tail * exp2f(g.past(qd));  // to the chunk's end
-      const float ecum = exp2f(wp + here);
-      // ---- the weights on A^T and E^T
+      const float ecum = g.ew[row] * exp2f(g.off(qd)), eall = exp2f(g.off(4));
+      // ---- the weights on this warp's block of A^T and E^T: keys 32 qd + lane, queries 32 I + c
       if (wtu(&bar_1, k, 91)) {
         tc_fence_after();
-        const uint32_t ta = tm + TG_A + 64 * wg + lq, te = tm + TG_E + 64 * wg + lq;
+        const uint32_t ta = tm + TG_A + 32 * I + lq, te = tm + TG_E + 32 * I + lq;
+        uint8_t* qt = sm + G_Q + (I >> 1) * TILE + row * 128;
+        const float fr = I > qd ? tail * exp2f(g.off(I) - g.off(qd + 1)) : 0.f, frd = fr * del;
         float col = 0.f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int I = 2 * wg + j;  // a block of 32 query columns
-          uint32_t pw[16], qw[16];
-          float rs = 0.f;
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pw[8], qw[8];
           if (I < qd) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) pw[c] = qw[c] = 0u;
+            for (int c = 0; c < 8; ++c) pw[c] = qw[c] = 0u;
+            if (lane < 16) gs.row[qd][32 * I + 16 * hf + lane] = 0.f;
           } else {
-            float a[32], e[32];
-            tmem_ldn<2>(ta + 32 * j, a);
-            tmem_ldn<2>(te + 32 * j, e);
-            const float fr = I > qd ? tail * exp2f(g.off(I) - g.off(qd + 1)) : 0.f;
+            float a[16], e[16];
+            tmem_ld16(ta + 16 * hf, a);
+            tmem_ld16(te + 16 * hf, e);
+            tmem_ld_wait();
+            const float4* tab = reinterpret_cast<const float4*>((I > qd ? g.ew : g.wp) + 32 * I + 16 * hf);
 #pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              float p[2], qq[2];
+            for (int c = 0; c < 16; c += 4) {
+              const float4 t4 = tab[c / 4];
+              const float tv[4] = {t4.x, t4.y, t4.z, t4.w};
+              float p[4], qq[4];
 #pragma unroll
-              for (int t = 0; t < 2; ++t) {
-                const float wi = g.wp[32 * I + c + t];
-                const float wt_ = I > qd ? fr * exp2f(wi) : (c + t >= lane ? exp2f(wi - wp) : 0.f);
-                p[t] = wt_ * a[c + t];
-                qq[t] = wt_ * del * e[c + t];
-                const float gg = I == qd && c + t == lane ? 0.f : qq[t] * a[c + t];
-                col += gg;
-                e[c + t] = gg;
+              for (int t = 0; t < 4; ++t) {
+                if (I > qd) {
+                  p[t] = tv[t] * fr * a[c + t];
+                  qq[t] = tv[t] * frd * e[c + t];
+                  e[c + t] = qq[t] * a[c + t];
+                } else {
+                  const int i_ = 16 * hf + c + t;
+                  const float wt_ = i_ >= lane ? exp2f(tv[t] - wp) : 0.f;
+                  p[t] = wt_ * a[c + t];
+                  qq[t] = wt_ * del * e[c + t];
+                  e[c + t] = i_ == lane ? 0.f : qq[t] * a[c + t];  // a pair with itself feels no decay
+                }
+                col += e[c + t];
               }
               pw[c / 2] = pack_bf16(p[0], p[1]);
+              pw[c / 2 + 1] = pack_bf16(p[2], p[3]);
               qw[c / 2] = pack_bf16(qq[0], qq[1]);
+              qw[c / 2 + 1] = pack_bf16(qq[2], qq[3]);
             }
-            rs = column_sums(e, lane);
+            const float rs = column_sums(e, lane);
+            if (lane < 16) gs.row[qd][32 * I + 16 * hf + lane] = rs;
           }
-          s_row[qd][32 * I + lane] = rs;
-          tmem_st16u(ta + 16 * j, pw);  // over columns this warp has read
-          tmem_st16u(te + 16 * j, qw);
-          uint8_t* qt = sm + G_Q + wg * TILE;
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            sts128(qt + row * 128 + (((4 * j + c) ^ (row & 7)) << 4), make_uint4(qw[4 * c], qw[4 * c + 1], qw[4 * c + 2], qw[4 * c + 3]));
+          tmem_st8u(ta + 8 * hf, pw);  // over columns this warp has read
+          tmem_st8u(te + 8 * hf, qw);
+          const int ch = 4 * (I & 1) + 2 * hf;
+          sts128(qt + ((ch ^ (row & 7)) << 4), make_uint4(qw[0], qw[1], qw[2], qw[3]));
+          sts128(qt + (((ch + 1) ^ (row & 7)) << 4), make_uint4(qw[4], qw[5], qw[6], qw[7]));
         }
-        s_col[wg][row] = col;
+        gs.col[I][row] = col;
         tmem_st_wait();
       }
       fence_proxy_async();
@@ -682,89 +759,109 @@ __global__ void __launch_bounds__(NT, 1)
       // ---- the carried states' parts of dB and dC
       if (wtu(&bar_2, k, 92)) {
         tc_fence_after();
-        float f[32], t[32], d = 0.f;
-        tmem_ldn<2>(tm + TG_B + 32 * wg + lq, f);
-        tile_row_cols<32>(sm + G_B, row, 32 * wg, t);
+        float f[16], f2[16], t[16], d = 0.f;
+        tmem_ld16(tm + TG_B + c0 + lq, f);
+        tmem_ld16(tm + TG_C + c0 + lq, f2);
+        tile_row_cols<16>(sm + G_B, row, c0, t);
+        tmem_ld_wait();
         const float fb = del * fend;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
+        for (int c = 0; c < 16; ++c) {
           f[c] *= fb;
           d = fmaf(f[c], t[c], d);
           aB[c] += f[c];
         }
-        s_w[wg][row] = d;
+        gs.w[I][row] = d;
         d = 0.f;
-        tmem_ldn<2>(tm + TG_C + 32 * wg + lq, f);
-        tile_row_cols<32>(sm + G_C, row, 32 * wg, t);
+        tile_row_cols<16>(sm + G_C, row, c0, t);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          f[c] *= ecum;
-          d = fmaf(f[c], t[c], d);
-          aC[c] += f[c];
+        for (int c = 0; c < 16; ++c) {
+          f2[c] *= ecum;
+          d = fmaf(f2[c], t[c], d);
+          aC[c] += f2[c];
         }
-        s_v[wg][row] = d;
+        gs.v[I][row] = d;
       }
       tc_fence_before();
       mbar_arrive(&bar_c);
+      if (I == 1 && i + 1 < w.nh) {  // the next head's gates, beside this one's products
+        put_gates(gates[k ^ 1], z + par_[i + 1].bias, live, par_[i + 1].A, row);
+        z = raw(i + 2);
+      }
+      // <S, R> over the two bf16 tiles: 8 values a thread
+      float sr = 0.f, dsk = 0.f;
+      if (in) {
+        const uint4 a = lds128(sm + G_S + k * STILE + threadIdx.x * 16), b = lds128(sm + G_R + k * STILE + threadIdx.x * 16);
+        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sr = fmaf(__uint_as_float(av[j] << 16), __uint_as_float(bv[j] << 16), sr);
+          sr = fmaf(__uint_as_float(av[j] & 0xffff0000u), __uint_as_float(bv[j] & 0xffff0000u), sr);
+        }
+      }
       // ---- dx
-      float dsk = 0.f;
       if (wtu(&bar_3, k, 93) && in) {
         tc_fence_after();
-        float u[32], x[32], y[32], d = 0.f;
-        tmem_ldn<2>(tm + TG_U + 32 * wg + lq, u);
-        tmem_ldn<2>(tm + TG_BR + 32 * wg + lq, x);
+        float u[16], br[16], x[16], y[16], d = 0.f;
+        tmem_ld16(tm + TG_U + c0 + lq, u);
+        tmem_ld16(tm + TG_BR + c0 + lq, br);
+        tile_row_cols<16>(xt, row, c0, x);
+        tile_row_cols<16>(yt, row, c0, y);
+        tmem_ld_wait();
+        const float sk = par_[i].skip;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) u[c] = fmaf(fend, x[c], u[c]);
-        tile_row_cols<32>(xt, row, 32 * wg, x);
-        tile_row_cols<32>(yt, row, 32 * wg, y);
-        const float sk = par(skip, h);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
+        for (int c = 0; c < 16; ++c) {
+          u[c] = fmaf(fend, br[c], u[c]);
           d = fmaf(x[c], u[c], d);
           dsk = fmaf(x[c], y[c], dsk);
           u[c] = live ? fmaf(del, u[c], sk * y[c]) : 0.f;
         }
-        s_u[wg][row] = d;
-        // <S, R> over the two bf16 tiles: 16 values a thread
-        float sr = 0.f;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int o = (threadIdx.x + 256 * c) * 16;
-          const uint4 a = lds128(sm + G_S + k * STILE + o), b = lds128(sm + G_R + k * STILE + o);
-          const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sr = fmaf(__uint_as_float(av[j] << 16), __uint_as_float(bv[j] << 16), sr);
-            sr = fmaf(__uint_as_float(av[j] & 0xffff0000u), __uint_as_float(bv[j] & 0xffff0000u), sr);
-          }
-        }
-        sr = warp_sum(sr);
-        dsk = warp_sum(dsk);
-        if (lane == 0) s_red[warp][0] = sr, s_red[warp][1] = dsk;
-        // the products that read x have been done since bar_2 (x R^T, E^T)
-        tile_put_cols<32>(xt, row, 32 * wg, u);
+        gs.u[I][row] = d;
+        tile_put_cols<16>(xt, row, c0, u);  // the products that read x have been done since bar_2
       }
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive(&bar_x);
-      sync_compute();  // the sums of both halves are in place
-      // ---- the gate's gradient: rows t of warps 0 .. 3
-      if (wg == 0) {
-        float q = s_v[0][row] + s_v[1][row] - (s_col[0][row] + s_col[1][row]);
+      sr = warp_sum(sr);
+      dsk = warp_sum(dsk);
+      if (lane == 0) gs.red[warp][0] = sr, gs.red[warp][1] = dsk;
+      // ---- the pairs' parts of dB and dC
+      if (wtu(&bar_4, k, 94)) {
+        tc_fence_after();
+        float f[16], f2[16];
+        tmem_ld16(tm + TG_B + c0 + lq, f);
+        tmem_ld16(tm + TG_C + c0 + lq, f2);
+        tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q += s_row[j][row];
-        const float ww = s_w[0][row] + s_w[1][row];
+        for (int c = 0; c < 16; ++c) {
+          aB[c] += f[c];
+          aC[c] += f2[c];
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&bar_free);
+      sync_grad();  // this head's sums and the next one's gates are in place
+      // ---- the gate's gradient, row by row (sigmoid(z) = 1 - exp(-delta))
+      if (I == 0) {
+        float q = 0.f, ww = 0.f, xu = 0.f, ds = 0.f;
+        sr = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          q += gs.v[j][row] - gs.col[j][row] + gs.row[j][row];
+          ww += gs.w[j][row];
+          xu += gs.u[j][row];
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sr += gs.red[j][0], ds += gs.red[j][1];
         const float suf = warp_suffix(q), pre = warp_prefix(ww);
         if (lane == 0) s_tot[qd][0] = suf;
         if (lane == 31) s_tot[qd][1] = pre;
         asm volatile("bar.sync 2, 128;" ::: "memory");
-        float dl = suf + (pre - ww), sr = 0.f, ds = 0.f;
+        float dl = suf + (pre - ww);
         for (int j = qd + 1; j < 4; ++j) dl += s_tot[j][0];
         for (int j = 0; j < qd; ++j) dl += s_tot[j][1];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sr += s_red[j][0], ds += s_red[j][1];
-        dl = fmaf(exp2f(g.off(4)), sr, dl);
-        const float dz = live ? (s_u[0][row] + s_u[1][row] + Ah * dl) / (1.f + expf(-zi)) : 0.f;
+        dl = fmaf(eall, sr, dl);
+        const float dz = live ? (xu + par_[i].A * dl) * -expm1f(-del) : 0.f;
         if (row < in_n) ddt[(r0 + row) * s.H + h] = from_f<bf16>(dz);
         const float dA = warp_sum(live ? del * dl : 0.f), db = warp_sum(dz);
         if (lane == 0) s_out[qd][0] = dA, s_out[qd][1] = db;
@@ -776,45 +873,28 @@ __global__ void __launch_bounds__(NT, 1)
           o[2] = s_out[0][1] + s_out[1][1] + s_out[2][1] + s_out[3][1];
         }
       }
-      // ---- the pairs' parts of dB and dC
-      if (wtu(&bar_4, k, 94)) {
-        tc_fence_after();
-        float f[32];
-        tmem_ldn<2>(tm + TG_B + 32 * wg + lq, f);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) aB[c] += f[c];
-        tmem_ldn<2>(tm + TG_C + 32 * wg + lq, f);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) aC[c] += f[c];
-      }
-      tc_fence_before();
-      mbar_arrive(&bar_free);
     }
-    if (row < in_n) {
-      const long o = ((r0 + row) * parts + w.part) * s.D + 32 * wg;
+    if (row < in_n && c0 < s.D) {
+      const long o = ((r0 + row) * parts + w.part) * s.D + c0;
+      if (!live) {
 #pragma unroll
-      for (int c = 0; c < 32; c += 8) {
-        if (32 * wg + c >= s.D) break;
-        if (!live) {
+        for (int c = 0; c < 16; ++c) aB[c] = aC[c] = 0.f;
+      }
+      if (direct) {
+        store_bf16<16>(static_cast<bf16*>(dB) + o, aB);
+        store_bf16<16>(static_cast<bf16*>(dC) + o, aC);
+      } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) aB[c + j] = aC[c + j] = 0.f;
-        }
-        if (direct) {
-          store_bf16<8>(static_cast<bf16*>(dB) + o + c, aB + c);
-          store_bf16<8>(static_cast<bf16*>(dC) + o + c, aC + c);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            *reinterpret_cast<float4*>(static_cast<float*>(dB) + o + c + j) = make_float4(aB[c + j], aB[c + j + 1], aB[c + j + 2], aB[c + j + 3]);
-            *reinterpret_cast<float4*>(static_cast<float*>(dC) + o + c + j) = make_float4(aC[c + j], aC[c + j + 1], aC[c + j + 2], aC[c + j + 3]);
-          }
+        for (int c = 0; c < 16; c += 4) {
+          *reinterpret_cast<float4*>(static_cast<float*>(dB) + o + c) = make_float4(aB[c], aB[c + 1], aB[c + 2], aB[c + 3]);
+          *reinterpret_cast<float4*>(static_cast<float*>(dC) + o + c) = make_float4(aC[c], aC[c + 1], aC[c + 2], aC[c + 3]);
         }
       }
     }
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == W_ISSUE) tmem_dealloc(tm, 512);
+  if (warp == WG_ISSUE) tmem_dealloc(tm, 512);
 }
 
 // ------------------------------------------------------------------ host
@@ -833,7 +913,7 @@ struct Parts {
     const long units = (long)s.B * chunks(s) * s.G;
     double best = 0;
     hs = 1;
-    for (int t = 1; t <= hg && t <= 16; ++t) {
+    for (int t = 1; t <= hg && t <= MAXH; ++t) {
       const long blocks = units * ((hg + t - 1) / t);
       const double cost = (double)((blocks + slots - 1) / slots) * (t + 1.0);
       if (t == 1 || cost < best) best = cost, hs = t;
@@ -896,8 +976,8 @@ cudaError_t scan_fwd_tc(const ScanIn& a, float* S, void* y, void* ws, const Scan
   const bf16 *dt = (const bf16*)a.dt, *A = (const bf16*)a.A, *skip = (const bf16*)a.skip, *bias = (const bf16*)a.dt_bias;
   int* err = status_word();
   if (states) {
-    LA_TRY_CUDA(cudaFuncSetAttribute(k_sums<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM(2)));
-    k_sums<2><<<grid, NT, S_SMEM(2), st>>>(m, dt, A, bias, a.lengths, pf, nullptr, tot, s, p.pg, p.hs, err);
+    LA_TRY_CUDA(cudaFuncSetAttribute(k_sums<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM(3)));
+    k_sums<3><<<grid, NT, S_SMEM(3), st>>>(m, dt, A, bias, a.lengths, pf, nullptr, tot, s, p.pg, p.hs, err);
     LA_TRY_CUDA(cudaGetLastError());
     LA_TRY_CUDA(scan_carry_bf16(pf, nullptr, sf, nullptr, tot, S, s.B * s.H, nch, s.D * s.M, st));
   }
@@ -929,7 +1009,7 @@ cudaError_t scan_bwd_tc(const ScanIn& a, const void* dy, const ScanGrads& d, voi
   const Parts p(s, sm_count());
   const bool direct = p.pg == 1;
   LA_TRY_CUDA(cudaFuncSetAttribute(k_grad, cudaFuncAttributeMaxDynamicSharedMemorySize, G_SMEM));
-  k_grad<<<dim3(nch, s.G * p.pg, s.B), NT, G_SMEM, st>>>(m, dt, A, skip, bias, a.lengths, (bf16*)d.x, (bf16*)d.dt,
+  k_grad<<<dim3(nch, s.G * p.pg, s.B), NTG, G_SMEM, st>>>(m, dt, A, skip, bias, a.lengths, (bf16*)d.x, (bf16*)d.dt,
                                                         direct ? d.B : base + w.pB, direct ? d.C : base + w.pC, pp, s, p.pg, p.hs, err);
   LA_TRY_CUDA(cudaGetLastError());
   if (!direct) LA_TRY_CUDA(scan_groups((float*)(base + w.pB), (float*)(base + w.pC), d.B, d.C, s, p.pg, st));
