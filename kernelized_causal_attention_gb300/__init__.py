@@ -28,6 +28,7 @@ eq. 7 (phi), §3.3 eq. 9-12, §3.3.1 eq. 13-15, §3.4 eq. 16-20.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -96,6 +97,8 @@ def library_path() -> str:
 def lib():
     """The loaded CUDA library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -147,9 +150,19 @@ def _pv(t):
     return t
 
 
+def _current_stream():
+    """The current device's current stream as an address."""
+    return torch.cuda.current_stream().cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):  # the same address without building a Stream object (3 us)
+    def _current_stream():  # noqa: F811
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -506,55 +519,68 @@ def decode_step_proj(x, W, S, Z, H, D, M, stream=None):
 # ------------------------- the layer with a data-dependent decay, and its encoder
 #
 # These wrappers check shapes, types and devices, allocate on the inputs' device and run on that
-# device's current stream (``with torch.cuda.stream(s):`` for another one).
+# device's current stream (``with torch.cuda.stream(s):`` for another one).  A step's kernels take a
+# few microseconds, so they are written to cost the host little more than the call itself.
 
-def _like(t, name, shape, dtype, device, optional=False):
-    """t has the shape, type and device that the call needs."""
-    if t is None and optional:
-        return
+def _take(t, name, shape, dtype, device):
+    """The address of a dense tensor of the shape, type and device that the call needs."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: a tensor is needed")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the call is on {device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: {t.dtype}, the call needs {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the call is on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    return t.data_ptr()
+
+
+def _take_opt(t, name, shape, dtype, device):
+    return None if t is None else _take(t, name, shape, dtype, device)
+
+
+def _take_rows(t, name, shape, dtype, device, lead):
+    """(address, row stride) of a token-major view whose first `lead` dimensions are batch (and row):
+    rows dense, and all rows of all batch entries evenly spaced."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: a tensor is needed")
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
-
-
-def _row_stride(t, name, lead):
-    """The row stride of a token-major view whose first `lead` dimensions are batch (and row): rows
-    dense, and all rows of all batch entries evenly spaced."""
-    want = 1
-    for n, st in zip(reversed(t.shape[lead:]), reversed(t.stride()[lead:])):
-        if n != 1 and st != want:
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {t.dtype}, the call needs {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, the call is on {device}")
+    st, want = t.stride(), 1
+    for i in range(len(shape) - 1, lead - 1, -1):
+        if shape[i] != 1 and st[i] != want:
             raise ValueError(f"{name}: every row must be dense")
-        want *= n
+        want *= shape[i]
+    B = shape[0]
     if lead == 1:
-        return t.stride(0) if t.shape[0] > 1 else want
-    B, N = t.shape[:2]
-    sb, sn = t.stride()[:2]
-    ld = sn if N > 1 else (sb if B > 1 else want)
-    if B > 1 and sb != N * ld:
+        return t.data_ptr(), st[0] if B > 1 else want
+    N = shape[1]
+    ld = st[1] if N > 1 else (st[0] if B > 1 else want)
+    if B > 1 and st[0] != N * ld:
         raise ValueError(f"{name}: batch entries must be N rows apart")
-    return ld
+    return t.data_ptr(), ld
 
 
-class _On:
-    """The device of the call's tensors as the current one, where it is not already."""
+def _on_device(f):
+    """f(x, ...) with x's device as the current one."""
+    @functools.wraps(f)
+    def call(x, *args, **kw):
+        if not isinstance(x, torch.Tensor) or not x.is_cuda or x.get_device() == torch.cuda.current_device():
+            return f(x, *args, **kw)
+        with torch.cuda.device(x.device):
+            return f(x, *args, **kw)
+    return call
 
-    def __init__(self, device):
-        if device.type != "cuda":
-            raise ValueError("tensors must be on a CUDA device")
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+def _need_cuda(t):
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a CUDA device")
 
 
 def _scratch(n, device):
@@ -562,111 +588,122 @@ def _scratch(n, device):
 
 
 def _conv_args(x, w, bias, lengths, lead):
-    C, dt, dev = x.shape[-1], _dtype_code(x), x.device
     if x.dim() != lead + 1 or w.dim() != 2:
         raise ValueError(f"x: {lead + 1} dimensions, w: [C, K]")
-    K = w.shape[1]
-    _like(w, "w", (C, K), x.dtype, dev)
-    _like(bias, "bias", (C,), x.dtype, dev, True)
-    _like(lengths, "lengths", (x.shape[0],), torch.int32, dev, True)
-    return C, K, dt, dev, _row_stride(x, "x", lead)
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    C, K = shape[-1], w.shape[1]
+    code = _dtype_code(x)
+    px, ld = _take_rows(x, "x", shape, dtype, dev, lead)
+    pw = _take(w, "w", (C, K), dtype, dev)
+    pb = _take_opt(bias, "bias", (C,), dtype, dev)
+    pn = _take_opt(lengths, "lengths", shape[:1], torch.int32, dev)
+    return shape, C, K, code, dtype, dev, px, ld, pw, pb, pn
 
 
+@_on_device
 def short_conv_fwd(x, w, bias=None, state=None, lengths=None, silu=True):
     """y [B,N,C] of the short causal depthwise convolution: x [B,N,C] (rows may be slices of wider
     ones), w [C,K], K = 2..4, bias [C]; state [B,K-1,C] holds the inputs before row 0 (zeros if None)
     and is updated in place; lengths: int32 [B] of valid rows."""
-    C, K, dt, dev, ld = _conv_args(x, w, bias, lengths, 2)
-    B, N = x.shape[:2]
-    _like(state, "state", (B, K - 1, C), x.dtype, dev, True)
-    with _On(dev):
-        y = torch.empty(B, N, C, dtype=x.dtype, device=dev)
-        la_short_conv_fwd(x, w, bias, lengths, state, y, B, N, C, K, ld, silu, dt)
+    (B, N, _), C, K, code, dtype, dev, px, ld, pw, pb, pn = _conv_args(x, w, bias, lengths, 2)
+    ps = _take_opt(state, "state", (B, K - 1, C), dtype, dev)
+    _need_cuda(x)
+    y = torch.empty((B, N, C), dtype=dtype, device=dev)
+    _check(lib().la_short_conv_fwd(px, pw, pb, pn, ps, y.data_ptr(), B, N, C, K, ld, int(silu), code, _stream(None)),
+           "la_short_conv_fwd")
     return y
 
 
+@_on_device
 def short_conv_bwd(x, w, bias, dy, lengths=None, silu=True):
     """(dx, dw, db) of sum(dy * y) for a history of zeros; db is None without a bias."""
-    C, K, dt, dev, ld = _conv_args(x, w, bias, lengths, 2)
-    B, N = x.shape[:2]
-    _like(dy, "dy", (B, N, C), x.dtype, dev)
-    with _On(dev):
-        dx, dw = torch.empty(B, N, C, dtype=x.dtype, device=dev), torch.empty_like(w)
-        db = None if bias is None else torch.empty_like(bias)
-        ws = _scratch(la_short_conv_workspace_bytes(B, N, C, K, dt), dev)
-        la_short_conv_bwd(x, w, bias, lengths, dy, dx, dw, db, ws, B, N, C, K, ld, silu, dt)
+    shape, C, K, code, dtype, dev, px, ld, pw, pb, pn = _conv_args(x, w, bias, lengths, 2)
+    B, N, _ = shape
+    pg = _take(dy, "dy", shape, dtype, dev)
+    _need_cuda(x)
+    dx, dw = torch.empty((B, N, C), dtype=dtype, device=dev), torch.empty_like(w)
+    db = None if bias is None else torch.empty_like(bias)
+    ws = _scratch(la_short_conv_workspace_bytes(B, N, C, K, code), dev)
+    _check(lib().la_short_conv_bwd(px, pw, pb, pn, pg, dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(),
+                                   _p(ws), _nbytes(ws), B, N, C, K, ld, int(silu), code, _stream(None)), "la_short_conv_bwd")
     return dx, dw, db
 
 
+@_on_device
 def short_conv_step(x, w, bias, state, silu=True):
     """y [B,C] for one row x [B,C] of each stream; state [B,K-1,C] is shifted in place."""
-    C, K, dt, dev, ld = _conv_args(x, w, bias, None, 1)
-    B = x.shape[0]
-    _like(state, "state", (B, K - 1, C), x.dtype, dev)
-    with _On(dev):
-        y = torch.empty(B, C, dtype=x.dtype, device=dev)
-        la_short_conv_step(x, w, bias, state, y, B, C, K, ld, silu, dt)
+    (B, _), C, K, code, dtype, dev, px, ld, pw, pb, _ = _conv_args(x, w, bias, None, 1)
+    ps = _take(state, "state", (B, K - 1, C), dtype, dev)
+    _need_cuda(x)
+    y = torch.empty((B, C), dtype=dtype, device=dev)
+    _check(lib().la_short_conv_step(px, pw, pb, ps, y.data_ptr(), B, C, K, ld, int(silu), code, _stream(None)),
+           "la_short_conv_step")
     return y
 
 
 def _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, lengths, lead):
+    """(pointers up to lengths, row strides, sizes (H, G, D, M), type code, type, device)."""
     if x.dim() != lead + 2 or Bm.dim() != lead + 2:
         raise ValueError(f"x, Bm and Cm: {lead + 2} dimensions")
-    rows, (H, M), (G, D) = tuple(x.shape[:lead]), x.shape[lead:], Bm.shape[lead:]
-    t, dev = x.dtype, x.device
+    shape, gshape, dtype, dev = x.shape, Bm.shape, x.dtype, x.device
+    rows = shape[:lead]
+    H, M, G, D = shape[lead], shape[lead + 1], gshape[lead], gshape[lead + 1]
     code = _dtype_code(x)
-    _like(dt, "dt", rows + (H,), t, dev)
-    for v, n in ((Bm, "Bm"), (Cm, "Cm")):
-        _like(v, n, rows + (G, D), t, dev)
-    _like(A, "A", (H,), t, dev)
-    _like(skip, "skip", (H,), t, dev, True)
-    _like(dt_bias, "dt_bias", (H,), t, dev, True)
-    _like(lengths, "lengths", rows[:1], torch.int32, dev, True)
-    strides = [_row_stride(v, n, lead) for v, n in ((x, "x"), (dt, "dt"), (Bm, "Bm"), (Cm, "Cm"))]
-    return (H, G, D, M), strides, code, dev
+    px, lx = _take_rows(x, "x", shape, dtype, dev, lead)
+    pt, lt = _take_rows(dt, "dt", rows + (H,), dtype, dev, lead)
+    pb, lb = _take_rows(Bm, "Bm", rows + (G, D), dtype, dev, lead)
+    pc, lc = _take_rows(Cm, "Cm", rows + (G, D), dtype, dev, lead)
+    h = (H,)
+    ptrs = (px, pt, _take(A, "A", h, dtype, dev), pb, pc, _take_opt(skip, "skip", h, dtype, dev),
+            _take_opt(dt_bias, "dt_bias", h, dtype, dev), _take_opt(lengths, "lengths", rows[:1], torch.int32, dev))
+    return ptrs, (lx, lt, lb, lc), (H, G, D, M), code, dtype, dev
 
 
+@_on_device
 def scan_fwd(x, dt, A, Bm, Cm, skip=None, dt_bias=None, S=None, lengths=None):
     """y [B,N,H,M] of the selective scan S_n = exp(delta_n A) S_{n-1} + B_n (delta_n x_n)^T,
     y_n = S_n^T C_n + skip x_n, delta = softplus(dt + dt_bias).  x [B,N,H,M], dt [B,N,H], Bm and Cm
     [B,N,G,D] (G divides H; rows may be slices of wider ones), A, skip, dt_bias [H].  S [B,H,D,M]
     (float32) is the state before row 0 (zeros if None), updated in place to the state after each
     sequence's last valid row; scan_step continues from it."""
-    (H, G, D, M), ld, code, dev = _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, lengths, 2)
+    ptrs, ld, (H, G, D, M), code, dtype, dev = _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, lengths, 2)
     B, N = x.shape[:2]
-    _like(S, "S", (B, H, D, M), torch.float32, dev, True)
-    with _On(dev):
-        y = torch.empty(B, N, H, M, dtype=x.dtype, device=dev)
-        ws = _scratch(la_scan_workspace_bytes(0, B, H, G, N, D, M, code), dev)
-        la_scan_fwd(x, dt, A, Bm, Cm, skip, dt_bias, lengths, S, y, ws, B, H, G, N, D, M, *ld, code)
+    pS = _take_opt(S, "S", (B, H, D, M), torch.float32, dev)
+    _need_cuda(x)
+    y = torch.empty((B, N, H, M), dtype=dtype, device=dev)
+    ws = _scratch(la_scan_workspace_bytes(0, B, H, G, N, D, M, code), dev)
+    _check(lib().la_scan_fwd(*ptrs, pS, y.data_ptr(), _p(ws), _nbytes(ws), B, H, G, N, D, M, *ld, code, _stream(None)),
+           "la_scan_fwd")
     return y
 
 
+@_on_device
 def scan_bwd(x, dt, A, Bm, Cm, skip, dt_bias, dy, lengths=None):
     """(dx, ddt, dA, dBm, dCm, dskip, ddt_bias) of sum(dy * y) for a zero state before row 0; dskip
     and ddt_bias are None without their parameters."""
-    (H, G, D, M), ld, code, dev = _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, lengths, 2)
+    ptrs, ld, (H, G, D, M), code, dtype, dev = _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, lengths, 2)
     B, N = x.shape[:2]
-    _like(dy, "dy", (B, N, H, M), x.dtype, dev)
-    with _On(dev):
-        new = lambda *shape: torch.empty(shape, dtype=x.dtype, device=dev)  # noqa: E731
-        dx, ddt, dA, dB, dC = new(B, N, H, M), new(B, N, H), new(H), new(B, N, G, D), new(B, N, G, D)
-        dskip, dbias = None if skip is None else new(H), None if dt_bias is None else new(H)
-        ws = _scratch(la_scan_workspace_bytes(1, B, H, G, N, D, M, code), dev)
-        la_scan_bwd(x, dt, A, Bm, Cm, skip, dt_bias, lengths, dy, dx, ddt, dA, dB, dC, dskip, dbias, ws,
-                    B, H, G, N, D, M, *ld, code)
-    return dx, ddt, dA, dB, dC, dskip, dbias
+    pg = _take(dy, "dy", x.shape, dtype, dev)
+    _need_cuda(x)
+    new = lambda *shape: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
+    d = [new(B, N, H, M), new(B, N, H), new(H), new(B, N, G, D), new(B, N, G, D), None if skip is None else new(H),
+         None if dt_bias is None else new(H)]
+    ws = _scratch(la_scan_workspace_bytes(1, B, H, G, N, D, M, code), dev)
+    _check(lib().la_scan_bwd(*ptrs, pg, *[None if t is None else t.data_ptr() for t in d], _p(ws), _nbytes(ws), B, H, G, N, D,
+                             M, *ld, code, _stream(None)), "la_scan_bwd")
+    return tuple(d)
 
 
+@_on_device
 def scan_step(x, dt, A, Bm, Cm, skip, dt_bias, S):
     """y [B,H,M] for one row of each stream: x [B,H,M], dt [B,H], Bm and Cm [B,G,D]; S [B,H,D,M]
     (float32) is updated in place."""
-    (H, G, D, M), ld, code, dev = _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, None, 1)
+    ptrs, ld, (H, G, D, M), code, dtype, dev = _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, None, 1)
     B = x.shape[0]
-    _like(S, "S", (B, H, D, M), torch.float32, dev)
-    with _On(dev):
-        y = torch.empty(B, H, M, dtype=x.dtype, device=dev)
-        la_scan_step(x, dt, A, Bm, Cm, skip, dt_bias, S, y, B, H, G, D, M, *ld, code)
+    pS = _take(S, "S", (B, H, D, M), torch.float32, dev)
+    _need_cuda(x)
+    y = torch.empty((B, H, M), dtype=dtype, device=dev)
+    _check(lib().la_scan_step(*ptrs[:7], pS, y.data_ptr(), B, H, G, D, M, *ld, code, _stream(None)), "la_scan_step")
     return y
 
 
@@ -675,57 +712,59 @@ def _cross_args(q, k, v, lengths):
         raise ValueError("q, k and v: 4 dimensions")
     B, H, Nq, D = q.shape
     Hk, Nk, M = k.shape[1], k.shape[2], v.shape[3]
-    code = _dtype_code(q)
-    _like(k, "k", (B, Hk, Nk, D), q.dtype, q.device)
-    _like(v, "v", (B, Hk, Nk, M), q.dtype, q.device)
-    _like(lengths, "lengths", (B,), torch.int32, q.device, True)
-    return (B, H, Hk, Nq, Nk, D, M), code, q.device
+    code, dtype, dev = _dtype_code(q), q.dtype, q.device
+    ptrs = (_take(q, "q", q.shape, dtype, dev), _take(k, "k", (B, Hk, Nk, D), dtype, dev),
+            _take(v, "v", (B, Hk, Nk, M), dtype, dev), _take_opt(lengths, "lengths", (B,), torch.int32, dev))
+    return ptrs, (B, H, Hk, Nq, Nk, D, M), code, dtype, dev
 
 
+@_on_device
 def cross_fwd(q, k, v, lengths=None):
     """(out, den, S, Z) of the kernelized cross attention of q [B,H,Nq,D] to an encoder's k [B,Hk,Nk,D]
     and v [B,Hk,Nk,M] (Hk divides H); lengths: int32 [B] of valid encoder states.  S [B,Hk,D,M] and
     Z [B,Hk,D] (float32) are all that cross_step needs of the encoder."""
-    size, code, dev = _cross_args(q, k, v, lengths)
+    ptrs, size, code, dtype, dev = _cross_args(q, k, v, lengths)
     B, H, Hk, Nq, Nk, D, M = size
-    with _On(dev):
-        out = torch.empty(B, H, Nq, M, dtype=q.dtype, device=dev)
-        den = torch.empty(B, H, Nq, dtype=torch.float32, device=dev)
-        S = torch.empty(B, Hk, D, M, dtype=torch.float32, device=dev)
-        Z = torch.empty(B, Hk, D, dtype=torch.float32, device=dev)
-        ws = _scratch(la_cross_workspace_bytes(0, *size, code), dev)
-        la_cross_fwd(q, k, v, lengths, out, den, S, Z, ws, *size, code)
+    _need_cuda(q)
+    out, den = torch.empty((B, H, Nq, M), dtype=dtype, device=dev), torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
+    S, Z = (torch.empty(n, dtype=torch.float32, device=dev) for n in ((B, Hk, D, M), (B, Hk, D)))
+    ws = _scratch(la_cross_workspace_bytes(0, *size, code), dev)
+    _check(lib().la_cross_fwd(*ptrs, out.data_ptr(), den.data_ptr(), S.data_ptr(), Z.data_ptr(), _p(ws), _nbytes(ws), *size,
+                              code, _stream(None)), "la_cross_fwd")
     return out, den, S, Z
 
 
+@_on_device
 def cross_bwd(q, k, v, lengths, out, den, S, Z, dout):
     """(dq, dk, dv) of sum(dout * out); out, den, S, Z from cross_fwd."""
-    size, code, dev = _cross_args(q, k, v, lengths)
+    ptrs, size, code, dtype, dev = _cross_args(q, k, v, lengths)
     B, H, Hk, Nq, Nk, D, M = size
-    for t, n in ((out, "out"), (dout, "dout")):
-        _like(t, n, (B, H, Nq, M), q.dtype, dev)
-    _like(den, "den", (B, H, Nq), torch.float32, dev)
-    _like(S, "S", (B, Hk, D, M), torch.float32, dev)
-    _like(Z, "Z", (B, Hk, D), torch.float32, dev)
-    with _On(dev):
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        ws = _scratch(la_cross_workspace_bytes(1, *size, code), dev)
-        la_cross_bwd(q, k, v, lengths, out, den, S, Z, dout, dq, dk, dv, ws, *size, code)
+    f32 = torch.float32
+    more = (_take(out, "out", (B, H, Nq, M), dtype, dev), _take(den, "den", (B, H, Nq), f32, dev),
+            _take(S, "S", (B, Hk, D, M), f32, dev), _take(Z, "Z", (B, Hk, D), f32, dev),
+            _take(dout, "dout", (B, H, Nq, M), dtype, dev))
+    _need_cuda(q)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ws = _scratch(la_cross_workspace_bytes(1, *size, code), dev)
+    _check(lib().la_cross_bwd(*ptrs, *more, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _p(ws), _nbytes(ws), *size, code,
+                              _stream(None)), "la_cross_bwd")
     return dq, dk, dv
 
 
+@_on_device
 def cross_step(q, S, Z):
     """y [B,H,M] for one token q [B,H,D] of each stream, from the kept S [B,Hk,D,M] and Z [B,Hk,D]."""
     if q.dim() != 3 or S.dim() != 4:
         raise ValueError("q: 3 dimensions, S: 4")
     B, H, D = q.shape
     Hk, M = S.shape[1], S.shape[3]
-    code = _dtype_code(q)
-    _like(S, "S", (B, Hk, D, M), torch.float32, q.device)
-    _like(Z, "Z", (B, Hk, D), torch.float32, q.device)
-    with _On(q.device):
-        y = torch.empty(B, H, M, dtype=q.dtype, device=q.device)
-        la_cross_step(q, S, Z, y, B, H, Hk, D, M, code)
+    code, dtype, dev = _dtype_code(q), q.dtype, q.device
+    pq = _take(q, "q", q.shape, dtype, dev)
+    pS = _take(S, "S", (B, Hk, D, M), torch.float32, dev)
+    pZ = _take(Z, "Z", (B, Hk, D), torch.float32, dev)
+    _need_cuda(q)
+    y = torch.empty((B, H, M), dtype=dtype, device=dev)
+    _check(lib().la_cross_step(pq, pS, pZ, y.data_ptr(), B, H, Hk, D, M, code, _stream(None)), "la_cross_step")
     return y
 
 
