@@ -23,6 +23,8 @@
 // This file: the fp32 kernels (chunks of 64 rows, FFMA), the carry and the
 // reductions both paths use, and the single-row step.  The fp32 chunk kernels
 // are bound by the FFMA rate (about 16 D M-sized products a row).
+#include <algorithm>
+
 #include "ffma.cuh"
 #include "scan.cuh"
 
@@ -102,55 +104,74 @@ __device__ __forceinline__ void put4(bf16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
-// Four values a thread: out[c] becomes the state before chunk c (REV: the state
-// gradient after it) from the chunks' own sums p, which may be the same memory.
-// The chunk walk is a chain of one fused multiply-add; the loads run eight
-// chunks ahead of it.
-template <bool REV, typename O>
-__device__ __forceinline__ void carry_walk(const float* p, O* out, const float* tot, long step, int nch, float4& run) {
+// One thread's chunks c0, c0 + dc, ... (n of them), four values of the state:
+// run <- exp(tot) run + p[c], and before that out[c] = run where out is wanted
+// (it may be p's own memory).  A chain of one fused multiply-add a chunk; the
+// loads run eight chunks ahead of it.
+template <typename O>
+__device__ __forceinline__ void carry_walk(const float* p, O* out, const float* tot, long step, int c0, int dc, int n, float4& run) {
   constexpr int U = 8;
-  for (int c0 = 0; c0 < nch; c0 += U) {
+  for (int k0 = 0; k0 < n; k0 += U) {
     float4 v[U];
     float e[U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int k = c0 + i, c = REV ? nch - 1 - k : k;
-      if (k < nch) {
+    for (int i = 0; i < U; ++i)
+      if (k0 + i < n) {
+        const int c = c0 + (k0 + i) * dc;
         v[i] = *reinterpret_cast<const float4*>(p + c * step);
         e[i] = expf(tot[c]);
       }
-    }
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int k = c0 + i, c = REV ? nch - 1 - k : k;
-      if (k < nch) {
-        put4(out + c * step, run);
+    for (int i = 0; i < U; ++i)
+      if (k0 + i < n) {
+        if (out != nullptr) put4(out + (c0 + (k0 + i) * dc) * step, run);
         run.x = fmaf(e[i], run.x, v[i].x);
         run.y = fmaf(e[i], run.y, v[i].y);
         run.z = fmaf(e[i], run.z, v[i].z);
         run.w = fmaf(e[i], run.w, v[i].w);
       }
-    }
   }
 }
 
+// The carry over the chunks (scan_carry): 32 x segs threads, 128 values of one
+// state, each thread row one segment of the chunks.  With several segments every
+// row first walks its own from zero, the starting states follow from those ends,
+// and the second walk (its loads from L2) writes: a chain of chunks / segs.
+constexpr int CARRY_SEGS = 16;
 template <typename O>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(32 * CARRY_SEGS)
     k_scan_carry(const float* fwd, const float* rev, O* fs, O* rs, const float* __restrict__ tot, float* __restrict__ S,
-                 int nch, int DM) {
-  const int e = (blockIdx.x * 128 + threadIdx.x) * 4;
-  const long bh = blockIdx.y;
-  if (e >= DM) return;
+                 int nch, int DM, int per) {
+  __shared__ float4 ends[CARRY_SEGS][32];
+  __shared__ float decay[CARRY_SEGS];
+  const int e = (blockIdx.x * 32 + threadIdx.x) * 4, seg = threadIdx.y, segs = blockDim.y;
+  const long bh = blockIdx.y, at = bh * nch * DM + e;
+  const bool back = blockIdx.z != 0, live = e < DM;
+  const float* p = (back ? rev : fwd) + at;
+  O* out = (back ? rs : fs) + at;
   const float* tt = tot + bh * nch;
-  const long at = bh * nch * DM + e;
+  const int first = seg * per, n = min(per, nch - first), c0 = back ? nch - 1 - first : first, dc = back ? -1 : 1;
   float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (blockIdx.z == 0) {
-    if (S != nullptr) run = *reinterpret_cast<const float4*>(S + bh * DM + e);
-    carry_walk<false>(fwd + at, fs + at, tt, DM, nch, run);
-    if (S != nullptr) *reinterpret_cast<float4*>(S + bh * DM + e) = run;
-  } else {
-    carry_walk<true>(rev + at, rs + at, tt, DM, nch, run);
+  if (segs > 1) {
+    if (live) carry_walk(p, static_cast<O*>(nullptr), tt, DM, c0, dc, n, run);
+    ends[seg][threadIdx.x] = run;
+    float l = 0.f;
+    for (int k = threadIdx.x; k < n; k += 32) l += tt[c0 + k * dc];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (threadIdx.x == 0) decay[seg] = expf(l);
+    __syncthreads();
   }
+  if (!live) return;
+  float* Sp = S == nullptr || back ? nullptr : S + bh * DM + e;
+  run = Sp != nullptr ? *reinterpret_cast<const float4*>(Sp) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < seg; ++k) {
+    const float d = decay[k];
+    const float4 v = ends[k][threadIdx.x];
+    run.x = fmaf(d, run.x, v.x), run.y = fmaf(d, run.y, v.y), run.z = fmaf(d, run.z, v.z), run.w = fmaf(d, run.w, v.w);
+  }
+  carry_walk(p, out, tt, DM, c0, dc, n, run);
+  if (Sp != nullptr && seg == segs - 1) *reinterpret_cast<float4*>(Sp) = run;
 }
 
 // y of one chunk and head.
@@ -519,8 +540,11 @@ size_t scan_cc_ws_bytes(const ScanShape& s, bool bwd) { return WsCC(s, bwd).end;
 template <typename O>
 static cudaError_t carry(const float* fwd, const float* rev, O* fs, O* rs, const float* tot, float* S, int BH, int nch, int DM,
                          cudaStream_t st) {
-  const dim3 grid((DM / 4 + 127) / 128, BH, rev == nullptr ? 1 : 2);
-  k_scan_carry<<<grid, 128, 0, st>>>(fwd, rev, fs, rs, tot, S, nch, DM);
+  // a second walk pays once a thread would otherwise make several round trips
+  // of eight chunks (512 chunks of 8 heads: 65 us in one walk)
+  const int segs = std::min(CARRY_SEGS, (nch + 31) / 32), per = (nch + segs - 1) / segs;
+  const dim3 grid((DM / 4 + 31) / 32, BH, rev == nullptr ? 1 : 2), block(32, (nch + per - 1) / per);
+  k_scan_carry<<<grid, block, 0, st>>>(fwd, rev, fs, rs, tot, S, nch, DM, per);
   return cudaGetLastError();
 }
 

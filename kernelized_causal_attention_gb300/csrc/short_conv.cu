@@ -8,8 +8,9 @@
 // All three directions are bound by HBM traffic (about 2 K flops an element).
 // A thread owns V neighbouring channels and walks a run of rows with the last K
 // inputs (and, backward, the last K values of g) in registers, so every row is
-// read once plus the K - 1 rows (backward 2 (K - 1)) before a run.  Sums and
-// SiLU are fp32; y, dx and the parameters' gradients are rounded once.
+// read once plus the K - 1 rows (backward 2 (K - 1)) before a run; rows are
+// loaded eight at a time before any is used.  Sums and SiLU are fp32; y, dx and
+// the parameters' gradients are rounded once.
 #include "common.cuh"
 #include "launch.h"
 
@@ -18,34 +19,38 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-// V neighbouring channels, loaded as one vector where V > 1 (the caller has
-// checked the alignment) and kept as fp32.
+// V neighbouring channels as one vector (V = 4: the caller has checked the
+// alignment), raw or as fp32.
 template <typename T, int V>
-struct Pack {
-  static_assert(sizeof(T) * V <= 16, "one load");
-  __device__ __forceinline__ static void ld(const T* p, float (&f)[V]) {
-    if constexpr (V == 1) {
-      f[0] = to_f(*p);
-    } else if constexpr (sizeof(T) == 4) {
-      const float4 u = *reinterpret_cast<const float4*>(p);
-      f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
-    } else {
-      const uint2 u = *reinterpret_cast<const uint2*>(p);
-      f[0] = __uint_as_float(u.x << 16), f[1] = __uint_as_float(u.x & 0xffff0000u);
-      f[2] = __uint_as_float(u.y << 16), f[3] = __uint_as_float(u.y & 0xffff0000u);
-    }
+struct Pack;
+template <typename T>
+struct Pack<T, 1> {
+  using Raw = T;
+  __device__ __forceinline__ static void open(const Raw& u, float (&f)[1]) { f[0] = to_f(u); }
+  __device__ __forceinline__ static void st(T* p, const float (&f)[1]) { *p = from_f<T>(f[0]); }
+};
+template <>
+struct Pack<float, 4> {
+  using Raw = float4;
+  __device__ __forceinline__ static void open(const Raw& u, float (&f)[4]) { f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w; }
+  __device__ __forceinline__ static void st(float* p, const float (&f)[4]) { *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <>
+struct Pack<bf16, 4> {
+  using Raw = uint2;
+  __device__ __forceinline__ static void open(const Raw& u, float (&f)[4]) {
+    f[0] = __uint_as_float(u.x << 16), f[1] = __uint_as_float(u.x & 0xffff0000u);
+    f[2] = __uint_as_float(u.y << 16), f[3] = __uint_as_float(u.y & 0xffff0000u);
   }
-  __device__ __forceinline__ static void st(T* p, const float (&f)[V]) {
-    if constexpr (V == 1) {
-      *p = from_f<T>(f[0]);
-    } else if constexpr (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    } else {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
-      *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    }
+  __device__ __forceinline__ static void st(bf16* p, const float (&f)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
 };
+template <typename T, int V>
+__device__ __forceinline__ void ld(const T* p, float (&f)[V]) {
+  Pack<T, V>::open(*reinterpret_cast<const typename Pack<T, V>::Raw*>(p), f);
+}
 
 template <int V>
 __device__ __forceinline__ void zero(float (&f)[V]) {
@@ -53,23 +58,28 @@ __device__ __forceinline__ void zero(float (&f)[V]) {
   for (int i = 0; i < V; ++i) f[i] = 0.f;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+// For bf16 results the hardware's exponential and reciprocal (a few 2^-22) do.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float x) {
+  return sizeof(T) == 4 ? 1.f / (1.f + expf(-x)) : __fdividef(1.f, 1.f + __expf(-x));
+}
 
 __device__ __forceinline__ int rows_of(const int* lengths, int b, int N) {
   return lengths == nullptr ? N : min(max(lengths[b], 0), N);
 }
 
+constexpr int U = 8;          // rows loaded at a time
 constexpr int FWD_RUN = 16;   // rows a thread walks (forward)
-constexpr int BWD_RUN = 32;   // rows a thread walks (backward)
+constexpr int BWD_WALK = 32;  // rows a thread reads (backward); the last K - 1 only complete the run before them
 constexpr int CG = 32;        // channel groups a block spans
 constexpr int RG = 8;         // row runs a block spans
-constexpr int BWD_ROWS = BWD_RUN * RG;
+constexpr int bwd_rows(int K) { return (BWD_WALK - (K - 1)) * RG; }
 
 // y, and the history in place.  Rows at or past the sequence's length are
 // written as zeros and not read.  The block of the first row group alone reads
 // the history and, after a barrier, writes the new one.
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(CG * RG)
+__global__ void __launch_bounds__(CG * RG, 3)
     k_conv_fwd(const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const int* __restrict__ lengths,
                T* state, T* __restrict__ y, int N, int C, long ldx, int silu) {
   const int c = (blockIdx.x * CG + threadIdx.x) * V;
@@ -93,35 +103,41 @@ __global__ void __launch_bounds__(CG * RG)
       for (int j = 0; j < K - 1; ++j) {  // the K - 1 rows before the run
         const int t = t0 - (K - 1) + j;
         if (t >= 0 && t < L)
-          Pack<T, V>::ld(xb + t * ldx, h[j + 1]);
+          ld<T, V>(xb + t * ldx, h[j + 1]);
         else if (t < 0 && sb != nullptr)
-          Pack<T, V>::ld(sb + (long)(t + K - 1) * C, h[j + 1]);
+          ld<T, V>(sb + (long)(t + K - 1) * C, h[j + 1]);
         else
           zero(h[j + 1]);
       }
       T* yb = y + ((long)b * N + t0) * C + c;
-#pragma unroll 4
-      for (int r = 0; r < FWD_RUN; ++r) {
-        const int t = t0 + r;
-        if (t >= N) break;
-        float o[V];
-        if (t < L) {
+#pragma unroll 1
+      for (int r0 = 0; r0 < FWD_RUN && t0 + r0 < N; r0 += U) {
+        typename Pack<T, V>::Raw in[U];
 #pragma unroll
-          for (int j = 0; j < K - 1; ++j)
+        for (int r = 0; r < U; ++r)
+          if (t0 + r0 + r < L) in[r] = *reinterpret_cast<const typename Pack<T, V>::Raw*>(xb + (t0 + r0 + r) * ldx);
 #pragma unroll
-            for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i];
-          Pack<T, V>::ld(xb + t * ldx, h[K - 1]);
+        for (int r = 0; r < U; ++r) {
+          const int t = t0 + r0 + r;
+          float o[V];
+          if (t < L) {
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float p = bs[i];
+            for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-            for (int j = 0; j < K; ++j) p = fmaf(wk[j][i], h[j][i], p);
-            o[i] = silu ? p * sigmoid(p) : p;
+              for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i];
+            Pack<T, V>::open(in[r], h[K - 1]);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              float p = bs[i];
+#pragma unroll
+              for (int j = 0; j < K; ++j) p = fmaf(wk[j][i], h[j][i], p);
+              o[i] = silu ? p * sigmoid<T>(p) : p;
+            }
+          } else {
+            zero(o);
           }
-        } else {
-          zero(o);
+          if (t < N) Pack<T, V>::st(yb + (long)(r0 + r) * C, o);
         }
-        Pack<T, V>::st(yb + (long)r * C, o);
       }
     }
     if (rg == 0 && state != nullptr) {
@@ -132,9 +148,9 @@ __global__ void __launch_bounds__(CG * RG)
         for (int j = 0; j < K - 1; ++j) {
           const int t = L - (K - 1) + j;
           if (t >= 0)
-            Pack<T, V>::ld(xb + t * ldx, n[j]);
+            ld<T, V>(xb + t * ldx, n[j]);
           else
-            Pack<T, V>::ld(sb + (long)(t + K - 1) * C, n[j]);
+            ld<T, V>(sb + (long)(t + K - 1) * C, n[j]);
         }
 #pragma unroll
         for (int j = 0; j < K - 1; ++j) Pack<T, V>::st(sb + (long)j * C, n[j]);
@@ -143,14 +159,15 @@ __global__ void __launch_bounds__(CG * RG)
   }
 }
 
-// dx, and each block's sums of g x and g over its BWD_ROWS rows into
+// dx, and each block's sums of g x and g over its rows into
 // part[group][K + 1][C] (fp32; the last plane is the bias's).  History zero.
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(CG * RG)
     k_conv_bwd(const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const int* __restrict__ lengths,
                const T* __restrict__ dy, T* __restrict__ dx, float* __restrict__ part, int N, int C, long ldx, int silu,
                int groups) {
-  __shared__ float red[RG][CG * V];
+  __shared__ float red[K + 1][RG][CG * V];
+  constexpr int RUN = BWD_WALK - (K - 1);
   const int c = (blockIdx.x * CG + threadIdx.x) * V;
   const bool live = c < C;
   const int b = blockIdx.z;
@@ -169,7 +186,7 @@ __global__ void __launch_bounds__(CG * RG)
     float sums[K + 1][V];
 #pragma unroll
     for (int j = 0; j <= K; ++j) zero(sums[j]);
-    const int t0 = rg * BWD_ROWS + threadIdx.y * BWD_RUN;
+    const int t0 = (rg * RG + threadIdx.y) * RUN;
     if (live && t0 < N) {
       // h: x rows t - K + 1 .. t;  g: rows t - K + 1 .. t of dy silu'(pre).
       // Row t's g completes dx of row t - K + 1, so the run looks K - 1 rows ahead.
@@ -180,69 +197,78 @@ __global__ void __launch_bounds__(CG * RG)
       for (int j = 0; j < K - 1; ++j) {
         const int t = t0 - (K - 1) + j;
         if (t >= 0 && t < L)
-          Pack<T, V>::ld(xb + t * ldx, h[j + 1]);
+          ld<T, V>(xb + t * ldx, h[j + 1]);
         else
           zero(h[j + 1]);
       }
-#pragma unroll 2
-      for (int r = 0; r < BWD_RUN + K - 1; ++r) {
-        const int t = t0 + r;
+#pragma unroll 1
+      for (int r0 = 0; r0 < BWD_WALK && t0 + r0 < N + K - 1; r0 += U) {
+        typename Pack<T, V>::Raw xi[U], gi[U];
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j)
-#pragma unroll
-          for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i], g[j][i] = g[j + 1][i];
-        if (t < L) {
-          float d[V];
-          Pack<T, V>::ld(xb + t * ldx, h[K - 1]);
-          Pack<T, V>::ld(gb + (long)t * C, d);
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            if (silu) {
-              float p = bs[i];
-#pragma unroll
-              for (int j = 0; j < K; ++j) p = fmaf(wk[j][i], h[j][i], p);
-              const float s = sigmoid(p);
-              d[i] *= s * (1.f + p * (1.f - s));
-            }
-            g[K - 1][i] = d[i];
-            if (r < BWD_RUN) {
-              sums[K][i] += d[i];
-#pragma unroll
-              for (int j = 0; j < K; ++j) sums[j][i] = fmaf(d[i], h[j][i], sums[j][i]);
-            }
+        for (int r = 0; r < U; ++r)
+          if (t0 + r0 + r < L) {
+            xi[r] = *reinterpret_cast<const typename Pack<T, V>::Raw*>(xb + (t0 + r0 + r) * ldx);
+            gi[r] = *reinterpret_cast<const typename Pack<T, V>::Raw*>(gb + (long)(t0 + r0 + r) * C);
           }
-        } else {
-          zero(h[K - 1]);
-          zero(g[K - 1]);
-        }
-        const int to = t - (K - 1);  // the row that is complete
-        if (r >= K - 1 && to < N) {
-          float o[V];
 #pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float s = 0.f;
+        for (int r = 0; r < U; ++r) {
+          const int t = t0 + r0 + r;
 #pragma unroll
-            for (int j = 0; j < K; ++j) s = fmaf(wk[K - 1 - j][i], g[j][i], s);
-            o[i] = to < L ? s : 0.f;
+          for (int j = 0; j < K - 1; ++j)
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i], g[j][i] = g[j + 1][i];
+          if (t < L) {
+            float d[V];
+            Pack<T, V>::open(xi[r], h[K - 1]);
+            Pack<T, V>::open(gi[r], d);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              if (silu) {
+                float p = bs[i];
+#pragma unroll
+                for (int j = 0; j < K; ++j) p = fmaf(wk[j][i], h[j][i], p);
+                const float s = sigmoid<T>(p);
+                d[i] *= s * (1.f + p * (1.f - s));
+              }
+              g[K - 1][i] = d[i];
+              if (r0 + r < RUN) {
+                sums[K][i] += d[i];
+#pragma unroll
+                for (int j = 0; j < K; ++j) sums[j][i] = fmaf(d[i], h[j][i], sums[j][i]);
+              }
+            }
+          } else {
+            zero(h[K - 1]);
+            zero(g[K - 1]);
           }
-          Pack<T, V>::st(ob + (long)to * C, o);
+          const int to = t - (K - 1);  // the row that is complete
+          if (r0 + r >= K - 1 && to < N) {
+            float o[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              float s = 0.f;
+#pragma unroll
+              for (int j = 0; j < K; ++j) s = fmaf(wk[K - 1 - j][i], g[j][i], s);
+              o[i] = to < L ? s : 0.f;
+            }
+            Pack<T, V>::st(ob + (long)to * C, o);
+          }
         }
       }
     }
     float* pb = part + ((long)b * groups + rg) * (K + 1) * C;
+    __syncthreads();  // the last group's sums have been read
 #pragma unroll
-    for (int j = 0; j <= K; ++j) {
-      __syncthreads();
+    for (int j = 0; j <= K; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) red[threadIdx.y][threadIdx.x * V + i] = sums[j][i];
-      __syncthreads();
-      for (int e = threadIdx.y * CG + threadIdx.x; e < CG * V; e += CG * RG) {
-        const int ch = blockIdx.x * CG * V + e;
-        float s = 0.f;
+      for (int i = 0; i < V; ++i) red[j][threadIdx.y][threadIdx.x * V + i] = sums[j][i];
+    __syncthreads();
+    for (int e = threadIdx.y * CG + threadIdx.x; e < (K + 1) * CG * V; e += CG * RG) {
+      const int j = e / (CG * V), x_ = e % (CG * V), ch = blockIdx.x * CG * V + x_;
+      float s = 0.f;
 #pragma unroll
-        for (int q = 0; q < RG; ++q) s += red[q][e];
-        if (ch < C) pb[(long)j * C + ch] = s;
-      }
+      for (int q = 0; q < RG; ++q) s += red[j][q][x_];
+      if (ch < C) pb[(long)j * C + ch] = s;
     }
   }
 }
@@ -285,21 +311,21 @@ __global__ void __launch_bounds__(128)
   float h[K][V], o[V];
   T* sb = state + (long)b * (K - 1) * C + c;
 #pragma unroll
-  for (int j = 0; j < K - 1; ++j) Pack<T, V>::ld(sb + (long)j * C, h[j]);
-  Pack<T, V>::ld(x + b * ldx + c, h[K - 1]);
+  for (int j = 0; j < K - 1; ++j) ld<T, V>(sb + (long)j * C, h[j]);
+  ld<T, V>(x + b * ldx + c, h[K - 1]);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     float p = bias == nullptr ? 0.f : to_f(bias[c + i]);
 #pragma unroll
     for (int j = 0; j < K; ++j) p = fmaf(to_f(w[(long)(c + i) * K + j]), h[j][i], p);
-    o[i] = silu ? p * sigmoid(p) : p;
+    o[i] = silu ? p * sigmoid<T>(p) : p;
   }
   Pack<T, V>::st(y + (long)b * C + c, o);
 #pragma unroll
   for (int j = 0; j < K - 1; ++j) Pack<T, V>::st(sb + (long)j * C, h[j + 1]);
 }
 
-int bwd_groups(int N) { return (N + BWD_ROWS - 1) / BWD_ROWS; }
+int bwd_groups(int N, int K) { return (N + bwd_rows(K) - 1) / bwd_rows(K); }
 
 // Vectors of four channels where every row starts on a vector: C and the row
 // stride multiples of four and every base aligned to four elements (all but x
@@ -331,7 +357,7 @@ bool by_four(const void* x, int C, long ldx, size_t elem) {
 }  // namespace
 
 size_t short_conv_bwd_ws_bytes(const ConvShape& s) {
-  return sizeof(float) * s.B * (size_t)bwd_groups(s.N) * (s.K + 1) * s.C;
+  return sizeof(float) * s.B * (size_t)bwd_groups(s.N, s.K) * (s.K + 1) * s.C;
 }
 
 cudaError_t short_conv_fwd(const void* x, const void* w, const void* bias, const int* lengths, void* state, void* y,
@@ -349,7 +375,7 @@ cudaError_t short_conv_fwd(const void* x, const void* w, const void* bias, const
 cudaError_t short_conv_bwd(const void* x, const void* w, const void* bias, const int* lengths, const void* dy, void* dx,
                            void* dw, void* db, float* ws, const ConvShape& s, cudaStream_t st) {
   const bool four = by_four(x, s.C, s.ldx, s.dtype == 0 ? 4 : 2);
-  const int per = CG * (four ? 4 : 1), groups = bwd_groups(s.N);
+  const int per = CG * (four ? 4 : 1), groups = bwd_groups(s.N, s.K);
   const dim3 grid((s.C + per - 1) / per, groups < 65535 ? groups : 65535, s.B), block(CG, RG);
   LA_CONV_DISPATCH(s.dtype, four, s.K,
                    (k_conv_bwd<T_, V_, K_><<<grid, block, 0, st>>>((const T_*)x, (const T_*)w, (const T_*)bias, lengths,
