@@ -32,7 +32,7 @@ constexpr float LOG2E = 1.4426950408889634f;
 constexpr int STILE = 64 * 64 * 2;
 
 // phi and min(phi, 1) = phi'.
-__device__ __forceinline__ float phif(float x) { return x > 0.f ? x + 1.f : exp2f(x * LOG2E); }
+__device__ __forceinline__ float phif(float x) { return x > 0.f ? x + 1.f : ex2_fast(x * LOG2E); }
 
 #define LA_WAITS()                                                          \
   auto wt = [&](uint64_t* bar, uint32_t parity, int code) -> bool {         \

@@ -23,8 +23,6 @@
 // This file: the fp32 kernels (chunks of 64 rows, FFMA), the carry and the
 // reductions both paths use, and the single-row step.  The fp32 chunk kernels
 // are bound by the FFMA rate (about 16 D M-sized products a row).
-#include <algorithm>
-
 #include "ffma.cuh"
 #include "scan.cuh"
 
@@ -133,10 +131,13 @@ __device__ __forceinline__ void carry_walk(const float* p, O* out, const float* 
   }
 }
 
-// The carry over the chunks (scan_carry): 32 x segs threads, 128 values of one
-// state, each thread row one segment of the chunks.  With several segments every
-// row first walks its own from zero, the starting states follow from those ends,
-// and the second walk (its loads from L2) writes: a chain of chunks / segs.
+// The carry over the chunks (scan_carry): cols x segs threads, 4 cols values of one
+// state, each thread row one segment of the chunks.  One segment: one walk, 128
+// columns a block (32 chunks of 64 heads, DRAM-bound: 9.2 us; four segments of
+// eight chunks held in registers, 12.3).  Several, for long sequences: every row
+// first walks its own from zero, the starting states follow from those ends, and
+// a second walk, its loads from L2, writes (512 chunks of 8 heads: 17 us, in one
+// walk 65).
 constexpr int CARRY_SEGS = 16;
 template <typename O>
 __global__ void __launch_bounds__(32 * CARRY_SEGS)
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(32 * CARRY_SEGS)
                  int nch, int DM, int per) {
   __shared__ float4 ends[CARRY_SEGS][32];
   __shared__ float decay[CARRY_SEGS];
-  const int e = (blockIdx.x * 32 + threadIdx.x) * 4, seg = threadIdx.y, segs = blockDim.y;
+  const int e = (blockIdx.x * blockDim.x + threadIdx.x) * 4, seg = threadIdx.y, segs = blockDim.y;
   const long bh = blockIdx.y, at = bh * nch * DM + e;
   const bool back = blockIdx.z != 0, live = e < DM;
   const float* p = (back ? rev : fwd) + at;
@@ -166,9 +167,9 @@ __global__ void __launch_bounds__(32 * CARRY_SEGS)
   float* Sp = S == nullptr || back ? nullptr : S + bh * DM + e;
   run = Sp != nullptr ? *reinterpret_cast<const float4*>(Sp) : make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k = 0; k < seg; ++k) {
-    const float d = decay[k];
-    const float4 v = ends[k][threadIdx.x];
-    run.x = fmaf(d, run.x, v.x), run.y = fmaf(d, run.y, v.y), run.z = fmaf(d, run.z, v.z), run.w = fmaf(d, run.w, v.w);
+    const float f = decay[k];
+    const float4 u = ends[k][threadIdx.x];
+    run.x = fmaf(f, run.x, u.x), run.y = fmaf(f, run.y, u.y), run.z = fmaf(f, run.z, u.z), run.w = fmaf(f, run.w, u.w);
   }
   carry_walk(p, out, tt, DM, c0, dc, n, run);
   if (Sp != nullptr && seg == segs - 1) *reinterpret_cast<float4*>(Sp) = run;
@@ -540,10 +541,8 @@ size_t scan_cc_ws_bytes(const ScanShape& s, bool bwd) { return WsCC(s, bwd).end;
 template <typename O>
 static cudaError_t carry(const float* fwd, const float* rev, O* fs, O* rs, const float* tot, float* S, int BH, int nch, int DM,
                          cudaStream_t st) {
-  // a second walk pays once a thread would otherwise make several round trips
-  // of eight chunks (512 chunks of 8 heads: 65 us in one walk)
-  const int segs = std::min(CARRY_SEGS, (nch + 31) / 32), per = (nch + segs - 1) / segs;
-  const dim3 grid((DM / 4 + 31) / 32, BH, rev == nullptr ? 1 : 2), block(32, (nch + per - 1) / per);
+  const int segs = nch <= 64 ? 1 : CARRY_SEGS, per = (nch + segs - 1) / segs, cols = segs == 1 ? 128 : 32;
+  const dim3 grid((DM / 4 + cols - 1) / cols, BH, rev == nullptr ? 1 : 2), block(cols, (nch + per - 1) / per);
   k_scan_carry<<<grid, block, 0, st>>>(fwd, rev, fs, rs, tot, S, nch, DM, per);
   return cudaGetLastError();
 }

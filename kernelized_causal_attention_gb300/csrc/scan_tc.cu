@@ -66,8 +66,8 @@ __device__ __forceinline__ void put_gates(Gates& g, float z, bool live, float A,
   const float tot = __shfl_sync(0xffffffffu, wp, 31);
   g.wp[row] = wp;
   g.del[row] = d;
-  g.cf[row] = d * exp2f(tot - wp);
-  g.ew[row] = exp2f(wp);
+  g.cf[row] = d * ex2_fast(tot - wp);
+  g.ew[row] = ex2_fast(wp);
   if ((row & 31) == 31) g.tot[row >> 5] = tot;
 }
 
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(NT, 2)
     for (int i = 0; i < w.nh; ++i) {
       const Gates& g = gates[i & 1];
       if (threadIdx.x == 0 && !back) tot[((long)w.b * s.H + w.h0 + i) * nch + blockIdx.x] = g.off(4) * LN2;
-      const float f = row >= w.rows ? 0.f : (back ? exp2f(g.wp[row] + g.off(q)) : g.cf[row] * exp2f(g.past(q)));
+      const float f = row >= w.rows ? 0.f : (back ? ex2_fast(g.wp[row] + g.off(q)) : g.cf[row] * ex2_fast(g.past(q)));
       const bool in = wtu(&bar_x[i & 1], (i >> 1) & 1, 64);
       uint4 u[4];
       const uint8_t* xt = sm + S_X + (i & 1) * TILE;
@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(NT, 2)
             float a[32];
             tmem_ldn<2>(ta + 32 * j, a);
             if (J < qd) {
-              const float f = exp2f(wp + here - g.off(J + 1));
+              const float f = ex2_fast(wp + here - g.off(J + 1));
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
                 const float4 u = *reinterpret_cast<const float4*>(&g.cf[32 * J + c]);
@@ -425,8 +425,8 @@ __global__ void __launch_bounds__(NT, 2)
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
                 const float4 u = *reinterpret_cast<const float4*>(&g.wp[32 * J + c]), d = *reinterpret_cast<const float4*>(&g.del[32 * J + c]);
-                const float p0 = c <= lane ? a[c] * (exp2f(wp - u.x) * d.x) : 0.f, p1 = c + 1 <= lane ? a[c + 1] * (exp2f(wp - u.y) * d.y) : 0.f;
-                const float p2 = c + 2 <= lane ? a[c + 2] * (exp2f(wp - u.z) * d.z) : 0.f, p3 = c + 3 <= lane ? a[c + 3] * (exp2f(wp - u.w) * d.w) : 0.f;
+                const float p0 = c <= lane ? a[c] * (ex2_fast(wp - u.x) * d.x) : 0.f, p1 = c + 1 <= lane ? a[c + 1] * (ex2_fast(wp - u.y) * d.y) : 0.f;
+                const float p2 = c + 2 <= lane ? a[c + 2] * (ex2_fast(wp - u.z) * d.z) : 0.f, p3 = c + 3 <= lane ? a[c + 3] * (ex2_fast(wp - u.w) * d.w) : 0.f;
                 pk[c / 2] = pack_bf16(p0, p1);
                 pk[c / 2 + 1] = pack_bf16(p2, p3);
               }
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(NT, 2)
         put_gates(gates[k ^ 1], z + par_[i + 1].bias, row < w.rows, par_[i + 1].A, row);
         z = raw(i + 2);
       }
-      const float e = exp2f(wp + here), sk = par_[i].skip;
+      const float e = ex2_fast(wp + here), sk = par_[i].skip;
       const bool x_in = wtu(&bar_x[k], (i >> 1) & 1, 77), live = row < w.rows;
       if (wtu(&bar_o, k, 78) && x_in) {
         tc_fence_after();
@@ -693,15 +693,15 @@ __global__ void __launch_bounds__(NTG, 1)
         mbar_arrive(&bar_clear);
       }
       const float wp = g.wp[row], del = g.del[row];
-      const float tail = exp2f(g.tot[qd] - wp);     // from this row to its block's end
-      const float fend = tail * exp2f(g.past(qd));  // to the chunk's end
-      const float ecum = g.ew[row] * exp2f(g.off(qd)), eall = exp2f(g.off(4));
+      const float tail = ex2_fast(g.tot[qd] - wp);     // from this row to its block's end
+      const float fend = tail * ex2_fast(g.past(qd));  // to the chunk's end
+      const float ecum = g.ew[row] * ex2_fast(g.off(qd)), eall = ex2_fast(g.off(4));
       // ---- the weights on this warp's block of A^T and E^T: keys 32 qd + lane, queries 32 I + c
       if (wtu(&bar_1, k, 91)) {
         tc_fence_after();
         const uint32_t ta = tm + TG_A + 32 * I + lq, te = tm + TG_E + 32 * I + lq;
         uint8_t* qt = sm + G_Q + (I >> 1) * TILE + row * 128;
-        const float fr = I > qd ? tail * exp2f(g.off(I) - g.off(qd + 1)) : 0.f, frd = fr * del;
+        const float fr = I > qd ? tail * ex2_fast(g.off(I) - g.off(qd + 1)) : 0.f, frd = fr * del;
         float col = 0.f;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -729,7 +729,7 @@ __global__ void __launch_bounds__(NTG, 1)
                   e[c + t] = qq[t] * a[c + t];
                 } else {
                   const int i_ = 16 * hf + c + t;
-                  const float wt_ = i_ >= lane ? exp2f(tv[t] - wp) : 0.f;
+                  const float wt_ = i_ >= lane ? ex2_fast(tv[t] - wp) : 0.f;
                   p[t] = wt_ * a[c + t];
                   qq[t] = wt_ * del * e[c + t];
                   e[c + t] = i_ == lane ? 0.f : qq[t] * a[c + t];  // a pair with itself feels no decay

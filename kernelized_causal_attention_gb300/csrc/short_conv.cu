@@ -9,7 +9,7 @@
 // A thread owns V neighbouring channels and walks a run of rows with the last K
 // inputs (and, backward, the last K values of g) in registers, so every row is
 // read once plus the K - 1 rows (backward 2 (K - 1)) before a run; rows are
-// loaded eight at a time before any is used.  Sums and SiLU are fp32; y, dx and
+// loaded four at a time, four rows ahead of their use.  Sums and SiLU are fp32; y, dx and
 // the parameters' gradients are rounded once.
 #include "common.cuh"
 #include "launch.h"
@@ -52,24 +52,41 @@ __device__ __forceinline__ void ld(const T* p, float (&f)[V]) {
   Pack<T, V>::open(*reinterpret_cast<const typename Pack<T, V>::Raw*>(p), f);
 }
 
+// The taps [j][channel] and the bias of V channels from c on.
+template <typename T, int V, int K>
+__device__ __forceinline__ void taps(const T* w, const T* bias, int c, float (&wk)[K][V], float (&bs)[V]) {
+  float f[K][V];  // V K neighbouring values, channel after channel
+#pragma unroll
+  for (int q = 0; q < K; ++q) ld<T, V>(w + (long)c * K + q * V, f[q]);
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < K; ++j) wk[j][i] = f[(i * K + j) / V][(i * K + j) % V];
+  if (bias != nullptr) {
+    ld<T, V>(bias + c, bs);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) bs[i] = 0.f;
+  }
+}
+
 template <int V>
 __device__ __forceinline__ void zero(float (&f)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) f[i] = 0.f;
 }
 
-// For bf16 results the hardware's exponential and reciprocal (a few 2^-22) do.
 template <typename T>
 __device__ __forceinline__ float sigmoid(float x) {
-  return sizeof(T) == 4 ? 1.f / (1.f + expf(-x)) : __fdividef(1.f, 1.f + __expf(-x));
+  return sizeof(T) == 4 ? 1.f / (1.f + expf(-x)) : rcp_fast(1.f + ex2_fast(-1.4426950408889634f * x));
 }
 
 __device__ __forceinline__ int rows_of(const int* lengths, int b, int N) {
   return lengths == nullptr ? N : min(max(lengths[b], 0), N);
 }
 
-constexpr int U = 8;          // rows loaded at a time
-constexpr int FWD_RUN = 16;   // rows a thread walks (forward)
+constexpr int U = 4;          // rows loaded at a time
+constexpr int FWD_RUN = 32;   // rows a thread walks (forward)
 constexpr int BWD_WALK = 32;  // rows a thread reads (backward); the last K - 1 only complete the run before them
 constexpr int CG = 32;        // channel groups a block spans
 constexpr int RG = 8;         // row runs a block spans
@@ -93,12 +110,7 @@ __global__ void __launch_bounds__(CG * RG, 3)
     const int t0 = (rg * RG + threadIdx.y) * FWD_RUN;
     if (live && t0 < N) {
       float wk[K][V], bs[V], h[K][V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        bs[i] = bias == nullptr ? 0.f : to_f(bias[c + i]);
-#pragma unroll
-        for (int j = 0; j < K; ++j) wk[j][i] = to_f(w[(long)(c + i) * K + j]);
-      }
+      taps<T, V, K>(w, bias, c, wk, bs);
 #pragma unroll
       for (int j = 0; j < K - 1; ++j) {  // the K - 1 rows before the run
         const int t = t0 - (K - 1) + j;
@@ -110,12 +122,20 @@ __global__ void __launch_bounds__(CG * RG, 3)
           zero(h[j + 1]);
       }
       T* yb = y + ((long)b * N + t0) * C + c;
-#pragma unroll 1
-      for (int r0 = 0; r0 < FWD_RUN && t0 + r0 < N; r0 += U) {
-        typename Pack<T, V>::Raw in[U];
+      using Raw = typename Pack<T, V>::Raw;
+      Raw next[U];
+      auto fetch = [&](int r0) {
 #pragma unroll
         for (int r = 0; r < U; ++r)
-          if (t0 + r0 + r < L) in[r] = *reinterpret_cast<const typename Pack<T, V>::Raw*>(xb + (t0 + r0 + r) * ldx);
+          if (r0 + r < FWD_RUN && t0 + r0 + r < L) next[r] = *reinterpret_cast<const Raw*>(xb + (t0 + r0 + r) * ldx);
+      };
+      fetch(0);
+#pragma unroll 1
+      for (int r0 = 0; r0 < FWD_RUN && t0 + r0 < N; r0 += U) {
+        Raw in[U];
+#pragma unroll
+        for (int r = 0; r < U; ++r) in[r] = next[r];
+        fetch(r0 + U);
 #pragma unroll
         for (int r = 0; r < U; ++r) {
           const int t = t0 + r0 + r;
@@ -176,12 +196,7 @@ __global__ void __launch_bounds__(CG * RG)
   const T* gb = dy + (long)b * N * C + c;
   T* ob = dx + (long)b * N * C + c;
   float wk[K][V], bs[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bs[i] = live && bias != nullptr ? to_f(bias[c + i]) : 0.f;
-#pragma unroll
-    for (int j = 0; j < K; ++j) wk[j][i] = live ? to_f(w[(long)(c + i) * K + j]) : 0.f;
-  }
+  if (live) taps<T, V, K>(w, bias, c, wk, bs);
   for (int rg = blockIdx.y; rg < groups; rg += gridDim.y) {
     float sums[K + 1][V];
 #pragma unroll
@@ -201,15 +216,23 @@ __global__ void __launch_bounds__(CG * RG)
         else
           zero(h[j + 1]);
       }
-#pragma unroll 1
-      for (int r0 = 0; r0 < BWD_WALK && t0 + r0 < N + K - 1; r0 += U) {
-        typename Pack<T, V>::Raw xi[U], gi[U];
+      using Raw = typename Pack<T, V>::Raw;
+      Raw xn[U], gn[U];
+      auto fetch = [&](int r0) {
 #pragma unroll
         for (int r = 0; r < U; ++r)
-          if (t0 + r0 + r < L) {
-            xi[r] = *reinterpret_cast<const typename Pack<T, V>::Raw*>(xb + (t0 + r0 + r) * ldx);
-            gi[r] = *reinterpret_cast<const typename Pack<T, V>::Raw*>(gb + (long)(t0 + r0 + r) * C);
+          if (r0 + r < BWD_WALK && t0 + r0 + r < L) {
+            xn[r] = *reinterpret_cast<const Raw*>(xb + (t0 + r0 + r) * ldx);
+            gn[r] = *reinterpret_cast<const Raw*>(gb + (long)(t0 + r0 + r) * C);
           }
+      };
+      fetch(0);
+#pragma unroll 1
+      for (int r0 = 0; r0 < BWD_WALK && t0 + r0 < N + K - 1; r0 += U) {
+        Raw xi[U], gi[U];
+#pragma unroll
+        for (int r = 0; r < U; ++r) xi[r] = xn[r], gi[r] = gn[r];
+        fetch(r0 + U);
 #pragma unroll
         for (int r = 0; r < U; ++r) {
           const int t = t0 + r0 + r;
