@@ -11,6 +11,8 @@
 // read once plus the K - 1 rows (backward 2 (K - 1)) before a run; rows are
 // loaded four at a time, four rows ahead of their use.  Sums and SiLU are fp32; y, dx and
 // the parameters' gradients are rounded once.
+#include <algorithm>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -70,6 +72,21 @@ __device__ __forceinline__ void taps(const T* w, const T* bias, int c, float (&w
   }
 }
 
+// c += a b over V channels, two to an instruction where V = 4.
+template <int V>
+__device__ __forceinline__ void fma_v(float (&c)[V], const float (&a)[V], const float (&b)[V]) {
+  if constexpr (V == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+      asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%0, %1};\n\t"
+          "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+          : "+f"(c[i]), "+f"(c[i + 1])
+          : "f"(a[i]), "f"(a[i + 1]), "f"(b[i]), "f"(b[i + 1]));
+  } else {
+    c[0] = fmaf(a[0], b[0], c[0]);
+  }
+}
+
 template <int V>
 __device__ __forceinline__ void zero(float (&f)[V]) {
 #pragma unroll
@@ -86,11 +103,8 @@ __device__ __forceinline__ int rows_of(const int* lengths, int b, int N) {
 }
 
 constexpr int U = 4;          // rows loaded at a time
-constexpr int FWD_RUN = 32;   // rows a thread walks (forward)
-constexpr int BWD_WALK = 32;  // rows a thread reads (backward); the last K - 1 only complete the run before them
 constexpr int CG = 32;        // channel groups a block spans
 constexpr int RG = 8;         // row runs a block spans
-constexpr int bwd_rows(int K) { return (BWD_WALK - (K - 1)) * RG; }
 
 // y, and the history in place.  Rows at or past the sequence's length are
 // written as zeros and not read.  The block of the first row group alone reads
@@ -98,7 +112,7 @@ constexpr int bwd_rows(int K) { return (BWD_WALK - (K - 1)) * RG; }
 template <typename T, int V, int K>
 __global__ void __launch_bounds__(CG * RG, 3)
     k_conv_fwd(const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const int* __restrict__ lengths,
-               T* state, T* __restrict__ y, int N, int C, long ldx, int silu) {
+               T* state, T* __restrict__ y, int N, int C, long ldx, int silu, int run) {
   const int c = (blockIdx.x * CG + threadIdx.x) * V;
   const int b = blockIdx.z;
   const bool live = c < C;
@@ -106,8 +120,8 @@ __global__ void __launch_bounds__(CG * RG, 3)
   const T* xb = x + (long)b * N * ldx + c;
   T* sb = state == nullptr ? nullptr : state + (long)b * (K - 1) * C + c;
   // grid.y is capped: a block walks row groups at the grid's stride
-  for (int rg = blockIdx.y; (long)rg * RG * FWD_RUN < N; rg += gridDim.y) {
-    const int t0 = (rg * RG + threadIdx.y) * FWD_RUN;
+  for (int rg = blockIdx.y; (long)rg * RG * run < N; rg += gridDim.y) {
+    const int t0 = (rg * RG + threadIdx.y) * run;
     if (live && t0 < N) {
       float wk[K][V], bs[V], h[K][V];
       taps<T, V, K>(w, bias, c, wk, bs);
@@ -125,38 +139,52 @@ __global__ void __launch_bounds__(CG * RG, 3)
       using Raw = typename Pack<T, V>::Raw;
       Raw next[U];
       auto fetch = [&](int r0) {
+        const T* p = xb + (t0 + r0) * ldx;
+        if (r0 < run && t0 + r0 + U <= L) {
 #pragma unroll
-        for (int r = 0; r < U; ++r)
-          if (r0 + r < FWD_RUN && t0 + r0 + r < L) next[r] = *reinterpret_cast<const Raw*>(xb + (t0 + r0 + r) * ldx);
+          for (int r = 0; r < U; ++r) next[r] = *reinterpret_cast<const Raw*>(p + r * ldx);
+        } else {
+#pragma unroll
+          for (int r = 0; r < U; ++r) {
+            next[r] = Raw{};
+            if (r0 < run && t0 + r0 + r < L) next[r] = *reinterpret_cast<const Raw*>(p + r * ldx);
+          }
+        }
       };
       fetch(0);
 #pragma unroll 1
-      for (int r0 = 0; r0 < FWD_RUN && t0 + r0 < N; r0 += U) {
+      for (int r0 = 0; r0 < run && t0 + r0 < N; r0 += U) {
         Raw in[U];
+        float o[U][V];
 #pragma unroll
         for (int r = 0; r < U; ++r) in[r] = next[r];
         fetch(r0 + U);
 #pragma unroll
-        for (int r = 0; r < U; ++r) {
-          const int t = t0 + r0 + r;
-          float o[V];
-          if (t < L) {
+        for (int r = 0; r < U; ++r) {  // rows past the length: zeros in, not used
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j)
+          for (int j = 0; j < K - 1; ++j)
 #pragma unroll
-              for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i];
-            Pack<T, V>::open(in[r], h[K - 1]);
+            for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i];
+          Pack<T, V>::open(in[r], h[K - 1]);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              float p = bs[i];
+          for (int i = 0; i < V; ++i) o[r][i] = bs[i];
 #pragma unroll
-              for (int j = 0; j < K; ++j) p = fmaf(wk[j][i], h[j][i], p);
-              o[i] = silu ? p * sigmoid<T>(p) : p;
-            }
-          } else {
-            zero(o);
+          for (int j = 0; j < K; ++j) fma_v(o[r], wk[j], h[j]);
+          if (silu) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) o[r][i] *= sigmoid<T>(o[r][i]);
           }
-          if (t < N) Pack<T, V>::st(yb + (long)(r0 + r) * C, o);
+        }
+        T* q = yb + (long)r0 * C;
+        if (t0 + r0 + U <= L) {
+#pragma unroll
+          for (int r = 0; r < U; ++r) Pack<T, V>::st(q + (long)r * C, o[r]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < U; ++r) {
+            if (t0 + r0 + r >= L) zero(o[r]);
+            if (t0 + r0 + r < N) Pack<T, V>::st(q + (long)r * C, o[r]);
+          }
         }
       }
     }
@@ -185,9 +213,9 @@ template <typename T, int V, int K>
 __global__ void __launch_bounds__(CG * RG)
     k_conv_bwd(const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const int* __restrict__ lengths,
                const T* __restrict__ dy, T* __restrict__ dx, float* __restrict__ part, int N, int C, long ldx, int silu,
-               int groups) {
+               int groups, int walk) {
+  const int run = walk - (K - 1);  // the last K - 1 rows of a walk only complete those before them
   __shared__ float red[K + 1][RG][CG * V];
-  constexpr int RUN = BWD_WALK - (K - 1);
   const int c = (blockIdx.x * CG + threadIdx.x) * V;
   const bool live = c < C;
   const int b = blockIdx.z;
@@ -201,7 +229,7 @@ __global__ void __launch_bounds__(CG * RG)
     float sums[K + 1][V];
 #pragma unroll
     for (int j = 0; j <= K; ++j) zero(sums[j]);
-    const int t0 = (rg * RG + threadIdx.y) * RUN;
+    const int t0 = (rg * RG + threadIdx.y) * run;
     if (live && t0 < N) {
       // h: x rows t - K + 1 .. t;  g: rows t - K + 1 .. t of dy silu'(pre).
       // Row t's g completes dx of row t - K + 1, so the run looks K - 1 rows ahead.
@@ -219,62 +247,69 @@ __global__ void __launch_bounds__(CG * RG)
       using Raw = typename Pack<T, V>::Raw;
       Raw xn[U], gn[U];
       auto fetch = [&](int r0) {
+        const T *p = xb + (t0 + r0) * ldx, *q = gb + (long)(t0 + r0) * C;
+        if (r0 < walk && t0 + r0 + U <= L) {
 #pragma unroll
-        for (int r = 0; r < U; ++r)
-          if (r0 + r < BWD_WALK && t0 + r0 + r < L) {
-            xn[r] = *reinterpret_cast<const Raw*>(xb + (t0 + r0 + r) * ldx);
-            gn[r] = *reinterpret_cast<const Raw*>(gb + (long)(t0 + r0 + r) * C);
+          for (int r = 0; r < U; ++r) {
+            xn[r] = *reinterpret_cast<const Raw*>(p + r * ldx);
+            gn[r] = *reinterpret_cast<const Raw*>(q + (long)r * C);
           }
+        } else {
+#pragma unroll
+          for (int r = 0; r < U; ++r) {
+            xn[r] = gn[r] = Raw{};
+            if (r0 < walk && t0 + r0 + r < L) {
+              xn[r] = *reinterpret_cast<const Raw*>(p + r * ldx);
+              gn[r] = *reinterpret_cast<const Raw*>(q + (long)r * C);
+            }
+          }
+        }
       };
       fetch(0);
 #pragma unroll 1
-      for (int r0 = 0; r0 < BWD_WALK && t0 + r0 < N + K - 1; r0 += U) {
+      for (int r0 = 0; r0 < walk && t0 + r0 < N + K - 1; r0 += U) {
         Raw xi[U], gi[U];
 #pragma unroll
         for (int r = 0; r < U; ++r) xi[r] = xn[r], gi[r] = gn[r];
         fetch(r0 + U);
+        const bool whole = r0 > 0 && t0 + r0 + U <= L;  // every row complete and stored
+        T* q = ob + (long)(t0 + r0 - (K - 1)) * C;
 #pragma unroll
         for (int r = 0; r < U; ++r) {
-          const int t = t0 + r0 + r;
 #pragma unroll
           for (int j = 0; j < K - 1; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) h[j][i] = h[j + 1][i], g[j][i] = g[j + 1][i];
-          if (t < L) {
-            float d[V];
-            Pack<T, V>::open(xi[r], h[K - 1]);
-            Pack<T, V>::open(gi[r], d);
+          Pack<T, V>::open(xi[r], h[K - 1]);
+          Pack<T, V>::open(gi[r], g[K - 1]);  // zero past the length
+          if (silu) {
+            float p[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) p[i] = bs[i];
+#pragma unroll
+            for (int j = 0; j < K; ++j) fma_v(p, wk[j], h[j]);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-              if (silu) {
-                float p = bs[i];
-#pragma unroll
-                for (int j = 0; j < K; ++j) p = fmaf(wk[j][i], h[j][i], p);
-                const float s = sigmoid<T>(p);
-                d[i] *= s * (1.f + p * (1.f - s));
-              }
-              g[K - 1][i] = d[i];
-              if (r0 + r < RUN) {
-                sums[K][i] += d[i];
-#pragma unroll
-                for (int j = 0; j < K; ++j) sums[j][i] = fmaf(d[i], h[j][i], sums[j][i]);
-              }
+              const float s = sigmoid<T>(p[i]);
+              g[K - 1][i] *= s * fmaf(p[i], 1.f - s, 1.f);
             }
-          } else {
-            zero(h[K - 1]);
-            zero(g[K - 1]);
           }
-          const int to = t - (K - 1);  // the row that is complete
-          if (r0 + r >= K - 1 && to < N) {
-            float o[V];
+          if (r0 + r < run) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-              float s = 0.f;
+            for (int i = 0; i < V; ++i) sums[K][i] += g[K - 1][i];
 #pragma unroll
-              for (int j = 0; j < K; ++j) s = fmaf(wk[K - 1 - j][i], g[j][i], s);
-              o[i] = to < L ? s : 0.f;
-            }
-            Pack<T, V>::st(ob + (long)to * C, o);
+            for (int j = 0; j < K; ++j) fma_v(sums[j], g[K - 1], h[j]);
+          }
+          float o[V];  // of row t - (K - 1), which is complete
+          zero(o);
+#pragma unroll
+          for (int j = 0; j < K; ++j) fma_v(o, wk[K - 1 - j], g[j]);
+          if (whole) {
+            Pack<T, V>::st(q + (long)r * C, o);
+          } else if (r0 + r >= K - 1) {
+            const int to = t0 + r0 + r - (K - 1);
+            if (to >= L) zero(o);
+            if (to < N) Pack<T, V>::st(q + (long)r * C, o);
           }
         }
       }
@@ -348,7 +383,26 @@ __global__ void __launch_bounds__(128)
   for (int j = 0; j < K - 1; ++j) Pack<T, V>::st(sb + (long)j * C, h[j + 1]);
 }
 
-int bwd_groups(int N, int K) { return (N + bwd_rows(K) - 1) / bwd_rows(K); }
+// Rows a thread walks (a multiple of U): the walk that minimises whole waves of
+// blocks times its length and start-up, `lost` of its rows being repeated.
+struct Walk {
+  int rows, groups;
+  Walk(int N, long columns, int lost, int per_sm) {
+    double best = 0;
+    rows = U, groups = 1;
+    for (int r = 2 * U; r <= 16 * U; r += U) {
+      const int g = (N + (r - lost) * RG - 1) / ((r - lost) * RG);
+      const long waves = (columns * g + per_sm * sm_count() - 1) / (per_sm * sm_count());
+      const double cost = (double)waves * (r + 6);
+      if (r == 2 * U || cost < best) best = cost, rows = r, groups = g;
+    }
+  }
+};
+
+Walk bwd_walk(const ConvShape& s, bool four) {
+  const int per = CG * (four ? 4 : 1);
+  return Walk(s.N, (long)s.B * ((s.C + per - 1) / per), s.K - 1, 2);
+}
 
 // Vectors of four channels where every row starts on a vector: C and the row
 // stride multiples of four and every base aligned to four elements (all but x
@@ -379,31 +433,34 @@ bool by_four(const void* x, int C, long ldx, size_t elem) {
 
 }  // namespace
 
-size_t short_conv_bwd_ws_bytes(const ConvShape& s) {
-  return sizeof(float) * s.B * (size_t)bwd_groups(s.N, s.K) * (s.K + 1) * s.C;
+size_t short_conv_bwd_ws_bytes(const ConvShape& s) {  // whichever form x's alignment leaves
+  const int g = std::max(bwd_walk(s, false).groups, bwd_walk(s, true).groups);
+  return sizeof(float) * s.B * (size_t)g * (s.K + 1) * s.C;
 }
 
 cudaError_t short_conv_fwd(const void* x, const void* w, const void* bias, const int* lengths, void* state, void* y,
                            const ConvShape& s, cudaStream_t st) {
   const bool four = by_four(x, s.C, s.ldx, s.dtype == 0 ? 4 : 2);
   const int per = CG * (four ? 4 : 1);
-  const int rg = (s.N + RG * FWD_RUN - 1) / (RG * FWD_RUN);
-  const dim3 grid((s.C + per - 1) / per, rg < 65535 ? rg : 65535, s.B), block(CG, RG);
+  const Walk plan(s.N, (long)s.B * ((s.C + per - 1) / per), 0, 3);
+  const dim3 grid((s.C + per - 1) / per, plan.groups < 65535 ? plan.groups : 65535, s.B), block(CG, RG);
   LA_CONV_DISPATCH(s.dtype, four, s.K,
                    (k_conv_fwd<T_, V_, K_><<<grid, block, 0, st>>>((const T_*)x, (const T_*)w, (const T_*)bias, lengths,
-                                                                   (T_*)state, (T_*)y, s.N, s.C, s.ldx, s.silu)));
+                                                                   (T_*)state, (T_*)y, s.N, s.C, s.ldx, s.silu, plan.rows)));
   return cudaGetLastError();
 }
 
 cudaError_t short_conv_bwd(const void* x, const void* w, const void* bias, const int* lengths, const void* dy, void* dx,
                            void* dw, void* db, float* ws, const ConvShape& s, cudaStream_t st) {
   const bool four = by_four(x, s.C, s.ldx, s.dtype == 0 ? 4 : 2);
-  const int per = CG * (four ? 4 : 1), groups = bwd_groups(s.N, s.K);
+  const int per = CG * (four ? 4 : 1);
+  const Walk plan = bwd_walk(s, four);
+  const int groups = plan.groups;
   const dim3 grid((s.C + per - 1) / per, groups < 65535 ? groups : 65535, s.B), block(CG, RG);
   LA_CONV_DISPATCH(s.dtype, four, s.K,
                    (k_conv_bwd<T_, V_, K_><<<grid, block, 0, st>>>((const T_*)x, (const T_*)w, (const T_*)bias, lengths,
                                                                    (const T_*)dy, (T_*)dx, ws, s.N, s.C, s.ldx, s.silu,
-                                                                   groups)));
+                                                                   groups, plan.rows)));
   const dim3 sgrid((s.C + 31) / 32, s.K + 1), sblock(32, RS);
   const int P = s.B * groups;
   if (s.dtype == 0)
