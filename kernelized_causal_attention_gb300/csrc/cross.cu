@@ -36,6 +36,7 @@ template <int D, int M, typename T>
 __global__ void __launch_bounds__(256)
     k_cross_sums(const T* __restrict__ k, const T* __restrict__ v, const int* __restrict__ lengths, float* __restrict__ rec,
                  int Hk, int N, int per) {
+  grid_dep_enter();
   extern __shared__ float sm[];
   float* kt = sm;                 // phi(k) [64][D + 4]
   float* vt = kt + 64 * (D + 4);  // v [64][M + 4]
@@ -69,6 +70,7 @@ __global__ void __launch_bounds__(256)
 // S and Z (or R and r) of every key head: the sum of its records, in order.
 __global__ void __launch_bounds__(256)
     k_cross_join(const float* __restrict__ rec, float* __restrict__ S, float* __restrict__ Z, int nrec, int DM, int D) {
+  grid_dep_enter();
   const int e = (blockIdx.x * 256 + threadIdx.x) * 4;
   const long bh = blockIdx.y;
   if (e >= DM + D) return;
@@ -88,6 +90,7 @@ template <int D, int M, typename T>
 __global__ void __launch_bounds__(256)
     k_cross_read(const T* __restrict__ q, const float* __restrict__ S, const float* __restrict__ Z, T* __restrict__ out,
                  float* __restrict__ den, int H, int Hk, int N) {
+  grid_dep_enter();
   extern __shared__ float sm[];
   float* qt = sm;             // phi(q)^T [D][FLD]
   float* ss = qt + D * FLD;   // S [D][M + 4]
@@ -127,6 +130,7 @@ __global__ void __launch_bounds__(256)
     k_cross_grad_q(const T* __restrict__ q, const float* __restrict__ den, const T* __restrict__ dout,
                    const float* __restrict__ S, const float* __restrict__ Z, T* __restrict__ dq,
                    float* __restrict__ rec, int H, int Hk, int N, int per) {
+  grid_dep_enter();
   extern __shared__ float sm[];
   float* qn = sm;                   // q, then e phi(q) [64][D + 4]
   float* gt = qn + 64 * (D + 4);    // dout^T [M][FLD]
@@ -202,6 +206,7 @@ __global__ void __launch_bounds__(256)
     k_cross_grad_k(const T* __restrict__ k, const T* __restrict__ v, const int* __restrict__ lengths,
                    const float* __restrict__ R, const float* __restrict__ r, T* __restrict__ dk, T* __restrict__ dv, int Hk,
                    int N) {
+  grid_dep_enter();
   extern __shared__ float sm[];
   float* kt = sm;                  // k^T, then phi(k)^T [D][FLD]
   float* vt = kt + D * FLD;        // v^T [M][FLD]
@@ -331,8 +336,7 @@ size_t rec_bytes(const CrossShape& s) { return (size_t)(s.D * s.M + s.D) * 4; }
 
 cudaError_t cross_join(const float* rec, float* S, float* Z, int heads, int nrec, const CrossShape& s, cudaStream_t st) {
   const int DM = s.D * s.M;
-  k_cross_join<<<dim3(((DM + s.D) / 4 + 255) / 256, heads), 256, 0, st>>>(rec, S, Z, nrec, DM, s.D);
-  return cudaGetLastError();
+  return launch_pdl(k_cross_join, dim3(((DM + s.D) / 4 + 255) / 256, heads), dim3(256), 0, st, rec, S, Z, nrec, DM, s.D);
 }
 
 namespace {
@@ -342,11 +346,12 @@ cudaError_t fwd(const void* q, const void* k, const void* v, const int* lengths,
   const Split p(s.B * s.Hk, s.Nk, FT);
   LA_DISPATCH_DM(s.D, s.M, {
     constexpr size_t b1 = 64 * (D_ + M_ + 8) * 4;
-    k_cross_sums<D_, M_, float><<<dim3(p.nseg, s.B * s.Hk), 256, b1, st>>>((const float*)k, (const float*)v, lengths, ws, s.Hk, s.Nk, p.per);
-    LA_TRY_CUDA(cudaGetLastError());
+    LA_TRY_CUDA(launch_pdl(k_cross_sums<D_, M_, float>, dim3(p.nseg, s.B * s.Hk), dim3(256), b1, st, (const float*)k, (const float*)v,
+                           lengths, ws, s.Hk, s.Nk, p.per));
     LA_TRY_CUDA(cross_join(ws, S, Z, s.B * s.Hk, p.nseg, s, st));
     constexpr size_t b2 = (D_ * FLD + D_ * (M_ + 4)) * 4;
-    k_cross_read<D_, M_, float><<<dim3((s.Nq + FT - 1) / FT, s.B * s.H), 256, b2, st>>>((const float*)q, S, Z, (float*)out, den, s.H, s.Hk, s.Nq);
+    LA_TRY_CUDA(launch_pdl(k_cross_read<D_, M_, float>, dim3((s.Nq + FT - 1) / FT, s.B * s.H), dim3(256), b2, st, (const float*)q,
+                           (const float*)S, (const float*)Z, (float*)out, den, s.H, s.Hk, s.Nq));
   });
   return cudaGetLastError();
 }
@@ -360,14 +365,13 @@ cudaError_t bwd(const void* q, const void* k, const void* v, const int* lengths,
   LA_DISPATCH_DM(s.D, s.M, {
     constexpr size_t b1 = (64 * (D_ + 4) + M_ * FLD + 64 * (M_ + 4) + M_ * (D_ + 4)) * 4;
     LA_TRY_CUDA(smem(&k_cross_grad_q<D_, M_, float>, b1));
-    k_cross_grad_q<D_, M_, float><<<dim3(p.nseg, s.B * s.H), 256, b1, st>>>((const float*)q, den, (const float*)dout, S, Z, (float*)dq,
-                                                                       ws, s.H, s.Hk, s.Nq, p.per);
-    LA_TRY_CUDA(cudaGetLastError());
+    LA_TRY_CUDA(launch_pdl(k_cross_grad_q<D_, M_, float>, dim3(p.nseg, s.B * s.H), dim3(256), b1, st, (const float*)q, den,
+                           (const float*)dout, S, Z, (float*)dq, ws, s.H, s.Hk, s.Nq, p.per));
     LA_TRY_CUDA(cross_join(ws, R, r, s.B * s.Hk, p.nseg * (s.H / s.Hk), s, st));
     constexpr size_t b2 = (D_ * FLD + M_ * FLD + D_ * (M_ + 4) + M_ * (D_ + 4)) * 4;
     LA_TRY_CUDA(smem(&k_cross_grad_k<D_, M_, float>, b2));
-    k_cross_grad_k<D_, M_, float><<<dim3((s.Nk + FT - 1) / FT, s.B * s.Hk), 256, b2, st>>>((const float*)k, (const float*)v, lengths, R, r,
-                                                                                       (float*)dk, (float*)dv, s.Hk, s.Nk);
+    LA_TRY_CUDA(launch_pdl(k_cross_grad_k<D_, M_, float>, dim3((s.Nk + FT - 1) / FT, s.B * s.Hk), dim3(256), b2, st, (const float*)k,
+                           (const float*)v, lengths, (const float*)R, (const float*)r, (float*)dk, (float*)dv, s.Hk, s.Nk));
   });
   return cudaGetLastError();
 }

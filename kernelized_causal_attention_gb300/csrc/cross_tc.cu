@@ -146,13 +146,7 @@ __global__ void __launch_bounds__(NT, 2)
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bh = blockIdx.y;
-  const int L = valid_rows(lengths, bh / Hk, N);
-  const int t0 = blockIdx.x * per, nt = min(per, (L + TC_C - 1) / TC_C - t0);
-  float* o = rec + (static_cast<long>(bh) * gridDim.x + blockIdx.x) * (D * M + D);
-  if (nt <= 0) {
-    for (int e = threadIdx.x; e < D * M + D; e += NT) o[e] = 0.f;
-    return;
-  }
+  grid_dep_launch();
   if (threadIdx.x == 0) {
     for (int k = 0; k < 2; ++k) {
       mbar_init(&bar_in[k], 1);
@@ -164,12 +158,18 @@ __global__ void __launch_bounds__(NT, 2)
     s_abort = 0;
   }
   if (warp == W_ISSUE) tmem_alloc(&tmem_base, 64);
+  grid_dep_wait();
+  const int L = valid_rows(lengths, bh / Hk, N);
+  const int t0 = blockIdx.x * per, nt = min(per, (L + TC_C - 1) / TC_C - t0);
+  float* o = rec + (static_cast<long>(bh) * gridDim.x + blockIdx.x) * (D * M + D);
   LA_WAITS()
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_base;
-  if (warp == W_ISSUE) {
+  if (nt <= 0) {
+    for (int e = threadIdx.x; e < D * M + D; e += NT) o[e] = 0.f;
+  } else if (warp == W_ISSUE) {
     if (lane == 0) {
       int issued = 0;
       auto load = [&](int i) {
@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(NT, 3)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bh = blockIdx.y;
   const long bhk = static_cast<long>(bh / H) * Hk + bh % H / (H / Hk);
   const int t0 = blockIdx.x * per, nt = min(per, (N + TC_C - 1) / TC_C - t0);
+  grid_dep_launch();
   if (threadIdx.x == 0) {
     mbar_init(&bar_in[0], 1);
     mbar_init(&bar_in[1], 1);
@@ -269,6 +270,7 @@ __global__ void __launch_bounds__(NT, 3)
     s_abort = 0;
   }
   if (warp == W_ISSUE) tmem_alloc(&tmem_base, 64);
+  grid_dep_wait();
   LA_WAITS()
   tc_fence_before();
   __syncthreads();
@@ -365,6 +367,7 @@ __global__ void __launch_bounds__(NT, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bh = blockIdx.y;
   const long bhk = static_cast<long>(bh / H) * Hk + bh % H / (H / Hk);
   const int t0 = blockIdx.x * per, nt = min(per, (N + TC_C - 1) / TC_C - t0);
+  grid_dep_launch();
   if (threadIdx.x == 0) {
     for (uint64_t* b : {&bar_in[0], &bar_in[1], &bar_1, &bar_2}) mbar_init(b, 1);
     for (uint64_t* b : {&bar_s, &bar_t, &bar_free}) mbar_init(b, 256);
@@ -372,6 +375,7 @@ __global__ void __launch_bounds__(NT, 2)
     s_abort = 0;
   }
   if (warp == W_ISSUE) tmem_alloc(&tmem_base, 128);
+  grid_dep_wait();
   LA_WAITS()
   tc_fence_before();
   __syncthreads();
@@ -506,6 +510,15 @@ __global__ void __launch_bounds__(NT, 2)
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bh = blockIdx.y;
+  grid_dep_launch();
+  if (threadIdx.x == 0) {
+    for (uint64_t* b : {&bar_in[0], &bar_in[1], &bar_2}) mbar_init(b, 1);
+    for (uint64_t* b : {&bar_s, &bar_t, &bar_free}) mbar_init(b, 256);
+    fence_barrier_init();
+    s_abort = 0;
+  }
+  if (warp == W_ISSUE) tmem_alloc(&tmem_base, 128);
+  grid_dep_wait();
   const int L = valid_rows(lengths, bh / Hk, N);
   const int t0 = blockIdx.x * per, t1 = min(t0 + per, (N + TC_C - 1) / TC_C);  // tiles of this block
   const int nt = min(t1, (L + TC_C - 1) / TC_C) - t0;                          // of which hold valid rows
@@ -515,20 +528,13 @@ __global__ void __launch_bounds__(NT, 2)
     for (int e = threadIdx.x; e < (n1 - n0) * D / 8; e += NT) *reinterpret_cast<uint4*>(dk + base * D + e * 8) = make_uint4(0u, 0u, 0u, 0u);
     for (int e = threadIdx.x; e < (n1 - n0) * M / 8; e += NT) *reinterpret_cast<uint4*>(dv + base * M + e * 8) = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (nt <= 0) return;
-  if (threadIdx.x == 0) {
-    for (uint64_t* b : {&bar_in[0], &bar_in[1], &bar_2}) mbar_init(b, 1);
-    for (uint64_t* b : {&bar_s, &bar_t, &bar_free}) mbar_init(b, 256);
-    fence_barrier_init();
-    s_abort = 0;
-  }
-  if (warp == W_ISSUE) tmem_alloc(&tmem_base, 128);
   LA_WAITS()
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tm = tmem_base;  // v R^T, then phi(k) R at + 64
-  if (warp == W_ISSUE) {
+  if (nt <= 0) {
+  } else if (warp == W_ISSUE) {
     if (lane == 0) {
       int issued = 0;
       auto load = [&](int i) {
@@ -655,11 +661,9 @@ cudaError_t cross_fwd_tc(const void* q, const void* k, const void* v, const int*
   int* err = status_word();
   LA_TRY_CUDA(room(k_ksum, K_SMEM));
   LA_TRY_CUDA(room(k_read, R_SMEM));
-  k_ksum<<<dim3(wk.nseg, s.B * s.Hk), NT, K_SMEM, st>>>(mk, mv, lengths, ws, s.Hk, s.Nk, s.D, s.M, wk.per, err);
-  LA_TRY_CUDA(cudaGetLastError());
+  LA_TRY_CUDA(launch_pdl(k_ksum, dim3(wk.nseg, s.B * s.Hk), dim3(NT), K_SMEM, st, mk, mv, lengths, ws, s.Hk, s.Nk, s.D, s.M, wk.per, err));
   LA_TRY_CUDA(cross_join(ws, S, Z, s.B * s.Hk, wk.nseg, s, st));
-  k_read<<<dim3(wq.nseg, s.B * s.H), NT, R_SMEM, st>>>(mq, mo, S, Z, den, s.H, s.Hk, s.Nq, s.D, s.M, wq.per, err);
-  return cudaGetLastError();
+  return launch_pdl(k_read, dim3(wq.nseg, s.B * s.H), dim3(NT), R_SMEM, st, mq, mo, S, Z, den, s.H, s.Hk, s.Nq, s.D, s.M, wq.per, err);
 }
 
 cudaError_t cross_bwd_tc(const void* q, const void* k, const void* v, const int* lengths, const float* den, const float* S,
@@ -677,12 +681,11 @@ cudaError_t cross_bwd_tc(const void* q, const void* k, const void* v, const int*
   int* err = status_word();
   LA_TRY_CUDA(room(k_grad_q, Q_SMEM));
   LA_TRY_CUDA(room(k_grad_k, V_SMEM));
-  k_grad_q<<<dim3(wq.nseg, s.B * s.H), NT, Q_SMEM, st>>>(mq, mg, md, den, S, Z, ws, s.H, s.Hk, s.Nq, s.D, s.M, wq.per, err);
-  LA_TRY_CUDA(cudaGetLastError());
+  LA_TRY_CUDA(launch_pdl(k_grad_q, dim3(wq.nseg, s.B * s.H), dim3(NT), Q_SMEM, st, mq, mg, md, den, S, Z, ws, s.H, s.Hk, s.Nq, s.D, s.M,
+                         wq.per, err));
   LA_TRY_CUDA(cross_join(ws, R, r, s.B * s.Hk, wq.nseg * (s.H / s.Hk), s, st));
-  k_grad_k<<<dim3(wk.nseg, s.B * s.Hk), NT, V_SMEM, st>>>(mk, mv, mdk, mdv, lengths, R, r, (bf16*)dk, (bf16*)dv, s.Hk, s.Nk,
-                                                         s.D, s.M, wk.per, err);
-  return cudaGetLastError();
+  return launch_pdl(k_grad_k, dim3(wk.nseg, s.B * s.Hk), dim3(NT), V_SMEM, st, mk, mv, mdk, mdv, lengths, R, r, (bf16*)dk, (bf16*)dv,
+                    s.Hk, s.Nk, s.D, s.M, wk.per, err);
 }
 
 }  // namespace la

@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(256)
                 const T* __restrict__ Cm, const T* __restrict__ bias, const int* __restrict__ lengths,
                 const T* __restrict__ dy, float* __restrict__ fwd, float* __restrict__ rev, float* __restrict__ tot,
                 ScanShape s) {
+  grid_dep_enter();
   extern __shared__ float sm[];
   float* tb = sm;                  // [64][D + 4]
   float* tx = tb + 64 * (D + 4);   // [64][M + 4]
@@ -143,6 +144,7 @@ template <typename O>
 __global__ void __launch_bounds__(32 * CARRY_SEGS)
     k_scan_carry(const float* fwd, const float* rev, O* fs, O* rs, const float* __restrict__ tot, float* __restrict__ S,
                  int nch, int DM, int per) {
+  grid_dep_enter();
   __shared__ float4 ends[CARRY_SEGS][32];
   __shared__ float decay[CARRY_SEGS];
   const int e = (blockIdx.x * blockDim.x + threadIdx.x) * 4, seg = threadIdx.y, segs = blockDim.y;
@@ -181,6 +183,7 @@ __global__ void __launch_bounds__(256)
     k_scan_out(const T* __restrict__ x, const T* __restrict__ dt, const T* __restrict__ A, const T* __restrict__ Bm,
                const T* __restrict__ Cm, const T* __restrict__ skip, const T* __restrict__ bias,
                const int* __restrict__ lengths, const float* __restrict__ prev, T* __restrict__ y, ScanShape s) {
+  grid_dep_enter();
   extern __shared__ float sm[];
   float* ct = sm;                   // C^T [D][FLD]
   float* bt = ct + D * FLD;         // B^T [D][FLD]
@@ -241,6 +244,7 @@ __global__ void __launch_bounds__(256)
                 const int* __restrict__ lengths, const T* __restrict__ dy, const float* __restrict__ prev,
                 const float* __restrict__ next, T* __restrict__ dx, T* __restrict__ ddt, float* __restrict__ pB,
                 float* __restrict__ pC, float* __restrict__ pp, ScanShape s) {
+  grid_dep_enter();
   extern __shared__ float sm[];
   constexpr int TS = 64 * FLD;  // one tile of up to 64 x 64
   float* ct = sm;               // C^T, then Q^T
@@ -412,6 +416,7 @@ __global__ void __launch_bounds__(256)
 template <typename T>
 __global__ void __launch_bounds__(256)
     k_scan_params(const float* __restrict__ pp, T* dA, T* dskip, T* dbias, int B, int H, int nch) {
+  grid_dep_enter();
   __shared__ float red[8];
   const int h = blockIdx.x;
   float a[3] = {0.f, 0.f, 0.f};
@@ -433,6 +438,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
     k_scan_groups(const float* __restrict__ pB, const float* __restrict__ pC, T* __restrict__ dB, T* __restrict__ dC, long n,
                   int pg, int D4) {
+  grid_dep_enter();
   const long e = (long)blockIdx.x * 256 + threadIdx.x;
   if (e >= n) return;
   const long row = e / D4;  // (b, n, g)
@@ -543,8 +549,7 @@ static cudaError_t carry(const float* fwd, const float* rev, O* fs, O* rs, const
                          cudaStream_t st) {
   const int segs = nch <= 64 ? 1 : CARRY_SEGS, per = (nch + segs - 1) / segs, cols = segs == 1 ? 128 : 32;
   const dim3 grid((DM / 4 + cols - 1) / cols, BH, rev == nullptr ? 1 : 2), block(cols, (nch + per - 1) / per);
-  k_scan_carry<<<grid, block, 0, st>>>(fwd, rev, fs, rs, tot, S, nch, DM, per);
-  return cudaGetLastError();
+  return launch_pdl(k_scan_carry<O>, grid, block, 0, st, fwd, rev, fs, rs, tot, S, nch, DM, per);
 }
 
 cudaError_t scan_carry(float* fwd, float* rev, const float* tot, float* S, int BH, int nch, int DM, cudaStream_t st) {
@@ -558,75 +563,63 @@ cudaError_t scan_carry_bf16(const float* fwd, const float* rev, void* fs, void* 
 
 cudaError_t scan_params(const float* pp, void* dA, void* dskip, void* dbias, const ScanShape& s, int nch, cudaStream_t st) {
   if (s.dtype == 0)
-    k_scan_params<float><<<s.H, 256, 0, st>>>(pp, (float*)dA, (float*)dskip, (float*)dbias, s.B, s.H, nch);
-  else
-    k_scan_params<bf16><<<s.H, 256, 0, st>>>(pp, (bf16*)dA, (bf16*)dskip, (bf16*)dbias, s.B, s.H, nch);
-  return cudaGetLastError();
+    return launch_pdl(k_scan_params<float>, dim3(s.H), dim3(256), 0, st, pp, (float*)dA, (float*)dskip, (float*)dbias, s.B, s.H, nch);
+  return launch_pdl(k_scan_params<bf16>, dim3(s.H), dim3(256), 0, st, pp, (bf16*)dA, (bf16*)dskip, (bf16*)dbias, s.B, s.H, nch);
 }
 
 cudaError_t scan_groups(const float* pB, const float* pC, void* dB, void* dC, const ScanShape& s, int pg, cudaStream_t st) {
   const long n = (long)s.B * s.N * s.G * (s.D / 4);
   const dim3 grid((unsigned)((n + 255) / 256), 2);
   if (s.dtype == 0)
-    k_scan_groups<float><<<grid, 256, 0, st>>>(pB, pC, (float*)dB, (float*)dC, n, pg, s.D / 4);
-  else
-    k_scan_groups<bf16><<<grid, 256, 0, st>>>(pB, pC, (bf16*)dB, (bf16*)dC, n, pg, s.D / 4);
-  return cudaGetLastError();
+    return launch_pdl(k_scan_groups<float>, grid, dim3(256), 0, st, pB, pC, (float*)dB, (float*)dC, n, pg, s.D / 4);
+  return launch_pdl(k_scan_groups<bf16>, grid, dim3(256), 0, st, pB, pC, (bf16*)dB, (bf16*)dC, n, pg, s.D / 4);
 }
 
-template <typename T>
-static cudaError_t fwd_cc(const ScanIn& a, float* S, void* y, char* ws, const ScanShape& s, cudaStream_t st) {
+cudaError_t scan_fwd_cc(const ScanIn& a, float* S, void* y, void* ws_, const ScanShape& s, cudaStream_t st) {
+  using T = float;
+  char* ws = static_cast<char*>(ws_);
   const WsCC w(s, false);
   const int nch = (s.N + FT - 1) / FT, BH = s.B * s.H;
-  float *tot = (float*)(ws + w.tot), *fwd = (float*)(ws + w.fwd);
+  float *tot = (float*)(ws + w.tot), *fwd = (float*)(ws + w.fwd), *none = nullptr;
   const bool states = nch > 1 || S != nullptr;
-  const dim3 grid(nch, BH);
+  const dim3 grid(nch, BH), block(256);
   const T *x = (const T*)a.x, *dt = (const T*)a.dt, *A = (const T*)a.A, *Bm = (const T*)a.B, *Cm = (const T*)a.C,
-          *skip = (const T*)a.skip, *bias = (const T*)a.dt_bias;
+          *skip = (const T*)a.skip, *bias = (const T*)a.dt_bias, *dy = nullptr;
   LA_DISPATCH_DM(s.D, s.M, {
     if (states) {
       constexpr size_t b1 = 64 * (D_ + M_ + 8) * 4;
-      k_scan_sums<D_, M_, T><<<grid, 256, b1, st>>>(x, dt, A, Bm, Cm, bias, a.lengths, nullptr, fwd, nullptr, tot, s);
-      LA_TRY_CUDA(cudaGetLastError());
+      LA_TRY_CUDA(launch_pdl(k_scan_sums<D_, M_, T>, grid, block, b1, st, x, dt, A, Bm, Cm, bias, a.lengths, dy, fwd, none, tot, s));
       LA_TRY_CUDA(scan_carry(fwd, nullptr, tot, S, BH, nch, D_ * M_, st));
     }
     constexpr size_t b2 = (2 * D_ * FLD + 64 * (M_ + 4) + D_ * (M_ + 4) + 64 * FLD) * 4;
     LA_TRY_CUDA(smem(&k_scan_out<D_, M_, T>, b2));
-    k_scan_out<D_, M_, T><<<grid, 256, b2, st>>>(x, dt, A, Bm, Cm, skip, bias, a.lengths, states ? fwd : nullptr, (T*)y, s);
+    return launch_pdl(k_scan_out<D_, M_, T>, grid, block, b2, st, x, dt, A, Bm, Cm, skip, bias, a.lengths,
+                      (const float*)(states ? fwd : nullptr), (T*)y, s);
   });
-  return cudaGetLastError();
+  return cudaErrorInvalidValue;
 }
 
-template <typename T>
-static cudaError_t bwd_cc(const ScanIn& a, const void* dy, const ScanGrads& d, char* ws, const ScanShape& s, cudaStream_t st) {
+cudaError_t scan_bwd_cc(const ScanIn& a, const void* dy_, const ScanGrads& d, void* ws_, const ScanShape& s, cudaStream_t st) {
+  using T = float;
+  char* ws = static_cast<char*>(ws_);
   const WsCC w(s, true);
   const int nch = (s.N + FT - 1) / FT, BH = s.B * s.H;
   float *tot = (float*)(ws + w.tot), *fwd = (float*)(ws + w.fwd), *rev = (float*)(ws + w.rev), *pB = (float*)(ws + w.pB),
         *pC = (float*)(ws + w.pC), *pp = (float*)(ws + w.pp);
-  const dim3 grid(nch, BH);
+  const dim3 grid(nch, BH), block(256);
   const T *x = (const T*)a.x, *dt = (const T*)a.dt, *A = (const T*)a.A, *Bm = (const T*)a.B, *Cm = (const T*)a.C,
-          *skip = (const T*)a.skip, *bias = (const T*)a.dt_bias;
+          *skip = (const T*)a.skip, *bias = (const T*)a.dt_bias, *dy = (const T*)dy_;
   LA_DISPATCH_DM(s.D, s.M, {
     constexpr size_t b1 = 64 * (D_ + M_ + 8) * 4;
-    k_scan_sums<D_, M_, T><<<grid, 256, b1, st>>>(x, dt, A, Bm, Cm, bias, a.lengths, (const T*)dy, fwd, rev, tot, s);
-    LA_TRY_CUDA(cudaGetLastError());
+    LA_TRY_CUDA(launch_pdl(k_scan_sums<D_, M_, T>, grid, block, b1, st, x, dt, A, Bm, Cm, bias, a.lengths, dy, fwd, rev, tot, s));
     LA_TRY_CUDA(scan_carry(fwd, rev, tot, nullptr, BH, nch, D_ * M_, st));
     constexpr size_t b2 = 12 * 64 * FLD * 4;
     LA_TRY_CUDA(smem(&k_scan_grad<D_, M_, T>, b2));
-    k_scan_grad<D_, M_, T><<<grid, 256, b2, st>>>(x, dt, A, Bm, Cm, skip, bias, a.lengths, (const T*)dy, fwd, rev, (T*)d.x,
-                                                 (T*)d.dt, pB, pC, pp, s);
+    LA_TRY_CUDA(launch_pdl(k_scan_grad<D_, M_, T>, grid, block, b2, st, x, dt, A, Bm, Cm, skip, bias, a.lengths, dy,
+                           (const float*)fwd, (const float*)rev, (T*)d.x, (T*)d.dt, pB, pC, pp, s));
   });
-  LA_TRY_CUDA(cudaGetLastError());
   LA_TRY_CUDA(scan_groups(pB, pC, d.B, d.C, s, s.H / s.G, st));
   return scan_params(pp, d.A, d.skip, d.dt_bias, s, nch, st);
-}
-
-cudaError_t scan_fwd_cc(const ScanIn& a, float* S, void* y, void* ws, const ScanShape& s, cudaStream_t st) {
-  return s.dtype == 0 ? fwd_cc<float>(a, S, y, (char*)ws, s, st) : fwd_cc<bf16>(a, S, y, (char*)ws, s, st);
-}
-
-cudaError_t scan_bwd_cc(const ScanIn& a, const void* dy, const ScanGrads& d, void* ws, const ScanShape& s, cudaStream_t st) {
-  return s.dtype == 0 ? bwd_cc<float>(a, dy, d, (char*)ws, s, st) : bwd_cc<bf16>(a, dy, d, (char*)ws, s, st);
 }
 
 template <typename T>

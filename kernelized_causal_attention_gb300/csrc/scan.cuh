@@ -1,11 +1,19 @@
-// Shared by the selective scan's CUDA-core (scan.cu) and tensor-core
-// (scan_tc.cu) kernels: the call's sizes and pointers, and the gate.
+// Shared by the convolution's, the scan's and the cross attention's kernels:
+// the start of a dependent kernel, the gate, valid rows, the carry and the sums.
 #pragma once
 
 #include "common.cuh"
 #include "launch.h"
+#include "tc_chunk.cuh"
 
 namespace la {
+
+// For kernels launched with launch_pdl: the next kernel may start as blocks
+// leave, and nothing before this in the stream is still running once it returns.
+__device__ __forceinline__ void grid_dep_enter() {
+  tcc::grid_dep_launch();
+  tcc::grid_dep_wait();
+}
 
 // softplus(x) = log(1 + exp(x)), written so that neither branch overflows.
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }

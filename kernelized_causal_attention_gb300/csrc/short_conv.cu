@@ -14,7 +14,7 @@
 #include <algorithm>
 
 #include "common.cuh"
-#include "launch.h"
+#include "scan.cuh"
 
 namespace la {
 namespace {
@@ -337,6 +337,7 @@ constexpr int RS = 8;
 template <typename T>
 __global__ void __launch_bounds__(32 * RS)
     k_conv_sum(const float* __restrict__ part, T* __restrict__ dw, T* __restrict__ db, int P, int C, int K) {
+  grid_dep_enter();
   __shared__ float red[RS][32];
   const int c = blockIdx.x * 32 + threadIdx.x, j = blockIdx.y;
   float s = 0.f;
@@ -464,10 +465,8 @@ cudaError_t short_conv_bwd(const void* x, const void* w, const void* bias, const
   const dim3 sgrid((s.C + 31) / 32, s.K + 1), sblock(32, RS);
   const int P = s.B * groups;
   if (s.dtype == 0)
-    k_conv_sum<float><<<sgrid, sblock, 0, st>>>(ws, (float*)dw, (float*)db, P, s.C, s.K);
-  else
-    k_conv_sum<bf16><<<sgrid, sblock, 0, st>>>(ws, (bf16*)dw, (bf16*)db, P, s.C, s.K);
-  return cudaGetLastError();
+    return launch_pdl(k_conv_sum<float>, sgrid, sblock, 0, st, (const float*)ws, (float*)dw, (float*)db, P, s.C, s.K);
+  return launch_pdl(k_conv_sum<bf16>, sgrid, sblock, 0, st, (const float*)ws, (bf16*)dw, (bf16*)db, P, s.C, s.K);
 }
 
 cudaError_t short_conv_step(const void* x, const void* w, const void* bias, void* state, void* y, const ConvShape& s,
