@@ -31,8 +31,11 @@ constexpr int W_ISSUE = 8;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int STILE = 64 * 64 * 2;
 
-// phi and min(phi, 1) = phi'.
-__device__ __forceinline__ float phif(float x) { return x > 0.f ? x + 1.f : ex2_fast(x * LOG2E); }
+// phi by a select: a branch around the exponential would diverge at every value.
+__device__ __forceinline__ float phif(float x) {
+  const float e = ex2_fast(fminf(x, 0.f) * LOG2E);
+  return x > 0.f ? x + 1.f : e;
+}
 
 #define LA_WAITS()                                                          \
   auto wt = [&](uint64_t* bar, uint32_t parity, int code) -> bool {         \

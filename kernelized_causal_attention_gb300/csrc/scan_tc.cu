@@ -261,12 +261,12 @@ __global__ void __launch_bounds__(NT, 2)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int o = row * 128 + (((4 * half + c) ^ (row & 7)) << 4);
-          const uint32_t v[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+          // a row past the length (or weighed by nothing) enters as zeros, whatever it holds
+          const uint32_t v[4] = {f != 0.f ? u[c].x : 0u, f != 0.f ? u[c].y : 0u, f != 0.f ? u[c].z : 0u, f != 0.f ? u[c].w : 0u};
           uint32_t t[3][4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            float a = f != 0.f ? __uint_as_float(v[k] << 16) * f : 0.f;
-            float b = f != 0.f ? __uint_as_float(v[k] & 0xffff0000u) * f : 0.f;
+            float a = __uint_as_float(v[k] << 16) * f, b = __uint_as_float(v[k] & 0xffff0000u) * f;
 #pragma unroll
             for (int j = 0; j < TERMS; ++j) {
               t[j][k] = pack_bf16(a, b);
@@ -436,8 +436,11 @@ __global__ void __launch_bounds__(NT, 2)
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
                 const float4 u = *reinterpret_cast<const float4*>(&g.wp[32 * J + c]), d = *reinterpret_cast<const float4*>(&g.del[32 * J + c]);
-                const float p0 = c <= lane ? a[c] * (ex2_fast(wp - u.x) * d.x) : 0.f, p1 = c + 1 <= lane ? a[c + 1] * (ex2_fast(wp - u.y) * d.y) : 0.f;
-                const float p2 = c + 2 <= lane ? a[c + 2] * (ex2_fast(wp - u.z) * d.z) : 0.f, p3 = c + 3 <= lane ? a[c + 3] * (ex2_fast(wp - u.w) * d.w) : 0.f;
+                // taken for masked pairs too and dropped by a select, not a branch
+                float p0 = a[c] * (ex2_fast(fminf(wp - u.x, 0.f)) * d.x), p1 = a[c + 1] * (ex2_fast(fminf(wp - u.y, 0.f)) * d.y);
+                float p2 = a[c + 2] * (ex2_fast(fminf(wp - u.z, 0.f)) * d.z), p3 = a[c + 3] * (ex2_fast(fminf(wp - u.w, 0.f)) * d.w);
+                p0 = c <= lane ? p0 : 0.f, p1 = c + 1 <= lane ? p1 : 0.f;
+                p2 = c + 2 <= lane ? p2 : 0.f, p3 = c + 3 <= lane ? p3 : 0.f;
                 pk[c / 2] = pack_bf16(p0, p1);
                 pk[c / 2 + 1] = pack_bf16(p2, p3);
               }
@@ -508,10 +511,10 @@ constexpr uint32_t TG_A = 0, TG_E = 128, TG_U = 256, TG_BR = 320, TG_B = 384, TG
 
 __device__ __forceinline__ void sync_grad() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
 
-// Sum over the warp's lanes of g[c] for each of 16 columns c, to lanes c and c + 16.
-__device__ __forceinline__ float column_sums(float (&g)[16], int lane) {
+// Sum over the warp's lanes of g[c] for each of 8 columns c, to lanes c, c + 8, ... .
+__device__ __forceinline__ float column_sums(float (&g)[8], int lane) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
+  for (int o = 4; o > 0; o >>= 1) {
     const bool up = lane & o;
 #pragma unroll
     for (int c = 0; c < o; ++c) {
@@ -519,6 +522,7 @@ __device__ __forceinline__ float column_sums(float (&g)[16], int lane) {
       g[c] = keep + __shfl_xor_sync(0xffffffffu, give, o);
     }
   }
+  g[0] += __shfl_xor_sync(0xffffffffu, g[0], 8);
   return g[0] + __shfl_xor_sync(0xffffffffu, g[0], 16);
 }
 
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(NTG, 1)
   extern __shared__ uint8_t smraw[];
   uint8_t* sm = align1024(smraw);
   __shared__ uint64_t bar_cb, bar_in[2], bar_clear, bar_1, bar_2, bar_3, bar_4, bar_p, bar_c, bar_x, bar_free;
-  __shared__ Gates gates[2];
+  __shared__ Gates gates[3];
   __shared__ Params par_[MAXH];
   __shared__ GateSums sums[2];
   __shared__ float s_tot[4][2], s_out[4][2];
@@ -681,14 +685,54 @@ __global__ void __launch_bounds__(NTG, 1)
       put_gates(gates[0], raw(0) + par_[0].bias, live, par_[0].A, row);
       z = raw(1);
     }
+    // The gate's gradient of head i, row by row (sigmoid(z) = 1 - exp(-delta)), by four
+    // warps whose score block the mask leaves empty, beside the next head's weights.
+    const int gw = warp == 7 ? 3 : warp - 1;  // warps 1, 2, 3 and 7
+    const bool gater = warp == 7 || (warp >= 1 && warp <= 3);
+    auto gate_gradient = [&](int i) {
+      const Gates& g = gates[i % 3];
+      const GateSums& gs = sums[i & 1];
+      const int t = 32 * gw + lane;
+      const float del = g.del[t];
+      float q = 0.f, ww = 0.f, xu = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        q += gs.v[j][t] - gs.col[j][t] + gs.row[j][t];
+        ww += gs.w[j][t];
+        xu += gs.u[j][t];
+      }
+      const float sr = warp_sum(lane < 16 ? gs.red[lane][0] : 0.f);
+      const float suf = warp_suffix(q), pre = warp_prefix(ww);
+      if (lane == 0) s_tot[gw][0] = suf;
+      if (lane == 31) s_tot[gw][1] = pre;
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+      float dl = suf + (pre - ww);
+      for (int j = gw + 1; j < 4; ++j) dl += s_tot[j][0];
+      for (int j = 0; j < gw; ++j) dl += s_tot[j][1];
+      dl = fmaf(ex2_fast(g.off(4)), sr, dl);
+      const float dz = t < w.rows ? (xu + par_[i].A * dl) * -expm1f(-del) : 0.f;
+      if (t < in_n) ddt[(r0 + t) * s.H + w.h0 + i] = from_f<bf16>(dz);
+      const float dA = warp_sum(t < w.rows ? del * dl : 0.f), db = warp_sum(dz);
+      if (lane == 0) s_out[gw][0] = dA, s_out[gw][1] = db;
+      asm volatile("bar.sync 2, 128;" ::: "memory");
+      if (gw == 0) {
+        const float ds = warp_sum(lane < 16 ? gs.red[lane][1] : 0.f);
+        if (lane == 0) {
+          float* o = pp + (((long)w.b * s.H + w.h0 + i) * nch + blockIdx.x) * 3;
+          o[0] = s_out[0][0] + s_out[1][0] + s_out[2][0] + s_out[3][0];
+          o[1] = ds;
+          o[2] = s_out[0][1] + s_out[1][1] + s_out[2][1] + s_out[3][1];
+        }
+      }
+    };
     float aB[16], aC[16];  // dB and dC of this row, columns c0 .. c0 + 15, over the heads
 #pragma unroll
     for (int c = 0; c < 16; ++c) aB[c] = aC[c] = 0.f;
     const bool cb = wtu(&bar_cb, 0, 89);
     sync_grad();
     for (int i = 0; i < w.nh; ++i) {
-      const int k = i & 1, h = w.h0 + i;
-      const Gates& g = gates[k];
+      const int k = i & 1;
+      const Gates& g = gates[i % 3];
       GateSums& gs = sums[k];
       uint8_t *xt = sm + G_X + k * TILE, *yt = sm + G_Y + k * TILE;
       const bool in = wtu(&bar_in[k], (i >> 1) & 1, 90) && cb;
@@ -707,7 +751,7 @@ __global__ void __launch_bounds__(NTG, 1)
       const float wp = g.wp[row], del = g.del[row];
       const float tail = ex2_fast(g.tot[qd] - wp);     // from this row to its block's end
       const float fend = tail * ex2_fast(g.past(qd));  // to the chunk's end
-      const float ecum = g.ew[row] * ex2_fast(g.off(qd)), eall = ex2_fast(g.off(4));
+      const float ecum = g.ew[row] * ex2_fast(g.off(qd));
       // ---- the weights on this warp's block of A^T and E^T: keys 32 qd + lane, queries 32 I + c
       if (wtu(&bar_1, k, 91)) {
         tc_fence_after();
@@ -716,58 +760,59 @@ __global__ void __launch_bounds__(NTG, 1)
         const float fr = I > qd ? tail * ex2_fast(g.off(I) - g.off(qd + 1)) : 0.f, frd = fr * del;
         float col = 0.f;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t pw[8], qw[8];
+        for (int o = 0; o < 4; ++o) {  // eight queries at a time
+          uint32_t pw[4], qw[4];
           if (I < qd) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) pw[c] = qw[c] = 0u;
-            if (lane < 16) gs.row[qd][32 * I + 16 * hf + lane] = 0.f;
+            for (int c = 0; c < 4; ++c) pw[c] = qw[c] = 0u;
           } else {
-            float a[16], e[16];
-            tmem_ld16(ta + 16 * hf, a);
-            tmem_ld16(te + 16 * hf, e);
+            float a[8], e[8], gg[8];
+            tmem_ld8(ta + 8 * o, a);
+            tmem_ld8(te + 8 * o, e);
             tmem_ld_wait();
-            const float4* tab = reinterpret_cast<const float4*>((I > qd ? g.ew : g.wp) + 32 * I + 16 * hf);
+            const float4* tab = reinterpret_cast<const float4*>((I > qd ? g.ew : g.wp) + 32 * I + 8 * o);
+            const float4 t0 = tab[0], t1 = tab[1];
+            float tv[8] = {t0.x, t0.y, t0.z, t0.w, t1.x, t1.y, t1.z, t1.w};
+            if (I > qd) {
 #pragma unroll
-            for (int c = 0; c < 16; c += 4) {
-              const float4 t4 = tab[c / 4];
-              const float tv[4] = {t4.x, t4.y, t4.z, t4.w};
-              float p[4], qq[4];
-#pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                if (I > qd) {
-                  p[t] = tv[t] * fr * a[c + t];
-                  qq[t] = tv[t] * frd * e[c + t];
-                  e[c + t] = qq[t] * a[c + t];
-                } else {
-                  const int i_ = 16 * hf + c + t;
-                  const float wt_ = i_ >= lane ? ex2_fast(tv[t] - wp) : 0.f;
-                  p[t] = wt_ * a[c + t];
-                  qq[t] = wt_ * del * e[c + t];
-                  e[c + t] = i_ == lane ? 0.f : qq[t] * a[c + t];  // a pair with itself feels no decay
-                }
-                col += e[c + t];
+              for (int c = 0; c < 8; ++c) {
+                e[c] *= tv[c] * frd;
+                gg[c] = e[c] * a[c];
+                a[c] *= tv[c] * fr;
               }
-              pw[c / 2] = pack_bf16(p[0], p[1]);
-              pw[c / 2 + 1] = pack_bf16(p[2], p[3]);
-              qw[c / 2] = pack_bf16(qq[0], qq[1]);
-              qw[c / 2 + 1] = pack_bf16(qq[2], qq[3]);
+            } else {
+              // (the exponential of a masked pair is dropped by a select: branches around
+              // them, pair by pair, took most of this stage)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                float wt_ = ex2_fast(fminf(tv[c] - wp, 0.f));
+                wt_ = 8 * o + c >= lane ? wt_ : 0.f;
+                e[c] *= wt_ * del;
+                gg[c] = 8 * o + c == lane ? 0.f : e[c] * a[c];  // a pair with itself feels no decay
+                a[c] *= wt_;
+              }
             }
-            const float rs = column_sums(e, lane);
-            if (lane < 16) gs.row[qd][32 * I + 16 * hf + lane] = rs;
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+              col += gg[c] + gg[c + 1];
+              pw[c / 2] = pack_bf16(a[c], a[c + 1]);
+              qw[c / 2] = pack_bf16(e[c], e[c + 1]);
+            }
+            const float rs = column_sums(gg, lane);
+            if (lane < 8) gs.row[qd][32 * I + 8 * o + lane] = rs;
           }
-          tmem_st8u(ta + 8 * hf, pw);  // over columns this warp has read
-          tmem_st8u(te + 8 * hf, qw);
-          const int ch = 4 * (I & 1) + 2 * hf;
-          sts128(qt + ((ch ^ (row & 7)) << 4), make_uint4(qw[0], qw[1], qw[2], qw[3]));
-          sts128(qt + (((ch + 1) ^ (row & 7)) << 4), make_uint4(qw[4], qw[5], qw[6], qw[7]));
+          tmem_st4u(ta + 4 * o, pw);  // over columns this warp has read
+          tmem_st4u(te + 4 * o, qw);
+          sts128(qt + (((4 * (I & 1) + o) ^ (row & 7)) << 4), make_uint4(qw[0], qw[1], qw[2], qw[3]));
         }
+        if (I < qd) gs.row[qd][32 * I + lane] = 0.f;
         gs.col[I][row] = col;
         tmem_st_wait();
       }
       fence_proxy_async();
       tc_fence_before();
       mbar_arrive(&bar_p);
+      if (i > 0 && gater) gate_gradient(i - 1);
       // ---- the carried states' parts of dB and dC
       if (wtu(&bar_2, k, 92)) {
         tc_fence_after();
@@ -797,7 +842,7 @@ __global__ void __launch_bounds__(NTG, 1)
       tc_fence_before();
       mbar_arrive(&bar_c);
       if (I == 1 && i + 1 < w.nh) {  // the next head's gates, beside this one's products
-        put_gates(gates[k ^ 1], z + par_[i + 1].bias, live, par_[i + 1].A, row);
+        put_gates(gates[(i + 1) % 3], z + par_[i + 1].bias, live, par_[i + 1].A, row);
         z = raw(i + 2);
       }
       // <S, R> over the two bf16 tiles: 8 values a thread
@@ -853,39 +898,8 @@ __global__ void __launch_bounds__(NTG, 1)
       tc_fence_before();
       mbar_arrive(&bar_free);
       sync_grad();  // this head's sums and the next one's gates are in place
-      // ---- the gate's gradient, row by row (sigmoid(z) = 1 - exp(-delta))
-      if (I == 0) {
-        float q = 0.f, ww = 0.f, xu = 0.f, ds = 0.f;
-        sr = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          q += gs.v[j][row] - gs.col[j][row] + gs.row[j][row];
-          ww += gs.w[j][row];
-          xu += gs.u[j][row];
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) sr += gs.red[j][0], ds += gs.red[j][1];
-        const float suf = warp_suffix(q), pre = warp_prefix(ww);
-        if (lane == 0) s_tot[qd][0] = suf;
-        if (lane == 31) s_tot[qd][1] = pre;
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-        float dl = suf + (pre - ww);
-        for (int j = qd + 1; j < 4; ++j) dl += s_tot[j][0];
-        for (int j = 0; j < qd; ++j) dl += s_tot[j][1];
-        dl = fmaf(eall, sr, dl);
-        const float dz = live ? (xu + par_[i].A * dl) * -expm1f(-del) : 0.f;
-        if (row < in_n) ddt[(r0 + row) * s.H + h] = from_f<bf16>(dz);
-        const float dA = warp_sum(live ? del * dl : 0.f), db = warp_sum(dz);
-        if (lane == 0) s_out[qd][0] = dA, s_out[qd][1] = db;
-        asm volatile("bar.sync 2, 128;" ::: "memory");
-        if (threadIdx.x == 0) {
-          float* o = pp + (((long)w.b * s.H + h) * nch + blockIdx.x) * 3;
-          o[0] = s_out[0][0] + s_out[1][0] + s_out[2][0] + s_out[3][0];
-          o[1] = ds;
-          o[2] = s_out[0][1] + s_out[1][1] + s_out[2][1] + s_out[3][1];
-        }
-      }
     }
+    if (gater) gate_gradient(w.nh - 1);
     if (row < in_n && c0 < s.D) {
       const long o = ((r0 + row) * parts + w.part) * s.D + c0;
       if (!live) {
