@@ -125,37 +125,38 @@ struct Maps {
 };
 
 // ------------------------------------------------------------- chunk sums
-// TERMS bf16 terms of the scaled operand, side by side along the product's N
-// (three for the forward pass, whose final state is an fp32 output: 2^-24; one
-// for the gradients, which are bf16).  blockIdx.y = part, or parts + part for
-// the reverse sums E = sum_i exp(cum_i) C_i dy_i^T.
-constexpr int S_A = 0, S_X = TILE, S_T = 3 * TILE;  // B or C; two x stages; the terms
-constexpr int S_SMEM(int terms) { return (3 + terms) * TILE + 1024; }
+// TERMS bf16 terms of the scaled operand: three where the state after the last
+// row is wanted (an fp32 output: 2^-24), two for the states that the outputs
+// read in bf16, one for those of the bf16 gradients.  The first term takes x's
+// place in shared memory and the third adds to the second's columns, so three
+// blocks share an SM: one's load, another's conversion and a third's products
+// overlap, and a head's own chain need not.  blockIdx.y = part, or parts + part
+// for the reverse sums E = sum_i exp(cum_i) C_i dy_i^T.
+constexpr int S_A = 0, S_T = TILE;  // B or C; the terms
+constexpr int S_SMEM(int terms) { return (1 + terms) * TILE + 1024; }
 
 template <int TERMS>
-__global__ void __launch_bounds__(NT, 2)
+__global__ void __launch_bounds__(NT, 3)
     k_sums(const __grid_constant__ Maps maps, const bf16* __restrict__ dt, const bf16* __restrict__ A,
            const bf16* __restrict__ bias, const int* __restrict__ lengths, float* __restrict__ fwd, float* __restrict__ rev,
            float* __restrict__ tot, ScanShape s, int pg, int hs, int* err) {
   extern __shared__ uint8_t smraw[];
   uint8_t* sm = align1024(smraw);
-  __shared__ uint64_t bar_a, bar_x[2], bar_t, bar_m, bar_fin;
+  __shared__ uint64_t bar_a, bar_x, bar_t, bar_m;
   __shared__ Gates gates[2];
   __shared__ Params par_[MAXH];
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
-  constexpr int COLS = TERMS > 1 ? 256 : 64;
+  constexpr int COLS = TERMS > 1 ? 128 : 64;
   const int parts = s.G * pg;
   const bool back = blockIdx.y >= parts;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nch = gridDim.x;
   grid_dep_launch();
   if (threadIdx.x == NT - 1) {
     mbar_init(&bar_a, 1);
-    mbar_init(&bar_x[0], 1);
-    mbar_init(&bar_x[1], 1);
+    mbar_init(&bar_x, 1);
     mbar_init(&bar_t, 256);
     mbar_init(&bar_m, 1);
-    mbar_init(&bar_fin, 1);
     fence_barrier_init();
     s_abort = 0;
   }
@@ -182,31 +183,37 @@ __global__ void __launch_bounds__(NT, 2)
   if (warp == W_ISSUE) {
     if (lane == 0) {
       const CUtensorMap* mx = back ? &maps.g : &maps.x;
-      int issued = 0;
       auto load = [&](int i) {
-        mbar_arrive_expect_tx(&bar_x[i & 1], TILE);
-        tma_load_4d(sm + S_X + (i & 1) * TILE, mx, &bar_x[i & 1], 0, w.h0 + i, w.n0, w.b);
-        ++issued;
+        mbar_arrive_expect_tx(&bar_x, TILE);
+        tma_load_4d(sm + S_T, mx, &bar_x, 0, w.h0 + i, w.n0, w.b);
       };
       load(0);
       mbar_arrive_expect_tx(&bar_a, TILE);
       tma_load_4d(sm + S_A, back ? &maps.C : &maps.B, &bar_a, 0, w.g, w.n0, w.b);
-      if (w.nh > 1) load(1);
-      constexpr uint32_t ID = idesc_bf16(64, 64 * TERMS, true, true);
+      constexpr uint32_t ID = idesc_bf16(64, COLS, true, true), ID1 = idesc_bf16(64, 64, true, true);
       const uint64_t da = sdesc(smem_u32(sm + S_A), 16, 1024), db = sdesc(smem_u32(sm + S_T), TILE, 1024);
-      const bool in = wt(&bar_a, 0, 66);
-      for (int i = 0; in && i < w.nh; ++i) {
-        if (!wt(&bar_t, i & 1, 61)) break;
+      int loads = 1;
+      bool ok = wt(&bar_a, 0, 66);
+      for (int i = 0; ok && i < w.nh; ++i) {
+        if (!(ok = wt(&bar_t, i & 1, 61))) break;
         tc_fence_after();
-        if (i + 2 < w.nh) load(i + 2);  // head i's stage has been read
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mma_bf16(tm, dadd(da, kk * 2048), dadd(db, kk * 2048), ID, kk > 0);
+        if (TERMS > 2)
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) mma_bf16(tm + 64, dadd(da, kk * 2048), dadd(db, 2 * TILE + kk * 2048), ID1, 1);
         mma_commit(&bar_m);
+        if (i + 1 < w.nh) {
+          if (!(ok = wt(&bar_m, i & 1, 67))) break;  // the terms have been read
+          load(i + 1);
+          ++loads;
+        }
       }
-      // nothing in flight at exit: the products' last commit, the loads
-      mma_commit(&bar_fin);
-      mbar_wait(&bar_fin, 0, WAIT_NS);
-      drain_loads<2>(bar_x, issued);
+      // nothing in flight at exit
+      mbar_wait(&bar_x, (loads - 1) & 1, WAIT_NS);
+      mbar_wait(&bar_a, 0, WAIT_NS);
+      mma_commit(&bar_a);
+      mbar_wait(&bar_a, 1, WAIT_NS);
     }
   } else {
     const int row = threadIdx.x & 127, half = threadIdx.x >> 7, q = row >> 5;
@@ -214,29 +221,6 @@ __global__ void __launch_bounds__(NT, 2)
     auto raw = [&](int i) { return i < w.nh && row < w.rows ? to_f(dt[(r0 + row) * s.lddt + w.h0 + i]) : 0.f; };
     const int qd = warp & 3, srow = 16 * qd + lane;
     const uint32_t lq = static_cast<uint32_t>(32 * qd) << 16;
-    auto drain = [&](int i, bool done) {  // head i's sums, its products done
-      if (done) {
-        tc_fence_after();
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float f[TERMS][16];
-#pragma unroll
-          for (int k = 0; k < TERMS; ++k) tmem_ld16(tm + lq + 64 * k + 32 * half + 16 * j, f[k]);
-          tmem_ld_wait();
-          if (TERMS > 1) {
-#pragma unroll
-            for (int c = 0; c < 16; ++c) f[0][c] += f[1][c] + f[TERMS - 1][c];
-          }
-          const int c0 = 32 * half + 16 * j;
-          if (lane < 16 && srow < s.D && c0 < s.M) {
-            float* o = out + (long)i * nch * DM + srow * s.M + c0;
-#pragma unroll
-            for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4*>(o + c) = make_float4(f[0][c], f[0][c + 1], f[0][c + 2], f[0][c + 3]);
-          }
-        }
-      }
-      tc_fence_before();
-    };
     float z = 0.f;
     if (half == 0) {
       put_gates(gates[0], raw(0) + par_[0].bias, row < w.rows, par_[0].A, row);
@@ -250,20 +234,14 @@ __global__ void __launch_bounds__(NT, 2)
       const Gates& g = gates[i & 1];
       if (threadIdx.x == 0 && !back) tot[((long)w.b * s.H + w.h0 + i) * nch + blockIdx.x] = g.off(4) * LN2;
       const float f = row >= w.rows ? 0.f : (back ? ex2_fast(g.wp[row] + g.off(q)) : g.cf[row] * ex2_fast(g.past(q)));
-      const bool in = wtu(&bar_x[i & 1], (i >> 1) & 1, 64);
-      uint4 u[4];
-      const uint8_t* xt = sm + S_X + (i & 1) * TILE;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) u[c] = lds128(xt + row * 128 + (((4 * half + c) ^ (row & 7)) << 4));
-      // the products that read the terms' tiles are done; their sums leave the accumulator
-      if (i > 0) drain(i - 1, wtu(&bar_m, (i - 1) & 1, 65));
-      if (in) {
+      if (wtu(&bar_x, i & 1, 64)) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          const int o = row * 128 + (((4 * half + c) ^ (row & 7)) << 4);
+          uint8_t* at = sm + S_T + row * 128 + (((4 * half + c) ^ (row & 7)) << 4);
+          const uint4 u = lds128(at);
           // a row past the length (or weighed by nothing) enters as zeros, whatever it holds
-          const uint32_t v[4] = {f != 0.f ? u[c].x : 0u, f != 0.f ? u[c].y : 0u, f != 0.f ? u[c].z : 0u, f != 0.f ? u[c].w : 0u};
-          uint32_t t[3][4];
+          const uint32_t v[4] = {f != 0.f ? u.x : 0u, f != 0.f ? u.y : 0u, f != 0.f ? u.z : 0u, f != 0.f ? u.w : 0u};
+          uint32_t t[TERMS][4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             float a = __uint_as_float(v[k] << 16) * f, b = __uint_as_float(v[k] & 0xffff0000u) * f;
@@ -275,18 +253,39 @@ __global__ void __launch_bounds__(NT, 2)
             }
           }
 #pragma unroll
-          for (int j = 0; j < TERMS; ++j) sts128(sm + S_T + j * TILE + o, make_uint4(t[j][0], t[j][1], t[j][2], t[j][3]));
+          for (int j = 0; j < TERMS; ++j) sts128(at + j * TILE, make_uint4(t[j][0], t[j][1], t[j][2], t[j][3]));
         }
       }
       fence_proxy_async();
+      tc_fence_before();
       mbar_arrive(&bar_t);
       if (half == 0 && i + 1 < w.nh) {  // the next head's gates, beside this one's products
         put_gates(gates[(i + 1) & 1], z + par_[i + 1].bias, row < w.rows, par_[i + 1].A, row);
         z = raw(i + 2);
       }
+      if (wtu(&bar_m, i & 1, 62)) {  // the sums, and the next head's rows on their way
+        tc_fence_after();
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float p[16], r[16];
+          tmem_ld16(tm + lq + 32 * half + 16 * j, p);
+          if (TERMS > 1) tmem_ld16(tm + lq + 64 + 32 * half + 16 * j, r);
+          tmem_ld_wait();
+          if (TERMS > 1) {
+#pragma unroll
+            for (int c = 0; c < 16; ++c) p[c] += r[c];
+          }
+          const int c0 = 32 * half + 16 * j;
+          if (lane < 16 && srow < s.D && c0 < s.M) {
+            float* o = out + (long)i * nch * DM + srow * s.M + c0;
+#pragma unroll
+            for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4*>(o + c) = make_float4(p[c], p[c + 1], p[c + 2], p[c + 3]);
+          }
+        }
+      }
       sync_compute();
     }
-    drain(w.nh - 1, wtu(&bar_m, (w.nh - 1) & 1, 62));
+    tc_fence_before();
   }
   leave(tm, COLS, W_ISSUE);
 }
@@ -1009,8 +1008,13 @@ cudaError_t scan_fwd_tc(const ScanIn& a, float* S, void* y, void* ws, const Scan
   const bf16 *dt = (const bf16*)a.dt, *A = (const bf16*)a.A, *skip = (const bf16*)a.skip, *bias = (const bf16*)a.dt_bias;
   int* err = status_word();
   if (states) {
-    LA_TRY_CUDA(cudaFuncSetAttribute(k_sums<3>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM(3)));
-    LA_TRY_CUDA(launch_pdl(k_sums<3>, grid, dim3(NT), S_SMEM(3), st, m, dt, A, bias, a.lengths, pf, static_cast<float*>(nullptr), tot, s, p.pg, p.hs, err));
+    const Parts ps(s, 3 * sm_count());
+    const dim3 sgrid(nch, s.G * ps.pg, s.B);
+    const int terms = S != nullptr ? 3 : 2;
+    auto sums = terms == 3 ? &k_sums<3> : &k_sums<2>;
+    LA_TRY_CUDA(cudaFuncSetAttribute(sums, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM(terms)));
+    LA_TRY_CUDA(launch_pdl(sums, sgrid, dim3(NT), S_SMEM(terms), st, m, dt, A, bias, a.lengths, pf, static_cast<float*>(nullptr), tot, s, ps.pg,
+                           ps.hs, err));
     LA_TRY_CUDA(scan_carry_bf16(pf, nullptr, sf, nullptr, tot, S, s.B * s.H, nch, s.D * s.M, st));
   }
   LA_TRY_CUDA(cudaFuncSetAttribute(k_out, cudaFuncAttributeMaxDynamicSharedMemorySize, O_SMEM));
@@ -1032,7 +1036,7 @@ cudaError_t scan_bwd_tc(const ScanIn& a, const void* dy, const ScanGrads& d, voi
   const bf16 *dt = (const bf16*)a.dt, *A = (const bf16*)a.A, *skip = (const bf16*)a.skip, *bias = (const bf16*)a.dt_bias;
   int* err = status_word();
   // the sums feed bf16 gradients only: one bf16 term
-  const Parts ps(s, sm_count());
+  const Parts ps(s, 3 * sm_count() / 2);  // either direction's share of three blocks an SM
   LA_TRY_CUDA(cudaFuncSetAttribute(k_sums<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM(1)));
   LA_TRY_CUDA(launch_whole(k_sums<1>, dim3(nch, 2 * s.G * ps.pg, s.B), dim3(NT), S_SMEM(1), st, m, dt, A, bias, a.lengths, pf, pr, tot, s, ps.pg, ps.hs, err));
   LA_TRY_CUDA(scan_carry_bf16(pf, pr, sf, sr, tot, nullptr, s.B * s.H, nch, s.D * s.M, st));
