@@ -94,6 +94,14 @@ struct Share {
   }
 };
 
+// Eight floats to a 32-byte boundary: a whole sector from one lane.
+__device__ __forceinline__ void store8(float* o, const float* f) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(o), "r"(__float_as_uint(f[0])), "r"(__float_as_uint(f[1])),
+               "r"(__float_as_uint(f[2])), "r"(__float_as_uint(f[3])), "r"(__float_as_uint(f[4])), "r"(__float_as_uint(f[5])),
+               "r"(__float_as_uint(f[6])), "r"(__float_as_uint(f[7]))
+               : "memory");
+}
+
 // Rows [rows, 128) of a swizzled [128][64] tile become zeros, by n threads.
 __device__ __forceinline__ void clear_rows(uint8_t* tile, int rows, int n = 256) {
   for (int v = rows * 8 + threadIdx.x; v < TILE / 16; v += n) sts128(tile + v * 16, make_uint4(0u, 0u, 0u, 0u));
@@ -279,7 +287,7 @@ __global__ void __launch_bounds__(NT, 3)
           if (lane < 16 && srow < s.D && c0 < s.M) {
             float* o = out + (long)i * nch * DM + srow * s.M + c0;
 #pragma unroll
-            for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4*>(o + c) = make_float4(p[c], p[c + 1], p[c + 2], p[c + 3]);
+            for (int c = 0; c < 16; c += 8) store8(o + c, p + c);
           }
         }
       }
@@ -922,7 +930,9 @@ __global__ void __launch_bounds__(NTG, 1)
 
 // ------------------------------------------------------------------ host
 
-size_t align16(size_t n) { return (n + 15) / 16 * 16; }
+constexpr size_t LINE = 128;  // the parts of the workspace start on lines
+size_t align_line(size_t n) { return (n + LINE - 1) / LINE * LINE; }
+char* first_line(void* ws) { return reinterpret_cast<char*>(align_line(reinterpret_cast<size_t>(ws))); }
 
 int chunks(const ScanShape& s) { return (s.N + TC_C - 1) / TC_C; }
 
@@ -950,18 +960,18 @@ struct WsTC {
   WsTC(const ScanShape& s, bool bwd) {
     const size_t n = (size_t)s.B * s.H * chunks(s), st = n * s.D * s.M;
     tot = 0;
-    pf = align16(n * 4);
+    pf = align_line(n * 4);
     sf = pf + st * 4;
-    end = sf + st * 2;
+    end = align_line(sf + st * 2);
     if (bwd) {
       const int pg = Parts(s, sm_count()).pg;
       const size_t part = pg == 1 ? 0 : (size_t)s.B * s.N * s.G * pg * s.D * 4;
       pr = end;
       sr = pr + st * 4;
-      pB = sr + st * 2;
-      pC = pB + part;
-      pp = pC + part;
-      end = pp + align16(n * 12);
+      pB = align_line(sr + st * 2);
+      pC = align_line(pB + part);
+      pp = align_line(pC + part);
+      end = pp + align_line(n * 12);
     }
   }
 };
@@ -988,11 +998,11 @@ cudaError_t launch_whole(void (*kernel)(Exp...), dim3 grid, dim3 block, size_t s
     if (e_ != cudaSuccess) return e_;      \
   } while (0)
 
-size_t scan_tc_ws_bytes(const ScanShape& s, bool bwd) { return WsTC(s, bwd).end; }
+size_t scan_tc_ws_bytes(const ScanShape& s, bool bwd) { return WsTC(s, bwd).end + LINE; }
 
 cudaError_t scan_fwd_tc(const ScanIn& a, float* S, void* y, void* ws, const ScanShape& s, cudaStream_t st) {
   const WsTC w(s, false);
-  char* base = static_cast<char*>(ws);
+  char* base = first_line(ws);
   float *tot = (float*)(base + w.tot), *pf = (float*)(base + w.pf);
   bf16* sf = (bf16*)(base + w.sf);
   const int nch = chunks(s);
@@ -1023,7 +1033,7 @@ cudaError_t scan_fwd_tc(const ScanIn& a, float* S, void* y, void* ws, const Scan
 
 cudaError_t scan_bwd_tc(const ScanIn& a, const void* dy, const ScanGrads& d, void* ws, const ScanShape& s, cudaStream_t st) {
   const WsTC w(s, true);
-  char* base = static_cast<char*>(ws);
+  char* base = first_line(ws);
   float *tot = (float*)(base + w.tot), *pf = (float*)(base + w.pf), *pr = (float*)(base + w.pr), *pp = (float*)(base + w.pp);
   bf16 *sf = (bf16*)(base + w.sf), *sr = (bf16*)(base + w.sr);
   const int nch = chunks(s);
