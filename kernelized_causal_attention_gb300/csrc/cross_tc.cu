@@ -12,9 +12,10 @@
 // and k_cross_join (cross.cu) between them.  All are bound by HBM traffic: the
 // products are a few hundred cycles a tile.
 //
-// What is not a bf16 input (phi, S, R) enters its products as two bf16 terms,
-// a = a0 + a1 to 2^-16, taking a0 b0 + a0 b1 + a1 b0: S stays accurate to fp32
-// tolerances and each bf16 result is rounded once.  Z and den are plain fp32 sums.
+// What is not a bf16 input (phi, S, R) enters its products as bf16 terms: three
+// (2^-24) where the sum is an fp32 output (S), elsewhere two, a = a0 + a1 to
+// 2^-16, taking a0 b0 + a0 b1 + a1 b0, so that each bf16 result is rounded once.
+// Z and den are plain fp32 sums.
 #include "launch.h"
 #include "scan.cuh"
 #include "tc.cuh"
@@ -51,21 +52,27 @@ __device__ __forceinline__ float phif(float x) {
 
 __device__ __forceinline__ void sync_compute() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-// Thirty-two floats as two bf16 terms into columns [col0, col0 + 32) of row r
-// of two swizzled tiles.
+// Thirty-two floats as bf16 terms into columns [col0, col0 + 32) of row r of
+// swizzled tiles: the first at `hi`, the others at `lo` and a tile further.
+template <int TERMS = 2>
 __device__ __forceinline__ void put_terms(uint8_t* hi, uint8_t* lo, int r, int col0, const float* f) {
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     const int o = r * 128 + ((((col0 >> 3) + c) ^ (r & 7)) << 4);
-    uint32_t h[4], l[4];
+    uint32_t t[TERMS][4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float a = f[8 * c + 2 * k], b = f[8 * c + 2 * k + 1];
-      h[k] = pack_bf16(a, b);
-      l[k] = pack_bf16(a - __uint_as_float(h[k] << 16), b - __uint_as_float(h[k] & 0xffff0000u));
+      float a = f[8 * c + 2 * k], b = f[8 * c + 2 * k + 1];
+#pragma unroll
+      for (int j = 0; j < TERMS; ++j) {
+        t[j][k] = pack_bf16(a, b);
+        a -= __uint_as_float(t[j][k] << 16);
+        b -= __uint_as_float(t[j][k] & 0xffff0000u);
+      }
     }
-    sts128(hi + o, make_uint4(h[0], h[1], h[2], h[3]));
-    sts128(lo + o, make_uint4(l[0], l[1], l[2], l[3]));
+    sts128(hi + o, make_uint4(t[0][0], t[0][1], t[0][2], t[0][3]));
+#pragma unroll
+    for (int j = 1; j < TERMS; ++j) sts128(lo + (j - 1) * TILE + o, make_uint4(t[j][0], t[j][1], t[j][2], t[j][3]));
   }
 }
 
@@ -109,10 +116,18 @@ __device__ __forceinline__ float column_sums(float (&g)[32], int lane) {  // ove
   return g[0];
 }
 
-// The 64 x 64 accumulator at column `ta` (M = 64 layout) to [D][M] floats at o.
+// The 64 x 64 accumulator at column `ta` (M = 64 layout), and the one behind it if
+// TWO, to [D][M] floats at o.
+template <bool TWO = false>
 __device__ __forceinline__ void store_state(uint32_t ta, float* o, int D, int M, int qd, int wg, int lane) {
   float f[32];
   tmem_ldn<2>(ta + (static_cast<uint32_t>(32 * qd) << 16) + 32 * wg, f);
+  if (TWO) {
+    float g[32];
+    tmem_ldn<2>(ta + 64 + (static_cast<uint32_t>(32 * qd) << 16) + 32 * wg, g);
+#pragma unroll
+    for (int c = 0; c < 32; ++c) f[c] += g[c];
+  }
   const int d = 16 * qd + lane;
   if (lane < 16 && d < D) {
 #pragma unroll
@@ -136,8 +151,9 @@ __device__ __forceinline__ void mma_terms(uint32_t d, uint32_t a0, uint32_t a1, 
 }
 
 // --------------------------------------------------------------- S and Z
-constexpr int K_STAGE = 3 * TILE;  // k (then phi's first term), v, phi's second term
-constexpr int K_SMEM = 2 * K_STAGE + 1024;
+constexpr int K_STAGE = 2 * TILE;  // k (then phi's first term), v
+constexpr int K_T = 2 * K_STAGE;   // phi's second and third terms
+constexpr int K_SMEM = K_T + 2 * TILE + 1024;
 
 __global__ void __launch_bounds__(NT, 2)
     k_ksum(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const int* __restrict__ lengths,
@@ -160,7 +176,7 @@ __global__ void __launch_bounds__(NT, 2)
     fence_barrier_init();
     s_abort = 0;
   }
-  if (warp == W_ISSUE) tmem_alloc(&tmem_base, 64);
+  if (warp == W_ISSUE) tmem_alloc(&tmem_base, 128);
   grid_dep_wait();
   const int L = valid_rows(lengths, bh / Hk, N);
   const int t0 = blockIdx.x * per, nt = min(per, (L + TC_C - 1) / TC_C - t0);
@@ -191,10 +207,10 @@ __global__ void __launch_bounds__(NT, 2)
         if (!wt(&bar_t[k], (i >> 1) & 1, 111)) break;
         tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {  // the two terms of phi(k)
-          const uint64_t da = sdesc(st + 2 * j * TILE, 16, 1024), db = sdesc(v, 16, 1024);
+        for (int j = 0; j < 3; ++j) {  // the terms of phi(k), the first in an accumulator of its own (fewer roundings of the large sum)
+          const uint64_t da = sdesc(j == 0 ? st : smem_u32(sm + K_T + (j - 1) * TILE), 16, 1024), db = sdesc(v, 16, 1024);
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk) mma_bf16(tm, dadd(da, kk * 2048), dadd(db, kk * 2048), ID, i > 0 || j > 0 || kk > 0);
+          for (int kk = 0; kk < 8; ++kk) mma_bf16(tm + (j > 0 ? 64 : 0), dadd(da, kk * 2048), dadd(db, kk * 2048), ID, i > 0 || j > 1 || kk > 0);
         }
         mma_commit(&bar_m[k]);
         if (i + 2 < nt) {
@@ -218,6 +234,7 @@ __global__ void __launch_bounds__(NT, 2)
         float x[32], f[32];
         tile_row_cols<32>(st, row, 32 * wg, x);
         phi_cols(x, f, 32 * wg, D);
+        if (i > 0) wtu(&bar_m[k ^ 1], ((i - 1) >> 1) & 1, 115);  // the second and third terms have been read
         if (row >= valid) {
 #pragma unroll
           for (int c = 0; c < 32; ++c) f[c] = 0.f;
@@ -227,14 +244,14 @@ __global__ void __launch_bounds__(NT, 2)
         }
 #pragma unroll
         for (int c = 0; c < 32; ++c) z[c] += f[c];
-        put_terms(st, st + 2 * TILE, row, 32 * wg, f);
+        put_terms<3>(st, sm + K_T, row, 32 * wg, f);
       }
       fence_proxy_async();
       mbar_arrive(&bar_t[k]);
     }
     if (wtu(&bar_m[(nt - 1) & 1], ((nt - 1) >> 1) & 1, 114)) {
       tc_fence_after();
-      store_state(tm, o, D, M, qd, wg, lane);
+      store_state<true>(tm, o, D, M, qd, wg, lane);
     }
     tc_fence_before();
     s_z[qd][32 * wg + lane] = column_sums(z, lane);
@@ -243,7 +260,7 @@ __global__ void __launch_bounds__(NT, 2)
   }
   __syncthreads();
   tc_fence_after();
-  if (warp == W_ISSUE) tmem_dealloc(tm, 64);
+  if (warp == W_ISSUE) tmem_dealloc(tm, 128);
 }
 
 // ------------------------------------------------------------------- read

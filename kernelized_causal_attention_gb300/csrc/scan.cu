@@ -31,13 +31,24 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
+// The log decays' prefix sums of a chunk in two floats (their difference is what
+// an exponential magnifies: in one float it cost 6e-7 in y).
+struct Cum {
+  float hi[64], lo[64];
+  __device__ __forceinline__ float decay(int i, int j) const { return expf((hi[i] - hi[j]) + (lo[i] - lo[j])); }  // j to i
+  __device__ __forceinline__ float from_start(int i) const { return expf(hi[i]) * (1.f + lo[i]); }
+  __device__ __forceinline__ float to_end(int j) const { return decay(63, j); }
+};
+
 // delta, cum and the raw gate's argument of a chunk's 64 rows (rows at or past
 // `rows`: delta 0, cum carried on).  Threads 0 .. 63; all must call.
 template <typename T>
-__device__ __forceinline__ void gates(const T* dt, long lddt, int rows, float bias, float A, float* delta, float* cum, float* z) {
+__device__ __forceinline__ void gates(const T* dt, long lddt, int rows, float bias, float A, float* delta, Cum& cum, float* z) {
+  __shared__ double first;
   const int t = threadIdx.x;
-  float d = 0.f, c = 0.f;
+  double c = 0;
   if (t < 64) {
+    float d = 0.f;
     if (t < rows) {
       const float x = to_f(dt[t * lddt]) + bias;
       if (z != nullptr) z[t] = x;
@@ -46,11 +57,15 @@ __device__ __forceinline__ void gates(const T* dt, long lddt, int rows, float bi
       z[t] = 0.f;
     }
     delta[t] = d;
-    c = warp_prefix(d * A);
-    cum[t] = c;
+    c = warp_prefix((double)d * (double)A);
+    if (t == 31) first = c;
   }
   __syncthreads();
-  if (t >= 32 && t < 64) cum[t] = c + cum[31];
+  if (t < 64) {
+    if (t >= 32) c += first;
+    cum.hi[t] = (float)c;
+    cum.lo[t] = (float)(c - (double)(float)c);
+  }
   __syncthreads();
 }
 
@@ -67,14 +82,14 @@ __global__ void __launch_bounds__(256)
   extern __shared__ float sm[];
   float* tb = sm;                  // [64][D + 4]
   float* tx = tb + 64 * (D + 4);   // [64][M + 4]
-  __shared__ float delta[64], cum[64];
+  __shared__ float delta[64];
+  __shared__ Cum cum;
   const int c = blockIdx.x, bh = blockIdx.y, b = bh / s.H, h = bh % s.H, g = h / (s.H / s.G);
   const int n0 = c * FT, nch = gridDim.x;
   const int rows = max(0, min(FT, valid_rows(lengths, b, s.N) - n0));
   const long r0 = (long)b * s.N + n0;
   gates(dt + r0 * s.lddt + h, s.lddt, rows, par(bias, h), par(A, h), delta, cum, (float*)nullptr);
-  const float end = cum[63];
-  if (threadIdx.x == 0) tot[(long)bh * nch + c] = end;
+  if (threadIdx.x == 0) tot[(long)bh * nch + c] = cum.hi[63];
   const int tx0 = (threadIdx.x & 15) * (M / 16), ty0 = (threadIdx.x >> 4) * (D / 16);
   for (int dir = 0; dir < (rev == nullptr ? 1 : 2); ++dir) {
     stage<T, D>((dir ? Cm + r0 * s.ldc : Bm + r0 * s.ldb) + g * D, dir ? s.ldc : s.ldb, rows, tb, D + 4, nullptr);
@@ -82,7 +97,7 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     for (int e = threadIdx.x; e < FT * M; e += 256) {
       const int r = e / M;
-      tx[r * (M + 4) + e % M] *= dir ? expf(cum[r]) : delta[r] * expf(end - cum[r]);
+      tx[r * (M + 4) + e % M] *= dir ? cum.from_start(r) : delta[r] * cum.to_end(r);
     }
     __syncthreads();
     float acc[D / 16][M / 16];
@@ -98,6 +113,7 @@ __global__ void __launch_bounds__(256)
 }
 
 __device__ __forceinline__ void put4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ float rest(float v) { return v - __bfloat162float(__float2bfloat16_rn(v)); }
 __device__ __forceinline__ void put4(bf16* p, float4 v) {
   const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
   *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
@@ -105,10 +121,10 @@ __device__ __forceinline__ void put4(bf16* p, float4 v) {
 
 // One thread's chunks c0, c0 + dc, ... (n of them), four values of the state:
 // run <- exp(tot) run + p[c], and before that out[c] = run where out is wanted
-// (it may be p's own memory).  A chain of one fused multiply-add a chunk; the
+// (it may be p's own memory) and low[c] = what its rounding to bf16 left.  A chain of one fused multiply-add a chunk; the
 // loads run eight chunks ahead of it.
 template <typename O>
-__device__ __forceinline__ void carry_walk(const float* p, O* out, const float* tot, long step, int c0, int dc, int n, float4& run) {
+__device__ __forceinline__ void carry_walk(const float* p, O* out, O* low, const float* tot, long step, int c0, int dc, int n, float4& run) {
   constexpr int U = 8;
   for (int k0 = 0; k0 < n; k0 += U) {
     float4 v[U];
@@ -124,6 +140,7 @@ __device__ __forceinline__ void carry_walk(const float* p, O* out, const float* 
     for (int i = 0; i < U; ++i)
       if (k0 + i < n) {
         if (out != nullptr) put4(out + (c0 + (k0 + i) * dc) * step, run);
+        if (low != nullptr) put4(low + (c0 + (k0 + i) * dc) * step, make_float4(rest(run.x), rest(run.y), rest(run.z), rest(run.w)));
         run.x = fmaf(e[i], run.x, v[i].x);
         run.y = fmaf(e[i], run.y, v[i].y);
         run.z = fmaf(e[i], run.z, v[i].z);
@@ -142,7 +159,7 @@ __device__ __forceinline__ void carry_walk(const float* p, O* out, const float* 
 constexpr int CARRY_SEGS = 16;
 template <typename O>
 __global__ void __launch_bounds__(32 * CARRY_SEGS)
-    k_scan_carry(const float* fwd, const float* rev, O* fs, O* rs, const float* __restrict__ tot, float* __restrict__ S,
+    k_scan_carry(const float* fwd, const float* rev, O* fs, O* rs, O* fl, O* rl, const float* __restrict__ tot, float* __restrict__ S,
                  int nch, int DM, int per) {
   grid_dep_enter();
   __shared__ float4 ends[CARRY_SEGS][32];
@@ -151,12 +168,12 @@ __global__ void __launch_bounds__(32 * CARRY_SEGS)
   const long bh = blockIdx.y, at = bh * nch * DM + e;
   const bool back = blockIdx.z != 0, live = e < DM;
   const float* p = (back ? rev : fwd) + at;
-  O* out = (back ? rs : fs) + at;
+  O *out = (back ? rs : fs) + at, *low = fl == nullptr ? nullptr : (back ? rl : fl) + at;
   const float* tt = tot + bh * nch;
   const int first = seg * per, n = min(per, nch - first), c0 = back ? nch - 1 - first : first, dc = back ? -1 : 1;
   float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
   if (segs > 1) {
-    if (live) carry_walk(p, static_cast<O*>(nullptr), tt, DM, c0, dc, n, run);
+    if (live) carry_walk(p, static_cast<O*>(nullptr), static_cast<O*>(nullptr), tt, DM, c0, dc, n, run);
     ends[seg][threadIdx.x] = run;
     float l = 0.f;
     for (int k = threadIdx.x; k < n; k += 32) l += tt[c0 + k * dc];
@@ -173,7 +190,7 @@ __global__ void __launch_bounds__(32 * CARRY_SEGS)
     const float4 u = ends[k][threadIdx.x];
     run.x = fmaf(f, run.x, u.x), run.y = fmaf(f, run.y, u.y), run.z = fmaf(f, run.z, u.z), run.w = fmaf(f, run.w, u.w);
   }
-  carry_walk(p, out, tt, DM, c0, dc, n, run);
+  carry_walk(p, out, low, tt, DM, c0, dc, n, run);
   if (Sp != nullptr && seg == segs - 1) *reinterpret_cast<float4*>(Sp) = run;
 }
 
@@ -190,7 +207,8 @@ __global__ void __launch_bounds__(256)
   float* xs = bt + D * FLD;         // x   [64][M + 4]
   float* ss = xs + 64 * (M + 4);    // S_prev [D][M + 4]
   float* pt = ss + D * (M + 4);     // P^T [64][FLD]
-  __shared__ float delta[64], cum[64];
+  __shared__ float delta[64];
+  __shared__ Cum cum;
   const int c = blockIdx.x, bh = blockIdx.y, b = bh / s.H, h = bh % s.H, g = h / (s.H / s.G);
   const int n0 = c * FT, nch = gridDim.x;
   const int rows = max(0, min(FT, valid_rows(lengths, b, s.N) - n0));
@@ -210,7 +228,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int i = i0 + r, j = j0 + q;
-        pt[j * FLD + i] = j <= i ? a[r][q] * delta[j] * expf(cum[i] - cum[j]) : 0.f;
+        pt[j * FLD + i] = j <= i ? a[r][q] * delta[j] * cum.decay(i, j) : 0.f;
       }
   }
   __syncthreads();
@@ -221,7 +239,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int q = 0; q < M / 16; ++q) acc[r][q] *= expf(cum[i0 + r]);
+      for (int q = 0; q < M / 16; ++q) acc[r][q] *= cum.from_start(i0 + r);
   }
   ffma_mm(acc, pt, FLD, xs, M + 4, FT);
   const float sk = par(skip, h);
@@ -259,7 +277,9 @@ __global__ void __launch_bounds__(256)
   float* rn = sm + 9 * TS;      // R
   float* rt = sm + 10 * TS;     // R^T
   float* st = sm + 11 * TS;     // S_prev^T
-  __shared__ float delta[64], cum[64], z[64], rowg[64], v[64], w[64], xdu[64], colg[16][64], red[8];
+  __shared__ Cum cum;
+  __shared__ float delta[64], z[64], v[64], w[64], xdu[64], red[8];
+  __shared__ double rowg[64], colg[16][64];
   const int c = blockIdx.x, bh = blockIdx.y, b = bh / s.H, h = bh % s.H, g = h / (s.H / s.G);
   const int n0 = c * FT, nch = gridDim.x;
   const int rows = max(0, min(FT, valid_rows(lengths, b, s.N) - n0));
@@ -276,7 +296,6 @@ __global__ void __launch_bounds__(256)
   for (int e = threadIdx.x; e < D * M; e += 256) sr = fmaf(Sp[e], Rp[e], sr);
   const float Ah = par(A, h), sk = par(skip, h);
   gates(dt + r0 * s.lddt + h, s.lddt, rows, par(bias, h), Ah, delta, cum, z);
-  const float end = cum[63];
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15, i0 = ty * 4, j0 = tx * 4;
   {
     float a[4][4], e[4][4];
@@ -285,26 +304,28 @@ __global__ void __launch_bounds__(256)
     ffma_mm(a, ct, FLD, bt, FLD, D);
     ffma_mm(e, gt, FLD, xt, FLD, M);
     __syncthreads();  // C^T has been read: Q^T takes its place
-    float rs[4] = {0.f, 0.f, 0.f, 0.f}, cs[4] = {0.f, 0.f, 0.f, 0.f};
+    // Row and column sums of the same G are subtracted below: in 64 bits what they
+    // share cancels exactly, in 32 it left 3e-6 in dA
+    double rs[4] = {0, 0, 0, 0}, cs[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int i = i0 + r, j = j0 + q;
-        const float wt = j <= i ? expf(cum[i] - cum[j]) : 0.f;
+        const float wt = j <= i ? cum.decay(i, j) : 0.f;
         const float p = wt * a[r][q], qq = wt * delta[j] * e[r][q];
         pn[i * FLD + j] = p;
         qn[i * FLD + j] = qq;
         ct[j * FLD + i] = qq;
         if (j < i) {  // a pair with itself feels no decay
-          const float gg = qq * a[r][q];
+          const double gg = qq * a[r][q];
           rs[r] += gg;
           cs[q] += gg;
         }
       }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float t = row_sum(rs[r]);
+      const double t = row_sum(rs[r]);
       if (tx == 0) rowg[i0 + r] = t;
     }
 #pragma unroll
@@ -321,7 +342,7 @@ __global__ void __launch_bounds__(256)
     ffma_mm(acc, gt, FLD, st, D + 4, M);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float f = expf(cum[i0 + r]);
+      const float f = cum.from_start(i0 + r);
       float t = 0.f;
 #pragma unroll
       for (int q = 0; q < CC; ++q) {
@@ -340,7 +361,7 @@ __global__ void __launch_bounds__(256)
     ffma_mm(acc, xt, FLD, rt, D + 4, M);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float f = delta[i0 + r] * expf(end - cum[i0 + r]);
+      const float f = delta[i0 + r] * cum.to_end(i0 + r);
       float t = 0.f;
 #pragma unroll
       for (int q = 0; q < CC; ++q) {
@@ -366,7 +387,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int q = 0; q < CC; ++q) acc[r][q] *= expf(end - cum[i0 + r]);
+      for (int q = 0; q < CC; ++q) acc[r][q] *= cum.to_end(i0 + r);
     ffma_mm(acc, pn, FLD, gn, M + 4, FT);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -386,18 +407,24 @@ __global__ void __launch_bounds__(256)
   }
   sr = block_sum(sr, red);
   dskip = block_sum(dskip, red);
+  if (threadIdx.x < 64) {
+    double cg = 0;
+#pragma unroll
+    for (int q = 0; q < 16; ++q) cg += colg[q][threadIdx.x];
+    rowg[threadIdx.x] -= cg;
+  }
   __syncthreads();
   float dA = 0.f, db = 0.f;
   const int t = threadIdx.x;
   if (t < 64) {
-    float dl = expf(end) * sr;
+    double pairs = 0;
+    float dl = cum.from_start(63) * sr;
     for (int i = t; i < 64; ++i) {
-      float cg = 0.f;
-#pragma unroll
-      for (int q = 0; q < 16; ++q) cg += colg[q][i];
-      dl += rowg[i] - cg + v[i];
+      pairs += rowg[i];
+      dl += v[i];
     }
     for (int j = 0; j < t; ++j) dl += w[j];
+    dl += (float)pairs;
     const float dd = xdu[t] + Ah * dl;
     const float dz = t < rows ? dd / (1.f + expf(-z[t])) : 0.f;
     if (n0 + t < s.N) ddt[(r0 + t) * s.H + h] = from_f<T>(dz);
@@ -545,20 +572,21 @@ struct WsCC {
 size_t scan_cc_ws_bytes(const ScanShape& s, bool bwd) { return WsCC(s, bwd).end; }
 
 template <typename O>
-static cudaError_t carry(const float* fwd, const float* rev, O* fs, O* rs, const float* tot, float* S, int BH, int nch, int DM,
+static cudaError_t carry(const float* fwd, const float* rev, O* fs, O* rs, O* fl, O* rl, const float* tot, float* S, int BH, int nch, int DM,
                          cudaStream_t st) {
   const int segs = nch <= 64 ? 1 : CARRY_SEGS, per = (nch + segs - 1) / segs, cols = segs == 1 ? 128 : 32;
   const dim3 grid((DM / 4 + cols - 1) / cols, BH, rev == nullptr ? 1 : 2), block(cols, (nch + per - 1) / per);
-  return launch_pdl(k_scan_carry<O>, grid, block, 0, st, fwd, rev, fs, rs, tot, S, nch, DM, per);
+  return launch_pdl(k_scan_carry<O>, grid, block, 0, st, fwd, rev, fs, rs, fl, rl, tot, S, nch, DM, per);
 }
 
 cudaError_t scan_carry(float* fwd, float* rev, const float* tot, float* S, int BH, int nch, int DM, cudaStream_t st) {
-  return carry(fwd, rev, fwd, rev, tot, S, BH, nch, DM, st);
+  float* none = nullptr;
+  return carry(fwd, rev, fwd, rev, none, none, tot, S, BH, nch, DM, st);
 }
 
-cudaError_t scan_carry_bf16(const float* fwd, const float* rev, void* fs, void* rs, const float* tot, float* S, int BH,
-                            int nch, int DM, cudaStream_t st) {
-  return carry(fwd, rev, (bf16*)fs, (bf16*)rs, tot, S, BH, nch, DM, st);
+cudaError_t scan_carry_bf16(const float* fwd, const float* rev, void* fs, void* rs, void* fl, void* rl, const float* tot,
+                            float* S, int BH, int nch, int DM, cudaStream_t st) {
+  return carry(fwd, rev, (bf16*)fs, (bf16*)rs, (bf16*)fl, (bf16*)rl, tot, S, BH, nch, DM, st);
 }
 
 cudaError_t scan_params(const float* pp, void* dA, void* dskip, void* dbias, const ScanShape& s, int nch, cudaStream_t st) {

@@ -27,11 +27,12 @@ template <typename T>
 __device__ __forceinline__ float par(const T* p, int h) { return p == nullptr ? 0.f : to_f(p[h]); }
 
 // Inclusive prefix sum over a warp.
-__device__ __forceinline__ float warp_prefix(float v) {
+template <typename F>
+__device__ __forceinline__ F warp_prefix(F v) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const float u = __shfl_up_sync(0xffffffffu, v, o);
+    const F u = __shfl_up_sync(0xffffffffu, v, o);
     if (lane >= o) v += u;
   }
   return v;
@@ -42,9 +43,10 @@ __device__ __forceinline__ float warp_prefix(float v) {
 // chunk c and rev[c] the state gradient after it; S, if given, is the state to
 // start from and becomes the last one.
 cudaError_t scan_carry(float* fwd, float* rev, const float* tot, float* S, int BH, int nch, int DM, cudaStream_t st);
-// The same, with the carried states rounded to bf16 into fs (and rs).
-cudaError_t scan_carry_bf16(const float* fwd, const float* rev, void* fs, void* rs, const float* tot, float* S, int BH,
-                            int nch, int DM, cudaStream_t st);
+// The same, with the carried states rounded to bf16 into fs (and rs), and what
+// that left, rounded, into fl and rl if given.
+cudaError_t scan_carry_bf16(const float* fwd, const float* rev, void* fs, void* rs, void* fl, void* rl, const float* tot,
+                            float* S, int BH, int nch, int DM, cudaStream_t st);
 
 // Sums the per-chunk parameter gradients pp[BH][nch][3] (A, skip, dt_bias) over
 // the batch and the chunks, in a fixed order.

@@ -129,13 +129,13 @@ __device__ __forceinline__ void leave(uint32_t tm, uint32_t cols, int issuer) {
 struct Maps {
   CUtensorMap x, B, C, g;  // g: dy
   CUtensorMap o;           // y, or dx
-  CUtensorMap S, R;        // the carried states
+  CUtensorMap S, R, Sl, Rl;  // the carried states, and what rounding them left
 };
 
 // ------------------------------------------------------------- chunk sums
 // TERMS bf16 terms of the scaled operand: three where the state after the last
-// row is wanted (an fp32 output: 2^-24), two for the states that the outputs
-// read in bf16, one for those of the bf16 gradients.  The first term takes x's
+// row is wanted (an fp32 output: 2^-24), two for the states that products read
+// in bf16 (one term would round them twice).  The first term takes x's
 // place in shared memory and the third adds to the second's columns, so three
 // blocks share an SM: one's load, another's conversion and a third's products
 // overlap, and a head's own chain need not.  blockIdx.y = part, or parts + part
@@ -155,7 +155,7 @@ __global__ void __launch_bounds__(NT, 3)
   __shared__ Params par_[MAXH];
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
-  constexpr int COLS = TERMS > 1 ? 128 : 64;
+  constexpr int COLS = 128;
   const int parts = s.G * pg;
   const bool back = blockIdx.y >= parts;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nch = gridDim.x;
@@ -277,12 +277,10 @@ __global__ void __launch_bounds__(NT, 3)
         for (int j = 0; j < 2; ++j) {
           float p[16], r[16];
           tmem_ld16(tm + lq + 32 * half + 16 * j, p);
-          if (TERMS > 1) tmem_ld16(tm + lq + 64 + 32 * half + 16 * j, r);
+          tmem_ld16(tm + lq + 64 + 32 * half + 16 * j, r);
           tmem_ld_wait();
-          if (TERMS > 1) {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) p[c] += r[c];
-          }
+          for (int c = 0; c < 16; ++c) p[c] += r[c];
           const int c0 = 32 * half + 16 * j;
           if (lane < 16 && srow < s.D && c0 < s.M) {
             float* o = out + (long)i * nch * DM + srow * s.M + c0;
@@ -499,6 +497,10 @@ __global__ void __launch_bounds__(NT, 2)
 //   A^T = B C^T, E^T = x dy^T;  P_ij = W_ij A_ij, Q_ij = W_ij delta_j E_ij
 //   du = P^T dy + f_j (B R),        f_j = exp(cum_end - cum_j)
 //   dB += Q^T C + delta_j f_j (x R^T),  dC += Q B + exp(cum_i) (dy S^T)
+// The carried states enter in two bf16 terms, so that what the gate's gradient is
+// summed from (pair sums, x . (B R), C . (S dy), <S, R>) is accurate to 2^-16 and
+// its sums over all rows, dA and ddt_bias, keep their digits where they cancel;
+// x . du is the pair sum and x . (B R), without the rounded P of dx.
 // dB and dC are summed over the block's heads in registers (fp32); a group's
 // blocks leave fp32 partial sums that scan_groups adds up (one block: the
 // gradients themselves).  The gate's gradient takes its pair sums G_ij =
@@ -507,12 +509,13 @@ __global__ void __launch_bounds__(NT, 2)
 //
 // Sixteen compute warps, one 32 x 32 score block each (warp mod 4 is the lane
 // quarter it can reach, warp / 4 the block's column), on one block an SM (all
-// 512 tensor-memory columns, 161 KB of tiles).  The next head's gates and the
+// 512 tensor-memory columns, 193 KB of tiles).  The next head's gates and the
 // last head's gate gradient are formed beside the products, the latter by the
 // warps that the masked triangle leaves idle.  Bound by the per-head chain and by
 // instruction issue, not by a unit's rate.
 constexpr int GT = 512, NTG = GT + 32, WG_ISSUE = GT / 32;
-constexpr int G_C = 0, G_B = TILE, G_X = 2 * TILE, G_Y = 4 * TILE, G_S = 6 * TILE, G_R = G_S + 2 * STILE, G_Q = G_R + 2 * STILE;
+constexpr int G_C = 0, G_B = TILE, G_X = 2 * TILE, G_Y = 4 * TILE, G_S = 6 * TILE, G_R = G_S + 4 * STILE, G_Q = G_R + 4 * STILE;
+// (a stage of S or R is two tiles, its terms)
 constexpr int G_SMEM = G_Q + 2 * TILE + 1024;
 constexpr uint32_t TG_A = 0, TG_E = 128, TG_U = 256, TG_BR = 320, TG_B = 384, TG_C = 448;
 
@@ -552,7 +555,7 @@ __device__ __forceinline__ float warp_suffix(float v) {  // inclusive, from the 
 // What the gate's gradient of a head is summed from, by row (and by the column
 // group that formed it).
 struct GateSums {
-  float row[4][128], col[4][128], v[4][128], w[4][128], u[4][128], red[16][2];
+  float row[4][128], col[4][128], self[128], v[4][128], w[4][128], red[16][2];
 };
 
 __global__ void __launch_bounds__(NTG, 1)
@@ -619,11 +622,14 @@ __global__ void __launch_bounds__(NTG, 1)
       int issued = 0;
       auto load = [&](int i) {
         const int k = i & 1, h = w.h0 + i;
-        mbar_arrive_expect_tx(&bar_in[k], 2 * TILE + 2 * STILE);
+        mbar_arrive_expect_tx(&bar_in[k], 2 * TILE + 4 * STILE);
         tma_load_4d(sm + G_X + k * TILE, &maps.x, &bar_in[k], 0, h, w.n0, w.b);
         tma_load_4d(sm + G_Y + k * TILE, &maps.g, &bar_in[k], 0, h, w.n0, w.b);
-        tma_load_3d(sm + G_S + k * STILE, &maps.S, &bar_in[k], 0, 0, (w.b * s.H + h) * nch + blockIdx.x);
-        tma_load_3d(sm + G_R + k * STILE, &maps.R, &bar_in[k], 0, 0, (w.b * s.H + h) * nch + blockIdx.x);
+        const int at = (w.b * s.H + h) * nch + blockIdx.x;
+        tma_load_3d(sm + G_S + 2 * k * STILE, &maps.S, &bar_in[k], 0, 0, at);
+        tma_load_3d(sm + G_S + (2 * k + 1) * STILE, &maps.Sl, &bar_in[k], 0, 0, at);
+        tma_load_3d(sm + G_R + 2 * k * STILE, &maps.R, &bar_in[k], 0, 0, at);
+        tma_load_3d(sm + G_R + (2 * k + 1) * STILE, &maps.Rl, &bar_in[k], 0, 0, at);
         ++issued;
       };
       load(0);
@@ -636,7 +642,7 @@ __global__ void __launch_bounds__(NTG, 1)
       for (int i = 0; ok && i < w.nh; ++i) {
         const int k = i & 1;
         const uint64_t dX = sdesc(smem_u32(sm + G_X + k * TILE), 16, 1024), dY = sdesc(smem_u32(sm + G_Y + k * TILE), 16, 1024);
-        const uint64_t dS = sdesc(smem_u32(sm + G_S + k * STILE), 16, 1024), dR = sdesc(smem_u32(sm + G_R + k * STILE), 16, 1024);
+        const uint64_t dS = sdesc(smem_u32(sm + G_S + 2 * k * STILE), 16, 1024), dR = sdesc(smem_u32(sm + G_R + 2 * k * STILE), 16, 1024);
         if (!(ok = wt(&bar_in[k], (i >> 1) & 1, 82) && (!cut || wt(&bar_clear, k, 83)))) break;
         tc_fence_after();
 #pragma unroll
@@ -647,11 +653,13 @@ __global__ void __launch_bounds__(NTG, 1)
         if (i > 0 && !(ok = wt(&bar_free, (i - 1) & 1, 84))) break;  // the last head's accumulators have been read
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_bf16(tm + TG_B, dadd(dX, 32 * kk), dadd(dR, 32 * kk), ID_KK, kk > 0);
+        for (int j = 0; j < 2; ++j)  // either term of the states
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_bf16(tm + TG_C, dadd(dY, 32 * kk), dadd(dS, 32 * kk), ID_KK, kk > 0);
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) mma_bf16(tm + TG_BR, dadd(dBt, 32 * kk), dadd(dR, kk * 2048), ID_KM, kk > 0);
+          for (int kk = 0; kk < 4; ++kk) {
+            mma_bf16(tm + TG_B, dadd(dX, 32 * kk), dadd(dR, j * STILE + 32 * kk), ID_KK, j > 0 || kk > 0);
+            mma_bf16(tm + TG_C, dadd(dY, 32 * kk), dadd(dS, j * STILE + 32 * kk), ID_KK, j > 0 || kk > 0);
+            mma_bf16(tm + TG_BR, dadd(dBt, 32 * kk), dadd(dR, j * STILE + kk * 2048), ID_KM, j > 0 || kk > 0);
+          }
         mma_commit(&bar_2);
         if (!(ok = wt(&bar_p, k, 85))) break;
         tc_fence_after();
@@ -701,13 +709,16 @@ __global__ void __launch_bounds__(NTG, 1)
       const GateSums& gs = sums[i & 1];
       const int t = 32 * gw + lane;
       const float del = g.del[t];
-      float q = 0.f, ww = 0.f, xu = 0.f;
+      float q = 0.f, ww = 0.f, col = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        q += gs.v[j][t] - gs.col[j][t] + gs.row[j][t];
-        ww += gs.w[j][t];
-        xu += gs.u[j][t];
+        q += gs.v[j][t] + gs.row[j][t];
+        ww += gs.w[j][t];  // x_j . (B_j R) f_j
+        col += gs.col[j][t];
       }
+      q -= del * col;
+      const float xu = col + gs.self[t] + ww;  // x_j . du_j: no rounded P in it
+      ww *= del;
       const float sr = warp_sum(lane < 16 ? gs.red[lane][0] : 0.f);
       const float suf = warp_suffix(q), pre = warp_prefix(ww);
       if (lane == 0) s_tot[gw][0] = suf;
@@ -764,8 +775,8 @@ __global__ void __launch_bounds__(NTG, 1)
         tc_fence_after();
         const uint32_t ta = tm + TG_A + 32 * I + lq, te = tm + TG_E + 32 * I + lq;
         uint8_t* qt = sm + G_Q + (I >> 1) * TILE + row * 128;
-        const float fr = I > qd ? tail * ex2_fast(g.off(I) - g.off(qd + 1)) : 0.f, frd = fr * del;
-        float col = 0.f;
+        const float fr = I > qd ? tail * ex2_fast(g.off(I) - g.off(qd + 1)) : 0.f;
+        float col = 0.f, self = 0.f;  // sums over this key's pairs, without delta
 #pragma unroll
         for (int o = 0; o < 4; ++o) {  // eight queries at a time
           uint32_t pw[4], qw[4];
@@ -783,9 +794,11 @@ __global__ void __launch_bounds__(NTG, 1)
             if (I > qd) {
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
-                e[c] *= tv[c] * frd;
+                const float wt_ = tv[c] * fr;
+                e[c] *= wt_;
                 gg[c] = e[c] * a[c];
-                a[c] *= tv[c] * fr;
+                e[c] *= del;
+                a[c] *= wt_;
               }
             } else {
               // (the exponential of a masked pair is dropped by a select: branches around
@@ -794,8 +807,13 @@ __global__ void __launch_bounds__(NTG, 1)
               for (int c = 0; c < 8; ++c) {
                 float wt_ = ex2_fast(fminf(tv[c] - wp, 0.f));
                 wt_ = 8 * o + c >= lane ? wt_ : 0.f;
-                e[c] *= wt_ * del;
-                gg[c] = 8 * o + c == lane ? 0.f : e[c] * a[c];  // a pair with itself feels no decay
+                e[c] *= wt_;
+                gg[c] = e[c] * a[c];
+                if (8 * o + c == lane) {  // a pair with itself feels no decay
+                  self = gg[c];
+                  gg[c] = 0.f;
+                }
+                e[c] *= del;
                 a[c] *= wt_;
               }
             }
@@ -805,6 +823,8 @@ __global__ void __launch_bounds__(NTG, 1)
               pw[c / 2] = pack_bf16(a[c], a[c + 1]);
               qw[c / 2] = pack_bf16(e[c], e[c + 1]);
             }
+#pragma unroll
+            for (int c = 0; c < 8; ++c) gg[c] *= del;
             const float rs = column_sums(gg, lane);
             if (lane < 8) gs.row[qd][32 * I + 8 * o + lane] = rs;
           }
@@ -814,6 +834,7 @@ __global__ void __launch_bounds__(NTG, 1)
         }
         if (I < qd) gs.row[qd][32 * I + lane] = 0.f;
         gs.col[I][row] = col;
+        if (I == qd) gs.self[row] = self;
         tmem_st_wait();
       }
       fence_proxy_async();
@@ -826,18 +847,11 @@ __global__ void __launch_bounds__(NTG, 1)
         float f[16], f2[16], t[16], d = 0.f;
         tmem_ld16(tm + TG_B + c0 + lq, f);
         tmem_ld16(tm + TG_C + c0 + lq, f2);
-        tile_row_cols<16>(sm + G_B, row, c0, t);
+        tile_row_cols<16>(sm + G_C, row, c0, t);
         tmem_ld_wait();
         const float fb = del * fend;
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          f[c] *= fb;
-          d = fmaf(f[c], t[c], d);
-          aB[c] += f[c];
-        }
-        gs.w[I][row] = d;
-        d = 0.f;
-        tile_row_cols<16>(sm + G_C, row, c0, t);
+        for (int c = 0; c < 16; ++c) aB[c] = fmaf(f[c], fb, aB[c]);
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           f2[c] *= ecum;
@@ -852,15 +866,18 @@ __global__ void __launch_bounds__(NTG, 1)
         put_gates(gates[(i + 1) % 3], z + par_[i + 1].bias, live, par_[i + 1].A, row);
         z = raw(i + 2);
       }
-      // <S, R> over the two bf16 tiles: 8 values a thread
+      // <S, R> over the tiles' terms: 8 values a thread
       float sr = 0.f, dsk = 0.f;
       if (in) {
-        const uint4 a = lds128(sm + G_S + k * STILE + threadIdx.x * 16), b = lds128(sm + G_R + k * STILE + threadIdx.x * 16);
-        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+        const uint8_t *sp = sm + G_S + 2 * k * STILE + threadIdx.x * 16, *rp = sm + G_R + 2 * k * STILE + threadIdx.x * 16;
+        const uint4 a0 = lds128(sp), a1 = lds128(sp + STILE), b0 = lds128(rp), b1 = lds128(rp + STILE);
+        const uint32_t av[4] = {a0.x, a0.y, a0.z, a0.w}, al[4] = {a1.x, a1.y, a1.z, a1.w}, bv[4] = {b0.x, b0.y, b0.z, b0.w},
+                       bl[4] = {b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          sr = fmaf(__uint_as_float(av[j] << 16), __uint_as_float(bv[j] << 16), sr);
-          sr = fmaf(__uint_as_float(av[j] & 0xffff0000u), __uint_as_float(bv[j] & 0xffff0000u), sr);
+          sr = fmaf(__uint_as_float(av[j] << 16) + __uint_as_float(al[j] << 16), __uint_as_float(bv[j] << 16) + __uint_as_float(bl[j] << 16), sr);
+          sr = fmaf(__uint_as_float(av[j] & 0xffff0000u) + __uint_as_float(al[j] & 0xffff0000u),
+                    __uint_as_float(bv[j] & 0xffff0000u) + __uint_as_float(bl[j] & 0xffff0000u), sr);
         }
       }
       // ---- dx
@@ -875,12 +892,12 @@ __global__ void __launch_bounds__(NTG, 1)
         const float sk = par_[i].skip;
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
+          d = fmaf(x[c], br[c], d);
           u[c] = fmaf(fend, br[c], u[c]);
-          d = fmaf(x[c], u[c], d);
           dsk = fmaf(x[c], y[c], dsk);
           u[c] = live ? fmaf(del, u[c], sk * y[c]) : 0.f;
         }
-        gs.u[I][row] = d;
+        gs.w[I][row] = fend * d;
         tile_put_cols<16>(xt, row, c0, u);  // the products that read x have been done since bar_2
       }
       fence_proxy_async();
@@ -956,7 +973,7 @@ struct Parts {
 };
 
 struct WsTC {
-  size_t tot, pf, sf, pr, sr, pB, pC, pp, end;
+  size_t tot, pf, sf, sl, pr, sr, rl, pB, pC, pp, end;
   WsTC(const ScanShape& s, bool bwd) {
     const size_t n = (size_t)s.B * s.H * chunks(s), st = n * s.D * s.M;
     tot = 0;
@@ -966,9 +983,11 @@ struct WsTC {
     if (bwd) {
       const int pg = Parts(s, sm_count()).pg;
       const size_t part = pg == 1 ? 0 : (size_t)s.B * s.N * s.G * pg * s.D * 4;
-      pr = end;
+      sl = end;
+      pr = align_line(sl + st * 2);
       sr = pr + st * 4;
-      pB = align_line(sr + st * 2);
+      rl = align_line(sr + st * 2);
+      pB = align_line(rl + st * 2);
       pC = align_line(pB + part);
       pp = align_line(pC + part);
       end = pp + align_line(n * 12);
@@ -1014,7 +1033,7 @@ cudaError_t scan_fwd_tc(const ScanIn& a, float* S, void* y, void* ws, const Scan
       !make_state_map(&m.S, sf, s.M, s.D, (long)s.B * s.H * nch))
     return cudaErrorInvalidValue;
   m.g = m.x;
-  m.R = m.S;
+  m.R = m.Sl = m.Rl = m.S;
   const bf16 *dt = (const bf16*)a.dt, *A = (const bf16*)a.A, *skip = (const bf16*)a.skip, *bias = (const bf16*)a.dt_bias;
   int* err = status_word();
   if (states) {
@@ -1025,7 +1044,7 @@ cudaError_t scan_fwd_tc(const ScanIn& a, float* S, void* y, void* ws, const Scan
     LA_TRY_CUDA(cudaFuncSetAttribute(sums, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM(terms)));
     LA_TRY_CUDA(launch_pdl(sums, sgrid, dim3(NT), S_SMEM(terms), st, m, dt, A, bias, a.lengths, pf, static_cast<float*>(nullptr), tot, s, ps.pg,
                            ps.hs, err));
-    LA_TRY_CUDA(scan_carry_bf16(pf, nullptr, sf, nullptr, tot, S, s.B * s.H, nch, s.D * s.M, st));
+    LA_TRY_CUDA(scan_carry_bf16(pf, nullptr, sf, nullptr, nullptr, nullptr, tot, S, s.B * s.H, nch, s.D * s.M, st));
   }
   LA_TRY_CUDA(cudaFuncSetAttribute(k_out, cudaFuncAttributeMaxDynamicSharedMemorySize, O_SMEM));
   return launch_pdl(k_out, grid, dim3(NT), O_SMEM, st, m, dt, A, skip, bias, a.lengths, (bf16*)y, s, p.pg, p.hs, states ? 1 : 0, err);
@@ -1035,21 +1054,20 @@ cudaError_t scan_bwd_tc(const ScanIn& a, const void* dy, const ScanGrads& d, voi
   const WsTC w(s, true);
   char* base = first_line(ws);
   float *tot = (float*)(base + w.tot), *pf = (float*)(base + w.pf), *pr = (float*)(base + w.pr), *pp = (float*)(base + w.pp);
-  bf16 *sf = (bf16*)(base + w.sf), *sr = (bf16*)(base + w.sr);
+  bf16 *sf = (bf16*)(base + w.sf), *sr = (bf16*)(base + w.sr), *sl = (bf16*)(base + w.sl), *rl = (bf16*)(base + w.rl);
   const int nch = chunks(s);
   const long n = (long)s.B * s.H * nch;
   Maps m;
   if (!row_maps(m, a, s) || !make_rows_map(&m.g, dy, s.M, s.H, (long)s.H * s.M, s.N, s.B) ||
       !make_rows_map(&m.o, d.x, s.M, s.H, (long)s.H * s.M, s.N, s.B) || !make_state_map(&m.S, sf, s.M, s.D, n) ||
-      !make_state_map(&m.R, sr, s.M, s.D, n))
+      !make_state_map(&m.R, sr, s.M, s.D, n) || !make_state_map(&m.Sl, sl, s.M, s.D, n) || !make_state_map(&m.Rl, rl, s.M, s.D, n))
     return cudaErrorInvalidValue;
   const bf16 *dt = (const bf16*)a.dt, *A = (const bf16*)a.A, *skip = (const bf16*)a.skip, *bias = (const bf16*)a.dt_bias;
   int* err = status_word();
-  // the sums feed bf16 gradients only: one bf16 term
   const Parts ps(s, 3 * sm_count() / 2);  // either direction's share of three blocks an SM
-  LA_TRY_CUDA(cudaFuncSetAttribute(k_sums<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM(1)));
-  LA_TRY_CUDA(launch_whole(k_sums<1>, dim3(nch, 2 * s.G * ps.pg, s.B), dim3(NT), S_SMEM(1), st, m, dt, A, bias, a.lengths, pf, pr, tot, s, ps.pg, ps.hs, err));
-  LA_TRY_CUDA(scan_carry_bf16(pf, pr, sf, sr, tot, nullptr, s.B * s.H, nch, s.D * s.M, st));
+  LA_TRY_CUDA(cudaFuncSetAttribute(k_sums<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM(2)));
+  LA_TRY_CUDA(launch_whole(k_sums<2>, dim3(nch, 2 * s.G * ps.pg, s.B), dim3(NT), S_SMEM(2), st, m, dt, A, bias, a.lengths, pf, pr, tot, s, ps.pg, ps.hs, err));
+  LA_TRY_CUDA(scan_carry_bf16(pf, pr, sf, sr, sl, rl, tot, nullptr, s.B * s.H, nch, s.D * s.M, st));
   const Parts p(s, sm_count());
   const bool direct = p.pg == 1;
   LA_TRY_CUDA(cudaFuncSetAttribute(k_grad, cudaFuncAttributeMaxDynamicSharedMemorySize, G_SMEM));
