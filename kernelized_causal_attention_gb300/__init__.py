@@ -524,17 +524,22 @@ def decode_step_proj(x, W, S, Z, H, D, M, stream=None):
 
 def _take(t, name, shape, dtype, device):
     """The address of a dense tensor of the shape, type and device that the call needs."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    raise _refusal(t, name, shape, dtype, device)
+
+
+def _refusal(t, name, shape, dtype, device):
+    """What is wrong with a tensor that _take or _take_rows has refused."""
     if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: a tensor is needed")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
+        return TypeError(f"{name}: a tensor is needed")
+    if tuple(t.shape) != tuple(shape):
+        return ValueError(f"{name}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
     if t.dtype != dtype:
-        raise TypeError(f"{name}: {t.dtype}, the call needs {dtype}")
+        return TypeError(f"{name}: {t.dtype}, the call needs {dtype}")
     if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the call is on {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    return t.data_ptr()
+        return ValueError(f"{name}: on {t.device}, the call is on {device}")
+    return ValueError(f"{name}: must be contiguous")
 
 
 def _take_opt(t, name, shape, dtype, device):
@@ -544,19 +549,18 @@ def _take_opt(t, name, shape, dtype, device):
 def _take_rows(t, name, shape, dtype, device, lead):
     """(address, row stride) of a token-major view whose first `lead` dimensions are batch (and row):
     rows dense, and all rows of all batch entries evenly spaced."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: a tensor is needed")
-    if t.shape != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, the call needs {tuple(shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name}: {t.dtype}, the call needs {dtype}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, the call is on {device}")
-    st, want = t.stride(), 1
-    for i in range(len(shape) - 1, lead - 1, -1):
-        if shape[i] != 1 and st[i] != want:
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype and t.device == device):
+        raise _refusal(t, name, shape, dtype, device)
+    st = t.stride()
+    want = shape[-1]
+    if len(shape) == lead:
+        want = 1
+    elif want != 1 and st[-1] != 1:
+        raise ValueError(f"{name}: every row must be dense")
+    if len(shape) == lead + 2:
+        if shape[lead] != 1 and st[lead] != want:
             raise ValueError(f"{name}: every row must be dense")
-        want *= shape[i]
+        want *= shape[lead]
     B = shape[0]
     if lead == 1:
         return t.data_ptr(), st[0] if B > 1 else want
@@ -583,8 +587,12 @@ def _need_cuda(t):
         raise ValueError("tensors must be on a CUDA device")
 
 
-def _scratch(n, device):
-    return None if n == 0 else torch.empty(n, dtype=torch.uint8, device=device)
+def _scratch(n, like):
+    """(workspace or None, its address, its size)"""
+    if n == 0:
+        return None, None, 0
+    ws = like.new_empty((n,), dtype=torch.uint8)
+    return ws, ws.data_ptr(), n
 
 
 def _conv_args(x, w, bias, lengths, lead):
@@ -608,7 +616,7 @@ def short_conv_fwd(x, w, bias=None, state=None, lengths=None, silu=True):
     (B, N, _), C, K, code, dtype, dev, px, ld, pw, pb, pn = _conv_args(x, w, bias, lengths, 2)
     ps = _take_opt(state, "state", (B, K - 1, C), dtype, dev)
     _need_cuda(x)
-    y = torch.empty((B, N, C), dtype=dtype, device=dev)
+    y = x.new_empty((B, N, C))
     _check(lib().la_short_conv_fwd(px, pw, pb, pn, ps, y.data_ptr(), B, N, C, K, ld, int(silu), code, _stream(None)),
            "la_short_conv_fwd")
     return y
@@ -621,11 +629,11 @@ def short_conv_bwd(x, w, bias, dy, lengths=None, silu=True):
     B, N, _ = shape
     pg = _take(dy, "dy", shape, dtype, dev)
     _need_cuda(x)
-    dx, dw = torch.empty((B, N, C), dtype=dtype, device=dev), torch.empty_like(w)
+    dx, dw = x.new_empty((B, N, C)), torch.empty_like(w)
     db = None if bias is None else torch.empty_like(bias)
-    ws = _scratch(la_short_conv_workspace_bytes(B, N, C, K, code), dev)
+    ws, pws, nws = _scratch(lib().la_short_conv_workspace_bytes(B, N, C, K, code), x)
     _check(lib().la_short_conv_bwd(px, pw, pb, pn, pg, dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(),
-                                   _p(ws), _nbytes(ws), B, N, C, K, ld, int(silu), code, _stream(None)), "la_short_conv_bwd")
+                                   pws, nws, B, N, C, K, ld, int(silu), code, _stream(None)), "la_short_conv_bwd")
     return dx, dw, db
 
 
@@ -635,7 +643,7 @@ def short_conv_step(x, w, bias, state, silu=True):
     (B, _), C, K, code, dtype, dev, px, ld, pw, pb, _ = _conv_args(x, w, bias, None, 1)
     ps = _take(state, "state", (B, K - 1, C), dtype, dev)
     _need_cuda(x)
-    y = torch.empty((B, C), dtype=dtype, device=dev)
+    y = x.new_empty((B, C))
     _check(lib().la_short_conv_step(px, pw, pb, ps, y.data_ptr(), B, C, K, ld, int(silu), code, _stream(None)),
            "la_short_conv_step")
     return y
@@ -670,9 +678,9 @@ def scan_fwd(x, dt, A, Bm, Cm, skip=None, dt_bias=None, S=None, lengths=None):
     B, N = x.shape[:2]
     pS = _take_opt(S, "S", (B, H, D, M), torch.float32, dev)
     _need_cuda(x)
-    y = torch.empty((B, N, H, M), dtype=dtype, device=dev)
-    ws = _scratch(la_scan_workspace_bytes(0, B, H, G, N, D, M, code), dev)
-    _check(lib().la_scan_fwd(*ptrs, pS, y.data_ptr(), _p(ws), _nbytes(ws), B, H, G, N, D, M, *ld, code, _stream(None)),
+    y = x.new_empty((B, N, H, M))
+    ws, pws, nws = _scratch(lib().la_scan_workspace_bytes(0, B, H, G, N, D, M, code), x)
+    _check(lib().la_scan_fwd(*ptrs, pS, y.data_ptr(), pws, nws, B, H, G, N, D, M, *ld, code, _stream(None)),
            "la_scan_fwd")
     return y
 
@@ -685,13 +693,13 @@ def scan_bwd(x, dt, A, Bm, Cm, skip, dt_bias, dy, lengths=None):
     B, N = x.shape[:2]
     pg = _take(dy, "dy", x.shape, dtype, dev)
     _need_cuda(x)
-    new = lambda *shape: torch.empty(shape, dtype=dtype, device=dev)  # noqa: E731
-    d = [new(B, N, H, M), new(B, N, H), new(H), new(B, N, G, D), new(B, N, G, D), None if skip is None else new(H),
-         None if dt_bias is None else new(H)]
-    ws = _scratch(la_scan_workspace_bytes(1, B, H, G, N, D, M, code), dev)
-    _check(lib().la_scan_bwd(*ptrs, pg, *[None if t is None else t.data_ptr() for t in d], _p(ws), _nbytes(ws), B, H, G, N, D,
+    new, h = x.new_empty, (H,)
+    d = (new((B, N, H, M)), new((B, N, H)), new(h), new((B, N, G, D)), new((B, N, G, D)), None if skip is None else new(h),
+         None if dt_bias is None else new(h))
+    ws, pws, nws = _scratch(lib().la_scan_workspace_bytes(1, B, H, G, N, D, M, code), x)
+    _check(lib().la_scan_bwd(*ptrs, pg, *[None if t is None else t.data_ptr() for t in d], pws, nws, B, H, G, N, D,
                              M, *ld, code, _stream(None)), "la_scan_bwd")
-    return tuple(d)
+    return d
 
 
 @_on_device
@@ -702,7 +710,7 @@ def scan_step(x, dt, A, Bm, Cm, skip, dt_bias, S):
     B = x.shape[0]
     pS = _take(S, "S", (B, H, D, M), torch.float32, dev)
     _need_cuda(x)
-    y = torch.empty((B, H, M), dtype=dtype, device=dev)
+    y = x.new_empty((B, H, M))
     _check(lib().la_scan_step(*ptrs[:7], pS, y.data_ptr(), B, H, G, D, M, *ld, code, _stream(None)), "la_scan_step")
     return y
 
@@ -726,10 +734,11 @@ def cross_fwd(q, k, v, lengths=None):
     ptrs, size, code, dtype, dev = _cross_args(q, k, v, lengths)
     B, H, Hk, Nq, Nk, D, M = size
     _need_cuda(q)
-    out, den = torch.empty((B, H, Nq, M), dtype=dtype, device=dev), torch.empty((B, H, Nq), dtype=torch.float32, device=dev)
-    S, Z = (torch.empty(n, dtype=torch.float32, device=dev) for n in ((B, Hk, D, M), (B, Hk, D)))
-    ws = _scratch(la_cross_workspace_bytes(0, *size, code), dev)
-    _check(lib().la_cross_fwd(*ptrs, out.data_ptr(), den.data_ptr(), S.data_ptr(), Z.data_ptr(), _p(ws), _nbytes(ws), *size,
+    new, f32 = q.new_empty, torch.float32
+    out, den = new((B, H, Nq, M)), new((B, H, Nq), dtype=f32)
+    S, Z = new((B, Hk, D, M), dtype=f32), new((B, Hk, D), dtype=f32)
+    ws, pws, nws = _scratch(lib().la_cross_workspace_bytes(0, *size, code), q)
+    _check(lib().la_cross_fwd(*ptrs, out.data_ptr(), den.data_ptr(), S.data_ptr(), Z.data_ptr(), pws, nws, *size,
                               code, _stream(None)), "la_cross_fwd")
     return out, den, S, Z
 
@@ -745,8 +754,8 @@ def cross_bwd(q, k, v, lengths, out, den, S, Z, dout):
             _take(dout, "dout", (B, H, Nq, M), dtype, dev))
     _need_cuda(q)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ws = _scratch(la_cross_workspace_bytes(1, *size, code), dev)
-    _check(lib().la_cross_bwd(*ptrs, *more, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _p(ws), _nbytes(ws), *size, code,
+    ws, pws, nws = _scratch(lib().la_cross_workspace_bytes(1, *size, code), q)
+    _check(lib().la_cross_bwd(*ptrs, *more, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), pws, nws, *size, code,
                               _stream(None)), "la_cross_bwd")
     return dq, dk, dv
 
@@ -763,7 +772,7 @@ def cross_step(q, S, Z):
     pS = _take(S, "S", (B, Hk, D, M), torch.float32, dev)
     pZ = _take(Z, "Z", (B, Hk, D), torch.float32, dev)
     _need_cuda(q)
-    y = torch.empty((B, H, M), dtype=dtype, device=dev)
+    y = q.new_empty((B, H, M))
     _check(lib().la_cross_step(pq, pS, pZ, y.data_ptr(), B, H, Hk, D, M, code, _stream(None)), "la_cross_step")
     return y
 

@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(NTG, 1)
     k_grad(const __grid_constant__ Maps maps, const bf16* __restrict__ dt, const bf16* __restrict__ A,
            const bf16* __restrict__ skip, const bf16* __restrict__ bias, const int* __restrict__ lengths,
            bf16* __restrict__ dx, bf16* __restrict__ ddt, void* dB, void* dC, float* __restrict__ pp, ScanShape s, int pg,
-           int hs, int* err) {
+           int hs, int states, int* err) {
   extern __shared__ uint8_t smraw[];
   uint8_t* sm = align1024(smraw);
   __shared__ uint64_t bar_cb, bar_in[2], bar_clear, bar_1, bar_2, bar_3, bar_4, bar_p, bar_c, bar_x, bar_free;
@@ -594,6 +594,11 @@ __global__ void __launch_bounds__(NTG, 1)
   tc_fence_after();
   const uint32_t tm = tmem_base;
   const bool cut = w.rows < in_n;
+  if (!states) {  // one chunk: the carried states are zeros, in every stage
+    for (int v = threadIdx.x; v < 8 * STILE / 16; v += NTG) sts128(sm + G_S + v * 16, make_uint4(0u, 0u, 0u, 0u));
+    fence_proxy_async();
+    __syncthreads();
+  }
 
   if (w.rows == 0) {  // nothing but rows past the sequence's length
     const int per = w.nh * s.M / 8;
@@ -622,15 +627,16 @@ __global__ void __launch_bounds__(NTG, 1)
       int issued = 0;
       auto load = [&](int i) {
         const int k = i & 1, h = w.h0 + i;
-        mbar_arrive_expect_tx(&bar_in[k], 2 * TILE + 4 * STILE);
+        mbar_arrive_expect_tx(&bar_in[k], 2 * TILE + (states ? 4 * STILE : 0));
         tma_load_4d(sm + G_X + k * TILE, &maps.x, &bar_in[k], 0, h, w.n0, w.b);
         tma_load_4d(sm + G_Y + k * TILE, &maps.g, &bar_in[k], 0, h, w.n0, w.b);
+        ++issued;
+        if (!states) return;
         const int at = (w.b * s.H + h) * nch + blockIdx.x;
         tma_load_3d(sm + G_S + 2 * k * STILE, &maps.S, &bar_in[k], 0, 0, at);
         tma_load_3d(sm + G_S + (2 * k + 1) * STILE, &maps.Sl, &bar_in[k], 0, 0, at);
         tma_load_3d(sm + G_R + 2 * k * STILE, &maps.R, &bar_in[k], 0, 0, at);
         tma_load_3d(sm + G_R + (2 * k + 1) * STILE, &maps.Rl, &bar_in[k], 0, 0, at);
-        ++issued;
       };
       load(0);
       if (w.nh > 1) load(1);
@@ -1064,16 +1070,19 @@ cudaError_t scan_bwd_tc(const ScanIn& a, const void* dy, const ScanGrads& d, voi
     return cudaErrorInvalidValue;
   const bf16 *dt = (const bf16*)a.dt, *A = (const bf16*)a.A, *skip = (const bf16*)a.skip, *bias = (const bf16*)a.dt_bias;
   int* err = status_word();
-  const Parts ps(s, 3 * sm_count() / 2);  // either direction's share of three blocks an SM
-  LA_TRY_CUDA(cudaFuncSetAttribute(k_sums<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM(2)));
-  LA_TRY_CUDA(launch_whole(k_sums<2>, dim3(nch, 2 * s.G * ps.pg, s.B), dim3(NT), S_SMEM(2), st, m, dt, A, bias, a.lengths, pf, pr, tot, s, ps.pg, ps.hs, err));
-  LA_TRY_CUDA(scan_carry_bf16(pf, pr, sf, sr, sl, rl, tot, nullptr, s.B * s.H, nch, s.D * s.M, st));
+  const bool states = nch > 1;
+  if (states) {
+    const Parts ps(s, 3 * sm_count() / 2);  // either direction's share of three blocks an SM
+    LA_TRY_CUDA(cudaFuncSetAttribute(k_sums<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, S_SMEM(2)));
+    LA_TRY_CUDA(launch_whole(k_sums<2>, dim3(nch, 2 * s.G * ps.pg, s.B), dim3(NT), S_SMEM(2), st, m, dt, A, bias, a.lengths, pf, pr, tot, s, ps.pg, ps.hs, err));
+    LA_TRY_CUDA(scan_carry_bf16(pf, pr, sf, sr, sl, rl, tot, nullptr, s.B * s.H, nch, s.D * s.M, st));
+  }
   const Parts p(s, sm_count());
   const bool direct = p.pg == 1;
   LA_TRY_CUDA(cudaFuncSetAttribute(k_grad, cudaFuncAttributeMaxDynamicSharedMemorySize, G_SMEM));
   LA_TRY_CUDA(launch_whole(k_grad, dim3(nch, s.G * p.pg, s.B), dim3(NTG), G_SMEM, st, m, dt, A, skip, bias, a.lengths, (bf16*)d.x,
                          (bf16*)d.dt, direct ? d.B : static_cast<void*>(base + w.pB), direct ? d.C : static_cast<void*>(base + w.pC),
-                         pp, s, p.pg, p.hs, err));
+                         pp, s, p.pg, p.hs, states ? 1 : 0, err));
   if (!direct) LA_TRY_CUDA(scan_groups((float*)(base + w.pB), (float*)(base + w.pC), d.B, d.C, s, p.pg, st));
   return scan_params(pp, d.A, d.skip, d.dt_bias, s, nch, st);
 }
