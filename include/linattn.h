@@ -334,7 +334,8 @@ la_status la_short_conv_step(const void* x, const void* w, const void* bias, voi
  * of the call's dtype; A <= 0 keeps the recurrence stable and is not checked.
  * y [B][N][H][M] dense.  S [B][H][D][M] float, read as the state before row 0
  * and replaced by the state after each sequence's last valid row, or NULL (from
- * zero, not returned).  G divides H; D and M in {16, 32, 64}; 1 <= B H <= 65535.
+ * zero, not returned).  G divides H; D and M in {16, 32, 64}; 1 <= B H <= 65535,
+ * H <= 32767.  dt, A and their products are finite.
  * workspace: la_scan_workspace_bytes(0, ...) bytes.
  */
 la_status la_scan_fwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm,
@@ -384,7 +385,8 @@ la_status la_cross_fwd(const void* q, const void* k, const void* v, const int* l
 /*
  * Its gradients: dq as q, dk as k and dv as v (rows past a sequence's length
  * zero; summed over the query heads of a key head).  out, den, S and Z are
- * la_cross_fwd's.  workspace: la_cross_workspace_bytes(1, ...) bytes.
+ * la_cross_fwd's (out is not read: dout . out is formed again from S).
+ * workspace: la_cross_workspace_bytes(1, ...) bytes.
  */
 la_status la_cross_bwd(const void* q, const void* k, const void* v, const int* lengths,
                        const void* out, const float* den, const float* S, const float* Z,

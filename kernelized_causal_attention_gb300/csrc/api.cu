@@ -118,6 +118,7 @@ int check_conv(int B, int N, int C, int K, int ldx, int dtype, int max_b) {
 
 int check_scan(const la::ScanShape& s, long long max_bh) {
   if (s.G < 1 || s.H < 1 || s.H % s.G != 0) return LA_ERR_INVALID_ARG;
+  if (s.H > 32767) return LA_ERR_INVALID_ARG;  // both directions' heads are grid rows of one launch
   return check_shape(s.B, s.H, s.N, s.D, s.M, s.dtype, max_bh);
 }
 

@@ -211,7 +211,7 @@ FAKE = 1 << 20
 @pytest.mark.parametrize("kw,code", [
     (dict(x=None), 1), (dict(dt=None), 1), (dict(A=None), 1), (dict(Bm=FAKE + 8), 1), (dict(Cm=None), 1), (dict(dt=FAKE + 2), 1),
     (dict(skip=FAKE + 4), 1), (dict(dt_bias=FAKE + 4), 1), (dict(S=FAKE + 4), 1), (dict(y=None), 1), (dict(lengths=FAKE + 1), 1),
-    (dict(G=3), 1), (dict(G=0), 1), (dict(H=0), 1), (dict(N=0), 1), (dict(B=65536), 1), (dict(D=128), 2), (dict(M=24), 2), (dict(D=0), 1),
+    (dict(G=3), 1), (dict(G=0), 1), (dict(H=32768, ldx=1 << 20, lddt=32768), 1), (dict(H=0), 1), (dict(N=0), 1), (dict(B=65536), 1), (dict(D=128), 2), (dict(M=24), 2), (dict(D=0), 1),
     (dict(ldx=60), 1), (dict(ldx=66), 1), (dict(ldb=15), 1), (dict(ldc=18), 1), (dict(lddt=3), 1), (dict(t=9), 1),
     (dict(wsb=16), 5), (dict(ws=None), 5), (dict(ws=FAKE + 4), 1),
 ])
