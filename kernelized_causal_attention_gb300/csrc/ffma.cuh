@@ -44,12 +44,16 @@ __device__ __forceinline__ void ffma_mm(float (&acc)[RR][CC], const float* X, in
 // Rows [0, rows) of a token-major matrix (row r at g + r * stride, W values)
 // into an fp32 tile, natural (nat[r * ldn + c]) and / or transposed
 // (tr[c * FLD + r]); rows at or past `rows` are zero and not read.  Every row
-// starts on a 16-byte boundary.
+// starts on a 16-byte boundary.  Neighbouring lanes take neighbouring rows, so
+// that both forms are written without bank conflicts (along the columns the
+// transposed one takes eight ways); a line of a row serves several turns from L1.
 template <typename T, int W>
 __device__ __forceinline__ void stage(const T* g, long stride, int rows, float* nat, int ldn, float* tr) {
   constexpr int VN = Vec16<T>::n, VPR = W / VN;
-  for (int e = threadIdx.x; e < FT * VPR; e += 256) {
-    const int r = e / VPR, c = (e % VPR) * VN;
+  const int r = threadIdx.x & 63;
+#pragma unroll
+  for (int v = threadIdx.x >> 6; v < VPR; v += 4) {
+    const int c = v * VN;
     float f[VN];
     if (r < rows) {
       Vec16<T>::unpack(*reinterpret_cast<const uint4*>(g + r * stride + c), f);
@@ -59,7 +63,7 @@ __device__ __forceinline__ void stage(const T* g, long stride, int rows, float* 
     }
     if (nat != nullptr) {
 #pragma unroll
-      for (int i = 0; i < VN; ++i) nat[r * ldn + c + i] = f[i];
+      for (int i = 0; i < VN; i += 4) *reinterpret_cast<float4*>(nat + r * ldn + c + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
     }
     if (tr != nullptr) {
 #pragma unroll
@@ -71,11 +75,16 @@ __device__ __forceinline__ void stage(const T* g, long stride, int rows, float* 
 // A [D][M] fp32 matrix into a tile, natural (ld M + 4) and / or transposed (ld D + 4).
 template <int D, int M>
 __device__ __forceinline__ void stage_state(const float* g, float* nat, float* tr) {
-  for (int e = threadIdx.x; e < D * M; e += 256) {
-    const int d = e / M, m = e % M;
-    const float v = g[e];
-    if (nat != nullptr) nat[d * (M + 4) + m] = v;
-    if (tr != nullptr) tr[m * (D + 4) + d] = v;
+  for (int e = threadIdx.x; e < D * M / 4; e += 256) {
+    const int d = e % D, m = e / D * 4;
+    const float4 v = *reinterpret_cast<const float4*>(g + d * M + m);
+    if (nat != nullptr) *reinterpret_cast<float4*>(nat + d * (M + 4) + m) = v;
+    if (tr != nullptr) {
+      tr[m * (D + 4) + d] = v.x;
+      tr[(m + 1) * (D + 4) + d] = v.y;
+      tr[(m + 2) * (D + 4) + d] = v.z;
+      tr[(m + 3) * (D + 4) + d] = v.w;
+    }
   }
 }
 

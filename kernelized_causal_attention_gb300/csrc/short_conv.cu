@@ -21,7 +21,7 @@ namespace {
 
 using bf16 = __nv_bfloat16;
 
-// V neighbouring channels as one vector (V = 4: the caller has checked the
+// V neighbouring channels as one vector (V > 1: the caller has checked the
 // alignment), raw or as fp32.
 template <typename T, int V>
 struct Pack;
@@ -36,6 +36,12 @@ struct Pack<float, 4> {
   using Raw = float4;
   __device__ __forceinline__ static void open(const Raw& u, float (&f)[4]) { f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w; }
   __device__ __forceinline__ static void st(float* p, const float (&f)[4]) { *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]); }
+};
+template <>
+struct Pack<float, 2> {
+  using Raw = float2;
+  __device__ __forceinline__ static void open(const Raw& u, float (&f)[2]) { f[0] = u.x, f[1] = u.y; }
+  __device__ __forceinline__ static void st(float* p, const float (&f)[2]) { *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]); }
 };
 template <>
 struct Pack<bf16, 4> {
@@ -72,12 +78,12 @@ __device__ __forceinline__ void taps(const T* w, const T* bias, int c, float (&w
   }
 }
 
-// c += a b over V channels, two to an instruction where V = 4.
+// c += a b over V channels, two to an instruction where V > 1.
 template <int V>
 __device__ __forceinline__ void fma_v(float (&c)[V], const float (&a)[V], const float (&b)[V]) {
-  if constexpr (V == 4) {
+  if constexpr (V > 1) {
 #pragma unroll
-    for (int i = 0; i < 4; i += 2)
+    for (int i = 0; i < V; i += 2)
       asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%0, %1};\n\t"
           "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
           : "+f"(c[i]), "+f"(c[i + 1])
@@ -210,7 +216,7 @@ __global__ void __launch_bounds__(CG * RG, 3)
 // dx, and each block's sums of g x and g over its rows into
 // part[group][K + 1][C] (fp32; the last plane is the bias's).  History zero.
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(CG * RG)
+__global__ void __launch_bounds__(CG * RG, V == 1 ? 1 : 2)
     k_conv_bwd(const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const int* __restrict__ lengths,
                const T* __restrict__ dy, T* __restrict__ dx, float* __restrict__ part, int N, int C, long ldx, int silu,
                int groups, int walk) {
@@ -400,17 +406,20 @@ struct Walk {
   }
 };
 
-Walk bwd_walk(const ConvShape& s, bool four) {
-  const int per = CG * (four ? 4 : 1);
-  return Walk(s.N, (long)s.B * ((s.C + per - 1) / per), s.K - 1, 2);
+Walk bwd_walk(const ConvShape& s, int v) {
+  return Walk(s.N, (long)s.B * ((s.C + CG * v - 1) / (CG * v)), s.K - 1, 2);
 }
 
-// Vectors of four channels where every row starts on a vector: C and the row
-// stride multiples of four and every base aligned to four elements (all but x
-// are 16-byte aligned by the interface).  Measured against one channel a
-// thread: see the sizes in the tests; the scalar form takes the rest.
-bool by_four(const void* x, int C, long ldx, size_t elem) {
-  return C % 4 == 0 && ldx % 4 == 0 && reinterpret_cast<uintptr_t>(x) % (4 * elem) == 0;
+// Channels a thread owns: four, or two for the gradients in fp32, whose rows in
+// flight would not fit the registers otherwise; one where a row may start off
+// such a vector (C, the row stride or x's base not its multiple; all other bases
+// are 16-byte aligned by the interface).  Measured at 4 x 2048 x 2304, K = 4:
+//   bf16 forward 22.5 us (one channel 45.1), gradients 38.9 (51.2);
+//   fp32 forward 34.8 (two channels 36.9, one 47.1), gradients 59.4 (four 66.2, one 63.5).
+constexpr int wide(bool bf, bool grad) { return grad && !bf ? 2 : 4; }
+int channels(const void* x, const ConvShape& s, bool grad) {
+  const int v = wide(s.dtype != 0, grad), elem = s.dtype == 0 ? 4 : 2;
+  return s.C % v == 0 && s.ldx % v == 0 && reinterpret_cast<uintptr_t>(x) % (v * elem) == 0 ? v : 1;
 }
 
 #define LA_CONV_CASE(T, V, Kv, BODY) \
@@ -421,13 +430,13 @@ bool by_four(const void* x, int C, long ldx, size_t elem) {
     else if ((K) == 3) LA_CONV_CASE(T, V, 3, BODY) \
     else LA_CONV_CASE(T, V, 4, BODY)          \
   } while (0)
-#define LA_CONV_DISPATCH(dtype, four, K, BODY)        \
+#define LA_CONV_DISPATCH(dtype, v, WF, K, BODY)       \
   do {                                                \
     if ((dtype) == 0) {                               \
-      if (four) LA_CONV_K(float, 4, K, BODY);         \
+      if ((v) > 1) LA_CONV_K(float, WF, K, BODY);     \
       else LA_CONV_K(float, 1, K, BODY);              \
     } else {                                          \
-      if (four) LA_CONV_K(bf16, 4, K, BODY);          \
+      if ((v) > 1) LA_CONV_K(bf16, 4, K, BODY);       \
       else LA_CONV_K(bf16, 1, K, BODY);               \
     }                                                 \
   } while (0)
@@ -435,17 +444,16 @@ bool by_four(const void* x, int C, long ldx, size_t elem) {
 }  // namespace
 
 size_t short_conv_bwd_ws_bytes(const ConvShape& s) {  // whichever form x's alignment leaves
-  const int g = std::max(bwd_walk(s, false).groups, bwd_walk(s, true).groups);
+  const int g = std::max(bwd_walk(s, 1).groups, bwd_walk(s, wide(s.dtype != 0, true)).groups);
   return sizeof(float) * s.B * (size_t)g * (s.K + 1) * s.C;
 }
 
 cudaError_t short_conv_fwd(const void* x, const void* w, const void* bias, const int* lengths, void* state, void* y,
                            const ConvShape& s, cudaStream_t st) {
-  const bool four = by_four(x, s.C, s.ldx, s.dtype == 0 ? 4 : 2);
-  const int per = CG * (four ? 4 : 1);
+  const int v = channels(x, s, false), per = CG * v;
   const Walk plan(s.N, (long)s.B * ((s.C + per - 1) / per), 0, 3);
   const dim3 grid((s.C + per - 1) / per, plan.groups < 65535 ? plan.groups : 65535, s.B), block(CG, RG);
-  LA_CONV_DISPATCH(s.dtype, four, s.K,
+  LA_CONV_DISPATCH(s.dtype, v, 4, s.K,
                    (k_conv_fwd<T_, V_, K_><<<grid, block, 0, st>>>((const T_*)x, (const T_*)w, (const T_*)bias, lengths,
                                                                    (T_*)state, (T_*)y, s.N, s.C, s.ldx, s.silu, plan.rows)));
   return cudaGetLastError();
@@ -453,12 +461,11 @@ cudaError_t short_conv_fwd(const void* x, const void* w, const void* bias, const
 
 cudaError_t short_conv_bwd(const void* x, const void* w, const void* bias, const int* lengths, const void* dy, void* dx,
                            void* dw, void* db, float* ws, const ConvShape& s, cudaStream_t st) {
-  const bool four = by_four(x, s.C, s.ldx, s.dtype == 0 ? 4 : 2);
-  const int per = CG * (four ? 4 : 1);
-  const Walk plan = bwd_walk(s, four);
+  const int v = channels(x, s, true), per = CG * v;
+  const Walk plan = bwd_walk(s, v);
   const int groups = plan.groups;
   const dim3 grid((s.C + per - 1) / per, groups < 65535 ? groups : 65535, s.B), block(CG, RG);
-  LA_CONV_DISPATCH(s.dtype, four, s.K,
+  LA_CONV_DISPATCH(s.dtype, v, 2, s.K,
                    (k_conv_bwd<T_, V_, K_><<<grid, block, 0, st>>>((const T_*)x, (const T_*)w, (const T_*)bias, lengths,
                                                                    (const T_*)dy, (T_*)dx, ws, s.N, s.C, s.ldx, s.silu,
                                                                    groups, plan.rows)));
@@ -471,10 +478,10 @@ cudaError_t short_conv_bwd(const void* x, const void* w, const void* bias, const
 
 cudaError_t short_conv_step(const void* x, const void* w, const void* bias, void* state, void* y, const ConvShape& s,
                             cudaStream_t st) {
-  const bool four = by_four(x, s.C, s.ldx, s.dtype == 0 ? 4 : 2);
-  const long n = (long)s.B * (s.C / (four ? 4 : 1));
+  const int v = channels(x, s, false);
+  const long n = (long)s.B * (s.C / v);
   const unsigned grid = (unsigned)((n + 127) / 128);
-  LA_CONV_DISPATCH(s.dtype, four, s.K,
+  LA_CONV_DISPATCH(s.dtype, v, 4, s.K,
                    (k_conv_step<T_, V_, K_><<<grid, 128, 0, st>>>((const T_*)x, (const T_*)w, (const T_*)bias, (T_*)state,
                                                                   (T_*)y, s.B, s.C, s.ldx, s.silu)));
   return cudaGetLastError();
