@@ -165,7 +165,6 @@ __global__ void __launch_bounds__(NT, 2)
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bh = blockIdx.y;
-  grid_dep_launch();
   if (threadIdx.x == 0) {
     for (int k = 0; k < 2; ++k) {
       mbar_init(&bar_in[k], 1);
@@ -176,8 +175,7 @@ __global__ void __launch_bounds__(NT, 2)
     fence_barrier_init();
     s_abort = 0;
   }
-  if (warp == W_ISSUE) tmem_alloc(&tmem_base, 128);
-  grid_dep_wait();
+  enter(&tmem_base, 128, warp == W_ISSUE);
   const int L = valid_rows(lengths, bh / Hk, N);
   const int t0 = blockIdx.x * per, nt = min(per, (L + TC_C - 1) / TC_C - t0);
   float* o = rec + (static_cast<long>(bh) * gridDim.x + blockIdx.x) * (D * M + D);
@@ -279,7 +277,6 @@ __global__ void __launch_bounds__(NT, 3)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bh = blockIdx.y;
   const long bhk = static_cast<long>(bh / H) * Hk + bh % H / (H / Hk);
   const int t0 = blockIdx.x * per, nt = min(per, (N + TC_C - 1) / TC_C - t0);
-  grid_dep_launch();
   if (threadIdx.x == 0) {
     mbar_init(&bar_in[0], 1);
     mbar_init(&bar_in[1], 1);
@@ -289,8 +286,7 @@ __global__ void __launch_bounds__(NT, 3)
     fence_barrier_init();
     s_abort = 0;
   }
-  if (warp == W_ISSUE) tmem_alloc(&tmem_base, 64);
-  grid_dep_wait();
+  enter(&tmem_base, 64, warp == W_ISSUE);
   LA_WAITS()
   tc_fence_before();
   __syncthreads();
@@ -387,15 +383,13 @@ __global__ void __launch_bounds__(NT, 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bh = blockIdx.y;
   const long bhk = static_cast<long>(bh / H) * Hk + bh % H / (H / Hk);
   const int t0 = blockIdx.x * per, nt = min(per, (N + TC_C - 1) / TC_C - t0);
-  grid_dep_launch();
   if (threadIdx.x == 0) {
     for (uint64_t* b : {&bar_in[0], &bar_in[1], &bar_1, &bar_2}) mbar_init(b, 1);
     for (uint64_t* b : {&bar_s, &bar_t, &bar_free}) mbar_init(b, 256);
     fence_barrier_init();
     s_abort = 0;
   }
-  if (warp == W_ISSUE) tmem_alloc(&tmem_base, 128);
-  grid_dep_wait();
+  enter(&tmem_base, 128, warp == W_ISSUE);
   LA_WAITS()
   tc_fence_before();
   __syncthreads();
@@ -530,15 +524,13 @@ __global__ void __launch_bounds__(NT, 2)
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bh = blockIdx.y;
-  grid_dep_launch();
   if (threadIdx.x == 0) {
     for (uint64_t* b : {&bar_in[0], &bar_in[1], &bar_2}) mbar_init(b, 1);
     for (uint64_t* b : {&bar_s, &bar_t, &bar_free}) mbar_init(b, 256);
     fence_barrier_init();
     s_abort = 0;
   }
-  if (warp == W_ISSUE) tmem_alloc(&tmem_base, 128);
-  grid_dep_wait();
+  enter(&tmem_base, 128, warp == W_ISSUE);
   const int L = valid_rows(lengths, bh / Hk, N);
   const int t0 = blockIdx.x * per, t1 = min(t0 + per, (N + TC_C - 1) / TC_C);  // tiles of this block
   const int nt = min(t1, (L + TC_C - 1) / TC_C) - t0;                          // of which hold valid rows

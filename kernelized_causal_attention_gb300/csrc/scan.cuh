@@ -15,6 +15,18 @@ __device__ __forceinline__ void grid_dep_enter() {
   tcc::grid_dep_wait();
 }
 
+// The same for a kernel that takes tensor memory, by one warp: only once the
+// kernel before is done, and the next kernel may start only once every block has
+// it.  A block that held tensor memory while it waited for a kernel one of whose
+// blocks still asked for some could keep both waiting.
+__device__ __forceinline__ void enter(uint32_t* base, uint32_t cols, bool allocates) {
+  tcc::grid_dep_wait();
+  if (allocates) {
+    tc::tmem_alloc(base, cols);
+    tcc::grid_dep_launch();
+  }
+}
+
 // softplus(x) = log(1 + exp(x)), written so that neither branch overflows.
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
 

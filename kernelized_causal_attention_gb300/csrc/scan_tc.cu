@@ -159,7 +159,6 @@ __global__ void __launch_bounds__(NT, 3)
   const int parts = s.G * pg;
   const bool back = blockIdx.y >= parts;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nch = gridDim.x;
-  grid_dep_launch();
   if (threadIdx.x == NT - 1) {
     mbar_init(&bar_a, 1);
     mbar_init(&bar_x, 1);
@@ -168,8 +167,7 @@ __global__ void __launch_bounds__(NT, 3)
     fence_barrier_init();
     s_abort = 0;
   }
-  if (warp == W_ISSUE) tmem_alloc(&tmem_base, COLS);
-  grid_dep_wait();
+  enter(&tmem_base, COLS, warp == W_ISSUE);
   const Share w(s, lengths, back ? blockIdx.y - parts : blockIdx.y, pg, hs);
   const int DM = s.D * s.M;
   float* out = (back ? rev : fwd) + (((long)w.b * s.H + w.h0) * nch + blockIdx.x) * DM;  // head h0 + i: + i nch DM
@@ -313,7 +311,6 @@ __global__ void __launch_bounds__(NT, 2)
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nch = gridDim.x;
-  grid_dep_launch();
   if (threadIdx.x == NT - 1) {
     mbar_init(&bar_cb, 1);
     mbar_init(&bar_x[0], 1);
@@ -325,8 +322,7 @@ __global__ void __launch_bounds__(NT, 2)
     fence_barrier_init();
     s_abort = 0;
   }
-  if (warp == W_ISSUE) tmem_alloc(&tmem_base, 256);
-  grid_dep_wait();
+  enter(&tmem_base, 256, warp == W_ISSUE);
   const Share w(s, lengths, blockIdx.y, pg, hs);
   const long r0 = (long)w.b * s.N + w.n0;
   w.params(par_, A, skip, bias);
@@ -441,9 +437,10 @@ __global__ void __launch_bounds__(NT, 2)
 #pragma unroll
               for (int c = 0; c < 32; c += 4) {
                 const float4 u = *reinterpret_cast<const float4*>(&g.wp[32 * J + c]), d = *reinterpret_cast<const float4*>(&g.del[32 * J + c]);
-                // taken for masked pairs too and dropped by a select, not a branch
-                float p0 = a[c] * (ex2_fast(fminf(wp - u.x, 0.f)) * d.x), p1 = a[c + 1] * (ex2_fast(fminf(wp - u.y, 0.f)) * d.y);
-                float p2 = a[c + 2] * (ex2_fast(fminf(wp - u.z, 0.f)) * d.z), p3 = a[c + 3] * (ex2_fast(fminf(wp - u.w, 0.f)) * d.w);
+                // taken for masked pairs too (an overflow or NaN there goes with them) and
+                // dropped by a select, not a branch
+                float p0 = a[c] * (ex2_fast(wp - u.x) * d.x), p1 = a[c + 1] * (ex2_fast(wp - u.y) * d.y);
+                float p2 = a[c + 2] * (ex2_fast(wp - u.z) * d.z), p3 = a[c + 3] * (ex2_fast(wp - u.w) * d.w);
                 p0 = c <= lane ? p0 : 0.f, p1 = c + 1 <= lane ? p1 : 0.f;
                 p2 = c + 2 <= lane ? p2 : 0.f, p3 = c + 3 <= lane ? p3 : 0.f;
                 pk[c / 2] = pack_bf16(p0, p1);
@@ -575,15 +572,13 @@ __global__ void __launch_bounds__(NTG, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nch = gridDim.x;
   const bool direct = pg == 1;  // dB and dC themselves, else partial sums
   const int parts = s.G * pg;
-  grid_dep_launch();
   if (threadIdx.x == GT) {
     for (uint64_t* b : {&bar_cb, &bar_in[0], &bar_in[1], &bar_1, &bar_2, &bar_3, &bar_4}) mbar_init(b, 1);
     for (uint64_t* b : {&bar_clear, &bar_p, &bar_c, &bar_x, &bar_free}) mbar_init(b, GT);
     fence_barrier_init();
     s_abort = 0;
   }
-  if (warp == WG_ISSUE) tmem_alloc(&tmem_base, 512);
-  grid_dep_wait();
+  enter(&tmem_base, 512, warp == WG_ISSUE);
   const Share w(s, lengths, blockIdx.y, pg, hs);
   const long r0 = (long)w.b * s.N + w.n0;
   const int in_n = min(TC_C, s.N - w.n0);  // rows of the chunk that exist
@@ -811,7 +806,7 @@ __global__ void __launch_bounds__(NTG, 1)
               // them, pair by pair, took most of this stage)
 #pragma unroll
               for (int c = 0; c < 8; ++c) {
-                float wt_ = ex2_fast(fminf(tv[c] - wp, 0.f));
+                float wt_ = ex2_fast(tv[c] - wp);
                 wt_ = 8 * o + c >= lane ? wt_ : 0.f;
                 e[c] *= wt_;
                 gg[c] = e[c] * a[c];
