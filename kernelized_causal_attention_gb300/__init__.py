@@ -33,6 +33,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "liblinattn.so")
@@ -546,6 +547,14 @@ def _take_opt(t, name, shape, dtype, device):
     return None if t is None else _take(t, name, shape, dtype, device)
 
 
+_INT = (1 << 31) - 1  # the interface's sizes and strides
+
+
+def _need_ints(*shapes):
+    if max(map(max, shapes)) > _INT:
+        raise ValueError(f"sizes above {_INT}")
+
+
 def _take_rows(t, name, shape, dtype, device, lead):
     """(address, row stride) of a token-major view whose first `lead` dimensions are batch (and row):
     rows dense, and all rows of all batch entries evenly spaced."""
@@ -563,11 +572,14 @@ def _take_rows(t, name, shape, dtype, device, lead):
         want *= shape[lead]
     B = shape[0]
     if lead == 1:
-        return t.data_ptr(), st[0] if B > 1 else want
-    N = shape[1]
-    ld = st[1] if N > 1 else (st[0] if B > 1 else want)
-    if B > 1 and st[0] != N * ld:
-        raise ValueError(f"{name}: batch entries must be N rows apart")
+        ld = st[0] if B > 1 else want
+    else:
+        N = shape[1]
+        ld = st[1] if N > 1 else (st[0] if B > 1 else want)
+        if B > 1 and st[0] != N * ld:
+            raise ValueError(f"{name}: batch entries must be N rows apart")
+    if ld > _INT:
+        raise ValueError(f"{name}: rows {ld} elements apart, at most {_INT}")
     return t.data_ptr(), ld
 
 
@@ -600,6 +612,7 @@ def _conv_args(x, w, bias, lengths, lead):
         raise ValueError(f"x: {lead + 1} dimensions, w: [C, K]")
     shape, dtype, dev = x.shape, x.dtype, x.device
     C, K = shape[-1], w.shape[1]
+    _need_ints(shape, w.shape)
     code = _dtype_code(x)
     px, ld = _take_rows(x, "x", shape, dtype, dev, lead)
     pw = _take(w, "w", (C, K), dtype, dev)
@@ -656,6 +669,7 @@ def _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, lengths, lead):
     shape, gshape, dtype, dev = x.shape, Bm.shape, x.dtype, x.device
     rows = shape[:lead]
     H, M, G, D = shape[lead], shape[lead + 1], gshape[lead], gshape[lead + 1]
+    _need_ints(shape, gshape)
     code = _dtype_code(x)
     px, lx = _take_rows(x, "x", shape, dtype, dev, lead)
     pt, lt = _take_rows(dt, "dt", rows + (H,), dtype, dev, lead)
@@ -720,6 +734,7 @@ def _cross_args(q, k, v, lengths):
         raise ValueError("q, k and v: 4 dimensions")
     B, H, Nq, D = q.shape
     Hk, Nk, M = k.shape[1], k.shape[2], v.shape[3]
+    _need_ints(q.shape, k.shape, v.shape)
     code, dtype, dev = _dtype_code(q), q.dtype, q.device
     ptrs = (_take(q, "q", q.shape, dtype, dev), _take(k, "k", (B, Hk, Nk, D), dtype, dev),
             _take(v, "v", (B, Hk, Nk, M), dtype, dev), _take_opt(lengths, "lengths", (B,), torch.int32, dev))
@@ -767,6 +782,7 @@ def cross_step(q, S, Z):
         raise ValueError("q: 3 dimensions, S: 4")
     B, H, D = q.shape
     Hk, M = S.shape[1], S.shape[3]
+    _need_ints(q.shape, S.shape)
     code, dtype, dev = _dtype_code(q), q.dtype, q.device
     pq = _take(q, "q", q.shape, dtype, dev)
     pS = _take(S, "S", (B, Hk, D, M), torch.float32, dev)
@@ -825,6 +841,7 @@ class _ShortConv(torch.autograd.Function):
         return short_conv_fwd(x, w, bias, None, lengths, silu)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         x, w, bias, lengths = ctx.saved_tensors
         return *short_conv_bwd(x, w, bias, dy.contiguous(), lengths, ctx.silu), None, None
@@ -837,6 +854,7 @@ class _Scan(torch.autograd.Function):
         return scan_fwd(x, dt, A, Bm, Cm, skip, dt_bias, None, lengths)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         *inputs, lengths = ctx.saved_tensors
         return *scan_bwd(*inputs, dy.contiguous(), lengths), None
@@ -851,6 +869,7 @@ class _Cross(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, lengths, out, den, S, Z = ctx.saved_tensors
         return *cross_bwd(q, k, v, lengths, out, den, S, Z, dout.contiguous()), None

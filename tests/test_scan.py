@@ -125,6 +125,13 @@ def test_slow_and_fast_decays(cuda, linattn, dtype, decay):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_growing_states(cuda, linattn, dtype):
+    """A > 0: nothing in the chunk form needs the decays to be below one."""
+    test_slow_and_fast_decays(cuda, linattn, dtype, -0.01)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("B,H,G,D,M,dtype", [(1, 1, 1, 16, 16, "f32"), (3, 4, 2, 64, 64, "bf16"), (40, 6, 1, 32, 64, "bf16"), (2, 5, 5, 64, 16, "f32")])
 def test_steps_continue_a_prompt(cuda, linattn, B, H, G, D, M, dtype):
     N, cut = 140, 131
@@ -235,6 +242,26 @@ def test_refusals_of_the_other_calls(linattn):
     assert bwd(F, None, F, need) == linattn.LA_ERR_INVALID_ARG
     step = lambda S, B=1, ldx=64: L.la_scan_step(F, F, F, F, F, None, None, S, F, B, 4, 1, 16, 16, ldx, 4, 16, 16, 0, None)  # noqa: E731
     assert step(None) == 1 and step(F, B=(1 << 18) + 1) == 1 and step(F, ldx=63) == 1
+
+
+def test_binding_refuses_strides_and_sizes_beyond_the_interface(linattn):
+    far = lambda *s: torch.empty_strided(s, (1 << 33, 1 << 32, 16, 1)[-len(s):], device="meta")  # noqa: E731
+    x, dt, A, b = (torch.empty(*s, device="meta") for s in ((2, 1, 4, 16), (2, 1, 4), (4,), (2, 1, 1, 16)))
+    with pytest.raises(ValueError, match="apart, at most"):
+        linattn.scan_fwd(far(2, 1, 4, 16), dt, A, b, b)
+    with pytest.raises(ValueError, match="apart, at most"):
+        linattn.scan_step(far(2, 4, 16).as_strided((2, 4, 16), (1 << 32, 16, 1)), dt[:, 0], A, b[:, 0], b[:, 0], None, None, b)
+    with pytest.raises(ValueError, match="sizes above"):
+        linattn.scan_fwd(torch.empty(1, (1 << 32) + 5, 4, 16, device="meta"), dt, A, b, b)
+
+
+@pytest.mark.gpu
+def test_no_second_derivatives(cuda, linattn):
+    x, b = torch.randn(1, 3, 2, 16, device=cuda, requires_grad=True), torch.randn(1, 3, 1, 16, device=cuda)
+    y = linattn.selective_scan(x, b[..., 0, :2].contiguous(), -torch.ones(2, device=cuda), b, b)
+    g, = torch.autograd.grad(y.square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.sum().backward()
 
 
 def test_binding_refuses(linattn):
