@@ -331,7 +331,7 @@ la_status la_short_conv_step(const void* x, const void* w, const void* bias, voi
  * x [B][N][H][M] (row stride ldx >= H M), dt [B][N][H] (lddt >= H; aligned to its
  * elements), Bm and Cm [B][N][G][D] (ldb, ldc >= G D); ldx, ldb and ldc are
  * multiples of 16 bytes.  A, skip (may be NULL) and dt_bias (may be NULL) are [H]
- * of the call's dtype; A <= 0 keeps the recurrence stable and is not checked.
+ * of the call's dtype; A <= 0 keeps the recurrence stable and is not checked (a state that grows may overflow).
  * y [B][N][H][M] dense.  S [B][H][D][M] float, read as the state before row 0
  * and replaced by the state after each sequence's last valid row, or NULL (from
  * zero, not returned).  G divides H; D and M in {16, 32, 64}; 1 <= B H <= 65535,

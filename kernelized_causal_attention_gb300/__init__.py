@@ -550,9 +550,11 @@ def _take_opt(t, name, shape, dtype, device):
 _INT = (1 << 31) - 1  # the interface's sizes and strides
 
 
-def _need_ints(*shapes):
-    if max(map(max, shapes)) > _INT:
-        raise ValueError(f"sizes above {_INT}")
+def _need_ints(*tensors):
+    """No size is beyond the interface's integers (only a tensor of as many elements can have one)."""
+    for t in tensors:
+        if t.numel() > _INT and max(t.shape) > _INT:
+            raise ValueError(f"sizes above {_INT}")
 
 
 def _take_rows(t, name, shape, dtype, device, lead):
@@ -612,7 +614,7 @@ def _conv_args(x, w, bias, lengths, lead):
         raise ValueError(f"x: {lead + 1} dimensions, w: [C, K]")
     shape, dtype, dev = x.shape, x.dtype, x.device
     C, K = shape[-1], w.shape[1]
-    _need_ints(shape, w.shape)
+    _need_ints(x, w)
     code = _dtype_code(x)
     px, ld = _take_rows(x, "x", shape, dtype, dev, lead)
     pw = _take(w, "w", (C, K), dtype, dev)
@@ -669,7 +671,7 @@ def _scan_args(x, dt, A, Bm, Cm, skip, dt_bias, lengths, lead):
     shape, gshape, dtype, dev = x.shape, Bm.shape, x.dtype, x.device
     rows = shape[:lead]
     H, M, G, D = shape[lead], shape[lead + 1], gshape[lead], gshape[lead + 1]
-    _need_ints(shape, gshape)
+    _need_ints(x, Bm)
     code = _dtype_code(x)
     px, lx = _take_rows(x, "x", shape, dtype, dev, lead)
     pt, lt = _take_rows(dt, "dt", rows + (H,), dtype, dev, lead)
@@ -734,7 +736,7 @@ def _cross_args(q, k, v, lengths):
         raise ValueError("q, k and v: 4 dimensions")
     B, H, Nq, D = q.shape
     Hk, Nk, M = k.shape[1], k.shape[2], v.shape[3]
-    _need_ints(q.shape, k.shape, v.shape)
+    _need_ints(q, k, v)
     code, dtype, dev = _dtype_code(q), q.dtype, q.device
     ptrs = (_take(q, "q", q.shape, dtype, dev), _take(k, "k", (B, Hk, Nk, D), dtype, dev),
             _take(v, "v", (B, Hk, Nk, M), dtype, dev), _take_opt(lengths, "lengths", (B,), torch.int32, dev))
@@ -782,7 +784,7 @@ def cross_step(q, S, Z):
         raise ValueError("q: 3 dimensions, S: 4")
     B, H, D = q.shape
     Hk, M = S.shape[1], S.shape[3]
-    _need_ints(q.shape, S.shape)
+    _need_ints(q, S)
     code, dtype, dev = _dtype_code(q), q.dtype, q.device
     pq = _take(q, "q", q.shape, dtype, dev)
     pS = _take(S, "S", (B, Hk, D, M), torch.float32, dev)

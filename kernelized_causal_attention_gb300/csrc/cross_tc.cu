@@ -9,8 +9,13 @@
 //   k_grad_q T = dout S^T;  gamma = -e^2 (phi(q) . T);  dq = (e T + gamma Z) phi'(q);
 //            R += (e phi(q))^T dout,  r += gamma phi(q)
 //   k_grad_k dk = (v R^T + r) phi'(k),  dv = phi(k) R
-// and k_cross_join (cross.cu) between them.  All are bound by HBM traffic: the
-// products are a few hundred cycles a tile.
+// and k_cross_join (cross.cu) between them.  The products are a few hundred
+// cycles a tile and phi with its splits into terms about as long, so what bounds
+// them is a tile's chain of load, phi, product and read-out at two or three blocks
+// an SM, and the launches.  16 x 8 query heads (4 key heads) x 512 queries, 2048
+// states, 64 x 64, device time with L2 flushed: forward 32 us (51 MB to read and
+// write once: 7.5), gradients 42 (92 MB: 14); by kernel, cold: k_ksum 16,
+// k_read 11, k_grad_q 17, k_grad_k 22, either join 5.7.
 //
 // What is not a bf16 input (phi, S, R) enters its products as bf16 terms: three
 // (2^-24) where the sum is an fp32 output (S), elsewhere two, a = a0 + a1 to
@@ -634,7 +639,9 @@ __global__ void __launch_bounds__(NT, 2)
 
 // ------------------------------------------------------------------ host
 
-// Tiles a block takes in turn: about one wave of the kernel's blocks.
+// Tiles a block takes in turn: about one wave of the kernel's blocks.  (A tile a
+// block and several waves measured the same within the noise and write more
+// records.)
 struct Walk {
   int per, nseg;
   Walk(int heads, int N, int per_sm) {

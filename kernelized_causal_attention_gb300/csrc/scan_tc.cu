@@ -10,9 +10,19 @@
 //   k_out    y = P x + exp(cum) (C S_prev) + skip x,
 //            P_ij = exp(cum_i - cum_j) delta_j (C_i . B_j)
 // Every chunk is independent in the first and the last, so blocks need no order
-// and two of them share an SM: one block's loads and CUDA-core work cover the
-// other's products.  A block takes one chunk and several heads of one group,
-// whose B and C tiles it loads once.
+// and three (k_sums) or two (k_out) share an SM: one block's loads and CUDA-core
+// work cover the other's products.  A block takes one chunk and several heads of
+// one group, whose B and C tiles it loads once.
+// Gradients: k_sums in both directions at once, the carry of both, k_grad (one
+// chunk a block again), and the sums over blocks.
+//
+// A chunk is one 128-row product tile.  Its states cost a head of 64 x 64 16 KB
+// (fp32) and 8 KB (bf16; 16 for the gradients) written and read again, beside 32 KB
+// of x and y; most of that stays in L2 for the next kernel.  Device time, L2
+// flushed, 4 x 2048 rows, 32 heads of 64 x 64, 2 groups: forward 56 us (72 MB to
+// read and write once: 10.6), with the final state 60, gradients 154 (110 MB: 16);
+// of the gradients k_sums takes 39, the carry 22 and k_grad 90 in a profile with
+// cold caches (forward: 24, 11, k_out 26).
 //
 // Decays: within 32 x 32 blocks off the diagonal exp(cum_i - cum_j) is a row
 // factor times a column factor, both taken from the end of the column's block
@@ -21,7 +31,8 @@
 //
 // Roundings: P and the carried states to bf16 before their products (half a
 // step, 2^-8, each on its own part of y), y once.  The chunk sums take w_j x_j
-// as three bf16 terms (2^-24), since the final state is an fp32 output.
+// as three bf16 terms (2^-24) where the final state, an fp32 output, is asked
+// for, else as two (2^-16).
 #include <cudaTypedefs.h>
 
 #include "rows_map.cuh"
@@ -138,7 +149,10 @@ struct Maps {
 // in bf16 (one term would round them twice).  The first term takes x's
 // place in shared memory and the third adds to the second's columns, so three
 // blocks share an SM: one's load, another's conversion and a third's products
-// overlap, and a head's own chain need not.  blockIdx.y = part, or parts + part
+// overlap, and a head's own chain need not (two blocks of twice the buffers: 66 us
+// for the 2 x 4096-row prompt, three 63; training 212 and 208).  The third term and
+// the state: 4 us of 60.  Bound by latency and issue (46 % of cycles) as much as by its 67 MB of
+// sums.  blockIdx.y = part, or parts + part
 // for the reverse sums E = sum_i exp(cum_i) C_i dy_i^T.
 constexpr int S_A = 0, S_T = TILE;  // B or C; the terms
 constexpr int S_SMEM(int terms) { return (1 + terms) * TILE + 1024; }
@@ -295,6 +309,10 @@ __global__ void __launch_bounds__(NT, 3)
 }
 
 // ------------------------------------------------------------------ outputs
+// A head's chain is scores, weights, P x, read-out; the next head's scores are
+// issued during the read-out and a second block fills the rest.  26 us for 256
+// blocks of 8 heads (55 MB read, 34 written: 2.4 times HBM's time); tensor pipe
+// 21 %, issue 43 %.
 constexpr int O_C = 0, O_B = TILE, O_X = 2 * TILE, O_S = 4 * TILE;  // C, B, two x stages, two state stages
 constexpr int O_SMEM = 4 * TILE + 2 * STILE + 1024;
 constexpr uint32_t T_A = 0, T_O = 128, T_CS = 192;  // scores (then P in place), P x, C S
@@ -508,8 +526,11 @@ __global__ void __launch_bounds__(NT, 2)
 // quarter it can reach, warp / 4 the block's column), on one block an SM (all
 // 512 tensor-memory columns, 193 KB of tiles).  The next head's gates and the
 // last head's gate gradient are formed beside the products, the latter by the
-// warps that the masked triangle leaves idle.  Bound by the per-head chain and by
-// instruction issue, not by a unit's rate.
+// warps that the masked triangle leaves idle.  90 us for 128 blocks of 16 heads,
+// 5.6 us a head: bound by the per-head chain and by instruction issue (50 % of
+// cycles), not by a unit's rate (tensor pipe 20 %, HBM 25 %).  Column sums deferred
+// past the products took 218 us and more for the training pass, a compute warp that
+// also issues 229, where this took 212: they spill.
 constexpr int GT = 512, NTG = GT + 32, WG_ISSUE = GT / 32;
 constexpr int G_C = 0, G_B = TILE, G_X = 2 * TILE, G_Y = 4 * TILE, G_S = 6 * TILE, G_R = G_S + 4 * STILE, G_Q = G_R + 4 * STILE;
 // (a stage of S or R is two tiles, its terms)

@@ -9,8 +9,12 @@
 // A thread owns V neighbouring channels and walks a run of rows with the last K
 // inputs (and, backward, the last K values of g) in registers, so every row is
 // read once plus the K - 1 rows (backward 2 (K - 1)) before a run; rows are
-// loaded four at a time, four rows ahead of their use.  Sums and SiLU are fp32; y, dx and
-// the parameters' gradients are rounded once.
+// loaded four at a time, four rows ahead of their use.  Sums and SiLU are fp32; y,
+// dx and the parameters' gradients are rounded once.  4 x 2048 x 2304 bf16, K = 4,
+// L2 flushed: forward 22.5 us (75 MB, 0.49 of the copy rate), gradients 38.9
+// (113 MB, 0.43): what is left is the start and the end of one wave of short walks
+// (issue 52 to 56 %).  A ring of eight rows in flight spilled: 80 us for both
+// against 61.
 #include <algorithm>
 
 #include "common.cuh"
