@@ -89,8 +89,7 @@ __device__ __forceinline__ void stage_state(const float* g, float* nat, float* t
 }
 
 // Sum over the 16 threads that hold one row (tx = 0 .. 15), to all of them.
-template <typename F>
-__device__ __forceinline__ F row_sum(F v) {
+__device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;

@@ -23,8 +23,8 @@
 // This file: the fp32 kernels (chunks of 64 rows, FFMA), the carry and the
 // reductions both paths use, and the single-row step.  The fp32 chunk kernels
 // are bound by the FFMA rate and their shared-memory operands: 4 x 2048 rows, 32
-// heads of 64 x 64, forward 405 us, gradients 1383 (8.6 and 21.5 Gflop, 21 and 16 Tflop/s); 2 x 784 rows,
-// 8 heads of 32 x 32, 38 and 71 (launches and single-chunk latency).
+// heads of 64 x 64, forward 405 us, gradients 1205 (8.6 and 21.5 Gflop, 21 and 18 Tflop/s); 2 x 784 rows,
+// 8 heads of 32 x 32, 38 and 52 (launches and single-chunk latency).
 #include "ffma.cuh"
 #include "scan.cuh"
 
@@ -255,6 +255,31 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// A sum in two floats: s + c to about 2^-45 (Knuth's exact addition), in plain
+// instructions (fp64 ones took a fifth of k_scan_grad's time).
+struct Two {
+  float s = 0.f, c = 0.f;
+  __device__ __forceinline__ void add(float g) {
+    const float t = __fadd_rn(s, g), z = __fsub_rn(t, s);
+    c = __fadd_rn(c, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(g, z)));
+    s = t;
+  }
+  __device__ __forceinline__ void add(float g, float gc) { add(g), c += gc; }
+  __device__ __forceinline__ void add_xor(int o) {
+    const float u = __shfl_xor_sync(0xffffffffu, s, o), uc = __shfl_xor_sync(0xffffffffu, c, o);
+    add(u, uc);
+  }
+};
+
+// k_scan_grad's shared memory (floats): what the head sizes need, so that two
+// blocks share an SM up to 32 x 32 and one above.
+template <int D, int M>
+struct GradTiles {
+  static constexpr int ct = 0, bt = ct + 64 * FLD, cn = bt + D * FLD, bn = cn + 64 * (D + 4), xt = bn + 64 * (D + 4),
+                       gt = xt + M * FLD, gn = gt + M * FLD, qn = gn + 64 * (M + 4), rn = qn + 64 * FLD,
+                       rt = rn + D * (M + 4), st = rt + M * (D + 4), end = st + M * (D + 4);
+};
+
 // Gradients of one chunk and head: dx, ddt, this head's dB and dC (fp32, one
 // partial a head) and the chunk's parameter sums.
 template <int D, int M, typename T>
@@ -266,22 +291,22 @@ __global__ void __launch_bounds__(256)
                 float* __restrict__ pC, float* __restrict__ pp, ScanShape s) {
   grid_dep_enter();
   extern __shared__ float sm[];
-  constexpr int TS = 64 * FLD;  // one tile of up to 64 x 64
-  float* ct = sm;               // C^T, then Q^T
-  float* bt = sm + TS;          // B^T
-  float* cn = sm + 2 * TS;      // C
-  float* bn = sm + 3 * TS;      // B
-  float* xt = sm + 4 * TS;      // x^T
-  float* gt = sm + 5 * TS;      // dy^T
-  float* gn = sm + 6 * TS;      // dy
-  float* pn = sm + 7 * TS;      // P
-  float* qn = sm + 8 * TS;      // Q
-  float* rn = sm + 9 * TS;      // R
-  float* rt = sm + 10 * TS;     // R^T
-  float* st = sm + 11 * TS;     // S_prev^T
+  using L = GradTiles<D, M>;
+  float* ct = sm + L::ct;  // C^T, then Q^T
+  float* bt = sm + L::bt;  // B^T
+  float* cn = sm + L::cn;  // C
+  float* bn = sm + L::bn;  // B
+  float* xt = sm + L::xt;  // x^T
+  float* gt = sm + L::gt;  // dy^T
+  float* gn = sm + L::gn;  // dy
+  float* qn = sm + L::qn;  // Q, then P
+  float* rn = sm + L::rn;  // R
+  float* rt = sm + L::rt;  // R^T
+  float* st = sm + L::st;  // S_prev^T
   __shared__ Cum cum;
   __shared__ float delta[64], z[64], v[64], w[64], xdu[64], red[8];
-  __shared__ double rowg[64], colg[16][64];
+  __shared__ float2 rowg[64], colg[8][64];
+  __shared__ float s_next[3], s_last;
   const int c = blockIdx.x, bh = blockIdx.y, b = bh / s.H, h = bh % s.H, g = h / (s.H / s.G);
   const int n0 = c * FT, nch = gridDim.x;
   const int rows = max(0, min(FT, valid_rows(lengths, b, s.N) - n0));
@@ -299,6 +324,7 @@ __global__ void __launch_bounds__(256)
   const float Ah = par(A, h), sk = par(skip, h);
   gates(dt + r0 * s.lddt + h, s.lddt, rows, par(bias, h), Ah, delta, cum, z);
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15, i0 = ty * 4, j0 = tx * 4;
+  float p[4][4];  // P, until Q has been read
   {
     float a[4][4], e[4][4];
     zero_acc(a);
@@ -306,32 +332,34 @@ __global__ void __launch_bounds__(256)
     ffma_mm(a, ct, FLD, bt, FLD, D);
     ffma_mm(e, gt, FLD, xt, FLD, M);
     __syncthreads();  // C^T has been read: Q^T takes its place
-    // Row and column sums of the same G are subtracted below: in 64 bits what they
-    // share cancels exactly, in 32 it left 3e-6 in dA
-    double rs[4] = {0, 0, 0, 0}, cs[4] = {0, 0, 0, 0};
+    // Row and column sums of the same G are subtracted below: in two floats what they
+    // share cancels, in one it left 3e-6 in dA
+    Two rs[4], cs[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int i = i0 + r, j = j0 + q;
         const float wt = j <= i ? cum.decay(i, j) : 0.f;
-        const float p = wt * a[r][q], qq = wt * delta[j] * e[r][q];
-        pn[i * FLD + j] = p;
+        p[r][q] = wt * a[r][q];
+        const float qq = wt * delta[j] * e[r][q];
         qn[i * FLD + j] = qq;
         ct[j * FLD + i] = qq;
-        if (j < i) {  // a pair with itself feels no decay
-          const double gg = qq * a[r][q];
-          rs[r] += gg;
-          cs[q] += gg;
-        }
+        const float gg = j < i ? __fmul_rn(qq, a[r][q]) : 0.f;  // a pair with itself feels no decay
+        rs[r].add(gg);
+        cs[q].add(gg);
       }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const double t = row_sum(rs[r]);
-      if (tx == 0) rowg[i0 + r] = t;
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) rs[r].add_xor(o);
+      if (tx == 0) rowg[i0 + r] = make_float2(rs[r].s, rs[r].c);
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) colg[ty][j0 + q] = cs[q];
+    for (int q = 0; q < 4; ++q) {
+      cs[q].add_xor(16);
+      if ((ty & 1) == 0) colg[ty >> 1][j0 + q] = make_float2(cs[q].s, cs[q].c);
+    }
   }
   __syncthreads();
   const long prow = (r0 * s.H + h) * D;  // this head's partial of row n0
@@ -378,6 +406,10 @@ __global__ void __launch_bounds__(256)
     for (int r = 0; r < 4; ++r)
       if (n0 + i0 + r < s.N) store_cols(pB + prow + (long)(i0 + r) * s.H * D + d0, acc[r]);
   }
+  __syncthreads();  // Q has been read: P takes its place
+#pragma unroll
+  for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(qn + (i0 + r) * FLD + j0) = make_float4(p[r][0], p[r][1], p[r][2], p[r][3]);
+  __syncthreads();
   float dskip = 0.f;
   {
     // dx
@@ -390,7 +422,7 @@ __global__ void __launch_bounds__(256)
     for (int r = 0; r < 4; ++r)
 #pragma unroll
       for (int q = 0; q < CC; ++q) acc[r][q] *= cum.to_end(i0 + r);
-    ffma_mm(acc, pn, FLD, gn, M + 4, FT);
+    ffma_mm(acc, qn, FLD, gn, M + 4, FT);
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int j = i0 + r;
@@ -409,24 +441,35 @@ __global__ void __launch_bounds__(256)
   }
   sr = block_sum(sr, red);
   dskip = block_sum(dskip, red);
-  if (threadIdx.x < 64) {
-    double cg = 0;
+  // dl: sums over the rows from t on, and over those before t
+  const int t = threadIdx.x, lane = t & 31;
+  Two pairs;
+  float from = 0.f, upto = 0.f, before = 0.f;
+  if (t < 64) {
+    pairs.add(rowg[t].x, rowg[t].y);
 #pragma unroll
-    for (int q = 0; q < 16; ++q) cg += colg[q][threadIdx.x];
-    rowg[threadIdx.x] -= cg;
+    for (int q = 0; q < 8; ++q) pairs.add(-colg[q][t].x, -colg[q][t].y);
+    from = v[t];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float ps = __shfl_down_sync(0xffffffffu, pairs.s, o), pc = __shfl_down_sync(0xffffffffu, pairs.c, o);
+      const float f = __shfl_down_sync(0xffffffffu, from, o);
+      if (lane + o < 32) pairs.add(ps, pc), from += f;
+    }
+    upto = warp_prefix(w[t]);
+    before = __shfl_up_sync(0xffffffffu, upto, 1);
+    if (lane == 0) before = 0.f;
+    if (t == 31) s_last = upto;
+    if (t == 32) s_next[0] = pairs.s, s_next[1] = pairs.c, s_next[2] = from;
   }
   __syncthreads();
   float dA = 0.f, db = 0.f;
-  const int t = threadIdx.x;
   if (t < 64) {
-    double pairs = 0;
-    float dl = cum.from_start(63) * sr;
-    for (int i = t; i < 64; ++i) {
-      pairs += rowg[i];
-      dl += v[i];
-    }
-    for (int j = 0; j < t; ++j) dl += w[j];
-    dl += (float)pairs;
+    if (t < 32)
+      pairs.add(s_next[0], s_next[1]), from += s_next[2];
+    else
+      before += s_last;
+    const float dl = fmaf(cum.from_start(63), sr, from + before) + (pairs.s + pairs.c);
     const float dd = xdu[t] + Ah * dl;
     const float dz = t < rows ? dd / (1.f + expf(-z[t])) : 0.f;
     if (n0 + t < s.N) ddt[(r0 + t) * s.H + h] = from_f<T>(dz);
@@ -644,7 +687,7 @@ cudaError_t scan_bwd_cc(const ScanIn& a, const void* dy_, const ScanGrads& d, vo
     constexpr size_t b1 = 64 * (D_ + M_ + 8) * 4;
     LA_TRY_CUDA(launch_pdl(k_scan_sums<D_, M_, T>, grid, block, b1, st, x, dt, A, Bm, Cm, bias, a.lengths, dy, fwd, rev, tot, s));
     LA_TRY_CUDA(scan_carry(fwd, rev, tot, nullptr, BH, nch, D_ * M_, st));
-    constexpr size_t b2 = 12 * 64 * FLD * 4;
+    constexpr size_t b2 = GradTiles<D_, M_>::end * 4;
     LA_TRY_CUDA(smem(&k_scan_grad<D_, M_, T>, b2));
     LA_TRY_CUDA(launch_pdl(k_scan_grad<D_, M_, T>, grid, block, b2, st, x, dt, A, Bm, Cm, skip, bias, a.lengths, dy,
                            (const float*)fwd, (const float*)rev, (T*)d.x, (T*)d.dt, pB, pC, pp, s));
