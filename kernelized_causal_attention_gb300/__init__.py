@@ -605,7 +605,7 @@ def _scratch(n, like):
     """(workspace or None, its address, its size)"""
     if n == 0:
         return None, None, 0
-    ws = like.new_empty((n,), dtype=torch.uint8)
+    ws = torch.empty((n,), dtype=torch.uint8, device=like.device)
     return ws, ws.data_ptr(), n
 
 
@@ -631,7 +631,7 @@ def short_conv_fwd(x, w, bias=None, state=None, lengths=None, silu=True):
     (B, N, _), C, K, code, dtype, dev, px, ld, pw, pb, pn = _conv_args(x, w, bias, lengths, 2)
     ps = _take_opt(state, "state", (B, K - 1, C), dtype, dev)
     _need_cuda(x)
-    y = x.new_empty((B, N, C))
+    y = torch.empty((B, N, C), dtype=dtype, device=dev)
     _check(lib().la_short_conv_fwd(px, pw, pb, pn, ps, y.data_ptr(), B, N, C, K, ld, int(silu), code, _stream(None)),
            "la_short_conv_fwd")
     return y
@@ -644,7 +644,7 @@ def short_conv_bwd(x, w, bias, dy, lengths=None, silu=True):
     B, N, _ = shape
     pg = _take(dy, "dy", shape, dtype, dev)
     _need_cuda(x)
-    dx, dw = x.new_empty((B, N, C)), torch.empty_like(w)
+    dx, dw = torch.empty((B, N, C), dtype=dtype, device=dev), torch.empty_like(w)
     db = None if bias is None else torch.empty_like(bias)
     ws, pws, nws = _scratch(lib().la_short_conv_workspace_bytes(B, N, C, K, code), x)
     _check(lib().la_short_conv_bwd(px, pw, pb, pn, pg, dx.data_ptr(), dw.data_ptr(), None if db is None else db.data_ptr(),
@@ -658,7 +658,7 @@ def short_conv_step(x, w, bias, state, silu=True):
     (B, _), C, K, code, dtype, dev, px, ld, pw, pb, _ = _conv_args(x, w, bias, None, 1)
     ps = _take(state, "state", (B, K - 1, C), dtype, dev)
     _need_cuda(x)
-    y = x.new_empty((B, C))
+    y = torch.empty((B, C), dtype=dtype, device=dev)
     _check(lib().la_short_conv_step(px, pw, pb, ps, y.data_ptr(), B, C, K, ld, int(silu), code, _stream(None)),
            "la_short_conv_step")
     return y
@@ -694,7 +694,7 @@ def scan_fwd(x, dt, A, Bm, Cm, skip=None, dt_bias=None, S=None, lengths=None):
     B, N = x.shape[:2]
     pS = _take_opt(S, "S", (B, H, D, M), torch.float32, dev)
     _need_cuda(x)
-    y = x.new_empty((B, N, H, M))
+    y = torch.empty((B, N, H, M), dtype=dtype, device=dev)
     ws, pws, nws = _scratch(lib().la_scan_workspace_bytes(0, B, H, G, N, D, M, code), x)
     _check(lib().la_scan_fwd(*ptrs, pS, y.data_ptr(), pws, nws, B, H, G, N, D, M, *ld, code, _stream(None)),
            "la_scan_fwd")
@@ -709,7 +709,7 @@ def scan_bwd(x, dt, A, Bm, Cm, skip, dt_bias, dy, lengths=None):
     B, N = x.shape[:2]
     pg = _take(dy, "dy", x.shape, dtype, dev)
     _need_cuda(x)
-    new, h = x.new_empty, (H,)
+    new, h = functools.partial(torch.empty, dtype=dtype, device=dev), (H,)
     d = (new((B, N, H, M)), new((B, N, H)), new(h), new((B, N, G, D)), new((B, N, G, D)), None if skip is None else new(h),
          None if dt_bias is None else new(h))
     ws, pws, nws = _scratch(lib().la_scan_workspace_bytes(1, B, H, G, N, D, M, code), x)
@@ -726,7 +726,7 @@ def scan_step(x, dt, A, Bm, Cm, skip, dt_bias, S):
     B = x.shape[0]
     pS = _take(S, "S", (B, H, D, M), torch.float32, dev)
     _need_cuda(x)
-    y = x.new_empty((B, H, M))
+    y = torch.empty((B, H, M), dtype=dtype, device=dev)
     _check(lib().la_scan_step(*ptrs[:7], pS, y.data_ptr(), B, H, G, D, M, *ld, code, _stream(None)), "la_scan_step")
     return y
 
@@ -751,9 +751,9 @@ def cross_fwd(q, k, v, lengths=None):
     ptrs, size, code, dtype, dev = _cross_args(q, k, v, lengths)
     B, H, Hk, Nq, Nk, D, M = size
     _need_cuda(q)
-    new, f32 = q.new_empty, torch.float32
-    out, den = new((B, H, Nq, M)), new((B, H, Nq), dtype=f32)
-    S, Z = new((B, Hk, D, M), dtype=f32), new((B, Hk, D), dtype=f32)
+    new = functools.partial(torch.empty, dtype=torch.float32, device=dev)
+    out, den = torch.empty((B, H, Nq, M), dtype=dtype, device=dev), new((B, H, Nq))
+    S, Z = new((B, Hk, D, M)), new((B, Hk, D))
     ws, pws, nws = _scratch(lib().la_cross_workspace_bytes(0, *size, code), q)
     _check(lib().la_cross_fwd(*ptrs, out.data_ptr(), den.data_ptr(), S.data_ptr(), Z.data_ptr(), pws, nws, *size,
                               code, _stream(None)), "la_cross_fwd")
@@ -790,7 +790,7 @@ def cross_step(q, S, Z):
     pS = _take(S, "S", (B, Hk, D, M), torch.float32, dev)
     pZ = _take(Z, "Z", (B, Hk, D), torch.float32, dev)
     _need_cuda(q)
-    y = q.new_empty((B, H, M))
+    y = torch.empty((B, H, M), dtype=dtype, device=dev)
     _check(lib().la_cross_step(pq, pS, pZ, y.data_ptr(), B, H, Hk, D, M, code, _stream(None)), "la_cross_step")
     return y
 

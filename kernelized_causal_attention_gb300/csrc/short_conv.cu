@@ -399,11 +399,12 @@ __global__ void __launch_bounds__(128)
 struct Walk {
   int rows, groups;
   Walk(int N, long columns, int lost, int per_sm) {
+    const long slots = (long)per_sm * sm_count();
     double best = 0;
     rows = U, groups = 1;
     for (int r = 2 * U; r <= 16 * U; r += U) {
       const int g = (N + (r - lost) * RG - 1) / ((r - lost) * RG);
-      const long waves = (columns * g + per_sm * sm_count() - 1) / (per_sm * sm_count());
+      const long waves = (columns * g + slots - 1) / slots;
       const double cost = (double)waves * (r + 6);
       if (r == 2 * U || cost < best) best = cost, rows = r, groups = g;
     }
