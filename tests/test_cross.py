@@ -82,6 +82,42 @@ def test_padded_states_are_not_read(cuda, linattn, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_offsets_beyond_32_bits(cuda, linattn, dtype):
+    """More than 2^31 elements of queries, then of encoder states: the last head's last rows equal those of
+    a call on them alone (a row of a product does not depend on the others)."""
+    H, D, M, tail, Ne = 8, 32, 32, 128, 150
+    N = ((1 << 31) // (H * D) + 3000) // 128 * 128
+    last = lambda t: t[:, :, -tail:].contiguous()  # noqa: E731
+    k, v = torch.randn(1, H, Ne, D, device=cuda).to(dtype), torch.randn(1, H, Ne, M, device=cuda).to(dtype)
+    q = torch.empty(1, H, N, D, dtype=dtype, device=cuda).normal_()
+    out, den, S, Z = linattn.cross_fwd(q, k, v)
+    few = linattn.cross_fwd(last(q), k, v)
+    assert torch.equal(out[:, -1, -tail:], few[0][:, -1]) and torch.equal(den[:, -1, -tail:], few[1][:, -1])
+    dout = torch.empty_like(out).normal_()
+    dq = linattn.cross_bwd(q, k, v, None, out, den, S, Z, dout)[0]
+    few_dq = linattn.cross_bwd(last(q), k, v, None, *few, last(dout))[0]
+    assert torch.equal(dq[:, -1, -tail:], few_dq[:, -1])
+    del out, den, dout, dq
+    # the long tensor as keys, of whose values only the last 100 of the last head are not zero
+    vl = torch.zeros(1, H, N, M, dtype=dtype, device=cuda)
+    vl[:, -1, -100:] = torch.randn(100, M, device=cuda).to(dtype)
+    out, den, S, Z = linattn.cross_fwd(k, q, vl)
+    phi = plain64.phi(q[0, -1, -100:].double()).T
+    bound = (100 + 64) * F32 + (2.0 ** -16 if dtype == torch.bfloat16 else 0)
+    err = (S[0, -1].double() - phi @ vl[0, -1, -100:].double()).abs()
+    assert (err <= bound * (phi @ vl[0, -1, -100:].double().abs())).all()
+    assert float(S[0, :-1].abs().max()) == 0.0
+    # Z: at most 1800 tiles of 64 rows summed in turn, then the blocks' sums
+    assert (Z[0, -1].double() / plain64.phi(q[0, -1].double()).sum(0) - 1).abs().max() <= 1800 * 64 * F32
+    dout = torch.randn(1, H, Ne, M, device=cuda).to(dtype)
+    grads = linattn.cross_bwd(k, q, vl, None, out, den, S, Z, dout)[1:]
+    few = linattn.cross_bwd(k, last(q), last(vl), None, out, den, S, Z, dout)[1:]
+    for a, b in zip(grads, few):
+        assert torch.equal(a[:, -1, -tail:], b[:, -1]) and torch.isfinite(b).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("B,H,Hk,D,M,dtype", [(1, 1, 1, 16, 16, "f32"), (3, 4, 2, 64, 64, "bf16"), (70, 6, 2, 32, 64, "bf16"), (2, 2, 2, 64, 16, "f32")])
 def test_step_reads_the_kept_states(cuda, linattn, B, H, Hk, D, M, dtype):
     q, k, v, _ = inputs(B, H, Hk, 1, 90, D, M, dtype, 2)

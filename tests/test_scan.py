@@ -104,6 +104,46 @@ def test_backward(cuda, linattn, B, N, H, G, D, M, dtype, lengths):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("N,H,G,D,M,dtype,lengths", [
+    (4300, 1, 1, 16, 16, "f32", [4290]),      # 68 chunks: the carry in segments
+    (8800, 2, 1, 16, 32, "bf16", [8500]),     # 69
+    (300, 40, 1, 16, 16, "bf16", None),       # more heads to a group than a block takes
+])
+def test_long_and_wide(cuda, linattn, N, H, G, D, M, dtype, lengths):
+    test_forward(cuda, linattn, 1, N, H, G, D, M, dtype, lengths)
+    test_backward(cuda, linattn, 1, N, H, G, D, M, dtype, lengths)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_offsets_beyond_32_bits(cuda, linattn, dtype):
+    """More than 2^31 elements; the last rows against the recurrence over them alone, which a decay of
+    at least exp(-1) a row makes exact after 200 rows."""
+    H, G, D, M, tail, warm = 64, 1, 16, 32, 400, 200
+    N = (1 << 31) // (H * M) + 777
+    t, rows = T[dtype], torch.empty(1, N, H * M, dtype=T[dtype], device=cuda).normal_()
+    bc = torch.empty(1, N, 2 * G * D, dtype=t, device=cuda).normal_()
+    dt = torch.full((1, N, H), 1.0, dtype=t, device=cuda)
+    A, skip = torch.full((H,), -1.0, dtype=t, device=cuda), torch.ones(H, dtype=t, device=cuda)
+    x, b, c = rows.unflatten(-1, (H, M)), bc[..., :G * D].unflatten(-1, (G, D)), bc[..., G * D:].unflatten(-1, (G, D))
+    args = [x, dt, A, b, c, skip, None]
+    cpu = [a if a is None else (a[:, -tail:] if a.dim() > 1 else a).cpu() for a in args]
+    p = {"dt": cpu[1], "A": cpu[2], "dt_bias": None}
+    y = linattn.scan_fwd(*args)[:, -tail:].cpu()
+    want, size = plain64.scan(*cpu, None), plain64.scan(*cpu, None, size=True)
+    within(y[:, warm:], want["y"][:, warm:], rel(p, tail, dtype) * size["y"][:, warm:], "y")
+    dy = torch.zeros_like(x)
+    dy[:, -tail + warm:] = torch.empty_like(dy[:, -tail + warm:]).normal_()
+    g = dy[:, -tail:].cpu()
+    want, size = plain64.scan(*cpu, None, None, g), plain64.scan(*cpu, None, None, g, size=True)
+    dx, ddt, dA, dB, dC, dskip, _ = linattn.scan_bwd(*args[:6], None, dy)
+    for k, got in (("dx", dx), ("dBm", dB), ("dCm", dC)):
+        got = got[:, -tail:].cpu()
+        within(got[:, warm:], want[k][:, warm:], rel(p, tail, dtype) * size[k][:, warm:], k)
+    assert float(dx[:, :1000].abs().max()) == 0.0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("decay", [0.0, 1e-4, 40.0])
 def test_slow_and_fast_decays(cuda, linattn, dtype, decay):

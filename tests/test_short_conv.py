@@ -91,6 +91,28 @@ def test_steps_continue_a_prompt(cuda, linattn, B, C, K, dtype, pad):
 
 
 @pytest.mark.gpu
+def test_offsets_beyond_32_bits(cuda, linattn):
+    """More than 2^31 elements in rows of a wider buffer: the last rows equal those of the tail alone."""
+    C, K, cut = 2304, 4, 300
+    N = (1 << 31) // C + 999
+    x = torch.empty(1, N, C + 8, dtype=torch.bfloat16, device=cuda).normal_()[..., :C]
+    w, b = torch.randn(C, K, device=cuda).bfloat16(), torch.randn(C, device=cuda).bfloat16()
+    y = linattn.short_conv_fwd(x, w, b)
+    hist = x[:, -cut - K + 1:-cut].contiguous()
+    assert torch.equal(y[:, -cut:], linattn.short_conv_fwd(x[:, -cut:], w, b, state=hist))
+    dy = torch.zeros_like(y)
+    dy[:, -cut:] = 1.0
+    dx, dw, db = linattn.short_conv_bwd(x, w, b, dy)
+    part = linattn.short_conv_bwd(x[:, -cut - K:], w, b, dy[:, -cut - K:].contiguous())
+    assert torch.equal(dx[:, -cut - K + 1:], part[0][:, 1:]) and float(dx[:, :-cut - K].abs().max()) == 0.0
+    # dw and db: the same terms in another order, 96 fp32 roundings of 300 terms below 1.1 x (|x| < 6) each
+    # side at most, and the result's own
+    for a, c in ((dw, part[1]), (db, part[2])):
+        err = (a.double() - c.double()).abs()
+        assert (err <= 2.01 * 2.0 ** -8 * c.double().abs() + 2 * 96 * 2.0 ** -24 * cut * 1.1 * 6).all()
+
+
+@pytest.mark.gpu
 def test_padded_rows_are_not_read(cuda, linattn):
     _, x, w, b, s, dy = inputs(2, 50, 32, 4, "bf16")
     n = torch.tensor([0, 13], dtype=torch.int32, device=cuda)
