@@ -15,7 +15,7 @@
 // tiles, FFMA), the sums over partial records, and the single-token read.  The
 // fp32 tile kernels are bound by the FFMA rate and their shared-memory operands:
 // 16 x 8 query heads (4 key heads) x 512 queries, 2048 states, 64 x 64: forward
-// 99 us, gradients 173 (1.6 and 3.2 Gflop, 16 to 18 Tflop/s).
+// 95 us, gradients 173 (1.6 and 3.2 Gflop, 16 to 18 Tflop/s).
 #include "ffma.cuh"
 #include "scan.cuh"
 

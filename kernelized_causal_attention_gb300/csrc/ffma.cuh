@@ -72,11 +72,13 @@ __device__ __forceinline__ void stage(const T* g, long stride, int rows, float* 
   }
 }
 
-// A [D][M] fp32 matrix into a tile, natural (ld M + 4) and / or transposed (ld D + 4).
+// A [D][M] fp32 matrix into a tile, natural (ld M + 4) and / or transposed (ld D + 4);
+// lanes along its rows where only the natural form is wanted, else down its columns
+// (the transposed form's banks).
 template <int D, int M>
 __device__ __forceinline__ void stage_state(const float* g, float* nat, float* tr) {
   for (int e = threadIdx.x; e < D * M / 4; e += 256) {
-    const int d = e % D, m = e / D * 4;
+    const int d = tr == nullptr ? e / (M / 4) : e % D, m = tr == nullptr ? e % (M / 4) * 4 : e / D * 4;
     const float4 v = *reinterpret_cast<const float4*>(g + d * M + m);
     if (nat != nullptr) *reinterpret_cast<float4*>(nat + d * (M + 4) + m) = v;
     if (tr != nullptr) {
