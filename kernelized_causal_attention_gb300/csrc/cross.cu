@@ -15,7 +15,7 @@
 // tiles, FFMA), the sums over partial records, and the single-token read.  The
 // fp32 tile kernels are bound by the FFMA rate and their shared-memory operands:
 // 16 x 8 query heads (4 key heads) x 512 queries, 2048 states, 64 x 64: forward
-// 95 us, gradients 173 (1.6 and 3.2 Gflop, 16 to 18 Tflop/s).
+// 89 us, gradients 169 (1.6 and 3.2 Gflop, 18 to 19 Tflop/s).
 #include "ffma.cuh"
 #include "scan.cuh"
 
@@ -50,9 +50,13 @@ __global__ void __launch_bounds__(256)
     const int rows = min(FT, L - c * FT);
     if (rows <= 0) break;
     const long r0 = (long)bh * N + (long)c * FT;
+    Rows<T, D> ku;
+    Rows<T, M> vu;
     __syncthreads();
-    stage<T, D>(k + r0 * D, D, rows, kt, D + 4, nullptr);
-    stage<T, M>(v + r0 * M, M, rows, vt, M + 4, nullptr);
+    ku.fetch(k + r0 * D, D, rows);
+    vu.fetch(v + r0 * M, M, rows);
+    ku.put(kt, D + 4, nullptr);
+    vu.put(vt, M + 4, nullptr);
     __syncthreads();
     phi_nat<D>(kt, rows);
     __syncthreads();
@@ -71,8 +75,8 @@ __global__ void __launch_bounds__(256)
 
 // S and Z (or R and r) of every key head: the sum of its records, in order.  A
 // launch of its own (4 to 6 us cold): summing the records in each block that reads
-// them, 4 to 13 of them, took longer (bf16 forward 32.8 us against 31.7, fp32 145
-// against 99 at the sizes above).
+// them, 4 to 13 of them, took longer (bf16 forward 32.8 us against 31.7; fp32, at
+// the sizes above and before the tile loads were gathered, 145 against 99).
 __global__ void __launch_bounds__(256)
     k_cross_join(const float* __restrict__ rec, float* __restrict__ S, float* __restrict__ Z, int nrec, int DM, int D) {
   grid_dep_enter();
@@ -102,8 +106,12 @@ __global__ void __launch_bounds__(256)
   __shared__ float zs[D], ds[64];
   const int n0 = blockIdx.x * FT, bh = blockIdx.y, rows = min(FT, N - n0);
   const long bhk = (long)(bh / H) * Hk + bh % H / (H / Hk), r0 = (long)bh * N + n0;
-  stage<T, D>(q + r0 * D, D, rows, nullptr, 0, qt);
-  stage_state<D, M>(S + bhk * D * M, ss, nullptr);
+  Rows<T, D> qu;
+  State<D, M, false> su;
+  qu.fetch(q + r0 * D, D, rows);
+  su.fetch(S + bhk * D * M);
+  qu.put(nullptr, 0, qt);
+  su.put(ss, nullptr);
   if (threadIdx.x < D) zs[threadIdx.x] = Z[bhk * D + threadIdx.x];
   __syncthreads();
   for (int e = threadIdx.x; e < D * 64; e += 256) qt[e / 64 * FLD + e % 64] = phi(qt[e / 64 * FLD + e % 64]);
@@ -144,7 +152,9 @@ __global__ void __launch_bounds__(256)
   __shared__ float zs[D], es[64], gs[64];
   const int seg = blockIdx.x, bh = blockIdx.y;
   const long bhk = (long)(bh / H) * Hk + bh % H / (H / Hk);
-  stage_state<D, M>(S + bhk * D * M, nullptr, st);
+  State<D, M, true> su;
+  su.fetch(S + bhk * D * M);
+  su.put(nullptr, st);
   if (threadIdx.x < D) zs[threadIdx.x] = Z[bhk * D + threadIdx.x];
   float R[D / 16][M / 16], rr = 0.f;
   zero_acc(R);
@@ -153,15 +163,15 @@ __global__ void __launch_bounds__(256)
   for (int c = seg * per; c < (seg + 1) * per && c * FT < N; ++c) {
     const int rows = min(FT, N - c * FT);
     const long r0 = (long)bh * N + (long)c * FT;
+    Rows<T, D> qu;
+    Rows<T, M> gu;
     __syncthreads();
-    stage<T, D>(q + r0 * D, D, rows, qn, D + 4, nullptr);
-    stage<T, M>(dout + r0 * M, M, rows, gn, M + 4, gt);
-    __syncthreads();
-    if (threadIdx.x < 64) {
-      const int i = threadIdx.x;
-      const float d = i < rows ? den[r0 + i] : 0.f;
-      es[i] = d != 0.f ? 1.f / d : 0.f;
-    }
+    qu.fetch(q + r0 * D, D, rows);
+    gu.fetch(dout + r0 * M, M, rows);
+    const float d = threadIdx.x < rows ? den[r0 + threadIdx.x] : 0.f;
+    qu.put(qn, D + 4, nullptr);
+    gu.put(gn, M + 4, gt);
+    if (threadIdx.x < 64) es[threadIdx.x] = d != 0.f ? 1.f / d : 0.f;
     __syncthreads();
     float acc[4][CC];
     zero_acc(acc);
@@ -222,9 +232,15 @@ __global__ void __launch_bounds__(256)
   const int rows = min(FT, max(0, valid_rows(lengths, bh / Hk, N) - n0));
   const long r0 = (long)bh * N + n0;
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  stage<T, D>(k + r0 * D, D, rows, nullptr, 0, kt);
-  stage<T, M>(v + r0 * M, M, rows, nullptr, 0, vt);
-  stage_state<D, M>(R + (long)bh * D * M, rn, rt);
+  Rows<T, D> ku;
+  Rows<T, M> vu;
+  State<D, M, true> ru;
+  ku.fetch(k + r0 * D, D, rows);
+  ku.put(nullptr, 0, kt);
+  vu.fetch(v + r0 * M, M, rows);
+  vu.put(nullptr, 0, vt);
+  ru.fetch(R + (long)bh * D * M);
+  ru.put(rn, rt);
   if (threadIdx.x < D) rs[threadIdx.x] = r[(long)bh * D + threadIdx.x];
   __syncthreads();
   constexpr int CK = D / 16, CV = M / 16;

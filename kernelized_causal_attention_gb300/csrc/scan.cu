@@ -23,8 +23,8 @@
 // This file: the fp32 kernels (chunks of 64 rows, FFMA), the carry and the
 // reductions both paths use, and the single-row step.  The fp32 chunk kernels
 // are bound by the FFMA rate and their shared-memory operands: 4 x 2048 rows, 32
-// heads of 64 x 64, forward 405 us, gradients 1205 (8.6 and 21.5 Gflop, 21 and 18 Tflop/s); 2 x 784 rows,
-// 8 heads of 32 x 32, 38 and 52 (launches and single-chunk latency).
+// heads of 64 x 64, forward 380 us, gradients 1018 (8.6 and 21.5 Gflop, 23 and 21 Tflop/s); 2 x 784 rows,
+// 8 heads of 32 x 32, 36 and 50 (launches and single-chunk latency).
 #include "ffma.cuh"
 #include "scan.cuh"
 
@@ -94,8 +94,12 @@ __global__ void __launch_bounds__(256)
   if (threadIdx.x == 0) tot[(long)bh * nch + c] = cum.hi[63];
   const int tx0 = (threadIdx.x & 15) * (M / 16), ty0 = (threadIdx.x >> 4) * (D / 16);
   for (int dir = 0; dir < (rev == nullptr ? 1 : 2); ++dir) {
-    stage<T, D>((dir ? Cm + r0 * s.ldc : Bm + r0 * s.ldb) + g * D, dir ? s.ldc : s.ldb, rows, tb, D + 4, nullptr);
-    stage<T, M>(dir ? dy + (r0 * s.H + h) * M : x + r0 * s.ldx + h * M, dir ? (long)s.H * M : s.ldx, rows, tx, M + 4, nullptr);
+    Rows<T, D> bu;
+    Rows<T, M> xu;
+    bu.fetch((dir ? Cm + r0 * s.ldc : Bm + r0 * s.ldb) + g * D, dir ? s.ldc : s.ldb, rows);
+    xu.fetch(dir ? dy + (r0 * s.H + h) * M : x + r0 * s.ldx + h * M, dir ? (long)s.H * M : s.ldx, rows);
+    bu.put(tb, D + 4, nullptr);
+    xu.put(tx, M + 4, nullptr);
     __syncthreads();
     for (int e = threadIdx.x; e < FT * M; e += 256) {
       const int r = e / M;
@@ -215,10 +219,17 @@ __global__ void __launch_bounds__(256)
   const int n0 = c * FT, nch = gridDim.x;
   const int rows = max(0, min(FT, valid_rows(lengths, b, s.N) - n0));
   const long r0 = (long)b * s.N + n0;
-  stage<T, D>(Cm + r0 * s.ldc + g * D, s.ldc, rows, nullptr, 0, ct);
-  stage<T, D>(Bm + r0 * s.ldb + g * D, s.ldb, rows, nullptr, 0, bt);
-  stage<T, M>(x + r0 * s.ldx + h * M, s.ldx, rows, xs, M + 4, nullptr);
-  if (prev != nullptr) stage_state<D, M>(prev + ((long)bh * nch + c) * D * M, ss, nullptr);
+  Rows<T, D> cu, bu;
+  Rows<T, M> xu;
+  State<D, M, false> su;
+  cu.fetch(Cm + r0 * s.ldc + g * D, s.ldc, rows);
+  bu.fetch(Bm + r0 * s.ldb + g * D, s.ldb, rows);
+  xu.fetch(x + r0 * s.ldx + h * M, s.ldx, rows);
+  if (prev != nullptr) su.fetch(prev + ((long)bh * nch + c) * D * M);
+  cu.put(nullptr, 0, ct);
+  bu.put(nullptr, 0, bt);
+  xu.put(xs, M + 4, nullptr);
+  if (prev != nullptr) su.put(ss, nullptr);
   gates(dt + r0 * s.lddt + h, s.lddt, rows, par(bias, h), par(A, h), delta, cum, (float*)nullptr);
   const int i0 = (threadIdx.x >> 4) * 4, j0 = (threadIdx.x & 15) * 4, m0 = (threadIdx.x & 15) * (M / 16);
   {
@@ -311,14 +322,23 @@ __global__ void __launch_bounds__(256)
   const int n0 = c * FT, nch = gridDim.x;
   const int rows = max(0, min(FT, valid_rows(lengths, b, s.N) - n0));
   const long r0 = (long)b * s.N + n0;
-  stage<T, D>(Cm + r0 * s.ldc + g * D, s.ldc, rows, cn, D + 4, ct);
-  stage<T, D>(Bm + r0 * s.ldb + g * D, s.ldb, rows, bn, D + 4, bt);
-  stage<T, M>(x + r0 * s.ldx + h * M, s.ldx, rows, nullptr, 0, xt);
-  stage<T, M>(dy + (r0 * s.H + h) * M, (long)s.H * M, rows, gn, M + 4, gt);
+  Rows<T, D> cu, bu;
+  Rows<T, M> xu, gu;
+  cu.fetch(Cm + r0 * s.ldc + g * D, s.ldc, rows);
+  bu.fetch(Bm + r0 * s.ldb + g * D, s.ldb, rows);
+  xu.fetch(x + r0 * s.ldx + h * M, s.ldx, rows);
+  gu.fetch(dy + (r0 * s.H + h) * M, (long)s.H * M, rows);
+  cu.put(cn, D + 4, ct);
+  bu.put(bn, D + 4, bt);
+  xu.put(nullptr, 0, xt);
+  gu.put(gn, M + 4, gt);
   const float* Sp = prev + ((long)bh * nch + c) * D * M;
   const float* Rp = next + ((long)bh * nch + c) * D * M;
-  stage_state<D, M>(Sp, nullptr, st);
-  stage_state<D, M>(Rp, rn, rt);
+  State<D, M, true> su, ru;
+  su.fetch(Sp);
+  ru.fetch(Rp);
+  su.put(nullptr, st);
+  ru.put(rn, rt);
   float sr = 0.f;
   for (int e = threadIdx.x; e < D * M; e += 256) sr = fmaf(Sp[e], Rp[e], sr);
   const float Ah = par(A, h), sk = par(skip, h);
