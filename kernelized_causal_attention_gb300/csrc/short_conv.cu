@@ -218,9 +218,11 @@ __global__ void __launch_bounds__(CG * RG, 3)
 }
 
 // dx, and each block's sums of g x and g over its rows into
-// part[group][K + 1][C] (fp32; the last plane is the bias's).  History zero.
+// part[group][K + 1][C] (fp32; the last plane is the bias's).  History zero.  (At
+// one channel a bound on the blocks makes the compiler take more than 64
+// registers: 76 us fp32 against 64.)
 template <typename T, int V, int K>
-__global__ void __launch_bounds__(CG * RG, V == 1 ? 1 : 2)
+__global__ void __launch_bounds__(CG * RG, V == 1 ? 0 : 2)
     k_conv_bwd(const T* __restrict__ x, const T* __restrict__ w, const T* __restrict__ bias, const int* __restrict__ lengths,
                const T* __restrict__ dy, T* __restrict__ dx, float* __restrict__ part, int N, int C, long ldx, int silu,
                int groups, int walk) {
