@@ -13,20 +13,6 @@ __device__ __forceinline__ float phi(float x) { return x > 0.f ? x + 1.f : expf(
 // Derivative of eq. 7: 1 for x > 0, exp(x) otherwise.
 __device__ __forceinline__ float dphi(float x) { return x > 0.f ? 1.f : expf(x); }
 
-// The hardware's base-2 exponential and reciprocal (relative error about 2^-22,
-// results below 2^-126 are zero): one instruction each, for values that are
-// rounded to bf16 or weigh terms that are.
-__device__ __forceinline__ float ex2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp_fast(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 

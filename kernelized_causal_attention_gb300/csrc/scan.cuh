@@ -27,6 +27,20 @@ __device__ __forceinline__ void enter(uint32_t* base, uint32_t cols, bool alloca
   }
 }
 
+// The hardware's base-2 exponential and reciprocal (relative error about 2^-22,
+// results below 2^-126 are zero): one instruction each, for values that are
+// rounded to bf16 or weigh terms that are.
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // softplus(x) = log(1 + exp(x)), written so that neither branch overflows.
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
 
