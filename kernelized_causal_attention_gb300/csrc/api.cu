@@ -66,6 +66,15 @@ int check_ws(int op, const Shape& s, const void* ws, size_t bytes) {
   return LA_OK;
 }
 
+// Tensor maps are encoded by the driver, which needs a current context, and a host
+// thread whose first call into CUDA this is (an autograd engine's at its first
+// gradient) has none yet: setting its device makes one current.
+void in_context() {
+  thread_local bool done = false;
+  int dev = 0;
+  if (!done) done = cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
+}
+
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? LA_OK : LA_ERR_CUDA; }
 
 // The RetNet decay must lie in [0, 1] (a NaN fails both comparisons).
@@ -222,6 +231,7 @@ int la_causal_fwd(const void* q, const void* k, const void* v, void* out, float*
   LA_TRY(la::causal_fwd_check(q, k, v, out, den, B, H, N, D, M, dtype));
   const Shape s{B, H, N, D, M, dtype};
   LA_TRY(check_ws(LA_OP_CAUSAL_FWD, s, workspace, workspace_bytes));
+  in_context();
   if (la::tc_eligible(s))
     return from_cuda(la::causal_fwd_tc(q, k, v, out, den, static_cast<float*>(workspace), s,
                                        static_cast<cudaStream_t>(stream)));
@@ -237,6 +247,7 @@ int la_causal_prefill(const void* q, const void* k, const void* v, void* out, fl
   LA_TRY(check_opt_ptr(den));
   const Shape s{B, H, N, D, M, dtype};
   LA_TRY(check_ws(LA_OP_CAUSAL_PREFILL, s, workspace, workspace_bytes));
+  in_context();
   if (la::tc_prefill_eligible(s))
     return from_cuda(la::causal_prefill_tc(q, k, v, out, den, S, Z, static_cast<float*>(workspace),
                                            s, static_cast<cudaStream_t>(stream)));
@@ -252,6 +263,7 @@ int la_causal_bwd(const void* q, const void* k, const void* v, const void* out, 
   LA_TRY(check_ptrs({q, k, v, out, den, dout, dq, dk, dv}));
   const Shape s{B, H, N, D, M, dtype};
   LA_TRY(check_ws(LA_OP_CAUSAL_BWD, s, workspace, workspace_bytes));
+  in_context();
   if (la::tc_eligible(s))
     return from_cuda(la::causal_bwd_tc(q, k, v, out, den, dout, dq, dk, dv,
                                        static_cast<float*>(workspace), s,
@@ -270,6 +282,7 @@ int la_noncausal_fwd(const void* q, const void* k, const void* v, const int* len
   LA_TRY(check_opt_ptr(lengths));
   const Shape s{B, H, N, D, M, dtype};
   LA_TRY(check_ws(LA_OP_NONCAUSAL_FWD, s, workspace, workspace_bytes));
+  in_context();
   return from_cuda(la::noncausal_fwd_cc(q, k, v, lengths, out, den, S, Z,
                                         static_cast<float*>(workspace), s,
                                         static_cast<cudaStream_t>(stream)));
@@ -285,6 +298,7 @@ int la_noncausal_bwd(const void* q, const void* k, const void* v, const int* len
   LA_TRY(check_opt_ptr(lengths));
   const Shape s{B, H, N, D, M, dtype};
   LA_TRY(check_ws(LA_OP_NONCAUSAL_BWD, s, workspace, workspace_bytes));
+  in_context();
   return from_cuda(la::noncausal_bwd_cc(q, k, v, lengths, out, den, S, Z, dout, dq, dk, dv,
                                         static_cast<float*>(workspace), s,
                                         static_cast<cudaStream_t>(stream)));
@@ -297,6 +311,7 @@ int la_causal_fwd_decay(const void* q, const void* k, const void* v, void* out, 
   LA_TRY(check_gamma(gamma));
   const Shape s{B, H, N, D, M, dtype};
   LA_TRY(check_ws(LA_OP_CAUSAL_FWD_DECAY, s, workspace, workspace_bytes));
+  in_context();
   if (la::tc_eligible(s) && gamma >= la::TC_DECAY_MIN)
     return from_cuda(la::causal_fwd_tc(q, k, v, out, den, static_cast<float*>(workspace), s,
                                        static_cast<cudaStream_t>(stream), false, gamma));
@@ -313,6 +328,7 @@ int la_causal_bwd_decay(const void* q, const void* k, const void* v, const void*
   LA_TRY(check_gamma(gamma));
   const Shape s{B, H, N, D, M, dtype};
   LA_TRY(check_ws(LA_OP_CAUSAL_BWD_DECAY, s, workspace, workspace_bytes));
+  in_context();
   if (la::tc_eligible(s) && gamma >= la::TC_DECAY_MIN)
     return from_cuda(la::causal_bwd_tc(q, k, v, out, den, dout, dq, dk, dv,
                                        static_cast<float*>(workspace), s,
@@ -335,6 +351,7 @@ int la_decode_step_proj(const void* x, const void* W, float* S, float* Z, void* 
                         int d_model, int D, int M, int dtype, void* stream) {
   LA_TRY(check_proj(B, H, d_model, D, M, dtype));
   LA_TRY(check_ptrs({x, W, S, Z, y}));
+  in_context();
   return from_cuda(la::decode_step_proj(x, W, S, Z, y, B, H, d_model, D, M,
                                         static_cast<cudaStream_t>(stream)));
 }
@@ -347,6 +364,7 @@ int la_causal_fwd_poly(const void* q, const void* k, const void* v, void* out, f
   LA_TRY(check_opt_ptr(den));
   const Shape s{B, H, N, D, M, dtype};
   LA_TRY(check_ws_poly(LA_OP_CAUSAL_FWD_POLY, s, workspace, workspace_bytes));
+  in_context();
   return from_cuda(la::causal_fwd_poly(q, k, v, out, den, workspace, s, static_cast<cudaStream_t>(stream)));
 }
 
@@ -358,6 +376,7 @@ int la_causal_bwd_poly(const void* q, const void* k, const void* v, const void* 
   LA_TRY(check_ptrs({q, k, v, out, den, dout, dq, dk, dv}));
   const Shape s{B, H, N, D, M, dtype};
   LA_TRY(check_ws_poly(LA_OP_CAUSAL_BWD_POLY, s, workspace, workspace_bytes));
+  in_context();
   return from_cuda(la::causal_bwd_poly(q, k, v, out, den, dout, dq, dk, dv, workspace, s,
                                        static_cast<cudaStream_t>(stream)));
 }
@@ -431,6 +450,7 @@ int la_scan_fwd(const void* x, const void* dt, const void* A, const void* Bm, co
   LA_TRY(check_room(workspace, workspace_bytes, scan_ws(s, false)));
   const la::ScanIn a{x, dt, A, Bm, Cm, skip, dt_bias, lengths};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  in_context();
   return from_cuda(dtype == LA_BF16 ? la::scan_fwd_tc(a, S, y, workspace, s, st) : la::scan_fwd_cc(a, S, y, workspace, s, st));
 }
 
@@ -451,6 +471,7 @@ int la_scan_bwd(const void* x, const void* dt, const void* A, const void* Bm, co
   const la::ScanIn a{x, dt, A, Bm, Cm, skip, dt_bias, lengths};
   const la::ScanGrads d{dx, ddt, dA, dB, dC, dskip, ddt_bias};
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  in_context();
   return from_cuda(dtype == LA_BF16 ? la::scan_bwd_tc(a, dy, d, workspace, s, st) : la::scan_bwd_cc(a, dy, d, workspace, s, st));
 }
 
@@ -480,6 +501,7 @@ int la_cross_fwd(const void* q, const void* k, const void* v, const int* lengths
   LA_TRY(check_ptrs({q, k, v, out, den, S, Z}));
   LA_TRY(check_to(lengths, 4, true));
   LA_TRY(check_room(workspace, workspace_bytes, la::cross_ws_bytes(s, false)));
+  in_context();
   return from_cuda(la::cross_fwd(q, k, v, lengths, out, den, S, Z, static_cast<float*>(workspace), s,
                                  static_cast<cudaStream_t>(stream)));
 }
@@ -492,6 +514,7 @@ int la_cross_bwd(const void* q, const void* k, const void* v, const int* lengths
   LA_TRY(check_ptrs({q, k, v, out, den, S, Z, dout, dq, dk, dv}));
   LA_TRY(check_to(lengths, 4, true));
   LA_TRY(check_room(workspace, workspace_bytes, la::cross_ws_bytes(s, true)));
+  in_context();
   return from_cuda(la::cross_bwd(q, k, v, lengths, den, S, Z, dout, dq, dk, dv, static_cast<float*>(workspace), s,
                                  static_cast<cudaStream_t>(stream)));
 }

@@ -1,6 +1,8 @@
 """The operators together, as a decoder layer uses them: rows are convolved, scanned and then read an
 encoder's states; a prompt is run at once and single tokens continue it; a training step and a decode
 step are captured into CUDA graphs."""
+import threading
+
 import pytest
 import torch
 
@@ -156,3 +158,89 @@ def test_two_streams_at_once(cuda):
     for i in range(2):
         for g in got[i]:
             assert torch.equal(g, want[i])
+
+
+def test_back_to_back_with_the_causal_kernels(cuda):
+    """The causal attention's kernels and these, launched one behind the other without a wait: every
+    kernel may start while the one before it ends, and both take tensor memory."""
+    w, rows, k, v, n = layer(8)
+    wd = {a: t.to(cuda) for a, t in w.items()}
+    rows, k, v = rows.to(cuda), k.to(cuda), v.to(cuda)
+    x, b, c = cut(rows[..., :C].contiguous())
+    dt, dy = rows[..., C:], torch.randn(B, N, H, M, device=cuda).bfloat16()
+    q, kk, vv = (torch.randn(2, 4, 700, 64, device=cuda).bfloat16() for _ in range(3))
+
+    def once():
+        out, den = la.causal_fwd(q, kk, vv)
+        y = la.scan_fwd(x, dt, wd["A"], b, c, wd["skip"], wd["dt_bias"])
+        f = la.cross_fwd(queries(y), k, v)
+        grads = la.causal_bwd(q, kk, vv, out, den, vv)
+        back = la.scan_bwd(x, dt, wd["A"], b, c, wd["skip"], wd["dt_bias"], dy)
+        out2, _ = la.causal_fwd(q, kk, vv)
+        return [out, y, *f, *grads, *back, *la.cross_bwd(queries(y), k, v, None, *f, f[0]), out2]
+
+    want = once()
+    torch.cuda.synchronize()
+    runs = [once() for _ in range(12)]
+    torch.cuda.synchronize()
+    for r in runs:
+        for a, t in zip(r, want):
+            assert torch.equal(a, t)
+    la.check_device_status()
+
+
+def test_first_call_of_a_host_thread(cuda):
+    """A host thread that has made no CUDA call yet (as an autograd engine's before its first gradient)
+    has no context of its own; every raw entry point works as its first call."""
+    w, rows, k, v, n = layer(9)
+    wd = {a: t.to(cuda) for a, t in w.items()}
+    rows, k, v = rows.to(cuda)[..., :C].contiguous(), k.to(cuda), v.to(cuda)
+    x, b, c = cut(rows)
+    dt = torch.randn(B, N, H, device=cuda).bfloat16()
+    y = la.scan_fwd(x, dt, wd["A"], b, c)
+    q = queries(y)
+    f = la.cross_fwd(q, k, v)
+    scan, cross = (B, H, G, N, D, M), (B, H, 2, N, NE, D, M)
+    ld = (C, H, C, C)
+    new = lambda *ts: [torch.full_like(t, float("nan")) for t in ts]  # noqa: E731
+    room = lambda n: torch.empty(n, dtype=torch.uint8, device=cuda)  # noqa: E731
+    s_ws = [room(la.la_scan_workspace_bytes(i, *scan, la.LA_BF16)) for i in (0, 1)]
+    c_ws = [room(la.la_cross_workspace_bytes(i, *cross, la.LA_BF16)) for i in (0, 1)]
+    conv_ws = room(la.la_short_conv_workspace_bytes(B, N, C, K, la.LA_BF16))
+    none = None
+    back = la.scan_bwd(x, dt, wd["A"], b, c, none, none, y)
+    cback = la.cross_bwd(q, k, v, none, *f, f[0])
+    conv, conv_back = la.short_conv_fwd(rows, wd["w"], wd["b"]), la.short_conv_bwd(rows, wd["w"], wd["b"], rows)
+    outs = {"scan_fwd": new(y), "scan_bwd": new(*back[:5]), "cross_fwd": new(*f), "cross_bwd": new(*cback), "conv_fwd": new(conv), "conv_bwd": new(*conv_back)}
+    stream = torch.cuda.current_stream().cuda_stream
+    a = [torch.randn(2, 4, 300, 64, device=cuda).bfloat16() for _ in range(3)]
+    causal, causal_ws = la.causal_fwd(*a), la.workspace(la.LA_OP_CAUSAL_FWD, 2, 4, 300, 64, 64, la.LA_BF16, cuda)
+    outs["causal_fwd"] = new(*causal)
+    o = outs
+    calls = {
+        "scan_fwd": lambda: la.la_scan_fwd(x, dt, wd["A"], b, c, none, none, none, none, *o["scan_fwd"], s_ws[0], *scan, *ld, la.LA_BF16, stream),
+        "scan_bwd": lambda: la.la_scan_bwd(x, dt, wd["A"], b, c, none, none, none, y, *o["scan_bwd"], none, none, s_ws[1], *scan, *ld, la.LA_BF16, stream),
+        "cross_fwd": lambda: la.la_cross_fwd(q, k, v, none, *o["cross_fwd"], c_ws[0], *cross, la.LA_BF16, stream),
+        "cross_bwd": lambda: la.la_cross_bwd(q, k, v, none, *f, f[0], *o["cross_bwd"], c_ws[1], *cross, la.LA_BF16, stream),
+        "conv_fwd": lambda: la.la_short_conv_fwd(rows, wd["w"], wd["b"], none, none, *o["conv_fwd"], B, N, C, K, C, 1, la.LA_BF16, stream),
+        "conv_bwd": lambda: la.la_short_conv_bwd(rows, wd["w"], wd["b"], none, rows, *o["conv_bwd"], conv_ws, B, N, C, K, C, 1, la.LA_BF16, stream),
+    }
+    calls["causal_fwd"] = lambda: la.la_causal_fwd(*a, *o["causal_fwd"], causal_ws, 2, 4, 300, 64, 64, la.LA_BF16, stream)
+    failed = {}
+
+    def first(name):
+        try:
+            calls[name]()
+        except Exception as e:  # noqa: BLE001
+            failed[name] = repr(e)
+
+    for name in calls:
+        t = threading.Thread(target=first, args=(name,))
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    want = {"scan_fwd": [y], "scan_bwd": back[:5], "cross_fwd": f, "cross_bwd": cback, "conv_fwd": [conv], "conv_bwd": conv_back, "causal_fwd": causal}
+    for name, got in outs.items():
+        for u, t in zip(got, want[name]):
+            assert torch.equal(u, t), name
