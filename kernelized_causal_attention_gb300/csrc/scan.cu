@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(32 * CARRY_SEGS)
     k_scan_carry(const float* fwd, const float* rev, O* fs, O* rs, O* fl, O* rl, const float* __restrict__ tot, float* __restrict__ S,
                  int nch, int DM, int per) {
   grid_dep_enter();
-  __shared__ float4 ends[CARRY_SEGS][32];
+  __shared__ float4 ends[CARRY_SEGS][32], start[32];
   __shared__ float decay[CARRY_SEGS];
   const int e = (blockIdx.x * blockDim.x + threadIdx.x) * 4, seg = threadIdx.y, segs = blockDim.y;
   const long bh = blockIdx.y, at = bh * nch * DM + e;
@@ -179,6 +179,9 @@ __global__ void __launch_bounds__(32 * CARRY_SEGS)
   const int first = seg * per, n = min(per, nch - first), c0 = back ? nch - 1 - first : first, dc = back ? -1 : 1;
   float4 run = make_float4(0.f, 0.f, 0.f, 0.f);
   if (segs > 1) {
+    // every segment starts from S and the last one replaces it: read before the barrier
+    // (by one thread for all: past 72 registers a block an SM less, 2.5 us of training)
+    if (seg == 0) start[threadIdx.x] = S != nullptr && !back && live ? *reinterpret_cast<const float4*>(S + bh * DM + e) : run;
     if (live) carry_walk(p, static_cast<O*>(nullptr), static_cast<O*>(nullptr), tt, DM, c0, dc, n, run);
     ends[seg][threadIdx.x] = run;
     float l = 0.f;
@@ -189,15 +192,16 @@ __global__ void __launch_bounds__(32 * CARRY_SEGS)
     __syncthreads();
   }
   if (!live) return;
-  float* Sp = S == nullptr || back ? nullptr : S + bh * DM + e;
-  run = Sp != nullptr ? *reinterpret_cast<const float4*>(Sp) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* Sp = S == nullptr || back ? nullptr : S + bh * DM + e;
+  const float4* from = segs > 1 ? start + threadIdx.x : reinterpret_cast<const float4*>(Sp);
+  run = from != nullptr ? *from : make_float4(0.f, 0.f, 0.f, 0.f);
   for (int k = 0; k < seg; ++k) {
     const float f = decay[k];
     const float4 u = ends[k][threadIdx.x];
     run.x = fmaf(f, run.x, u.x), run.y = fmaf(f, run.y, u.y), run.z = fmaf(f, run.z, u.z), run.w = fmaf(f, run.w, u.w);
   }
   carry_walk(p, out, low, tt, DM, c0, dc, n, run);
-  if (Sp != nullptr && seg == segs - 1) *reinterpret_cast<float4*>(Sp) = run;
+  if (S != nullptr && !back && seg == segs - 1) *reinterpret_cast<float4*>(S + bh * DM + e) = run;
 }
 
 // y of one chunk and head.

@@ -319,3 +319,23 @@ def test_binding_refuses(linattn):
         linattn.scan_fwd(z(2, 5, 16, 4).transpose(2, 3), dt, A, b, b)
     with pytest.raises(ValueError, match="S: shape"):
         linattn.scan_fwd(x, dt, A, b, b, S=z(2, 4, 16, 17))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,dtype", [(64 * 65, "f32"), (64 * 66, "f32"), (128 * 66 - 5, "bf16"), (128 * 79, "bf16")])
+def test_segments_of_the_carry_start_from_the_given_state(cuda, linattn, N, dtype):
+    """Above 64 chunks the carry runs in segments, all of which start from S while the last one replaces it (at
+    66 chunks that one is a single chunk and ends first).  With hardly any decay S reaches every row of y."""
+    B, H, G, D, M = 2, 3, 1, 16, 16
+    p, _, S = inputs(B, N, H, G, D, M, dtype, 7, 1e-4)
+    S = 8 * S
+    h, d = place(p, H, G, D, M, "cpu"), place(p, H, G, D, M, cuda)
+    want, size = (plain64.scan(*[h[k] for k in PARAMS], S, size=s) for s in (False, True))
+    runs = []
+    for _ in range(6):
+        Sd = S.to(cuda)
+        runs.append((linattn.scan_fwd(*[d[k] for k in PARAMS], S=Sd), Sd))
+    within(runs[0][0], want["y"], rel(p, N, dtype) * size["y"], "y")
+    within(runs[0][1], want["S"], (rel(p, N, "f32") + 2.0 ** -24) * size["S"], "S")
+    for y, Sd in runs[1:]:
+        assert torch.equal(y, runs[0][0]) and torch.equal(Sd, runs[0][1])
