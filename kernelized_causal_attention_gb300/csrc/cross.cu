@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(256)
         f[k] = i < rows ? phi(x[k]) : 0.f;
         t = fmaf(f[k], acc[r][k], t);
       }
-      const float g = -e * e * row_sum(t);
+      const float g = -e * (e * row_sum(t));  // (e times e first leaves fp32's range from den = 5e-20 on)
       if (tx == 0) gs[i] = g;
 #pragma unroll
       for (int k = 0; k < CC; ++k) {

@@ -6,7 +6,7 @@
 // head with two TMA stages, two or three blocks an SM:
 //   k_ksum   S += phi(k)^T v,  Z += phi(k) in fp32 on the CUDA cores
 //   k_read   out = (phi(q) S) / den,  den = phi(q) . Z in fp32 on the CUDA cores
-//   k_grad_q T = dout S^T;  gamma = -e^2 (phi(q) . T);  dq = (e T + gamma Z) phi'(q);
+//   k_grad_q T = dout S^T;  gamma = -e (e phi(q) . T);  dq = (e T + gamma Z) phi'(q);
 //            R += (e phi(q))^T dout,  r += gamma phi(q)
 //   k_grad_k dk = (v R^T + r) phi'(k),  dv = phi(k) R
 // and k_cross_join (cross.cu) between them.  The products are a few hundred
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(NT, 2)
       }
       s_dot[wg][row] = dot;
       sync_compute();
-      const float gam = -e * e * (s_dot[0][row] + s_dot[1][row]);
+      const float gam = -e * (e * (s_dot[0][row] + s_dot[1][row]));  // (e times e first leaves fp32's range from den = 5e-20 on)
       const bool done = wtu(&bar_2, k, 137);  // the products that read e phi(q) are done
       if (got && done) {
 #pragma unroll
