@@ -37,9 +37,10 @@ constexpr int W_ISSUE = 8;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr int STILE = 64 * 64 * 2;
 
-// phi by a select: a branch around the exponential would diverge at every value.
+// phi by a select: a branch around the exponential would diverge at every value.  (An
+// infinite exponential of x > 0 is not selected; a NaN is: a minimum would drop it.)
 __device__ __forceinline__ float phif(float x) {
-  const float e = ex2_fast(fminf(x, 0.f) * LOG2E);
+  const float e = ex2_fast(x * LOG2E);
   return x > 0.f ? x + 1.f : e;
 }
 

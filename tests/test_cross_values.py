@@ -59,3 +59,40 @@ def test_small_features(cuda, linattn, dtype, at_q, at_k, rows, D, M):
     got, e = run(linattn, *(t.to(cuda) for t in (q, k, v, dout))), errors(q, k, dtype)
     for name in got:
         within(got[name], want[name], bound(name, e, want, size, dtype), name)
+
+
+def places(want):
+    """Where the 64-bit form is NaN or infinite."""
+    return {n: ~torch.isfinite(t) for n, t in want.items()}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("which,value", [("q", float("nan")), ("k", float("nan")), ("v", float("nan")), ("dout", float("nan")),
+                                         ("q", float("inf")), ("k", float("inf")), ("v", float("-inf")), ("q", float("-inf"))])
+def test_live_nan_and_inf(cuda, linattn, dtype, which, value):
+    """A NaN or an infinity that counts reaches the outputs it enters and no others; -inf in q alone is phi = 0."""
+    g = torch.Generator().manual_seed(6)
+    t = [torch.randn(s, generator=g).to(T[dtype]) for s in ((2, 4, 140, 32), (2, 2, 150, 32), (2, 2, 150, 64), (2, 4, 140, 64))]
+    clean = run(linattn, *(u.to(cuda) for u in t))
+    bad = [u.clone() for u in t]
+    bad[("q", "k", "v", "dout").index(which)][1, 1, 130, 7] = value
+    got = run(linattn, *(u.to(cuda) for u in bad))
+    want = plain64.cross(*bad[:3], None, bad[3])
+    at = places(want)
+    assert any(m.any() for m in at.values()) == (value != float("-inf") or which != "q")
+    for n, m in at.items():
+        assert torch.equal(~torch.isfinite(got[n].cpu()), m), n
+        # the other batch entry is not touched at all
+        assert torch.equal(got[n][0], clean[n][0]), n
+
+
+@pytest.mark.gpu
+def test_a_nan_prompt_and_its_steps_agree(cuda, linattn):
+    g = torch.Generator().manual_seed(7)
+    q, k, v = (torch.randn(s, generator=g).bfloat16().to(cuda) for s in ((1, 2, 1, 64), (1, 2, 9, 64), (1, 2, 9, 64)))
+    q[0, 1, 0, 3] = float("nan")
+    out, _, S, Z = linattn.cross_fwd(q, k, v)
+    y = linattn.cross_step(q[:, :, 0].contiguous(), S, Z)
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(y[0, 1]).all()
+    assert torch.isfinite(out[0, 0]).all() and torch.isfinite(y[0, 0]).all()
