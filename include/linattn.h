@@ -335,7 +335,9 @@ la_status la_short_conv_step(const void* x, const void* w, const void* bias, voi
  * y [B][N][H][M] dense.  S [B][H][D][M] float, read as the state before row 0
  * and replaced by the state after each sequence's last valid row, or NULL (from
  * zero, not returned).  G divides H; D and M in {16, 32, 64}; 1 <= B H <= 65535,
- * H <= 32767.  dt, A and their products are finite.
+ * H <= 32767.  dt, A and their products are finite.  A NaN or an infinity in a valid row
+ * of x, Bm or Cm stays in the state as the recurrence has it, and may reach the rows before
+ * it in its own chunk too (128 rows in bf16, 64 in fp32: products with masked weights).
  * workspace: la_scan_workspace_bytes(0, ...) bytes.
  */
 la_status la_scan_fwd(const void* x, const void* dt, const void* A, const void* Bm, const void* Cm,

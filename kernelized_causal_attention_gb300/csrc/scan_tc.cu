@@ -253,14 +253,15 @@ __global__ void __launch_bounds__(NT, 3)
     for (int i = 0; i < w.nh; ++i) {
       const Gates& g = gates[i & 1];
       if (threadIdx.x == 0 && !back) tot[((long)w.b * s.H + w.h0 + i) * nch + blockIdx.x] = g.off(4) * LN2;
-      const float f = row >= w.rows ? 0.f : (back ? ex2_fast(g.wp[row] + g.off(q)) : g.cf[row] * ex2_fast(g.past(q)));
+      const bool live = row < w.rows;
+      const float f = !live ? 0.f : (back ? ex2_fast(g.wp[row] + g.off(q)) : g.cf[row] * ex2_fast(g.past(q)));
       if (wtu(&bar_x, i & 1, 64)) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint8_t* at = sm + S_T + row * 128 + (((4 * half + c) ^ (row & 7)) << 4);
           const uint4 u = lds128(at);
-          // a row past the length (or weighed by nothing) enters as zeros, whatever it holds
-          const uint32_t v[4] = {f != 0.f ? u.x : 0u, f != 0.f ? u.y : 0u, f != 0.f ? u.z : 0u, f != 0.f ? u.w : 0u};
+          // a row past the length enters as zeros, whatever it holds (one weighed by 0 does not: its NaN counts)
+          const uint32_t v[4] = {live ? u.x : 0u, live ? u.y : 0u, live ? u.z : 0u, live ? u.w : 0u};
           uint32_t t[TERMS][4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {

@@ -339,3 +339,30 @@ def test_segments_of_the_carry_start_from_the_given_state(cuda, linattn, N, dtyp
     within(runs[0][1], want["S"], (rel(p, N, "f32") + 2.0 ** -24) * size["S"], "S")
     for y, Sd in runs[1:]:
         assert torch.equal(y, runs[0][0]) and torch.equal(Sd, runs[0][1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("decay", [1.0, 200.0])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_live_nan_stays_in_the_state(cuda, linattn, dtype, decay, value):
+    """What the recurrence makes of a row that is not a number: every later row of its column and the final
+    state, even where the decay over the rest of the chunk is zero (0 times NaN); earlier chunks, other heads
+    and other sequences are untouched, and so are the gradients' rows after the chunk."""
+    B, N, H, G, D, M, at = 2, 420, 3, 1, 32, 16, 140
+    p, dy, S = inputs(B, N, H, G, D, M, dtype, 8, decay)
+    p["dt_bias"] = torch.zeros_like(p["dt_bias"])
+    p["rows"][1, at, M + 5] = value  # x of head 1, column 5
+    d = place(p, H, G, D, M, cuda)
+    Sd = S.to(cuda)
+    y = linattn.scan_fwd(*[d[k] for k in PARAMS], S=Sd)
+    assert not torch.isfinite(y[1, at:, 1, 5]).any() and not torch.isfinite(Sd[1, 1, :, 5]).any()
+    free = torch.ones_like(y, dtype=torch.bool)
+    free[1, 128:, 1, 5] = False  # (its own chunk's earlier rows may hold it too)
+    assert torch.isfinite(y[free]).all()
+    free = torch.ones_like(Sd, dtype=torch.bool)
+    free[1, 1, :, 5] = False
+    assert torch.isfinite(Sd[free]).all()
+    ddt, dA = (linattn.scan_bwd(*[d[k] for k in PARAMS], dy.to(cuda))[i] for i in (1, 2))
+    assert not torch.isfinite(dA[1]) and torch.isfinite(dA[[0, 2]]).all()
+    assert not torch.isfinite(ddt[1, at, 1]) and torch.isfinite(ddt[0]).all() and torch.isfinite(ddt[1, :, [0, 2]]).all()
