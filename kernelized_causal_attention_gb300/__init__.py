@@ -29,6 +29,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 import threading
 
@@ -586,13 +587,16 @@ def _take_rows(t, name, shape, dtype, device, lead):
 
 
 def _on_device(f):
-    """f(x, ...) with x's device as the current one."""
+    """f with the device of its first argument (given by position or by name) as the current one."""
+    first = next(iter(inspect.signature(f).parameters))
+
     @functools.wraps(f)
-    def call(x, *args, **kw):
+    def call(*args, **kw):
+        x = args[0] if args else kw.get(first)
         if not isinstance(x, torch.Tensor) or not x.is_cuda or x.get_device() == torch.cuda.current_device():
-            return f(x, *args, **kw)
+            return f(*args, **kw)
         with torch.cuda.device(x.device):
-            return f(x, *args, **kw)
+            return f(*args, **kw)
     return call
 
 
