@@ -839,6 +839,12 @@ def noncausal_linear_attention(q, k, v, lengths=None):
     return _NonCausal.apply(q, k, v, lengths)
 
 
+def _gradient(t):
+    """A gradient as the calls need it: autograd hands over views, with any strides and from any address."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _ShortConv(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, w, bias, lengths, silu):
@@ -850,7 +856,7 @@ class _ShortConv(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         x, w, bias, lengths = ctx.saved_tensors
-        return *short_conv_bwd(x, w, bias, dy.contiguous(), lengths, ctx.silu), None, None
+        return *short_conv_bwd(x, w, bias, _gradient(dy), lengths, ctx.silu), None, None
 
 
 class _Scan(torch.autograd.Function):
@@ -863,7 +869,7 @@ class _Scan(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy):
         *inputs, lengths = ctx.saved_tensors
-        return *scan_bwd(*inputs, dy.contiguous(), lengths), None
+        return *scan_bwd(*inputs, _gradient(dy), lengths), None
 
 
 class _Cross(torch.autograd.Function):
@@ -878,7 +884,7 @@ class _Cross(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         q, k, v, lengths, out, den, S, Z = ctx.saved_tensors
-        return *cross_bwd(q, k, v, lengths, out, den, S, Z, dout.contiguous()), None
+        return *cross_bwd(q, k, v, lengths, out, den, S, Z, _gradient(dout)), None
 
 
 def short_conv(x, w, bias=None, lengths=None, silu=True):
