@@ -387,7 +387,7 @@ la_status la_cross_fwd(const void* q, const void* k, const void* v, const int* l
 /*
  * Its gradients: dq as q, dk as k and dv as v (rows past a sequence's length
  * zero; summed over the query heads of a key head).  out, den, S and Z are
- * la_cross_fwd's (out is not read: dout . out is formed again from S).
+ * la_cross_fwd's (out is not read and may be NULL: dout . out is formed again from S).
  * workspace: la_cross_workspace_bytes(1, ...) bytes.
  */
 la_status la_cross_bwd(const void* q, const void* k, const void* v, const int* lengths,

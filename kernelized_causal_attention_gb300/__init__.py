@@ -766,11 +766,11 @@ def cross_fwd(q, k, v, lengths=None):
 
 @_on_device
 def cross_bwd(q, k, v, lengths, out, den, S, Z, dout):
-    """(dq, dk, dv) of sum(dout * out); out, den, S, Z from cross_fwd."""
+    """(dq, dk, dv) of sum(dout * out); out (not read, may be None), den, S, Z from cross_fwd."""
     ptrs, size, code, dtype, dev = _cross_args(q, k, v, lengths)
     B, H, Hk, Nq, Nk, D, M = size
     f32 = torch.float32
-    more = (_take(out, "out", (B, H, Nq, M), dtype, dev), _take(den, "den", (B, H, Nq), f32, dev),
+    more = (_take_opt(out, "out", (B, H, Nq, M), dtype, dev), _take(den, "den", (B, H, Nq), f32, dev),
             _take(S, "S", (B, Hk, D, M), f32, dev), _take(Z, "Z", (B, Hk, D), f32, dev),
             _take(dout, "dout", (B, H, Nq, M), dtype, dev))
     _need_cuda(q)
@@ -877,14 +877,14 @@ class _Cross(torch.autograd.Function):
     def forward(ctx, q, k, v, lengths):
         q, k, v = q.contiguous(), k.contiguous(), v.contiguous()
         out, den, S, Z = cross_fwd(q, k, v, lengths)
-        ctx.save_for_backward(q, k, v, lengths, out, den, S, Z)
+        ctx.save_for_backward(q, k, v, lengths, den, S, Z)
         return out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
-        q, k, v, lengths, out, den, S, Z = ctx.saved_tensors
-        return *cross_bwd(q, k, v, lengths, out, den, S, Z, _gradient(dout)), None
+        q, k, v, lengths, den, S, Z = ctx.saved_tensors
+        return *cross_bwd(q, k, v, lengths, None, den, S, Z, _gradient(dout)), None
 
 
 def short_conv(x, w, bias=None, lengths=None, silu=True):

@@ -511,7 +511,8 @@ int la_cross_bwd(const void* q, const void* k, const void* v, const int* lengths
                  size_t workspace_bytes, int B, int H, int Hk, int Nq, int Nk, int D, int M, int dtype, void* stream) {
   const la::CrossShape s{B, H, Hk, Nq, Nk, D, M, dtype};
   LA_TRY(check_cross(s, 65535));
-  LA_TRY(check_ptrs({q, k, v, out, den, S, Z, dout, dq, dk, dv}));
+  LA_TRY(check_ptrs({q, k, v, den, S, Z, dout, dq, dk, dv}));
+  LA_TRY(check_opt_ptr(out));
   LA_TRY(check_to(lengths, 4, true));
   LA_TRY(check_room(workspace, workspace_bytes, la::cross_ws_bytes(s, true)));
   in_context();
