@@ -16,12 +16,12 @@ from plain64 import BF16, F32, within
 T = {"f32": torch.float32, "bf16": torch.bfloat16}
 
 
-def errors(q, k, dtype):
-    """The relative bounds of each output before its last rounding."""
+def errors(q, k, dtype, joins=64):
+    """The relative bounds of each output before its last rounding; joins: half steps beside one a row of S and Z."""
     Nq, Nk, r = q.shape[2], k.shape[2], q.shape[1] // k.shape[1]
     two, three = (2.0 ** -16, 2.0 ** -24) if dtype == "bf16" else (0.0, 0.0)
     p = (2 * max(float(q.abs().max()), float(k.abs().max())) + 8) * F32
-    e = {"S": p + three + (Nk + 64) * F32, "Z": p + (Nk + 64) * F32}
+    e = {"S": p + three + (Nk + joins) * F32, "Z": p + (Nk + joins) * F32}
     e["den"] = p + e["Z"] + 64 * F32
     e["out"] = p + e["S"] + 3 * two + e["den"] + 132 * F32
     t = e["S"] + two + 128 * F32                     # dout S^T
