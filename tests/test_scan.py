@@ -6,7 +6,8 @@ and the carried states rounds by less than 3 x 64 half steps of that size and th
 decays add ``scan_step_size``; the carry over c chunks adds 2 roundings a chunk.
 With bf16 inputs the scores and the carried states are rounded to bf16 once
 before their products (half a step each; a term passes through one of the two)
-and the result once more.
+and the result once more.  (Of the gradients the gate's, and of the states the last one, are
+rounded less: test_scan_bounds.py has the bounds of just that.)
 """
 import pytest
 import torch
