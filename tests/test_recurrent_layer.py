@@ -244,3 +244,37 @@ def test_first_call_of_a_host_thread(cuda):
     for name, got in outs.items():
         for u, t in zip(got, want[name]):
             assert torch.equal(u, t), name
+
+
+def test_decode_step_in_a_graph(cuda):
+    """One token of the whole layer, captured once: replays on new rows go through the same histories and states as the
+    eager calls, bit for bit."""
+    w, rows, k, v, n = layer(10)
+    wd = {a: t.to(cuda) for a, t in w.items()}
+    rows, k, v, n = rows.to(cuda), k.to(cuda), v.to(cuda), n.to(cuda)
+    _, _, SE, ZE = la.cross_fwd(torch.zeros(B, H, 1, D, dtype=torch.bfloat16, device=cuda), k, v, n)
+    new = lambda: (torch.zeros(B, K - 1, C, dtype=torch.bfloat16, device=cuda), torch.zeros(B, H, D, M, device=cuda))  # noqa: E731
+
+    def step(row, hist, S):
+        u = la.short_conv_step(row[:, :C], wd["w"], wd["b"], hist)
+        x, b, c = cut(u)
+        y = la.scan_step(x, row[:, C:], wd["A"], b, c, wd["skip"], wd["dt_bias"], S)
+        return la.cross_step(y[..., :D].contiguous(), SE, ZE)
+
+    row, (hist, S) = rows[:, 0].clone(), new()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(row, hist, S)
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        out = step(row, hist, S)
+    hist.zero_(), S.zero_()
+    hist2, S2 = new()
+    for t in range(12):
+        row.copy_(rows[:, t])
+        graph.replay()
+        assert torch.equal(out, step(rows[:, t], hist2, S2)) and torch.isfinite(out).all()
+    assert torch.equal(hist, hist2) and torch.equal(S, S2)
+    la.check_device_status()
