@@ -118,7 +118,9 @@ __global__ void __launch_bounds__(256)
   __syncthreads();
   if (threadIdx.x < 64) {
     float s = 0.f;
-    for (int d = 0; d < D; ++d) s = fmaf(qt[d * FLD + threadIdx.x], zs[d], s);
+    bool some = false;  // no states: Z = 0, and den = 0 whatever q holds
+    for (int d = 0; d < D; ++d) s = fmaf(qt[d * FLD + threadIdx.x], zs[d], s), some |= zs[d] != 0.f;
+    s = some ? s : 0.f;
     ds[threadIdx.x] = s;
     if (threadIdx.x < rows) den[r0 + threadIdx.x] = s;
   }
@@ -168,7 +170,8 @@ __global__ void __launch_bounds__(256)
     __syncthreads();
     qu.fetch(q + r0 * D, D, rows);
     gu.fetch(dout + r0 * M, M, rows);
-    const float d = threadIdx.x < rows ? den[r0 + threadIdx.x] : 0.f;
+    const float d = (threadIdx.x & 63) < rows ? den[r0 + (threadIdx.x & 63)] : 0.f;
+    if (d == 0.f) qu.clear(), gu.clear();  // no states: zeros, whatever q and dout hold
     qu.put(qn, D + 4, nullptr);
     gu.put(gn, M + 4, gt);
     if (threadIdx.x < 64) es[threadIdx.x] = d != 0.f ? 1.f / d : 0.f;
@@ -298,7 +301,7 @@ __global__ void __launch_bounds__(256)
     if (t < D) {
       const float f = phi(to_f(q[bh * D + t]));
       sq[t] = f;
-      dp = f * z;
+      dp = z != 0.f ? f * z : 0.f;  // Z = 0: den = 0, whatever q holds
     }
     if (t < 64) {
 #pragma unroll

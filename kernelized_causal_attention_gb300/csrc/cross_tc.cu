@@ -278,6 +278,7 @@ __global__ void __launch_bounds__(NT, 3)
   uint8_t* sm = align1024(smraw);
   __shared__ uint64_t bar_in[2], bar_t, bar_o, bar_free;
   __shared__ float zs[64], s_den[2][128];
+  __shared__ int s_some[2];  // whether Z holds anything
   __shared__ uint32_t tmem_base;
   __shared__ int s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bh = blockIdx.y;
@@ -331,8 +332,14 @@ __global__ void __launch_bounds__(NT, 3)
   } else {
     const int qd = warp & 3, wg = warp >> 2, row = 32 * qd + lane;
     put_state(S + bhk * D * M, sm + R_S, sm + R_S + STILE, D, M);
-    if (threadIdx.x < 64) zs[threadIdx.x] = threadIdx.x < D ? Z[bhk * D + threadIdx.x] : 0.f;
+    if (threadIdx.x < 64) {
+      const float z = threadIdx.x < D ? Z[bhk * D + threadIdx.x] : 0.f;
+      zs[threadIdx.x] = z;
+      const int any = __any_sync(0xffffffffu, z != 0.f);
+      if (lane == 0) s_some[warp] = any;
+    }
     sync_compute();
+    const bool some = s_some[0] | s_some[1];  // no states: den = 0, whatever q holds
     for (int i = 0; i < nt; ++i) {
       const int k = i & 1, n = (t0 + i) * TC_C + row;
       uint8_t* q = sm + R_Q + k * TILE;
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(NT, 3)
       tc_fence_before();
       mbar_arrive(&bar_t);
       sync_compute();
-      const float d = s_den[0][row] + s_den[1][row];
+      const float d = some ? s_den[0][row] + s_den[1][row] : 0.f;
       if (wg == 0 && n < N) den[static_cast<long>(bh) * N + n] = d;
       if (wtu(&bar_o, k, 124)) {
         tc_fence_after();
@@ -490,6 +497,7 @@ __global__ void __launch_bounds__(NT, 2)
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
           t[c] = fmaf(e, t[c], gam * zs[32 * wg + c]) * (pos >> c & 1 ? 1.f : f[c]);
+          t[c] = dn != 0.f ? t[c] : 0.f;  // no states: zeros, whatever q and dout hold
           f[c] *= gam;
         }
         tile_put_cols<32>(q, row, 32 * wg, t);

@@ -64,6 +64,10 @@ struct Rows {
       if (r < rows && v < VPR) u[k] = *reinterpret_cast<const uint4*>(g + r * stride + v * VN);
     }
   }
+  __device__ __forceinline__ void clear() {  // this thread's row, threadIdx.x mod 64
+#pragma unroll
+    for (int k = 0; k < NV; ++k) u[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
   __device__ __forceinline__ void put(float* nat, int ldn, float* tr) const {
     const int r = threadIdx.x & 63;
 #pragma unroll

@@ -96,3 +96,20 @@ def test_a_nan_prompt_and_its_steps_agree(cuda, linattn):
     y = linattn.cross_step(q[:, :, 0].contiguous(), S, Z)
     assert torch.isnan(out[0, 1]).all() and torch.isnan(y[0, 1]).all()
     assert torch.isfinite(out[0, 0]).all() and torch.isfinite(y[0, 0]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_a_sequence_without_states_gives_zeros(cuda, linattn, dtype, value):
+    """A padded batch entry: no encoder state, and queries and gradients that hold anything."""
+    g = torch.Generator().manual_seed(9)
+    q, k, v, dout = (torch.randn(s, generator=g).to(T[dtype]).to(cuda) for s in ((2, 4, 140, 32), (2, 2, 150, 32), (2, 2, 150, 64), (2, 4, 140, 64)))
+    n = torch.tensor([0, 77], dtype=torch.int32, device=cuda)
+    clean = run(linattn, q, k, v, dout, n)
+    q[0], dout[0], k[0], v[0] = value, value, value, value
+    for name, t in run(linattn, q, k, v, dout, n).items():
+        assert float(t[0].abs().max()) == 0.0, name
+        assert torch.equal(t[1], clean[name][1]), name
+    y = linattn.cross_step(q[:, :, 0].contiguous(), clean["S"], clean["Z"])
+    assert float(y[0].abs().max()) == 0.0 and torch.isfinite(y[1]).all()
