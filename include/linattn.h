@@ -375,7 +375,8 @@ la_status la_scan_step(const void* x, const void* dt, const void* A, const void*
  * and values k [B][Hk][Nk][D], v [B][Hk][Nk][M] of another length, H / Hk query
  * heads to a key head (Hk divides H):
  *   S = sum_{j<L_b} phi(k_j) v_j^T,  Z = sum_{j<L_b} phi(k_j)   ([B][Hk][D][M], [B][Hk][D]),
- *   out_i = phi(q_i)^T S / den_i,  den_i = phi(q_i)^T Z; zeros where L_b = 0.
+ *   out_i = phi(q_i)^T S / den_i,  den_i = phi(q_i)^T Z; zeros where L_b = 0,
+ * whatever q holds (and dout, in the gradients).
  * lengths are the encoder's.  Outputs out [B][H][Nq][M], den [B][H][Nq], S and Z
  * (all required).  workspace: la_cross_workspace_bytes(0, ...) bytes.
  */

@@ -3,7 +3,8 @@
 // keys and values from an encoder).  Per batch entry and key head,
 //   S = sum_{j<L_b} phi(k_j) v_j^T,  Z = sum_{j<L_b} phi(k_j),
 // and for each of the H / Hk query heads that share it
-//   out_i = S^T phi(q_i) / den_i,  den_i = phi(q_i) . Z;  L_b = 0 gives zeros.
+//   out_i = S^T phi(q_i) / den_i,  den_i = phi(q_i) . Z;  L_b = 0 gives zeros (of den and
+//   the gradients too), whatever q and dout hold.
 // Gradients, with e_i = 1 / den_i and gamma_i = -e_i (dout_i . out_i):
 //   dphi(q_i) = e_i S dout_i + gamma_i Z,   dout_i . out_i = e_i phi(q_i) . (S dout_i)
 //   R = sum_i e_i phi(q_i) dout_i^T,  r = sum_i gamma_i phi(q_i)   (over the query heads too)

@@ -140,7 +140,7 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return s;
 }
 
-// RR x CC outputs of this thread times a factor of their row, as T.
+// CC neighbouring outputs of one row, as T.
 template <typename T, int CC>
 __device__ __forceinline__ void store_cols(T* p, const float (&f)[CC]) {
 #pragma unroll
