@@ -269,3 +269,43 @@ def test_final_state_of_few_rows(cuda, linattn, B, N, H, G, D, M):
     d, S = place(p, H, G, D, M, cuda), torch.zeros(B, H, D, M, device=cuda)
     linattn.scan_fwd(*[d[k] for k in PARAMS], S=S)
     within(S, want, b, "S")
+
+
+def one_live_row(N, row, heavy):
+    """Rows that forget everything (`heavy`) before rows that hardly do; x is not zero in one of the latter alone."""
+    g = torch.Generator().manual_seed(13)
+    B, H, G, D, M = 2, 3, 1, 32, 64
+    r = lambda *s: torch.randn(s, generator=g)  # noqa: E731
+    x, Bm, Cm = torch.zeros(B, N, H, M), r(B, N, G, D).bfloat16(), r(B, N, G, D).bfloat16()
+    x[:, row] = r(B, H, M)
+    dt = torch.where(torch.arange(N)[None, :, None] < heavy, 1.0, -5.0) + 0.25 * r(B, N, H)
+    a = [x.bfloat16(), dt.bfloat16(), torch.tensor([-16.0, -11.0, -13.5]).bfloat16(), Bm, Cm, None, None]
+    want, size = (plain64.scan(*a, torch.zeros(B, H, D, M), size=s)["S"] for s in (False, True))
+    delta, _, A = plain64.gate(*a[1:3], None, None)
+    z, tot = float(dt.abs().max()) + 1, float((delta * A.abs())[:, row + 1:].sum(1).max())
+    return a, (delta, A), want, ((9 + z + 16 + 12) * tot + 24 + 8 + z + 11 + 8 + 4 * (N // CH + 1)) * F32 * size + 2.0 ** -24 * size
+
+
+ROWS = [(128, 126, 120), (128, 61, 60), (300, 206, 204)]
+
+
+@pytest.mark.parametrize("N,row,heavy", ROWS)
+def test_bounds_refuse_a_difference_of_sums(N, row, heavy):
+    """The decay from a row to the end of its 32-row block in fp32: as a sum of its own, and as a difference of two."""
+    (x, _, _, Bm, _, _, _), (delta, A), want, b = one_live_row(N, row, heavy)
+    l, first = (delta * A).float(), row // 32 * 32
+    block = l[:, first:first + 32]
+    wp = torch.cumsum(block, 1)
+    rest = (delta * A)[:, first + 32:].sum(1)
+    for f, near in ((within, block[:, row - first + 1:].flip(1).sum(1)), (fails, wp[:, -1] - wp[:, row - first])):
+        w = delta[:, row] * torch.exp(near.double() + rest)
+        f(torch.einsum("bd,bhm->bhdm", Bm[:, row, 0].double(), w[..., None] * x[:, row].double()), want, b, "S")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,row,heavy", ROWS)
+def test_state_behind_rows_that_forget(cuda, linattn, N, row, heavy):
+    a, _, want, b = one_live_row(N, row, heavy)
+    S = torch.zeros(want.shape, device=cuda)
+    linattn.scan_fwd(*[None if t is None else t.to(cuda) for t in a], S=S)
+    within(S, want, b, "S")
