@@ -286,7 +286,7 @@ def one_live_row(N, row, heavy):
     return a, (delta, A), want, ((9 + z + 16 + 12) * tot + 24 + 8 + z + 11 + 8 + 4 * (N // CH + 1)) * F32 * size + 2.0 ** -24 * size
 
 
-ROWS = [(128, 126, 120), (128, 61, 60), (300, 206, 204)]
+ROWS = [(128, 126, 120), (128, 61, 60), (224, 215, 212)]
 
 
 @pytest.mark.parametrize("N,row,heavy", ROWS)
