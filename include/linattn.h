@@ -74,6 +74,9 @@ enum {
 typedef int la_dtype;
 enum { LA_F32 = 0, LA_BF16 = 1 };
 
+/* 8-bit codes of packed states */
+enum { LA_CODE_I8 = 0, LA_CODE_E4M3 = 1 };
+
 /* operation ids for la_workspace_bytes */
 #define LA_OP_CAUSAL_FWD 0
 #define LA_OP_CAUSAL_BWD 1
@@ -406,6 +409,123 @@ size_t la_cross_workspace_bytes(int bwd, int B, int H, int Hk, int Nq, int Nk, i
  */
 la_status la_cross_step(const void* q, const float* S, const float* Z, void* y, int B, int H,
                         int Hk, int D, int M, la_dtype dtype, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Around the recurrent layer: the gated recurrence, the layer norm, rotary
+ * positions and packed states.  Row strides, lengths and alignment as for the
+ * layer above.
+ */
+
+/*
+ * Gated recurrence: one decay and one state a channel, both gates of every row's
+ * own.  With s = sigmoid(r), g = sigmoid(i), a = exp(-scale softplus(lam) s),
+ *   h_n = a_n h_{n-1} + sqrt(1 - a_n^2) g_n x_n,  y_n = h_n.
+ * x, r, i [B][N][C] (row strides ldx, ldr, ldi >= C; aligned to their elements),
+ * lam [C] of the call's dtype, scale > 0; y [B][N][C].  h [B][C] float, read as
+ * the state before row 0 and replaced by the state after each sequence's last
+ * valid row, or NULL (from zero, not returned).  kept: NULL, or
+ * la_gated_kept_bytes(...) bytes that receive what la_gated_bwd needs of this
+ * call.  lam and scale softplus(lam) are finite.  1 <= B <= 65535,
+ * 1 <= N <= 2^24, 1 <= C <= 65536.  workspace: la_gated_workspace_bytes(0, ...).
+ */
+la_status la_gated_fwd(const void* x, const void* r, const void* i, const void* lam,
+                       const int* lengths, float* h, void* kept, void* y, void* workspace,
+                       size_t workspace_bytes, int B, int N, int C, int ldx, int ldr, int ldi,
+                       float scale, la_dtype dtype, void* stream);
+size_t la_gated_kept_bytes(int B, int N, int C, la_dtype dtype);
+
+/*
+ * Its gradients from dy [B][N][C]: dx, dr, di [B][N][C] and dlam [C], for the
+ * forward call that wrote kept (its h before row 0 is a constant) and a final state
+ * that nothing reads.  Where 1 - a^2 is zero (a closed gate) its root's gradient is
+ * taken as zero, the limit of the gradients of r and lam.  Deterministic.
+ * workspace: la_gated_workspace_bytes(1, ...).
+ */
+la_status la_gated_bwd(const void* x, const void* r, const void* i, const void* lam,
+                       const int* lengths, const void* kept, const void* dy, void* dx, void* dr,
+                       void* di, void* dlam, void* workspace, size_t workspace_bytes, int B, int N,
+                       int C, int ldx, int ldr, int ldi, float scale, la_dtype dtype, void* stream);
+size_t la_gated_workspace_bytes(int bwd, int B, int N, int C, la_dtype dtype);
+
+/*
+ * One row for each of B streams: x, r, i [B][C] (rows ldx, ldr, ldi apart), y
+ * [B][C]; h [B][C] is updated in place.  1 <= B <= 2^20.  No workspace.
+ */
+la_status la_gated_step(const void* x, const void* r, const void* i, const void* lam, float* h,
+                        void* y, int B, int C, int ldx, int ldr, int ldi, float scale,
+                        la_dtype dtype, void* stream);
+
+/*
+ * Layer norm of each of G groups of C / G neighbouring columns (G = 1: the whole
+ * row; G = H: every head of a scan's output by itself), behind a residual sum:
+ *   s = x + residual, rounded to dtype (x itself with a NULL residual),
+ *   y = (s - mean) rstd w + b,  rstd = 1 / sqrt(mean((s - mean)^2) + eps).
+ * x, residual [B][N][C] (row strides ldx, ldr >= C; aligned to their elements),
+ * w, b (may be NULL) [C]; y, s [B][N][C] (s only with a residual); mean, rstd
+ * [B][N][G] float (both or neither).  eps >= 0.  Statistics are fp32.  Rows past a
+ * sequence's length: zeros in every output.  1 <= C <= 65536, C / G <= 8192 (else
+ * LA_ERR_UNSUPPORTED), B N G < 2^31.  One launch, no workspace.
+ */
+la_status la_norm_fwd(const void* x, const void* residual, const void* w, const void* b,
+                      const int* lengths, void* y, void* s, float* mean, float* rstd, float eps,
+                      int B, int N, int C, int G, int ldx, int ldr, la_dtype dtype, void* stream);
+
+/*
+ * Its gradients: s (row stride lds), mean and rstd are the forward call's (x and ldx
+ * without a residual), dy [B][N][C], ds [B][N][C] the gradient that reaches s by
+ * another way, or NULL.  dx [B][N][C], the gradient of x and of the residual
+ * alike; dw [C], db [C] (may be NULL), summed over all valid rows in fp32.
+ * Two launches; deterministic.  workspace: la_norm_workspace_bytes(...).
+ */
+la_status la_norm_bwd(const void* s, const void* w, const float* mean, const float* rstd,
+                      const int* lengths, const void* dy, const void* ds, void* dx, void* dw,
+                      void* db, void* workspace, size_t workspace_bytes, int B, int N, int C, int G,
+                      int lds, la_dtype dtype, void* stream);
+size_t la_norm_workspace_bytes(int B, int N, int C, int G, la_dtype dtype);
+
+/*
+ * Rotary positions of queries and keys: pair j (of R / 2) of every head's row at
+ * position p turns by the angle p turns[j] 2^-64 of a whole turn,
+ *   (a, b) -> gain (a cos - b sin, b cos + a sin)   (inverse: the angle negated),
+ * where the pairs are (x[j], x[j + R/2]), or (x[2j], x[2j+1]) with interleaved != 0;
+ * columns R to D - 1 are copied.  The inverse call on output gradients gives the
+ * input gradients.  turns: uint64 [R / 2] (the product wraps, so the angle is exact
+ * at any position).
+ * q [B][N][H][D] and k [B][N][Hk][D] (rows ldq, ldk elements apart; aligned to
+ * their elements; k NULL with Hk = 0), or with head_major != 0 dense [B][H][N][D] and
+ * [B][Hk][N][D] (ldq, ldk not read).  oq and ok: dense tensors of the same layout, or
+ * oq == q and ok == k (in place, in rows as far apart).  Other overlaps are not allowed.
+ * positions: int32 [B], of row 0 of every sequence, or [B][N] with per_row != 0,
+ * or NULL (row n is at n).  Rows past a sequence's length: zeros, or left as they
+ * were in place.  R even, 2 <= R <= D <= 1024 (larger: LA_ERR_UNSUPPORTED), H, Hk
+ * <= 32767, B N < 2^31.  One launch, no workspace.
+ */
+la_status la_rotary(const void* q, const void* k, void* oq, void* ok, const void* turns,
+                    const int* positions, const int* lengths, float gain, int B, int N, int H,
+                    int Hk, int D, int R, int ldq, int ldk, int per_row, int interleaved,
+                    int head_major, int inverse, la_dtype dtype, void* stream);
+
+/*
+ * A state in 8 bits: S [B][H][D][M] float becomes code [B][H][D][M] (int8 for
+ * LA_CODE_I8, e4m3 for LA_CODE_E4M3) and scale [B][H][D] float,
+ *   scale = max_m |S| / top, code = round(S / scale),  top = 127 or 448,
+ * (IEEE quotients, ties to even), and back, S = code scale.  A row of zeros has
+ * scale 0; a row that holds a NaN or an infinity has scale NaN (and comes back as
+ * NaN); rows below 2^-119 lose bits.  D and M in {16, 32, 64}, 1 <= B H <= 2^20.
+ */
+la_status la_state_pack(const float* S, void* code, float* scale, int B, int H, int D, int M,
+                        int format, void* stream);
+la_status la_state_unpack(const void* code, const float* scale, float* S, int B, int H, int D,
+                          int M, int format, void* stream);
+
+/*
+ * la_cross_step from a packed S: y = phi(q)^T (scale code) / phi(q)^T Z, accumulated
+ * in fp32.  q [B][H][D], code [B][Hk][D][M], scale and Z [B][Hk][D].
+ */
+la_status la_cross_step_packed(const void* q, const void* code, const float* scale, const float* Z,
+                               void* y, int B, int H, int Hk, int D, int M, int format,
+                               la_dtype dtype, void* stream);
 
 /*
  * Reads the status word of the current GPU after all work queued on

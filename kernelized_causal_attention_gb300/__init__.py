@@ -14,13 +14,16 @@ place of pointers): ``la_causal_fwd``, ``la_causal_bwd``, ``la_causal_prefill``,
 ``la_decode_step_proj``, the degree-2 polynomial ``la_causal_fwd_poly``,
 ``la_causal_bwd_poly``, the short convolution's ``la_short_conv_fwd``, ``la_short_conv_bwd``,
 ``la_short_conv_step``, the selective scan's ``la_scan_fwd``, ``la_scan_bwd``, ``la_scan_step``, the cross
-attention's ``la_cross_fwd``, ``la_cross_bwd``, ``la_cross_step``, ``la_workspace_bytes``, ``la_device_status``.
+attention's ``la_cross_fwd``, ``la_cross_bwd``, ``la_cross_step``, the gated recurrence's ``la_gated_fwd``,
+``la_gated_bwd``, ``la_gated_step``, the layer norm's ``la_norm_fwd``, ``la_norm_bwd``, ``la_rotary``, the packed states'
+``la_state_pack``, ``la_state_unpack``, ``la_cross_step_packed``, ``la_workspace_bytes``, ``la_device_status``.
 Convenience wrappers that allocate outputs with torch: ``causal_fwd``,
 ``causal_bwd``, ``causal_prefill``, ``noncausal_fwd``, ``noncausal_bwd``, ``decode_step``, ``decode_step_proj``,
 ``causal_fwd_poly``, ``causal_bwd_poly``, ``short_conv_fwd``, ``short_conv_bwd``, ``short_conv_step``,
-``scan_fwd``, ``scan_bwd``, ``scan_step``, ``cross_fwd``, ``cross_bwd``, ``cross_step`` and the
-autograd functions ``causal_linear_attention`` / ``noncausal_linear_attention`` /
-``short_conv`` / ``selective_scan`` / ``cross_linear_attention``.
+``scan_fwd``, ``scan_bwd``, ``scan_step``, ``cross_fwd``, ``cross_bwd``, ``cross_step``, ``gated_fwd``, ``gated_bwd``,
+``gated_step``, ``norm_fwd``, ``norm_bwd``, ``rotary_turns``, ``rotary_fwd``, ``rotary_bwd``, ``state_pack``, ``state_unpack``,
+``cross_step_packed`` and the autograd functions ``causal_linear_attention`` / ``noncausal_linear_attention`` /
+``short_conv`` / ``selective_scan`` / ``cross_linear_attention`` / ``gated_recurrence`` / ``layer_norm`` / ``rotary``.
 
 The method is Katharopoulos et al., "Transformers are RNNs" (part 2/3):
 eq. 7 (phi), §3.3 eq. 9-12, §3.3.1 eq. 13-15, §3.4 eq. 16-20.
@@ -30,6 +33,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import inspect
+import math
 import os
 import threading
 
@@ -41,6 +45,7 @@ LIB_PATH = os.path.join(_HERE, "_lib", "liblinattn.so")
 
 LA_OK, LA_ERR_INVALID_ARG, LA_ERR_UNSUPPORTED, LA_ERR_CUDA, LA_ERR_TIMEOUT, LA_ERR_WORKSPACE = range(6)
 LA_F32, LA_BF16 = 0, 1
+LA_CODE_I8, LA_CODE_E4M3 = 0, 1
 (LA_OP_CAUSAL_FWD, LA_OP_CAUSAL_BWD, LA_OP_NONCAUSAL_FWD, LA_OP_NONCAUSAL_BWD, LA_OP_DECODE,
  LA_OP_CAUSAL_PREFILL, LA_OP_CAUSAL_FWD_DECAY, LA_OP_CAUSAL_BWD_DECAY, LA_OP_DECODE_PROJ,
  LA_OP_CAUSAL_FWD_POLY, LA_OP_CAUSAL_BWD_POLY) = range(11)
@@ -77,6 +82,18 @@ _SIGS = {
     "la_cross_fwd": ("p p p p p p p p p z i i i i i i i i p", ctypes.c_int),
     "la_cross_bwd": ("p p p p p p p p p p p p p z i i i i i i i i p", ctypes.c_int),
     "la_cross_step": ("p p p p i i i i i i p", ctypes.c_int),
+    "la_gated_workspace_bytes": ("i i i i i", ctypes.c_size_t),
+    "la_gated_kept_bytes": ("i i i i", ctypes.c_size_t),
+    "la_gated_fwd": ("p p p p p p p p p z i i i i i i f i p", ctypes.c_int),
+    "la_gated_bwd": ("p p p p p p p p p p p p z i i i i i i f i p", ctypes.c_int),
+    "la_gated_step": ("p p p p p p i i i i i f i p", ctypes.c_int),
+    "la_norm_workspace_bytes": ("i i i i i", ctypes.c_size_t),
+    "la_norm_fwd": ("p p p p p p p p p f i i i i i i i p", ctypes.c_int),
+    "la_norm_bwd": ("p p p p p p p p p p p z i i i i i i p", ctypes.c_int),
+    "la_rotary": ("p p p p p p p f i i i i i i i i i i i i i p", ctypes.c_int),
+    "la_state_pack": ("p p p i i i i i p", ctypes.c_int),
+    "la_state_unpack": ("p p p i i i i i p", ctypes.c_int),
+    "la_cross_step_packed": ("p p p p p i i i i i i i p", ctypes.c_int),
     "la_device_status": ("p i p", ctypes.c_int),
     "la_selftest_wait": ("p u", ctypes.c_int),
 }
@@ -340,6 +357,65 @@ def la_cross_bwd(q, k, v, lengths, out, den, S, Z, dout, dq, dk, dv, workspace, 
 def la_cross_step(q, S, Z, y, B, H, Hk, D, M, dtype, stream=None):
     _check(lib().la_cross_step(_p(q), _p(S), _p(Z), _p(y), B, H, Hk, D, M, dtype, _stream(stream)),
            "la_cross_step")
+
+
+def la_gated_workspace_bytes(bwd, B, N, C, dtype) -> int:
+    return int(lib().la_gated_workspace_bytes(int(bwd), B, N, C, dtype))
+
+
+def la_gated_kept_bytes(B, N, C, dtype) -> int:
+    return int(lib().la_gated_kept_bytes(B, N, C, dtype))
+
+
+def la_gated_fwd(x, r, i, lam, lengths, h, kept, y, workspace, B, N, C, ldx, ldr, ldi, scale, dtype, stream=None):
+    _check(lib().la_gated_fwd(_pv(x), _pv(r), _pv(i), _p(lam), _p(lengths), _p(h), _p(kept), _p(y), _p(workspace),
+                              _nbytes(workspace), B, N, C, ldx, ldr, ldi, float(scale), dtype, _stream(stream)), "la_gated_fwd")
+
+
+def la_gated_bwd(x, r, i, lam, lengths, kept, dy, dx, dr, di, dlam, workspace, B, N, C, ldx, ldr, ldi, scale, dtype,
+                 stream=None):
+    _check(lib().la_gated_bwd(_pv(x), _pv(r), _pv(i), _p(lam), _p(lengths), _p(kept), _p(dy), _p(dx), _p(dr), _p(di), _p(dlam),
+                              _p(workspace), _nbytes(workspace), B, N, C, ldx, ldr, ldi, float(scale), dtype, _stream(stream)),
+           "la_gated_bwd")
+
+
+def la_gated_step(x, r, i, lam, h, y, B, C, ldx, ldr, ldi, scale, dtype, stream=None):
+    _check(lib().la_gated_step(_pv(x), _pv(r), _pv(i), _p(lam), _p(h), _p(y), B, C, ldx, ldr, ldi, float(scale), dtype,
+                               _stream(stream)), "la_gated_step")
+
+
+def la_norm_workspace_bytes(B, N, C, G, dtype) -> int:
+    return int(lib().la_norm_workspace_bytes(B, N, C, G, dtype))
+
+
+def la_norm_fwd(x, residual, w, b, lengths, y, s, mean, rstd, eps, B, N, C, G, ldx, ldr, dtype, stream=None):
+    _check(lib().la_norm_fwd(_pv(x), _pv(residual), _p(w), _p(b), _p(lengths), _p(y), _p(s), _p(mean), _p(rstd), float(eps), B, N, C,
+                             G, ldx, ldr, dtype, _stream(stream)), "la_norm_fwd")
+
+
+def la_norm_bwd(s, w, mean, rstd, lengths, dy, ds, dx, dw, db, workspace, B, N, C, G, lds, dtype, stream=None):
+    _check(lib().la_norm_bwd(_pv(s), _p(w), _p(mean), _p(rstd), _p(lengths), _p(dy), _p(ds), _p(dx), _p(dw), _p(db), _p(workspace),
+                             _nbytes(workspace), B, N, C, G, lds, dtype, _stream(stream)), "la_norm_bwd")
+
+
+def la_rotary(q, k, oq, ok, turns, positions, lengths, gain, B, N, H, Hk, D, R, ldq, ldk, per_row, interleaved, head_major, inverse,
+              dtype, stream=None):
+    _check(lib().la_rotary(_pv(q), _pv(k), _pv(oq), _pv(ok), _p(turns), _p(positions), _p(lengths), float(gain), B, N, H, Hk, D, R,
+                           ldq, ldk, int(per_row), int(interleaved), int(head_major), int(inverse), dtype, _stream(stream)),
+           "la_rotary")
+
+
+def la_state_pack(S, code, scale, B, H, D, M, format, stream=None):
+    _check(lib().la_state_pack(_p(S), _p(code), _p(scale), B, H, D, M, format, _stream(stream)), "la_state_pack")
+
+
+def la_state_unpack(code, scale, S, B, H, D, M, format, stream=None):
+    _check(lib().la_state_unpack(_p(code), _p(scale), _p(S), B, H, D, M, format, _stream(stream)), "la_state_unpack")
+
+
+def la_cross_step_packed(q, code, scale, Z, y, B, H, Hk, D, M, format, dtype, stream=None):
+    _check(lib().la_cross_step_packed(_p(q), _p(code), _p(scale), _p(Z), _p(y), B, H, Hk, D, M, format, dtype, _stream(stream)),
+           "la_cross_step_packed")
 
 
 def la_device_status(clear=True, stream=None):
@@ -799,6 +875,237 @@ def cross_step(q, S, Z):
     return y
 
 
+# ----------------------------- around the recurrent layer: gated recurrence, norm, positions, packed states
+
+def _gated_args(x, r, i, lam, lengths, scale, lead):
+    """(pointers up to lengths, row strides, rows' shape, type code, type, device)"""
+    if x.dim() != lead + 1:
+        raise ValueError(f"x: {lead + 1} dimensions")
+    shape, dtype, dev = x.shape, x.dtype, x.device
+    _need_ints(x)
+    if not 0 < scale < float("inf"):
+        raise ValueError("scale: a positive number is needed")
+    code = _dtype_code(x)
+    px, lx = _take_rows(x, "x", shape, dtype, dev, lead)
+    pr, lr = _take_rows(r, "r", shape, dtype, dev, lead)
+    pi, li = _take_rows(i, "i", shape, dtype, dev, lead)
+    ptrs = (px, pr, pi, _take(lam, "lam", shape[-1:], dtype, dev), _take_opt(lengths, "lengths", shape[:1], torch.int32, dev))
+    return ptrs, (lx, lr, li), shape, code, dtype, dev
+
+
+@_on_device
+def gated_fwd(x, r, i, lam, h=None, scale=8.0, lengths=None, keep=False):
+    """y [B,N,C] of the gated recurrence h_n = a_n h_{n-1} + sqrt(1 - a_n^2) sigmoid(i_n) x_n,
+    a_n = exp(-scale softplus(lam) sigmoid(r_n)).  x, r, i [B,N,C] (rows may be slices of wider ones),
+    lam [C].  h [B,C] (float32) is the state before row 0 (zeros if None), updated in place to the state
+    after each sequence's last valid row; gated_step continues from it.  keep: (y, kept), where kept is
+    what gated_bwd needs of this call."""
+    ptrs, ld, (B, N, C), code, dtype, dev = _gated_args(x, r, i, lam, lengths, scale, 2)
+    ph = _take_opt(h, "h", (B, C), torch.float32, dev)
+    _need_cuda(x)
+    y = torch.empty((B, N, C), dtype=dtype, device=dev)
+    kept = torch.empty((lib().la_gated_kept_bytes(B, N, C, code) // 4,), dtype=torch.float32, device=dev) if keep else None
+    ws, pws, nws = _scratch(lib().la_gated_workspace_bytes(0, B, N, C, code), x)
+    _check(lib().la_gated_fwd(*ptrs, ph, None if kept is None else kept.data_ptr(), y.data_ptr(), pws, nws, B, N, C, *ld, scale,
+                              code, _stream(None)), "la_gated_fwd")
+    return (y, kept) if keep else y
+
+
+@_on_device
+def gated_bwd(x, r, i, lam, kept, dy, scale=8.0, lengths=None):
+    """(dx, dr, di, dlam) of sum(dy * y); kept from gated_fwd(..., keep=True)."""
+    ptrs, ld, (B, N, C), code, dtype, dev = _gated_args(x, r, i, lam, lengths, scale, 2)
+    _need_cuda(x)
+    pk = _take(kept, "kept", (lib().la_gated_kept_bytes(B, N, C, code) // 4,), torch.float32, dev)
+    pg = _take(dy, "dy", x.shape, dtype, dev)
+    new = functools.partial(torch.empty, dtype=dtype, device=dev)
+    d = (new((B, N, C)), new((B, N, C)), new((B, N, C)), new((C,)))
+    ws, pws, nws = _scratch(lib().la_gated_workspace_bytes(1, B, N, C, code), x)
+    _check(lib().la_gated_bwd(*ptrs, pk, pg, *[t.data_ptr() for t in d], pws, nws, B, N, C, *ld, scale, code, _stream(None)),
+           "la_gated_bwd")
+    return d
+
+
+@_on_device
+def gated_step(x, r, i, lam, h, scale=8.0):
+    """y [B,C] for one row of each stream: x, r, i [B,C]; h [B,C] (float32) is updated in place."""
+    ptrs, ld, (B, C), code, dtype, dev = _gated_args(x, r, i, lam, None, scale, 1)
+    ph = _take(h, "h", (B, C), torch.float32, dev)
+    _need_cuda(x)
+    y = torch.empty((B, C), dtype=dtype, device=dev)
+    _check(lib().la_gated_step(*ptrs[:4], ph, y.data_ptr(), B, C, *ld, scale, code, _stream(None)), "la_gated_step")
+    return y
+
+
+def _norm_rows(x, name, groups, lengths):
+    """(address, row stride, (B, N, C), type code, type, device, address of the lengths) of rows [N,C] or [B,N,C]."""
+    if x.dim() not in (2, 3):
+        raise ValueError(f"{name}: 2 or 3 dimensions")
+    lead, shape, dtype, dev = x.dim() - 1, x.shape, x.dtype, x.device
+    if lengths is not None and lead != 2:
+        raise ValueError(f"lengths: {name} must have 3 dimensions")
+    if groups < 1 or shape[-1] % groups:
+        raise ValueError(f"groups: {groups} does not divide {shape[-1]} columns")
+    _need_ints(x)
+    code = _dtype_code(x)
+    p, ld = _take_rows(x, name, shape, dtype, dev, lead)
+    return p, ld, (shape if lead == 2 else (1, *shape)), code, dtype, dev, _take_opt(lengths, "lengths", shape[:1], torch.int32, dev)
+
+
+@_on_device
+def norm_fwd(x, w, b=None, residual=None, groups=1, eps=1e-5, lengths=None):
+    """(y, s, mean, rstd) of the layer norm of s = x + residual (x itself without one) over each of `groups`
+    groups of neighbouring columns: y = (s - mean) rstd w + b.  x, residual [N,C] or [B,N,C] (rows may be
+    slices of wider ones), w, b [C]; mean, rstd [...,groups] (float32); lengths: int32 [B] of valid rows."""
+    px, ld, (B, N, C), code, dtype, dev, pn = _norm_rows(x, "x", groups, lengths)
+    pr, lr = (None, C) if residual is None else _take_rows(residual, "residual", x.shape, dtype, dev, x.dim() - 1)
+    pw, pb = _take(w, "w", (C,), dtype, dev), _take_opt(b, "b", (C,), dtype, dev)
+    _need_cuda(x)
+    y = torch.empty(x.shape, dtype=dtype, device=dev)
+    s = x if residual is None else torch.empty(x.shape, dtype=dtype, device=dev)
+    mean, rstd = (torch.empty((*x.shape[:-1], groups), dtype=torch.float32, device=dev) for _ in range(2))
+    _check(lib().la_norm_fwd(px, pr, pw, pb, pn, y.data_ptr(), None if residual is None else s.data_ptr(), mean.data_ptr(),
+                             rstd.data_ptr(), eps, B, N, C, groups, ld, lr, code, _stream(None)), "la_norm_fwd")
+    return y, s, mean, rstd
+
+
+@_on_device
+def norm_bwd(s, w, mean, rstd, dy, ds=None, groups=1, bias=True, lengths=None):
+    """(dx, dw, db) of sum(dy * y) + sum(ds * s) for norm_fwd's s, mean and rstd; dx is the gradient of x and of
+    the residual alike; db is None with bias=False."""
+    ps, ld, (B, N, C), code, dtype, dev, pn = _norm_rows(s, "s", groups, lengths)
+    stat = (*s.shape[:-1], groups)
+    ptrs = (_take(w, "w", (C,), dtype, dev), _take(mean, "mean", stat, torch.float32, dev), _take(rstd, "rstd", stat, torch.float32, dev),
+            pn, _take(dy, "dy", s.shape, dtype, dev), _take_opt(ds, "ds", s.shape, dtype, dev))
+    _need_cuda(s)
+    dx, dw = torch.empty(s.shape, dtype=dtype, device=dev), torch.empty_like(w)
+    db = torch.empty_like(w) if bias else None
+    ws, pws, nws = _scratch(lib().la_norm_workspace_bytes(B, N, C, groups, code), s)
+    _check(lib().la_norm_bwd(ps, *ptrs, dx.data_ptr(), dw.data_ptr(), db.data_ptr() if bias else None, pws, nws, B, N, C, groups, ld, code,
+                             _stream(None)), "la_norm_bwd")
+    return dx, dw, db
+
+
+def rotary_turns(dim, base=10000.0, factor=1.0, original=None, fast=32.0, slow=1.0, device="cuda"):
+    """(turns, gain) for rotary_fwd: the frequencies base^(-2j/dim) of dim / 2 pairs as whole numbers of 2^-64 turns a
+    position (int64 [dim/2]), kept by the caller.  A factor above one stretches the positions for longer contexts:
+    every pair by it, or, given the `original` length, the pairs that turn less than `slow` times within it fully, those
+    that turn more than `fast` times not at all and those between by a share, with a gain of 0.1 log(factor) + 1."""
+    if dim < 2 or dim % 2 or not base > 0 or not factor >= 1 or (original is not None and not (original > 0 and fast > slow >= 0)):
+        raise ValueError("rotary_turns: an even dim, base > 0, factor >= 1, original > 0 and fast > slow >= 0 are needed")
+    turns = []
+    for j in range(dim // 2):
+        f = float(base) ** (-2.0 * j / dim) / (2 * math.pi)
+        whole = 0.0 if original is None else min(1.0, max(0.0, (original * f - slow) / (fast - slow)))
+        turns.append(round(f * (whole + (1 - whole) / factor) * 2.0 ** 64) % (1 << 64))
+    signed = [t - (1 << 64) if t >> 63 else t for t in turns]
+    return torch.tensor(signed, dtype=torch.int64, device=device), 0.1 * math.log(factor) + 1 if original is not None else 1.0
+
+
+def _rotary(q, k, turns, positions, gain, interleaved, head_major, lengths, inplace, inverse):
+    step = q.dim() == 3
+    if q.dim() not in (3, 4) or (step and (head_major or lengths is not None)):
+        raise ValueError("q: 4 dimensions, or 3 (one row a stream, token-major, without lengths)")
+    dtype, dev, code = q.dtype, q.device, _dtype_code(q)
+    _need_ints(q)
+    lead = q.dim() - 2
+    if head_major:
+        B, H, N, D = q.shape
+        kshape = None if k is None else (B, k.shape[1], N, D)
+        pq, lq = _take(q, "q", q.shape, dtype, dev), 0
+        pk, lk = (None, 0) if k is None else (_take(k, "k", kshape, dtype, dev), 0)
+    else:
+        B, H, D = q.shape[0], q.shape[-2], q.shape[-1]
+        N = 1 if step else q.shape[1]
+        kshape = None if k is None else (*q.shape[:lead], k.shape[-2], D)
+        pq, lq = _take_rows(q, "q", q.shape, dtype, dev, lead)
+        pk, lk = (None, 0) if k is None else _take_rows(k, "k", kshape, dtype, dev, lead)
+    Hk = 0 if k is None else kshape[1 if head_major else -2]
+    if turns.dim() != 1:
+        raise ValueError("turns: 1 dimension")
+    pt = _take(turns, "turns", turns.shape, torch.int64, dev)
+    per_row = positions is not None and positions.dim() == 2
+    pp = _take_opt(positions, "positions", (B, N) if per_row else (B,), torch.int32, dev)
+    pn = _take_opt(lengths, "lengths", (B,), torch.int32, dev)
+    _need_cuda(q)
+    oq = q if inplace else torch.empty(q.shape, dtype=dtype, device=dev)
+    ok = k if inplace or k is None else torch.empty(kshape, dtype=dtype, device=dev)
+    _check(lib().la_rotary(pq, pk, oq.data_ptr(), None if k is None else ok.data_ptr(), pt, pp, pn, gain, B, N, H, Hk, D,
+                           2 * turns.shape[0], lq, lk, per_row, bool(interleaved), bool(head_major), inverse, code, _stream(None)),
+           "la_rotary")
+    return oq, ok
+
+
+@_on_device
+def rotary_fwd(q, k, turns, positions=None, gain=1.0, interleaved=False, head_major=False, lengths=None, inplace=False):
+    """(q', k') with the first 2 len(turns) columns of every head turned by its row's position (rotary_turns gives turns
+    and gain).  q [B,N,H,D] and k [B,N,Hk,D] or None (rows may be slices of wider ones), dense [B,H,N,D] with head_major,
+    or [B,H,D] for one row a stream; positions: int32 [B] (of each sequence's row 0) or [B,N], None: rows at 0, 1, ...
+    Pairs are halves (j, j + R/2), or neighbours with interleaved.  inplace: q and k themselves, rows past a
+    sequence's length left as they were."""
+    return _rotary(q, k, turns, positions, gain, interleaved, head_major, lengths, inplace, False)
+
+
+@_on_device
+def rotary_bwd(dq, dk, turns, positions=None, gain=1.0, interleaved=False, head_major=False, lengths=None, inplace=False):
+    """The gradients of rotary_fwd's inputs from those of its outputs."""
+    return _rotary(dq, dk, turns, positions, gain, interleaved, head_major, lengths, inplace, True)
+
+
+_CODES = {torch.int8: LA_CODE_I8, torch.float8_e4m3fn: LA_CODE_E4M3}
+
+
+def _code_of(dtype):
+    if dtype not in _CODES:
+        raise TypeError(f"unsupported code {dtype}: use int8 or float8_e4m3fn")
+    return _CODES[dtype]
+
+
+@_on_device
+def state_pack(S, code=torch.int8):
+    """(codes, scale): a state S [B,H,D,M] (float32) in 8 bits (int8 or float8_e4m3fn) with one fp32 scale [B,H,D] a row."""
+    if S.dim() != 4:
+        raise ValueError("S: 4 dimensions")
+    B, H, D, M = S.shape
+    fmt, dev = _code_of(code), S.device
+    p = _take(S, "S", S.shape, torch.float32, dev)
+    _need_cuda(S)
+    codes, scale = torch.empty((B, H, D, M), dtype=code, device=dev), torch.empty((B, H, D), dtype=torch.float32, device=dev)
+    _check(lib().la_state_pack(p, codes.data_ptr(), scale.data_ptr(), B, H, D, M, fmt, _stream(None)), "la_state_pack")
+    return codes, scale
+
+
+@_on_device
+def state_unpack(codes, scale):
+    """The state [B,H,D,M] (float32) that state_pack's codes and scale stand for."""
+    if codes.dim() != 4:
+        raise ValueError("codes: 4 dimensions")
+    B, H, D, M = codes.shape
+    fmt, dev = _code_of(codes.dtype), codes.device
+    ptrs = _take(codes, "codes", codes.shape, codes.dtype, dev), _take(scale, "scale", (B, H, D), torch.float32, dev)
+    _need_cuda(codes)
+    S = torch.empty((B, H, D, M), dtype=torch.float32, device=dev)
+    _check(lib().la_state_unpack(*ptrs, S.data_ptr(), B, H, D, M, fmt, _stream(None)), "la_state_unpack")
+    return S
+
+
+@_on_device
+def cross_step_packed(q, codes, scale, Z):
+    """cross_step from an S that state_pack has put into 8 bits: q [B,H,D], codes [B,Hk,D,M], scale and Z [B,Hk,D]."""
+    if q.dim() != 3 or codes.dim() != 4:
+        raise ValueError("q: 3 dimensions, codes: 4")
+    B, H, D = q.shape
+    Hk, M = codes.shape[1], codes.shape[3]
+    _need_ints(q, codes)
+    code, fmt, dtype, dev = _dtype_code(q), _code_of(codes.dtype), q.dtype, q.device
+    ptrs = (_take(q, "q", q.shape, dtype, dev), _take(codes, "codes", (B, Hk, D, M), codes.dtype, dev),
+            _take(scale, "scale", (B, Hk, D), torch.float32, dev), _take(Z, "Z", (B, Hk, D), torch.float32, dev))
+    _need_cuda(q)
+    y = torch.empty((B, H, M), dtype=dtype, device=dev)
+    _check(lib().la_cross_step_packed(*ptrs, y.data_ptr(), B, H, Hk, D, M, fmt, code, _stream(None)), "la_cross_step_packed")
+    return y
+
+
 class _Causal(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v):
@@ -901,3 +1208,72 @@ def selective_scan(x, dt, A, Bm, Cm, skip=None, dt_bias=None, lengths=None):
 def cross_linear_attention(q, k, v, lengths=None):
     """Kernelized cross attention to an encoder's states (cross_fwd) with its gradients."""
     return _Cross.apply(q, k, v, lengths)
+
+
+class _Gated(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, r, i, lam, scale, lengths):
+        y, kept = gated_fwd(x, r, i, lam, None, scale, lengths, keep=True)
+        ctx.save_for_backward(x, r, i, lam, kept, lengths)
+        ctx.scale = scale
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        *inputs, lengths = ctx.saved_tensors
+        return *gated_bwd(*inputs, _gradient(dy), ctx.scale, lengths), None, None
+
+
+class _Norm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, w, b, residual, groups, eps, lengths):
+        y, s, mean, rstd = norm_fwd(x, w, b, residual, groups, eps, lengths)
+        ctx.save_for_backward(s, w, mean, rstd, lengths)
+        ctx.how = groups, b is not None, residual is not None
+        ctx.set_materialize_grads(False)
+        return y if residual is None else (y, s)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, ds=None):
+        s, w, mean, rstd, lengths = ctx.saved_tensors
+        groups, bias, residual = ctx.how
+        if dy is None and ds is None:
+            return (None,) * 7
+        dy = torch.zeros(s.shape, dtype=s.dtype, device=s.device) if dy is None else _gradient(dy)
+        dx, dw, db = norm_bwd(s, w, mean, rstd, dy, None if ds is None else _gradient(ds), groups, bias, lengths)
+        return dx, dw, db, dx if residual else None, None, None, None
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, turns, how):
+        ctx.save_for_backward(turns, how["positions"], how["lengths"])
+        ctx.how = {n: how[n] for n in ("gain", "interleaved", "head_major")}
+        ctx.keys = k is not None
+        oq, ok = rotary_fwd(q, k, turns, **how)
+        return (oq, ok) if ctx.keys else oq
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dq, dk=None):
+        turns, positions, lengths = ctx.saved_tensors
+        dq, dk = rotary_bwd(_gradient(dq), _gradient(dk) if ctx.keys else None, turns, positions=positions, lengths=lengths, **ctx.how)
+        return dq, dk, None, None
+
+
+def gated_recurrence(x, r, i, lam, scale=8.0, lengths=None):
+    """gated_fwd with its gradients (zero state before row 0)."""
+    return _Gated.apply(x, r, i, lam, scale, lengths)
+
+
+def layer_norm(x, w, b=None, residual=None, groups=1, eps=1e-5, lengths=None):
+    """norm_fwd with its gradients: y, or (y, s) with a residual, s = x + residual."""
+    return _Norm.apply(x, w, b, residual, groups, eps, lengths)
+
+
+def rotary(q, k, turns, positions=None, gain=1.0, interleaved=False, head_major=False, lengths=None):
+    """rotary_fwd with its gradients: (q', k'), k' None without k."""
+    out = _Rotary.apply(q, k, turns, dict(positions=positions, gain=gain, interleaved=interleaved, head_major=head_major, lengths=lengths))
+    return out if k is not None else (out, None)

@@ -152,6 +152,29 @@ size_t scan_ws(const la::ScanShape& s, bool bwd) {
   return s.dtype == LA_BF16 ? la::scan_tc_ws_bytes(s, bwd) : la::scan_cc_ws_bytes(s, bwd);
 }
 
+bool typed(int dtype) { return dtype == LA_F32 || dtype == LA_BF16; }
+
+int check_gated(const la::GatedShape& s, int max_b) {
+  if (s.B < 1 || s.N < 1 || s.C < 1 || s.B > max_b || s.N > (1 << 24) || s.C > 65536) return LA_ERR_INVALID_ARG;
+  if (s.ldx < s.C || s.ldr < s.C || s.ldi < s.C || !typed(s.dtype)) return LA_ERR_INVALID_ARG;
+  return s.scale > 0.f && s.scale <= 3.0e38f ? LA_OK : LA_ERR_INVALID_ARG;
+}
+
+int check_norm(const la::NormShape& s) {
+  if (s.B < 1 || s.N < 1 || s.C < 1 || s.G < 1 || s.C > 65536 || s.C % s.G != 0) return LA_ERR_INVALID_ARG;
+  if ((long long)s.B * s.N > INT32_MAX / s.G || s.ldx < s.C || s.ldr < s.C || !typed(s.dtype)) return LA_ERR_INVALID_ARG;
+  return s.C / s.G > la::kNormMax ? LA_ERR_UNSUPPORTED : LA_OK;
+}
+
+int check_rotary(const la::RotaryShape& s) {
+  if (s.B < 1 || s.N < 1 || s.H < 1 || s.Hk < 0 || s.H > 32767 || s.Hk > 32767 || (long long)s.B * s.N > INT32_MAX) return LA_ERR_INVALID_ARG;
+  if (s.R < 2 || s.R % 2 != 0 || s.D < s.R || !typed(s.dtype)) return LA_ERR_INVALID_ARG;
+  if (!s.head_major && (s.ldq < (long)s.H * s.D || (s.Hk > 0 && s.ldk < (long)s.Hk * s.D))) return LA_ERR_INVALID_ARG;
+  return s.D > 1024 ? LA_ERR_UNSUPPORTED : LA_OK;
+}
+
+int check_code(int code) { return code == LA_CODE_I8 || code == LA_CODE_E4M3 ? LA_OK : LA_ERR_INVALID_ARG; }
+
 }  // namespace
 
 namespace la {
@@ -526,6 +549,127 @@ int la_cross_step(const void* q, const float* S, const float* Z, void* y, int B,
   LA_TRY(check_cross(s, 1ll << 20));
   LA_TRY(check_ptrs({q, S, Z, y}));
   return from_cuda(la::cross_step(q, S, Z, y, s, static_cast<cudaStream_t>(stream)));
+}
+
+size_t la_gated_workspace_bytes(int bwd, int B, int N, int C, int dtype) {
+  const la::GatedShape s{B, N, C, C, C, C, 1.f, dtype};
+  return check_gated(s, 65535) == LA_OK ? la::gated_ws_bytes(s, bwd != 0) : 0;
+}
+
+size_t la_gated_kept_bytes(int B, int N, int C, int dtype) {
+  const la::GatedShape s{B, N, C, C, C, C, 1.f, dtype};
+  return check_gated(s, 65535) == LA_OK ? la::gated_kept_bytes(s) : 0;
+}
+
+int la_gated_fwd(const void* x, const void* r, const void* i, const void* lam, const int* lengths, float* h, void* kept, void* y,
+                 void* workspace, size_t workspace_bytes, int B, int N, int C, int ldx, int ldr, int ldi, float scale, int dtype,
+                 void* stream) {
+  const la::GatedShape s{B, N, C, ldx, ldr, ldi, scale, dtype};
+  LA_TRY(check_gated(s, 65535));
+  for (const void* p : {x, r, i}) LA_TRY(check_to(p, elem(dtype)));
+  LA_TRY(check_ptrs({lam, y}));
+  LA_TRY(check_opt_ptr(h));
+  LA_TRY(check_opt_ptr(kept));
+  LA_TRY(check_to(lengths, 4, true));
+  LA_TRY(check_room(workspace, workspace_bytes, la::gated_ws_bytes(s, false)));
+  return from_cuda(la::gated_fwd(x, r, i, lam, lengths, h, static_cast<float*>(kept), y, static_cast<float*>(workspace), s,
+                                 static_cast<cudaStream_t>(stream)));
+}
+
+int la_gated_bwd(const void* x, const void* r, const void* i, const void* lam, const int* lengths, const void* kept, const void* dy,
+                 void* dx, void* dr, void* di, void* dlam, void* workspace, size_t workspace_bytes, int B, int N, int C, int ldx, int ldr,
+                 int ldi, float scale, int dtype, void* stream) {
+  const la::GatedShape s{B, N, C, ldx, ldr, ldi, scale, dtype};
+  LA_TRY(check_gated(s, 65535));
+  for (const void* p : {x, r, i}) LA_TRY(check_to(p, elem(dtype)));
+  LA_TRY(check_ptrs({lam, kept, dy, dx, dr, di, dlam}));
+  LA_TRY(check_to(lengths, 4, true));
+  LA_TRY(check_room(workspace, workspace_bytes, la::gated_ws_bytes(s, true)));
+  return from_cuda(la::gated_bwd(x, r, i, lam, lengths, static_cast<const float*>(kept), dy, dx, dr, di, dlam,
+                                 static_cast<float*>(workspace), s, static_cast<cudaStream_t>(stream)));
+}
+
+int la_gated_step(const void* x, const void* r, const void* i, const void* lam, float* h, void* y, int B, int C, int ldx, int ldr, int ldi,
+                  float scale, int dtype, void* stream) {
+  const la::GatedShape s{B, 1, C, ldx, ldr, ldi, scale, dtype};
+  LA_TRY(check_gated(s, 1 << 20));
+  for (const void* p : {x, r, i}) LA_TRY(check_to(p, elem(dtype)));
+  LA_TRY(check_ptrs({lam, h, y}));
+  return from_cuda(la::gated_step(x, r, i, lam, h, y, s, static_cast<cudaStream_t>(stream)));
+}
+
+size_t la_norm_workspace_bytes(int B, int N, int C, int G, int dtype) {
+  const la::NormShape s{B, N, C, G, C, C, dtype};
+  return check_norm(s) == LA_OK ? la::norm_bwd_ws_bytes(s) : 0;
+}
+
+int la_norm_fwd(const void* x, const void* residual, const void* w, const void* b, const int* lengths, void* y, void* s, float* mean,
+                float* rstd, float eps, int B, int N, int C, int G, int ldx, int ldr, int dtype, void* stream) {
+  const la::NormShape sh{B, N, C, G, ldx, residual == nullptr ? C : ldr, dtype};
+  LA_TRY(check_norm(sh));
+  LA_TRY(check_to(x, elem(dtype)));
+  LA_TRY(check_to(residual, elem(dtype), true));
+  LA_TRY(check_ptrs({w, y}));
+  for (const void* p : {b, static_cast<const void*>(s), static_cast<const void*>(mean), static_cast<const void*>(rstd)}) LA_TRY(check_opt_ptr(p));
+  if ((residual != nullptr && s == nullptr) || (mean == nullptr) != (rstd == nullptr)) return LA_ERR_INVALID_ARG;
+  if (!(eps >= 0.f && eps <= 3.0e38f)) return LA_ERR_INVALID_ARG;
+  LA_TRY(check_to(lengths, 4, true));
+  return from_cuda(la::norm_fwd(x, residual, w, b, lengths, y, s, mean, rstd, eps, sh, static_cast<cudaStream_t>(stream)));
+}
+
+int la_norm_bwd(const void* s, const void* w, const float* mean, const float* rstd, const int* lengths, const void* dy, const void* ds,
+                void* dx, void* dw, void* db, void* workspace, size_t workspace_bytes, int B, int N, int C, int G, int lds, int dtype,
+                void* stream) {
+  const la::NormShape sh{B, N, C, G, lds, C, dtype};
+  LA_TRY(check_norm(sh));
+  LA_TRY(check_to(s, elem(dtype)));
+  LA_TRY(check_ptrs({w, mean, rstd, dy, dx, dw}));
+  for (const void* p : {ds, static_cast<const void*>(db)}) LA_TRY(check_opt_ptr(p));
+  LA_TRY(check_to(lengths, 4, true));
+  LA_TRY(check_room(workspace, workspace_bytes, la::norm_bwd_ws_bytes(sh)));
+  return from_cuda(la::norm_bwd(s, w, mean, rstd, lengths, dy, ds, dx, dw, db, static_cast<float*>(workspace), sh,
+                                static_cast<cudaStream_t>(stream)));
+}
+
+int la_rotary(const void* q, const void* k, void* oq, void* ok, const void* turns, const int* positions, const int* lengths, float gain,
+              int B, int N, int H, int Hk, int D, int R, int ldq, int ldk, int per_row, int interleaved, int head_major, int inverse,
+              int dtype, void* stream) {
+  const la::RotaryShape s{B, N, H, Hk, D, R, ldq, ldk, per_row != 0, interleaved != 0, head_major != 0, inverse != 0, dtype};
+  LA_TRY(check_rotary(s));
+  LA_TRY(check_to(q, elem(dtype)));
+  LA_TRY(check_to(oq, q == oq ? elem(dtype) : 16));
+  if ((Hk == 0) != (k == nullptr) || (Hk == 0) != (ok == nullptr) || (Hk > 0 && (q == oq) != (k == ok))) return LA_ERR_INVALID_ARG;
+  LA_TRY(check_to(k, elem(dtype), true));
+  LA_TRY(check_to(ok, k == ok ? elem(dtype) : 16, true));
+  LA_TRY(check_to(turns, 8));
+  LA_TRY(check_to(positions, 4, true));
+  LA_TRY(check_to(lengths, 4, true));
+  if (!(gain >= -3.0e38f && gain <= 3.0e38f)) return LA_ERR_INVALID_ARG;
+  return from_cuda(la::rotary(q, k, oq, ok, static_cast<const unsigned long long*>(turns), positions, lengths, s, gain,
+                              static_cast<cudaStream_t>(stream)));
+}
+
+int la_state_pack(const float* S, void* code, float* scale, int B, int H, int D, int M, int format, void* stream) {
+  LA_TRY(check_code(format));
+  LA_TRY(check_shape(B, H, 1, D, M, LA_F32, 1ll << 20));
+  LA_TRY(check_ptrs({S, code, scale}));
+  return from_cuda(la::state_pack(S, code, scale, (long)B * H * D, M, format, static_cast<cudaStream_t>(stream)));
+}
+
+int la_state_unpack(const void* code, const float* scale, float* S, int B, int H, int D, int M, int format, void* stream) {
+  LA_TRY(check_code(format));
+  LA_TRY(check_shape(B, H, 1, D, M, LA_F32, 1ll << 20));
+  LA_TRY(check_ptrs({S, code, scale}));
+  return from_cuda(la::state_unpack(code, scale, S, (long)B * H * D, M, format, static_cast<cudaStream_t>(stream)));
+}
+
+int la_cross_step_packed(const void* q, const void* code, const float* scale, const float* Z, void* y, int B, int H, int Hk, int D, int M,
+                         int format, int dtype, void* stream) {
+  const la::CrossShape s{B, H, Hk, 1, 1, D, M, dtype};
+  LA_TRY(check_code(format));
+  LA_TRY(check_cross(s, 1ll << 20));
+  LA_TRY(check_ptrs({q, code, scale, Z, y}));
+  return from_cuda(la::cross_step_packed(q, code, scale, Z, y, format, s, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -212,6 +212,50 @@ cudaError_t cross_bwd_tc(const void* q, const void* k, const void* v, const int*
                          cudaStream_t st);
 cudaError_t cross_step(const void* q, const float* S, const float* Z, void* y, const CrossShape& s, cudaStream_t st);
 
+// States in 8 bits (states.cu); fmt: 0 int8, 1 e4m3.
+cudaError_t state_pack(const float* S, void* code, float* scale, long rows, int M, int fmt, cudaStream_t st);
+cudaError_t state_unpack(const void* code, const float* scale, float* S, long rows, int M, int fmt, cudaStream_t st);
+cudaError_t cross_step_packed(const void* q, const void* code, const float* scale, const float* Z, void* y, int fmt, const CrossShape& s,
+                              cudaStream_t st);
+
+// The gated recurrence (gated.cu): rows ldx, ldr, ldi elements apart.
+struct GatedShape {
+  int B, N, C;
+  long ldx, ldr, ldi;
+  float scale;
+  int dtype;
+};
+size_t gated_kept_bytes(const GatedShape& s);
+size_t gated_ws_bytes(const GatedShape& s, bool bwd);
+cudaError_t gated_fwd(const void* x, const void* r, const void* i, const void* lam, const int* lengths, float* h, float* kept, void* y,
+                      float* ws, const GatedShape& s, cudaStream_t st);
+cudaError_t gated_bwd(const void* x, const void* r, const void* i, const void* lam, const int* lengths, const float* kept, const void* dy,
+                      void* dx, void* dr, void* di, void* dlam, float* ws, const GatedShape& s, cudaStream_t st);
+cudaError_t gated_step(const void* x, const void* r, const void* i, const void* lam, float* h, void* y, const GatedShape& s, cudaStream_t st);
+
+// The layer norm (norm.cu): G groups of C / G columns; rows ldx and ldr elements apart.
+constexpr int kNormMax = 8192;  // columns of a group
+struct NormShape {
+  int B, N, C, G;
+  long ldx, ldr;
+  int dtype;
+};
+size_t norm_bwd_ws_bytes(const NormShape& s);
+cudaError_t norm_fwd(const void* x, const void* res, const void* w, const void* b, const int* lengths, void* y, void* s, float* mean,
+                     float* rstd, float eps, const NormShape& sh, cudaStream_t st);
+cudaError_t norm_bwd(const void* s, const void* w, const float* mean, const float* rstd, const int* lengths, const void* dy, const void* ds,
+                     void* dx, void* dw, void* db, float* ws, const NormShape& sh, cudaStream_t st);
+
+// Rotary positions (rotary.cu): token-major rows ldq and ldk elements apart, or dense head-major tensors.
+struct RotaryShape {
+  int B, N, H, Hk, D, R;
+  long ldq, ldk;
+  int per_row, interleaved, head_major, inverse;
+  int dtype;
+};
+cudaError_t rotary(const void* q, const void* k, void* oq, void* ok, const unsigned long long* turns, const int* positions,
+                   const int* lengths, const RotaryShape& s, float gain, cudaStream_t st);
+
 }  // namespace la
 
 // Expands the body once per supported (D, M) pair with constexpr D_ and M_ in scope.
