@@ -572,7 +572,7 @@ int la_gated_fwd(const void* x, const void* r, const void* i, const void* lam, c
   LA_TRY(check_opt_ptr(kept));
   LA_TRY(check_to(lengths, 4, true));
   LA_TRY(check_room(workspace, workspace_bytes, la::gated_ws_bytes(s, false)));
-  return from_cuda(la::gated_fwd(x, r, i, lam, lengths, h, static_cast<float*>(kept), y, static_cast<float*>(workspace), s,
+  return from_cuda(la::gated_fwd(x, r, i, lam, lengths, h, static_cast<float*>(kept), y, workspace, s,
                                  static_cast<cudaStream_t>(stream)));
 }
 
@@ -585,8 +585,8 @@ int la_gated_bwd(const void* x, const void* r, const void* i, const void* lam, c
   LA_TRY(check_ptrs({lam, kept, dy, dx, dr, di, dlam}));
   LA_TRY(check_to(lengths, 4, true));
   LA_TRY(check_room(workspace, workspace_bytes, la::gated_ws_bytes(s, true)));
-  return from_cuda(la::gated_bwd(x, r, i, lam, lengths, static_cast<const float*>(kept), dy, dx, dr, di, dlam,
-                                 static_cast<float*>(workspace), s, static_cast<cudaStream_t>(stream)));
+  return from_cuda(la::gated_bwd(x, r, i, lam, lengths, static_cast<const float*>(kept), dy, dx, dr, di, dlam, workspace, s,
+                                 static_cast<cudaStream_t>(stream)));
 }
 
 int la_gated_step(const void* x, const void* r, const void* i, const void* lam, float* h, void* y, int B, int C, int ldx, int ldr, int ldi,

@@ -6,11 +6,17 @@
 //   dr = (1 - s) Q,  dlam = sigmoid(lam) / softplus(lam) sum Q.
 // (u / beta goes to zero with u, so a closed gate has no infinite term.)
 //
-// The recurrence is associative: a tile of TILE rows turns its first state h into
-// A h + H, so a first pass forms every tile's (A, H), a second carries the states over
-// the tiles, and a third replays each tile from its state.  A thread owns two channels
-// and a strip of rows, whose a and b it keeps in registers between its own pass and the
-// replay; a tile's strips are joined through shared memory.
+// The recurrence is associative: a tile of rows turns its first state h into A h + H.
+// One pass a direction reads every row once: resident blocks take tiles of rows of CH
+// channels in turn, the next tile's rows on their way into shared memory (a warp's own
+// rows, 16 bytes a copy) while one is worked on.  A thread has two channels of a strip of
+// rows, whose a and b it keeps in registers; the strips are joined through shared memory,
+// the tile's (A, H) goes to device memory, the tiles before it are looked up, and the
+// strips are replayed from the state that these give.  Blocks run all at once (a
+// cooperative launch) and take tiles in order, every grid's width one, so the first tile
+// that is not done waits for none.
+// The state passed on is the same sequence of fused multiply-adds whichever tiles had
+// theirs already, so results repeat bit for bit.
 #include <algorithm>
 
 #include "scan.cuh"
@@ -19,401 +25,621 @@ namespace la {
 namespace {
 
 using bf16 = __nv_bfloat16;
+using u64 = unsigned long long;
 
-constexpr int STRIP = 8;            // rows of a thread
-constexpr int WARPS = 8;            // strips of a tile
-constexpr int TILE = STRIP * WARPS;
-constexpr int CH = 64;              // channels of a tile, two a lane
-
-// 1 - exp(-u) for u >= 0 to about an ulp, also where u is tiny (a decay close to one is
-// one minus it): the series below 1/2 (next term 6e-9), the exponential above.
+constexpr int CH = 64;      // channels of a tile, two a lane
+constexpr int WARPS = 8;    // strips of a tile
+constexpr int KEEP = 64;    // rows of a gradient tile, and between the states kept for it
+constexpr int FWD_WINDOW = 16, BACK_WINDOW = 32;  // tiles looked up before one must have its state
 template <typename T>
-__device__ __forceinline__ float one_minus_exp(float u) {
-  float p = fmaf(u, -1.f / 40320, 1.f / 5040);
-  p = fmaf(u, p, -1.f / 720);
-  p = fmaf(u, p, 1.f / 120);
-  p = fmaf(u, p, -1.f / 24);
-  p = fmaf(u, p, 1.f / 6);
-  p = fmaf(u, p, -0.5f);
-  p = fmaf(u, p, 1.f);
-  float w = u * p;
-  if (!(u < 0.5f)) w = 1.f - (sizeof(T) == 4 ? expf(-u) : ex2_fast(-1.4426950408889634f * u));
-  return w;
-}
-
-// bf16: the hardware's exponential and reciprocal, 2^-22 beside the 2^-9 of the rows.
+constexpr int FWD = sizeof(T) == 4 ? 8 : 16;  // rows of a strip, forward: 48 KB of rows a tile
 template <typename T>
-__device__ __forceinline__ float sigmoid(float x) {
-  return sizeof(T) == 4 ? 1.f / (1.f + expf(-x)) : rcp_fast(1.f + ex2_fast(-1.4426950408889634f * x));
-}
+constexpr int BACK_STAGES = sizeof(T) == 4 ? 1 : 2;  // 64 and 32 KB of rows a gradient tile
 
+// ---------------------------------------------------------- two channels at once
+
+__device__ __forceinline__ u64 pk(float x, float y) {
+  u64 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  return v;
+}
+__device__ __forceinline__ float2 un(u64 v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ u64 two(float x) { return pk(x, x); }
+__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
+  u64 v;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+  u64 v;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
+  return v;
+}
+__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
+  u64 v;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
+  return v;
+}
 __device__ __forceinline__ float rsqrt_fast(float x) {
   float y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-struct Gate {
-  float u, a, beta, ub;  // ub = u / beta
-};
-template <typename T>
-__device__ __forceinline__ Gate gate(float k, float s) {
-  Gate q;
-  q.u = k * s;
-  const float w = one_minus_exp<T>(q.u), om = w * (2.f - w);
-  q.a = 1.f - w;
-  const float ri = om > 1e-36f ? rsqrt_fast(om) : om == om ? 0.f : om;  // a NaN stays
-  q.beta = om * ri;
-  q.ub = q.u * ri;
-  return q;
+__device__ __forceinline__ u64 ex2_2(u64 v) {
+  const float2 f = un(v);
+  return pk(ex2_fast(f.x), ex2_fast(f.y));
+}
+__device__ __forceinline__ u64 rcp_2(u64 v) {
+  const float2 f = un(v);
+  return pk(rcp_fast(f.x), rcp_fast(f.y));
 }
 
-// Two neighbouring channels of a row, as one vector (PAIR: aligned, both there) or one by one.
-template <typename T>
-struct Two;
-template <>
-struct Two<float> {
-  float2 v;
-};
-template <>
-struct Two<bf16> {
-  uint32_t v;
-};
-template <bool PAIR>
-__device__ __forceinline__ Two<float> load2(const float* p, bool second) {
-  if (PAIR) return {*reinterpret_cast<const float2*>(p)};
-  return {make_float2(p[0], second ? p[1] : 0.f)};
+// w = 1 - exp(-u) for u >= 0, relative error 2^-21 at most and 2^-24 where u < 1, so that a
+// decay close to one is one minus it: a polynomial fitted to w / u on [0, 1], the
+// exponential above.
+__device__ __forceinline__ u64 near_one(u64 u) {
+  u64 p = fma2(u, two(0.00012918687f), two(-0.0013011073f));
+  p = fma2(u, p, two(0.00827588f));
+  p = fma2(u, p, two(-0.041647043f));
+  p = fma2(u, p, two(0.16666345f));
+  p = fma2(u, p, two(-0.4999998f));
+  p = fma2(u, p, two(1.f));
+  return mul2(u, p);
 }
-template <bool PAIR>
-__device__ __forceinline__ Two<bf16> load2(const bf16* p, bool second) {
-  if (PAIR) return {*reinterpret_cast<const uint32_t*>(p)};
+__device__ __forceinline__ u64 minus_one(u64 w) { return fma2(w, two(-1.f), two(1.f)); }
+// beta = sqrt(w (1 + a)); zero where that is below 1e-36.
+__device__ __forceinline__ u64 root(u64 w, u64 a) {
+  const u64 om = fma2(w, a, w);
+  const float2 f = un(om);
+  return mul2(om, pk(rsqrt_fast(fmaxf(f.x, 1e-36f)), rsqrt_fast(fmaxf(f.y, 1e-36f))));
+}
+
+// A row's gates: s, g, a and beta.  Both sigmoids, 1 / (1 + e) each, come from one
+// reciprocal of the product, unless that is near overflow or NaN (arguments below -69 in
+// sum); `quick` stays true where the short forms hold, and the full form gives a channel
+// for which they do the same bits.
+__device__ __forceinline__ void gates_quick(u64 r, u64 i, u64 k, u64& s, u64& g, u64& a, u64& beta, bool& quick) {
+  const u64 scale = two(-1.4426950408889634f), one = two(1.f);
+  const u64 d1 = add2(ex2_2(mul2(r, scale)), one), d2 = add2(ex2_2(mul2(i, scale)), one), p = mul2(d1, d2), q = rcp_2(p);
+  s = mul2(q, d2), g = mul2(q, d1);
+  const u64 u = mul2(k, s), w = near_one(u);
+  const float2 pf = un(p), uf = un(u);
+  quick = quick & (pf.x < 1e30f) & (pf.y < 1e30f) & (uf.x < 1.f) & (uf.y < 1.f);
+  a = minus_one(w);
+  beta = root(w, a);
+}
+__device__ __forceinline__ u64 pick(bool x, bool y, u64 a, u64 b) {
+  const float2 af = un(a), bf = un(b);
+  return pk(x ? af.x : bf.x, y ? af.y : bf.y);
+}
+__device__ __forceinline__ void gates(u64 r, u64 i, u64 k, u64& s, u64& g, u64& a, u64& beta) {
+  const u64 scale = two(-1.4426950408889634f), one = two(1.f);
+  const u64 d1 = add2(ex2_2(mul2(r, scale)), one), d2 = add2(ex2_2(mul2(i, scale)), one), p = mul2(d1, d2), q = rcp_2(p);
+  const float2 pf = un(p);
+  s = pick(pf.x < 1e30f, pf.y < 1e30f, mul2(q, d2), rcp_2(d1)), g = pick(pf.x < 1e30f, pf.y < 1e30f, mul2(q, d1), rcp_2(d2));
+  const u64 u = mul2(k, s);
+  const float2 uf = un(u);
+  const u64 w = pick(uf.x < 1.f, uf.y < 1.f, near_one(u), fma2(ex2_2(mul2(u, two(-1.4426950408889634f))), two(-1.f), one));
+  a = minus_one(w);
+  beta = root(w, a);
+}
+
+// ------------------------------------------------------------------------- rows
+
+// Two neighbouring channels, as they lie in memory.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  using type = u64;
+};
+template <>
+struct Raw<bf16> {
+  using type = uint32_t;
+};
+__device__ __forceinline__ u64 open(u64 t) { return t; }
+__device__ __forceinline__ u64 open(uint32_t t) { return pk(__uint_as_float(t << 16), __uint_as_float(t & 0xffff0000u)); }
+template <typename T>
+__device__ __forceinline__ typename Raw<T>::type close(u64 v) {
+  if constexpr (sizeof(T) == 4) {
+    return v;
+  } else {
+    const float2 f = un(v);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+    return *reinterpret_cast<const uint32_t*>(&b);
+  }
+}
+// The same from and to any address, channel by channel.
+__device__ __forceinline__ u64 gather(const float* p, int n) { return pk(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f); }
+__device__ __forceinline__ uint32_t gather(const bf16* p, int n) {
   const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
-  return {static_cast<uint32_t>(q[0]) | (second ? static_cast<uint32_t>(q[1]) << 16 : 0u)};
+  return (n > 0 ? static_cast<uint32_t>(q[0]) : 0u) | (n > 1 ? static_cast<uint32_t>(q[1]) << 16 : 0u);
 }
-__device__ __forceinline__ float2 open(const Two<float>& t) { return t.v; }
-__device__ __forceinline__ float2 open(const Two<bf16>& t) { return make_float2(__uint_as_float(t.v << 16), __uint_as_float(t.v & 0xffff0000u)); }
-template <bool PAIR>
-__device__ __forceinline__ void store2(float* p, float2 v, bool second) {
-  if (PAIR) {
-    *reinterpret_cast<float2*>(p) = v;
-  } else {
-    p[0] = v.x;
-    if (second) p[1] = v.y;
-  }
+__device__ __forceinline__ void scatter(float* p, int n, u64 v) {
+  const float2 f = un(v);
+  if (n > 0) p[0] = f.x;
+  if (n > 1) p[1] = f.y;
 }
-template <bool PAIR>
-__device__ __forceinline__ void store2(bf16* p, float2 v, bool second) {
-  if (PAIR) {
-    *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(v.x, v.y);
-  } else {
-    p[0] = __float2bfloat16_rn(v.x);
-    if (second) p[1] = __float2bfloat16_rn(v.y);
-  }
+__device__ __forceinline__ void scatter(bf16* p, int n, uint32_t v) {
+  unsigned short* q = reinterpret_cast<unsigned short*>(p);
+  if (n > 0) q[0] = static_cast<unsigned short>(v);
+  if (n > 1) q[1] = static_cast<unsigned short>(v >> 16);
 }
 
 struct Rows {
   const void *x, *r, *i, *lam;
   const int* lengths;
+  const float* rate;  // scale softplus(lam), with zeros up to a multiple of CH (null: from lam)
   long ldx, ldr, ldi;
-  int N, C, groups, tiles;  // groups of CH channels, tiles of TILE rows
+  int B, N, C, groups, tiles;  // groups of CH channels; tiles of a direction's rows
   float scale;
 };
 
-// Where a thread works.
-struct Place {
-  int tile, c, b, t0, L;  // its strip's first row, the sequence's valid rows
-  bool first, second;     // which of its channels exist
-  __device__ __forceinline__ explicit Place(const Rows& a) {
-    tile = blockIdx.x / a.groups;
-    c = (blockIdx.x % a.groups) * CH + 2 * (threadIdx.x & 31);
-    b = blockIdx.y;
-    t0 = tile * TILE + (threadIdx.x >> 5) * STRIP;
-    L = valid_rows(a.lengths, b, a.N);
-    first = c < a.C;
-    second = c + 1 < a.C;
-  }
+// Tiles that pass states on: by tile and column (batch entry and group) A, H and then the
+// state behind the tile, 32 words each.
+struct Chain {
+  u64* word;
+  int* err;
 };
 
-template <typename T, bool PAIR>
-__device__ __forceinline__ float2 rates(const Rows& a, const Place& p) {
-  if (!p.first) return make_float2(0.f, 0.f);
-  const float2 l = open(load2<PAIR>(static_cast<const T*>(a.lam) + p.c, p.second));
-  return make_float2(a.scale * softplus(l.x), p.second ? a.scale * softplus(l.y) : 0.f);
-}
-
-template <typename T, bool PAIR>
-__device__ __forceinline__ void fetch(Two<T> (&v)[STRIP], const void* base, long ld, const Rows& a, const Place& p) {
-  const T* q = static_cast<const T*>(base) + ((long)p.b * a.N + p.t0) * ld + p.c;
-#pragma unroll
-  for (int j = 0; j < STRIP; ++j) {
-    v[j] = Two<T>{};
-    if (p.first && p.t0 + j < p.L) v[j] = load2<PAIR>(q + j * ld, p.second);
-  }
-}
-
-// (A, H) of the strips of a tile, by strip and lane.
-struct Strips {
-  float2 A[WARPS][32], H[WARPS][32];
+struct Job {
+  int tile, col, b, c0, L;  // c0: first channel; L: the sequence's valid rows; tile < 0: none
 };
 
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
+__device__ __forceinline__ Job job_of(const Rows& a, int number, int total, bool reverse) {
+  Job j{-1, 0, 0, 0, 0};
+  if (number < total) {
+    const int cols = a.groups * a.B, t = number / cols;
+    j.col = number - t * cols;
+    j.tile = reverse ? a.tiles - 1 - t : t;
+    j.b = j.col / a.groups;
+    j.c0 = (j.col - j.b * a.groups) * CH;
+    j.L = valid_rows(a.lengths, j.b, a.N);
+  }
+  return j;
+}
 
-// a and b = beta g x of a strip; rows past the length keep the state.
 template <typename T>
-__device__ __forceinline__ void decays(float2 (&av)[STRIP], float2 (&bv)[STRIP], const Two<T> (&x)[STRIP], const Two<T> (&r)[STRIP],
-                                       const Two<T> (&g)[STRIP], float2 k, const Place& p) {
+__device__ __forceinline__ u64 rates(const Rows& a, int c) {
+  if (a.rate != nullptr) return *reinterpret_cast<const u64*>(a.rate + c);
+  const float2 l = un(open(gather(static_cast<const T*>(a.lam) + c, a.C - c)));
+  return pk(c < a.C ? a.scale * softplus(l.x) : 0.f, c + 1 < a.C ? a.scale * softplus(l.y) : 0.f);
+}
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* to, const void* from, int bytes) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(to)), "l"(from), "r"(bytes) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(to)), "l"(from), "r"(bytes) : "memory");
+}
+
+// A warp's RW rows from t0 on of CH channels from c0 on into its own rows of shared
+// memory; zeros past the length and the width.  UNIT: the bytes that rows, widths and
+// strides are whole multiples of: 16 or 4, asynchronous copies of that many, or 2.
+template <typename T, int UNIT, int RW>
+__device__ __forceinline__ void bring(T* to, const void* base, long ld, const Rows& a, const Job& j, int t0) {
+  const int lane = threadIdx.x & 31;
+  const T* from = static_cast<const T*>(base) + ((long)j.b * a.N + t0) * ld + j.c0;
+  if constexpr (UNIT == 16) {
+    constexpr int E = 16 / sizeof(T), LR = CH / E, PER = 32 / LR;  // lanes a row, rows an instruction
+    const int c = (lane % LR) * E, r0 = lane / LR;
+    const bool wide = j.c0 + c < a.C;
+    const T* q = from + r0 * ld + c;
+    T* o = to + r0 * CH + c;
 #pragma unroll
-  for (int j = 0; j < STRIP; ++j) {
-    av[j] = make_float2(1.f, 1.f), bv[j] = make_float2(0.f, 0.f);
-    if (p.t0 + j < p.L) {
-      const float2 xf = open(x[j]), rf = open(r[j]), gf = open(g[j]);
-      const Gate g0 = gate<T>(k.x, sigmoid<T>(rf.x)), g1 = gate<T>(k.y, sigmoid<T>(rf.y));
-      av[j] = make_float2(g0.a, g1.a);
-      bv[j] = make_float2(g0.beta * (sigmoid<T>(gf.x) * xf.x), g1.beta * (sigmoid<T>(gf.y) * xf.y));
+    for (int r = 0; r < RW; r += PER) {
+      const bool in = wide && t0 + r0 + r < j.L;
+      copy_async<16>(o + r * CH, in ? q : base, in ? 16 : 0);
+      q += PER * ld;
     }
+  } else if constexpr (UNIT == 4) {
+    constexpr int E = 4 / sizeof(T);
+    for (int c = lane * E; c < CH; c += 32 * E) {
+      const bool wide = j.c0 + c < a.C;
+      const T* q = from + c;
+#pragma unroll
+      for (int r = 0; r < RW; ++r) {
+        const bool in = wide && t0 + r < j.L;
+        copy_async<4>(to + r * CH + c, in ? q : base, in ? 4 : 0);
+        q += ld;
+      }
+    }
+  } else {
+    const int n = a.C - j.c0 - 2 * lane;
+#pragma unroll
+    for (int r = 0; r < RW; ++r)
+      reinterpret_cast<typename Raw<T>::type*>(to)[r * (CH / 2) + lane] = gather(from + r * ld + 2 * lane, t0 + r < j.L ? n : 0);
   }
 }
 
-__device__ __forceinline__ long record(const Rows& a, const Place& p) { return ((long)p.b * a.tiles + p.tile) * a.C + p.c; }
+// The way back: a warp's RW rows, as far as there are N.
+template <typename T, int UNIT, int RW>
+__device__ __forceinline__ void leave(T* out, const T* from, const Rows& a, const Job& j, int t0) {
+  const int lane = threadIdx.x & 31;
+  T* to = out + ((long)j.b * a.N + t0) * a.C + j.c0;
+  if constexpr (UNIT == 16) {
+    constexpr int E = 16 / sizeof(T), LR = CH / E, PER = 32 / LR;
+    const int c = (lane % LR) * E, r0 = lane / LR;
+    const bool wide = j.c0 + c < a.C;
+#pragma unroll
+    for (int r = 0; r < RW; r += PER)
+      if (wide && t0 + r0 + r < a.N)
+        *reinterpret_cast<uint4*>(to + (long)(r0 + r) * a.C + c) = *reinterpret_cast<const uint4*>(from + (r0 + r) * CH + c);
+  } else {
+    const int n = a.C - j.c0 - 2 * lane;
+#pragma unroll 4
+    for (int r = 0; r < RW; ++r)
+      if (t0 + r < a.N) scatter(to + (long)r * a.C + 2 * lane, n, reinterpret_cast<const typename Raw<T>::type*>(from)[r * (CH / 2) + lane]);
+  }
+}
 
-// A tile's (A, H) from its rows.
-template <typename T, bool PAIR>
-__global__ void __launch_bounds__(32 * WARPS) k_gated_sums(const Rows a, float* __restrict__ recA, float* __restrict__ recH) {
-  __shared__ Strips st;
-  const Place p(a);
+// -------------------------------------------------------------------- the chain
+
+// Words of a tile start as EMPTY, a pair of NaNs that no sum gives (those are the
+// canonical one), and say by themselves that they have come: a tile's words need no
+// order among them, and one round trip brings them.
+constexpr u64 EMPTY = ~0ull;
+__device__ __forceinline__ void put(u64* p, u64 v) { asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory"); }
+__device__ __forceinline__ u64 look(const u64* p) {
+  u64 v;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+  return v;
+}
+
+template <int WINDOW>
+struct Shared {
+  u64 A[2][WARPS][32], H[2][WARPS][32];  // (A, H) of the strips, by lane; alternate tiles use alternate halves
+  u64 wA[WINDOW][32], wH[WINDOW][32];    // of the tiles looked up; wH: the state where kind is 2
+  u64 start[2][32];                      // the caller's state
+  int kind[WINDOW];
+};
+
+// What the n tiles before this one (the j-th is entry at + j step of the chain) pass on:
+// the nearest state, moved on by the tiles since.  All threads call it; warp w looks
+// up the tiles w, w + WARPS, ...  The tile that is WINDOW back must have its state.
+// A wait of two seconds gives up: zero, and the code in the status word.
+template <int WINDOW>
+__device__ __forceinline__ u64 look_up(Shared<WINDOW>& sh, const Chain& ch, long at, long step, int n, int code) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  Two<T> x[STRIP], r[STRIP], g[STRIP];
-  fetch<T, PAIR>(r, a.r, a.ldr, a, p);
-  fetch<T, PAIR>(g, a.i, a.ldi, a, p);
-  fetch<T, PAIR>(x, a.x, a.ldx, a, p);
-  float2 av[STRIP], bv[STRIP];
-  decays<T>(av, bv, x, r, g, rates<T, PAIR>(a, p), p);
-  float2 A = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int j = 0; j < STRIP; ++j) {
-    H = fma2(av[j], H, bv[j]);
-    A = make_float2(A.x * av[j].x, A.y * av[j].y);
-  }
-  st.A[w][lane] = A, st.H[w][lane] = H;
-  __syncthreads();
-  if (w == 0 && p.first) {
-#pragma unroll
-    for (int i = 1; i < WARPS; ++i) {
-      const float2 Ai = st.A[i][lane];
-      H = fma2(Ai, H, st.H[i][lane]);
-      A = make_float2(A.x * Ai.x, A.y * Ai.y);
+  int found = -1;
+#pragma unroll 1
+  for (int base = 0; base < WINDOW && found < 0; base += WARPS) {
+    const int j = base + w;
+    if (j < n) {
+      const u64* p = ch.word + (at + j * step) * 96 + lane;
+      u64 A, H, t0 = 0;
+      int kind = 0;
+      for (int tries = 0; kind == 0; ++tries) {
+        const u64 S = look(p + 64);
+        A = look(p), H = look(p + 32);
+        if (__all_sync(0xffffffffu, S != EMPTY)) {
+          H = S, kind = 2;
+        } else if (j != WINDOW - 1 && __all_sync(0xffffffffu, (A != EMPTY) & (H != EMPTY))) {
+          kind = 1;
+        } else if ((tries & 255) == 255) {
+          const u64 now = tc::globaltimer_ns();
+          if (t0 == 0) t0 = now;
+          if (__any_sync(0xffffffffu, now - t0 > 2000000000ull)) {
+            if (lane == 0) tcc::fail(ch.err, code);
+            H = 0ull, kind = 2;
+          }
+        }
+      }
+      if (kind == 1) sh.wA[j][lane] = A;
+      sh.wH[j][lane] = H;
+      if (lane == 0) sh.kind[j] = kind;
     }
-    const long at = record(a, p);
-    recA[at] = A.x, recH[at] = H.x;
-    if (p.second) recA[at + 1] = A.y, recH[at + 1] = H.y;
+    __syncthreads();
+    const int top = min(base + WARPS, n);
+    for (int i = base; i < top; ++i)
+      if (sh.kind[i] == 2) {
+        found = i;
+        break;
+      }
   }
+  u64 s = sh.wH[found][lane];
+  for (int i = found - 1; i >= 0; --i) s = fma2(sh.wA[i][lane], s, sh.wH[i][lane]);
+  return s;
 }
 
-// The states before each tile, into keep; h, if given, starts the recurrence and
-// becomes the last state.
-__global__ void __launch_bounds__(128) k_gated_carry(const float* __restrict__ recA, const float* __restrict__ recH, float* __restrict__ keep,
-                                                     float* __restrict__ h, int C, int tiles, int reverse) {
-  grid_dep_enter();
-  const int c = blockIdx.x * 128 + threadIdx.x;
-  if (c >= C) return;
-  const long at = (long)blockIdx.y * tiles * C + c;
-  float s = h == nullptr ? 0.f : h[(long)blockIdx.y * C + c];
-#pragma unroll 8
-  for (int t = 0; t < tiles; ++t) {
-    const long e = at + (long)(reverse ? tiles - 1 - t : t) * C;
-    keep[e] = s;
-    s = fmaf(recA[e], s, recH[e]);
-  }
-  if (h != nullptr) h[(long)blockIdx.y * C + c] = s;
-}
-
-// y from the state before the tile: keep's, or, where the sequence is one tile, the
-// caller's h (zero if null), which then becomes the last state; kept takes it.
-template <typename T, bool PAIR>
-__global__ void __launch_bounds__(32 * WARPS) k_gated_out(const Rows a, const float* __restrict__ keep, float* h, float* __restrict__ kept, T* __restrict__ y) {
-  __shared__ Strips st;
-  const Place p(a);
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  Two<T> x[STRIP], r[STRIP], g[STRIP];
-  if (keep != nullptr) grid_dep_enter();
-  fetch<T, PAIR>(r, a.r, a.ldr, a, p);
-  fetch<T, PAIR>(g, a.i, a.ldi, a, p);
-  fetch<T, PAIR>(x, a.x, a.ldx, a, p);
-  float2 av[STRIP], bv[STRIP];
-  decays<T>(av, bv, x, r, g, rates<T, PAIR>(a, p), p);
-  float2 A = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int j = 0; j < STRIP; ++j) {
-    H = fma2(av[j], H, bv[j]);
-    A = make_float2(A.x * av[j].x, A.y * av[j].y);
-  }
-  st.A[w][lane] = A, st.H[w][lane] = H;
-  float2 s = make_float2(0.f, 0.f);
-  if (p.first && (keep != nullptr || h != nullptr)) {
-    const float* from = keep != nullptr ? keep + record(a, p) : h + (long)p.b * a.C + p.c;
-    s.x = from[0];
-    if (p.second) s.y = from[1];
-  }
-  if (kept != nullptr && w == 0 && p.first) {
-    float* to = kept + record(a, p);
-    to[0] = s.x;
-    if (p.second) to[1] = s.y;
-  }
-  __syncthreads();
-  for (int i = 0; i < w; ++i) s = fma2(st.A[i][lane], s, st.H[i][lane]);
-  T* o = y + ((long)p.b * a.N + p.t0) * a.C + p.c;
-#pragma unroll
-  for (int j = 0; j < STRIP; ++j) {
-    s = fma2(av[j], s, bv[j]);
-    if (p.first && p.t0 + j < a.N) store2<PAIR>(o + (long)j * a.C, p.t0 + j < p.L ? s : make_float2(0.f, 0.f), p.second);
-  }
-  if (keep == nullptr && h != nullptr && w == WARPS - 1 && p.first) {  // h's readers are this block, before its barrier
-    float* to = h + (long)p.b * a.C + p.c;
-    to[0] = s.x;
-    if (p.second) to[1] = s.y;
-  }
-}
-
-// The gradient's tile: from X, what arrives at its last row, to P X + Y, what leaves its
-// first one (X_n = a_n (dy_n + X_{n+1})).
-template <typename T, bool PAIR>
-__global__ void __launch_bounds__(32 * WARPS) k_gated_back(const Rows a, const T* __restrict__ dy, float* __restrict__ recP, float* __restrict__ recY) {
-  __shared__ Strips st;
-  const Place p(a);
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  Two<T> r[STRIP], d[STRIP];
-  fetch<T, PAIR>(r, a.r, a.ldr, a, p);
-  fetch<T, PAIR>(d, dy, a.C, a, p);
-  const float2 k = rates<T, PAIR>(a, p);
-  float2 P = make_float2(1.f, 1.f), Y = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int j = STRIP - 1; j >= 0; --j)
-    if (p.t0 + j < p.L) {
-      const float2 rf = open(r[j]), df = open(d[j]);
-      const float2 av = make_float2(gate<T>(k.x, sigmoid<T>(rf.x)).a, gate<T>(k.y, sigmoid<T>(rf.y)).a);
-      Y = make_float2(av.x * (df.x + Y.x), av.y * (df.y + Y.y));
-      P = make_float2(P.x * av.x, P.y * av.y);
-    }
-  st.A[w][lane] = P, st.H[w][lane] = Y;
-  __syncthreads();
-  if (w == WARPS - 1 && p.first) {
-#pragma unroll
-    for (int i = WARPS - 2; i >= 0; --i) {
-      const float2 Pi = st.A[i][lane];
-      Y = fma2(Pi, Y, st.H[i][lane]);
-      P = make_float2(P.x * Pi.x, P.y * Pi.y);
-    }
-    const long at = record(a, p);
-    recP[at] = P.x, recY[at] = Y.x;
-    if (p.second) recP[at + 1] = P.y, recY[at + 1] = Y.y;
-  }
-}
-
-// All gradients of a tile, from the state before it (keep) and the gradient that
-// arrives at its last row (arrive; null: zero), and its sums of Q.
-template <typename T, bool PAIR>
-__global__ void __launch_bounds__(32 * WARPS) k_gated_grad(const Rows a, const T* __restrict__ dy, const float* __restrict__ keep,
-                                                           const float* __restrict__ arrive, T* __restrict__ dx, T* __restrict__ dr,
-                                                           T* __restrict__ di, float* __restrict__ sums) {
-  __shared__ Strips f, v;
-  const Place p(a);
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  if (arrive != nullptr) grid_dep_enter();
-  Two<T> x[STRIP], r[STRIP], g[STRIP], d[STRIP];
-  fetch<T, PAIR>(r, a.r, a.ldr, a, p);
-  fetch<T, PAIR>(g, a.i, a.ldi, a, p);
-  fetch<T, PAIR>(x, a.x, a.ldx, a, p);
-  fetch<T, PAIR>(d, dy, a.C, a, p);
-  const float2 k = rates<T, PAIR>(a, p);
-  float2 av[STRIP], bv[STRIP];
-  decays<T>(av, bv, x, r, g, k, p);
-  float2 A = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f), Y = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int j = 0; j < STRIP; ++j) {
-    H = fma2(av[j], H, bv[j]);
-    A = make_float2(A.x * av[j].x, A.y * av[j].y);
-  }
-#pragma unroll
-  for (int j = STRIP - 1; j >= 0; --j) {
-    const float2 df = open(d[j]);
-    Y = make_float2(av[j].x * (df.x + Y.x), av[j].y * (df.y + Y.y));
-  }
-  f.A[w][lane] = A, f.H[w][lane] = H;
-  v.H[w][lane] = Y;
-  const long at = record(a, p);
-  float2 s = make_float2(0.f, 0.f), X = s;
-  if (p.first) {
-    s.x = keep[at];
-    if (arrive != nullptr) X.x = arrive[at];
-    if (p.second) {
-      s.y = keep[at + 1];
-      if (arrive != nullptr) X.y = arrive[at + 1];
-    }
-  }
-  __syncthreads();
-  for (int i = 0; i < w; ++i) s = fma2(f.A[i][lane], s, f.H[i][lane]);
-  for (int i = WARPS - 1; i > w; --i) X = fma2(f.A[i][lane], X, v.H[i][lane]);
-  float2 before[STRIP];
-#pragma unroll
-  for (int j = 0; j < STRIP; ++j) {
-    before[j] = s;
-    s = fma2(av[j], s, bv[j]);
-  }
-  float2 sum = make_float2(0.f, 0.f);
-  const long row = ((long)p.b * a.N + p.t0) * a.C + p.c;
-#pragma unroll
-  for (int j = STRIP - 1; j >= 0; --j) {
-    float2 ox = make_float2(0.f, 0.f), orr = ox, oi = ox;
-    if (p.t0 + j < p.L) {
-      const float2 xf = open(x[j]), rf = open(r[j]), gf = open(g[j]), df = open(d[j]);
-      auto one = [](float xv, float rv, float gv, float dv, float kk, float hb, float& X1, float& acc, float& o0, float& o1, float& o2) {
-        const float s1 = sigmoid<T>(rv), g1 = sigmoid<T>(gv);
-        const Gate q = gate<T>(kk, s1);
-        const float G = dv + X1, gx = g1 * xv, aG = q.a * G;
-        const float Q = aG * (q.a * gx * q.ub - q.u * hb);
-        X1 = aG;
-        acc += Q;
-        o0 = G * q.beta * g1;
-        o1 = Q * (1.f - s1);
-        o2 = G * q.beta * gx * (1.f - g1);
-      };
-      one(xf.x, rf.x, gf.x, df.x, k.x, before[j].x, X.x, sum.x, ox.x, orr.x, oi.x);
-      one(xf.y, rf.y, gf.y, df.y, k.y, before[j].y, X.y, sum.y, ox.y, orr.y, oi.y);
-    }
-    if (p.first && p.t0 + j < a.N) {
-      store2<PAIR>(dx + row + (long)j * a.C, ox, p.second);
-      store2<PAIR>(dr + row + (long)j * a.C, orr, p.second);
-      store2<PAIR>(di + row + (long)j * a.C, oi, p.second);
-    }
-  }
-  __syncthreads();  // v is read
-  v.A[w][lane] = sum;
-  __syncthreads();
-  if (w == 0 && p.first) {
-#pragma unroll
-    for (int i = 1; i < WARPS; ++i) {
-      const float2 o = v.A[i][lane];
-      sum.x += o.x, sum.y += o.y;
-    }
-    sums[at] = sum.x;
-    if (p.second) sums[at + 1] = sum.y;
-  }
-}
-
-// dlam from the [n][C] sums of Q, 32 channels a block, eight rows at a time.
+// A call's words to EMPTY, and the channels' rates.
 template <typename T>
-__global__ void __launch_bounds__(256) k_gated_lam(const float* __restrict__ sums, const T* __restrict__ lam, T* __restrict__ dlam, long n, int C) {
-  __shared__ float red[8][33];
+__global__ void __launch_bounds__(256) k_gated_start(const Chain ch, long n, float* rate, const T* __restrict__ lam, float scale, int C, int padded) {
+  const long e = (long)blockIdx.x * 256 + threadIdx.x, step = (long)gridDim.x * 256;
+  for (long i = e; i < n * 48; i += step) reinterpret_cast<ulonglong2*>(ch.word)[i] = make_ulonglong2(EMPTY, EMPTY);
+  for (long i = e; i < padded; i += step) rate[i] = i < C ? scale * softplus(to_f(lam[i])) : 0.f;
+}
+
+// ---------------------------------------------------------------------- forward
+
+template <typename T, int UNIT, bool CHAIN>
+__global__ void __launch_bounds__(32 * WARPS, 2)
+    k_gated_fwd(const Rows a, const Chain ch, float* h, float* __restrict__ kept, T* __restrict__ y, int total) {
+  constexpr int RW = FWD<T>, ROWS = WARPS * RW;
+  using R = typename Raw<T>::type;
+  extern __shared__ __align__(16) unsigned char room[];
+  __shared__ Shared<FWD_WINDOW> sh;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, cols = a.groups * a.B;
+  auto own = [&](int stage, int t) { return reinterpret_cast<T*>(room) + ((stage * 3 + t) * ROWS + w * RW) * CH; };
+  auto request = [&](int stage, const Job& j) {
+    const int t0 = j.tile * ROWS + w * RW;
+    if (j.tile >= 0 && t0 < j.L) {
+      bring<T, UNIT, RW>(own(stage, 1), a.r, a.ldr, a, j, t0);
+      bring<T, UNIT, RW>(own(stage, 2), a.i, a.ldi, a, j, t0);
+      bring<T, UNIT, RW>(own(stage, 0), a.x, a.ldx, a, j, t0);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  Job job = job_of(a, blockIdx.x, total, false);
+  request(0, job);
+  for (int stage = 0, t = blockIdx.x; job.tile >= 0; stage ^= 1) {
+    t += gridDim.x;
+    const Job next = job_of(a, t, total, false);
+    const int t0 = job.tile * ROWS + w * RW, c = job.c0 + 2 * lane, n = a.C - c;
+    const bool live = job.tile == 0 || job.tile * ROWS < job.L;  // nothing behind the length passes anything on
+    const u64 k = live ? rates<T>(a, c) : 0ull;
+    if (CHAIN) {
+      request(stage ^ 1, next);
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(CHAIN ? 1 : 0) : "memory");
+    __syncwarp();
+    R* px = reinterpret_cast<R*>(own(stage, 0)) + lane;
+    const R *pr = reinterpret_cast<const R*>(own(stage, 1)) + lane, *pi = reinterpret_cast<const R*>(own(stage, 2)) + lane;
+    float* hp = h == nullptr ? nullptr : h + (long)job.b * a.C + c;
+    u64 av[RW], bv[RW], A = two(1.f), H = 0ull;
+    if (live) {
+      bool quick = t0 + RW <= job.L;
+      if (quick) {
+#pragma unroll
+        for (int j = 0; j < RW; ++j) {
+          u64 s, g, beta;
+          gates_quick(open(pr[j * (CH / 2)]), open(pi[j * (CH / 2)]), k, s, g, av[j], beta, quick);
+          bv[j] = mul2(beta, mul2(g, open(px[j * (CH / 2)])));
+        }
+      }
+      if (!quick) {
+#pragma unroll
+        for (int j = 0; j < RW; ++j) {
+          av[j] = two(1.f), bv[j] = 0ull;  // rows past the length keep the state
+          if (t0 + j < job.L) {
+            u64 s, g, beta;
+            gates(open(pr[j * (CH / 2)]), open(pi[j * (CH / 2)]), k, s, g, av[j], beta);
+            bv[j] = mul2(beta, mul2(g, open(px[j * (CH / 2)])));
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < RW; ++j) {
+        H = fma2(av[j], H, bv[j]);
+        A = mul2(A, av[j]);
+      }
+      sh.A[stage][w][lane] = A, sh.H[stage][w][lane] = H;
+      if (job.tile == 0 && w == 0) sh.start[stage][lane] = hp == nullptr ? 0ull : gather(hp, n);
+    }
+    __syncthreads();
+    if (live) {
+      u64 s = job.tile == 0 ? sh.start[stage][lane] : 0ull;
+      const bool last = (job.tile + 1) * ROWS >= job.L;  // of the tiles with valid rows
+      if (CHAIN) {
+        const long entry = (long)job.tile * cols + job.col;
+        u64* word = ch.word + entry * 96 + lane;
+        if (w == 0 && !last) {
+#pragma unroll
+          for (int i = 1; i < WARPS; ++i) {
+            const u64 Ai = sh.A[stage][i][lane];
+            H = fma2(Ai, H, sh.H[stage][i][lane]);
+            A = mul2(A, Ai);
+          }
+          if (job.tile > 0) put(word, A), put(word + 32, H);
+        }
+        if (job.tile > 0) s = look_up(sh, ch, entry - cols, -cols, job.tile, 91);
+        if (w == 0 && !last) {
+          if (job.tile == 0) __threadfence();  // h is read before another tile replaces it
+          put(word + 64, fma2(A, s, H));
+        }
+      }
+      for (int i = 0; i < w; ++i) s = fma2(sh.A[stage][i][lane], s, sh.H[stage][i][lane]);
+      float* to = kept == nullptr ? nullptr : kept + ((long)job.b * ((a.N + KEEP - 1) / KEEP) + t0 / KEEP) * a.C + c;
+      if (to != nullptr && t0 % KEEP == 0 && t0 < a.N) scatter(to, n, s);
+#pragma unroll
+      for (int j = 0; j < RW; ++j) {
+        s = fma2(av[j], s, bv[j]);
+        px[j * (CH / 2)] = t0 + j < job.L ? close<T>(s) : R{};
+      }
+      if (hp != nullptr && w == WARPS - 1 && last) {
+        __threadfence();
+        scatter(hp, n, s);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < RW; ++j) px[j * (CH / 2)] = R{};
+    }
+    __syncwarp();
+    leave<T, UNIT, RW>(y, own(stage, 0), a, job, t0);
+    __syncwarp();  // the rows are out before the next ones come in
+    job = next;
+  }
+}
+
+// -------------------------------------------------------------------- gradients
+
+// All gradients of a tile, from the state before it (kept), and its sums of Q.  What
+// arrives at a tile's last row is X = a G of the row behind it, passed on from the back:
+// X_n = a_n (dy_n + X_{n+1}).  s, g, a and the states before the rows stay in registers,
+// beta goes where the row's r and i were.
+template <typename T, int UNIT, bool CHAIN>
+__global__ void __launch_bounds__(32 * WARPS, 2)
+    k_gated_bwd(const Rows a, const Chain ch, const T* __restrict__ dy, const float* __restrict__ kept, T* __restrict__ dx, T* __restrict__ dr,
+                T* __restrict__ di, float* __restrict__ sums, int total) {
+  constexpr int RW = KEEP / WARPS, STAGES = CHAIN ? BACK_STAGES<T> : 1;
+  using R = typename Raw<T>::type;
+  extern __shared__ __align__(16) unsigned char room[];
+  __shared__ Shared<BACK_WINDOW> sh;
+  __shared__ u64 sY[2][WARPS][32], total_of[WARPS][32];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, cols = a.groups * a.B;
+  auto own = [&](int stage, int t) { return reinterpret_cast<T*>(room) + ((stage * 4 + t) * KEEP + w * RW) * CH; };
+  auto request = [&](int stage, const Job& j) {
+    const int t0 = j.tile * KEEP + w * RW;
+    if (j.tile >= 0 && t0 < j.L) {
+      bring<T, UNIT, RW>(own(stage, 1), a.r, a.ldr, a, j, t0);
+      bring<T, UNIT, RW>(own(stage, 2), a.i, a.ldi, a, j, t0);
+      bring<T, UNIT, RW>(own(stage, 0), a.x, a.ldx, a, j, t0);
+      bring<T, UNIT, RW>(own(stage, 3), dy, a.C, a, j, t0);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  tcc::grid_dep_launch();
+  Job job = job_of(a, blockIdx.x, total, true);
+  request(0, job);
+  for (int half = 0, t = blockIdx.x; job.tile >= 0; half ^= 1) {
+    const int stage = STAGES > 1 ? half : 0;
+    t += gridDim.x;
+    const Job next = job_of(a, t, total, true);
+    const int t0 = job.tile * KEEP + w * RW, c = job.c0 + 2 * lane, n = a.C - c;
+    const bool live = job.tile * KEEP < job.L;
+    const long rec = ((long)job.b * a.tiles + job.tile) * a.C + c;
+    const u64 k = live ? rates<T>(a, c) : 0ull;
+    u64 s = live ? gather(kept + rec, n) : 0ull, X = 0ull, sum = 0ull;
+    if (CHAIN) {
+      if (STAGES > 1) request(stage ^ 1, next);
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(STAGES > 1 ? 1 : 0) : "memory");
+    __syncwarp();
+    R *px = reinterpret_cast<R*>(own(stage, 0)) + lane, *pr = reinterpret_cast<R*>(own(stage, 1)) + lane,
+      *pi = reinterpret_cast<R*>(own(stage, 2)) + lane;
+    const R* pd = reinterpret_cast<const R*>(own(stage, 3)) + lane;
+    u64 sv[RW], gv[RW], av[RW], bv[RW], A = two(1.f), H = 0ull, Y = 0ull;
+    if (live) {
+      bool quick = t0 + RW <= job.L;
+      float2 beta_of[RW];
+      if (quick) {
+#pragma unroll
+        for (int j = 0; j < RW; ++j) {
+          u64 beta;
+          gates_quick(open(pr[j * (CH / 2)]), open(pi[j * (CH / 2)]), k, sv[j], gv[j], av[j], beta, quick);
+          bv[j] = mul2(beta, mul2(gv[j], open(px[j * (CH / 2)])));
+          beta_of[j] = un(beta);
+        }
+      }
+      if (!quick) {
+#pragma unroll
+        for (int j = 0; j < RW; ++j) {
+          av[j] = two(1.f), sv[j] = gv[j] = bv[j] = 0ull, beta_of[j] = make_float2(0.f, 0.f);
+          if (t0 + j < job.L) {
+            u64 beta;
+            gates(open(pr[j * (CH / 2)]), open(pi[j * (CH / 2)]), k, sv[j], gv[j], av[j], beta);
+            bv[j] = mul2(beta, mul2(gv[j], open(px[j * (CH / 2)])));
+            beta_of[j] = un(beta);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < RW; ++j) {
+        if constexpr (sizeof(T) == 4) {
+          pr[j * (CH / 2)] = pk(beta_of[j].x, beta_of[j].y);
+        } else {
+          pr[j * (CH / 2)] = __float_as_uint(beta_of[j].x), pi[j * (CH / 2)] = __float_as_uint(beta_of[j].y);
+        }
+        H = fma2(av[j], H, bv[j]);
+        A = mul2(A, av[j]);
+      }
+#pragma unroll
+      for (int j = RW - 1; j >= 0; --j) Y = mul2(av[j], add2(t0 + j < job.L ? open(pd[j * (CH / 2)]) : 0ull, Y));
+      sh.A[half][w][lane] = A, sh.H[half][w][lane] = H, sY[half][w][lane] = Y;
+    }
+    __syncthreads();
+    if (live) {
+      if (CHAIN) {
+        const int last = (job.L - 1) / KEEP;
+        const long entry = (long)job.tile * cols + job.col;
+        u64* word = ch.word + entry * 96 + lane;
+        if (w == WARPS - 1 && job.tile > 0) {
+#pragma unroll
+          for (int i = WARPS - 2; i >= 0; --i) {
+            const u64 Ai = sh.A[half][i][lane];
+            Y = fma2(Ai, Y, sY[half][i][lane]);
+            A = mul2(A, Ai);
+          }
+          if (job.tile < last) put(word, A), put(word + 32, Y);
+        }
+        if (job.tile < last) X = look_up(sh, ch, entry + cols, cols, last - job.tile, 92);
+        if (w == WARPS - 1 && job.tile > 0) put(word + 64, fma2(A, X, Y));
+      }
+      for (int i = 0; i < w; ++i) s = fma2(sh.A[half][i][lane], s, sh.H[half][i][lane]);
+      for (int i = WARPS - 1; i > w; --i) X = fma2(sh.A[half][i][lane], X, sY[half][i][lane]);
+#pragma unroll
+      for (int j = 0; j < RW; ++j) {  // bv becomes the state before the row
+        const u64 after = fma2(av[j], s, bv[j]);
+        bv[j] = s;
+        s = after;
+      }
+#pragma unroll
+      for (int j = RW - 1; j >= 0; --j) {
+        u64 ox = 0ull, orr = 0ull, oi = 0ull;
+        if (t0 + j < job.L) {
+          const u64 one = two(1.f), neg = two(-1.f);
+          u64 beta;
+          if constexpr (sizeof(T) == 4)
+            beta = pr[j * (CH / 2)];
+          else
+            beta = pk(__uint_as_float(pr[j * (CH / 2)]), __uint_as_float(pi[j * (CH / 2)]));
+          const float2 bf = un(beta);
+          const u64 inverse = pk(rcp_fast(fmaxf(bf.x, 1e-18f)), rcp_fast(fmaxf(bf.y, 1e-18f)));  // u is zero where beta is
+          const u64 G = add2(open(pd[j * (CH / 2)]), X), gx = mul2(gv[j], open(px[j * (CH / 2)]));
+          X = mul2(av[j], G);
+          // Q = a G (a g x u / beta - u h)
+          const u64 u = mul2(k, sv[j]);
+          const u64 Q = mul2(X, fma2(mul2(u, neg), bv[j], mul2(mul2(av[j], gx), mul2(u, inverse))));
+          sum = add2(sum, Q);
+          const u64 Gb = mul2(G, beta);
+          ox = mul2(Gb, gv[j]);
+          orr = mul2(Q, fma2(sv[j], neg, one));
+          oi = mul2(mul2(Gb, gx), fma2(gv[j], neg, one));
+        }
+        px[j * (CH / 2)] = close<T>(ox), pr[j * (CH / 2)] = close<T>(orr), pi[j * (CH / 2)] = close<T>(oi);
+      }
+      total_of[w][lane] = sum;
+    } else {
+#pragma unroll
+      for (int j = 0; j < RW; ++j) px[j * (CH / 2)] = pr[j * (CH / 2)] = pi[j * (CH / 2)] = R{};
+    }
+    __syncthreads();
+    if (w == 0) {
+      if (live) {
+#pragma unroll
+        for (int i = 1; i < WARPS; ++i) sum = add2(sum, total_of[i][lane]);
+      }
+      scatter(sums + rec, n, sum);
+    }
+    leave<T, UNIT, RW>(dx, own(stage, 0), a, job, t0);
+    leave<T, UNIT, RW>(dr, own(stage, 1), a, job, t0);
+    leave<T, UNIT, RW>(di, own(stage, 2), a, job, t0);
+    __syncwarp();  // the rows are out before the next ones come in
+    if (CHAIN && STAGES == 1) request(0, next);
+    job = next;
+  }
+}
+
+// dlam from the [n][C] sums of Q: 32 channels a block, 32 rows at a time, in a fixed order.
+template <typename T>
+__global__ void __launch_bounds__(1024) k_gated_lam(const float* __restrict__ sums, const T* __restrict__ lam, T* __restrict__ dlam, long n, int C) {
+  __shared__ float red[32][33];
   grid_dep_enter();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
   float v = 0.f;
   if (c < C)
-    for (long i = ty; i < n; i += 8) v += sums[i * C + c];
+#pragma unroll 4
+    for (long i = ty; i < n; i += 32) v += sums[i * C + c];
   red[ty][tx] = v;
   __syncthreads();
   if (ty == 0 && c < C) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) v += red[i][tx];
+    for (int i = 1; i < 32; ++i) v += red[i][tx];
     // sigmoid / softplus, which goes to one on the left: below -20 both are exp(lam) to fp32
     const float l = to_f(lam[c]), ratio = l < -20.f ? 1.f : 1.f / ((1.f + expf(-l)) * softplus(l));
     dlam[c] = from_f<T>(v * ratio);
@@ -423,72 +649,128 @@ __global__ void __launch_bounds__(256) k_gated_lam(const float* __restrict__ sum
 // One row a stream: h <- a h + beta g x, y = h.
 template <typename T, bool PAIR>
 __global__ void __launch_bounds__(256) k_gated_step(const Rows a, float* __restrict__ h, T* __restrict__ y) {
+  using R = typename Raw<T>::type;
   const long b = blockIdx.x / a.groups;  // groups of 512 channels here
-  const int c = 2 * ((blockIdx.x % a.groups) * 256 + threadIdx.x);
-  if (c >= a.C) return;
-  const bool second = c + 1 < a.C;
-  const float2 x = open(load2<PAIR>(static_cast<const T*>(a.x) + b * a.ldx + c, second));
-  const float2 r = open(load2<PAIR>(static_cast<const T*>(a.r) + b * a.ldr + c, second));
-  const float2 g = open(load2<PAIR>(static_cast<const T*>(a.i) + b * a.ldi + c, second));
-  const float2 l = open(load2<PAIR>(static_cast<const T*>(a.lam) + c, second));
-  float2 s = open(load2<PAIR>(h + b * a.C + c, second));
-  const Gate g0 = gate<T>(a.scale * softplus(l.x), sigmoid<T>(r.x)), g1 = gate<T>(a.scale * softplus(l.y), sigmoid<T>(r.y));
-  s = make_float2(fmaf(g0.a, s.x, g0.beta * (sigmoid<T>(g.x) * x.x)), fmaf(g1.a, s.y, g1.beta * (sigmoid<T>(g.y) * x.y)));
-  store2<PAIR>(h + b * a.C + c, s, second);
-  store2<PAIR>(y + b * a.C + c, s, second);
+  const int c = 2 * ((blockIdx.x % a.groups) * 256 + threadIdx.x), n = a.C - c;
+  if (n <= 0) return;
+  auto get = [&](const void* base, long ld) {
+    const T* p = static_cast<const T*>(base) + b * ld + c;
+    return open(PAIR ? *reinterpret_cast<const R*>(p) : gather(p, n));
+  };
+  float* hp = h + b * a.C + c;
+  const u64 x = get(a.x, a.ldx), r = get(a.r, a.ldr), i = get(a.i, a.ldi);
+  const float2 l = un(get(a.lam, 0));
+  u64 st = PAIR ? *reinterpret_cast<const u64*>(hp) : gather(hp, n), s, g, av, beta;
+  gates(r, i, pk(a.scale * softplus(l.x), a.scale * softplus(l.y)), s, g, av, beta);
+  st = fma2(av, st, mul2(beta, mul2(g, x)));
+  if (PAIR) {
+    *reinterpret_cast<u64*>(hp) = st;
+    *reinterpret_cast<R*>(y + b * a.C + c) = close<T>(st);
+  } else {
+    scatter(hp, n, st);
+    scatter(y + b * a.C + c, n, close<T>(st));
+  }
 }
 
 Rows rows(const void* x, const void* r, const void* i, const void* lam, const int* lengths, const GatedShape& s) {
-  return Rows{x, r, i, lam, lengths, s.ldx, s.ldr, s.ldi, s.N, s.C, (s.C + CH - 1) / CH, (s.N + TILE - 1) / TILE, s.scale};
+  return Rows{x, r, i, lam, lengths, nullptr, s.ldx, s.ldr, s.ldi, s.B, s.N, s.C, (s.C + CH - 1) / CH, 0, s.scale};
 }
 
-// Pairs of channels as vectors: even widths and strides, aligned rows.
-bool pairs(const Rows& a, int dtype) {
+// Rows, widths and strides in whole vectors of `bytes`.
+bool whole(const Rows& a, int dtype, int bytes) {
   const uintptr_t low = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.r) | reinterpret_cast<uintptr_t>(a.i);
-  return ((a.ldx | a.ldr | a.ldi | a.C) & 1) == 0 && low % (dtype == 0 ? 8 : 4) == 0;
+  return ((a.ldx | a.ldr | a.ldi | a.C) & (bytes / (dtype == 0 ? 4 : 2) - 1)) == 0 && low % bytes == 0;
 }
 
-size_t records(const GatedShape& s) { return (size_t)s.B * ((s.N + TILE - 1) / TILE) * s.C; }
+int fwd_rows(int dtype) { return (dtype == 0 ? FWD<float> : FWD<bf16>)*WARPS; }
+size_t entries(const GatedShape& s, int rows_) { return (size_t)((s.N + rows_ - 1) / rows_) * ((s.C + CH - 1) / CH) * s.B; }
+size_t align16(size_t n) { return (n + 15) / 16 * 16; }
+size_t padded(const GatedShape& s) { return (size_t)(s.C + CH - 1) / CH * CH; }
+size_t chain_bytes(const GatedShape& s, size_t n) { return 4 * padded(s) + n * 96 * sizeof(u64); }
+size_t records(const GatedShape& s) { return (size_t)s.B * ((s.N + KEEP - 1) / KEEP) * s.C; }
 
-template <typename T, bool PAIR>
-cudaError_t fwd(const Rows& a, float* h, float* keep, void* y, float* ws, const GatedShape& s, cudaStream_t st) {
-  const dim3 grid(a.tiles * a.groups, s.B), block(32 * WARPS);
+// The chain in a workspace, cleared by a launch of its own.
+template <typename T>
+cudaError_t chain(Chain& ch, Rows& a, char* ws, size_t n, const GatedShape& s, cudaStream_t st) {
+  float* rate = reinterpret_cast<float*>(ws);
+  a.rate = rate;
+  ch.word = reinterpret_cast<u64*>(rate + padded(s));
+  ch.err = status_word();
+  const size_t most = std::max(48 * n, padded(s));
+  const unsigned grid = static_cast<unsigned>(std::min<size_t>((most + 255) / 256, 8 * sm_count()));
+  k_gated_start<T><<<grid, 256, 0, st>>>(ch, static_cast<long>(n), rate, (const T*)a.lam, s.scale, s.C, static_cast<int>(padded(s)));
+  return cudaGetLastError();
+}
+
+template <typename K>
+cudaError_t room(K kernel, size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+}
+
+// A cooperative launch: all blocks run at once, or the launch fails.
+template <typename... Exp, typename... Act>
+cudaError_t together(void (*kernel)(Exp...), size_t tiles, size_t smem, cudaStream_t st, Act&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<size_t>(tiles, 2 * sm_count())));
+  cfg.blockDim = dim3(32 * WARPS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Act>(args)...);
+}
+
+template <typename T, int UNIT>
+cudaError_t fwd(Rows a, float* h, float* kept, void* y, void* ws, const GatedShape& s, cudaStream_t st) {
+  constexpr int ROWS = FWD<T> * WARPS;
+  constexpr size_t stage = 3 * ROWS * CH * sizeof(T);
+  a.tiles = (s.N + ROWS - 1) / ROWS;
+  const size_t n = entries(s, ROWS);
+  const dim3 block(32 * WARPS);
+  Chain ch{};
+  cudaError_t e;
   if (a.tiles == 1) {
-    k_gated_out<T, PAIR><<<grid, block, 0, st>>>(a, nullptr, h, keep, (T*)y);
+    if ((e = room(k_gated_fwd<T, UNIT, false>, stage)) != cudaSuccess) return e;
+    k_gated_fwd<T, UNIT, false><<<static_cast<unsigned>(n), block, stage, st>>>(a, ch, h, kept, (T*)y, static_cast<int>(n));
     return cudaGetLastError();
   }
-  float *recA = ws, *recH = ws + records(s), *to = keep != nullptr ? keep : ws + 2 * records(s);
-  k_gated_sums<T, PAIR><<<grid, block, 0, st>>>(a, recA, recH);
-  cudaError_t e = launch_pdl(k_gated_carry, dim3((s.C + 127) / 128, s.B), dim3(128), 0, st, (const float*)recA, (const float*)recH, to, h,
-                                  s.C, a.tiles, 0);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k_gated_out<T, PAIR>, grid, block, 0, st, a, (const float*)to, h, (float*)nullptr, (T*)y);
+  if ((e = room(k_gated_fwd<T, UNIT, true>, 2 * stage)) != cudaSuccess) return e;
+  if ((e = chain<T>(ch, a, static_cast<char*>(ws), n, s, st)) != cudaSuccess) return e;
+  return together(k_gated_fwd<T, UNIT, true>, n, 2 * stage, st, a, ch, h, kept, (T*)y, static_cast<int>(n));
 }
 
-template <typename T, bool PAIR>
-cudaError_t bwd(const Rows& a, const float* keep, const void* dy, void* dx, void* dr, void* di, void* dlam, float* ws, const GatedShape& s,
+template <typename T, int UNIT>
+cudaError_t bwd(Rows a, const float* kept, const void* dy, void* dx, void* dr, void* di, void* dlam, void* ws, const GatedShape& s,
                 cudaStream_t st) {
-  const dim3 grid(a.tiles * a.groups, s.B), block(32 * WARPS);
-  float *sums = ws, *recP = ws + records(s), *recY = recP + records(s), *arrive = recY + records(s);
+  constexpr size_t stage = 4 * KEEP * CH * sizeof(T);
+  a.tiles = (s.N + KEEP - 1) / KEEP;
+  const size_t n = entries(s, KEEP);
+  const dim3 block(32 * WARPS);
+  float* sums = static_cast<float*>(ws);
+  Chain ch{};
+  cudaError_t e;
   if (a.tiles == 1) {
-    k_gated_grad<T, PAIR><<<grid, block, 0, st>>>(a, (const T*)dy, keep, nullptr, (T*)dx, (T*)dr, (T*)di, sums);
+    if ((e = room(k_gated_bwd<T, UNIT, false>, stage)) != cudaSuccess) return e;
+    k_gated_bwd<T, UNIT, false><<<static_cast<unsigned>(n), block, stage, st>>>(a, ch, (const T*)dy, kept, (T*)dx, (T*)dr, (T*)di, sums, static_cast<int>(n));
+    e = cudaGetLastError();
   } else {
-    k_gated_back<T, PAIR><<<grid, block, 0, st>>>(a, (const T*)dy, recP, recY);
-    cudaError_t e = launch_pdl(k_gated_carry, dim3((s.C + 127) / 128, s.B), dim3(128), 0, st, (const float*)recP, (const float*)recY, arrive,
-                                    (float*)nullptr, s.C, a.tiles, 1);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(k_gated_grad<T, PAIR>, grid, block, 0, st, a, (const T*)dy, keep, (const float*)arrive, (T*)dx, (T*)dr, (T*)di, sums);
-    if (e != cudaSuccess) return e;
+    if ((e = room(k_gated_bwd<T, UNIT, true>, BACK_STAGES<T> * stage)) != cudaSuccess) return e;
+    if ((e = chain<T>(ch, a, static_cast<char*>(ws) + align16(4 * records(s)), n, s, st)) != cudaSuccess) return e;
+    e = together(k_gated_bwd<T, UNIT, true>, n, BACK_STAGES<T> * stage, st, a, ch, (const T*)dy, kept, (T*)dx, (T*)dr, (T*)di, sums,
+                 static_cast<int>(n));
   }
-  return launch_pdl(k_gated_lam<T>, dim3((s.C + 31) / 32), dim3(256), 0, st, (const float*)sums, (const T*)a.lam, (T*)dlam,
-                         (long)s.B * a.tiles, s.C);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_gated_lam<T>, dim3((s.C + 31) / 32), dim3(1024), 0, st, (const float*)sums, (const T*)a.lam, (T*)dlam,
+                    (long)s.B * a.tiles, s.C);
 }
 
 template <typename T, bool PAIR>
-cudaError_t step(const Rows& a, float* h, void* y, const GatedShape& s, cudaStream_t st) {
-  Rows wide = a;
-  wide.groups = (s.C + 511) / 512;
-  k_gated_step<T, PAIR><<<wide.groups * s.B, 256, 0, st>>>(wide, h, (T*)y);
+cudaError_t step(Rows a, float* h, void* y, const GatedShape& s, cudaStream_t st) {
+  a.groups = (s.C + 511) / 512;
+  k_gated_step<T, PAIR><<<a.groups * s.B, 256, 0, st>>>(a, h, (T*)y);
   return cudaGetLastError();
 }
 
@@ -496,27 +778,30 @@ cudaError_t step(const Rows& a, float* h, void* y, const GatedShape& s, cudaStre
 
 size_t gated_kept_bytes(const GatedShape& s) { return 4 * records(s); }
 size_t gated_ws_bytes(const GatedShape& s, bool bwd) {
-  if (bwd) return 4 * records(s) * (s.N > TILE ? 4 : 1);
-  return s.N > TILE ? 12 * records(s) : 0;
+  if (!bwd) return s.N > fwd_rows(s.dtype) ? chain_bytes(s, entries(s, fwd_rows(s.dtype))) : 0;
+  return align16(4 * records(s)) + (s.N > KEEP ? chain_bytes(s, entries(s, KEEP)) : 0);
 }
 
-#define LA_GATED(f, ...)                                                        \
-  (s.dtype == 0 ? pairs(a, 0) ? f<float, true>(__VA_ARGS__) : f<float, false>(__VA_ARGS__) \
-                : pairs(a, 1) ? f<bf16, true>(__VA_ARGS__) : f<bf16, false>(__VA_ARGS__))
+#define LA_GATED(f, ...)                                                               \
+  (s.dtype == 0 ? whole(a, 0, 16) ? f<float, 16>(__VA_ARGS__) : f<float, 4>(__VA_ARGS__) \
+   : whole(a, 1, 16) ? f<bf16, 16>(__VA_ARGS__)                                        \
+   : whole(a, 1, 4)  ? f<bf16, 4>(__VA_ARGS__)                                         \
+                     : f<bf16, 2>(__VA_ARGS__))
 
 cudaError_t gated_fwd(const void* x, const void* r, const void* i, const void* lam, const int* lengths, float* h, float* kept, void* y,
-                      float* ws, const GatedShape& s, cudaStream_t st) {
+                      void* ws, const GatedShape& s, cudaStream_t st) {
   const Rows a = rows(x, r, i, lam, lengths, s);
   return LA_GATED(fwd, a, h, kept, y, ws, s, st);
 }
 cudaError_t gated_bwd(const void* x, const void* r, const void* i, const void* lam, const int* lengths, const float* kept, const void* dy,
-                      void* dx, void* dr, void* di, void* dlam, float* ws, const GatedShape& s, cudaStream_t st) {
+                      void* dx, void* dr, void* di, void* dlam, void* ws, const GatedShape& s, cudaStream_t st) {
   const Rows a = rows(x, r, i, lam, lengths, s);
   return LA_GATED(bwd, a, kept, dy, dx, dr, di, dlam, ws, s, st);
 }
 cudaError_t gated_step(const void* x, const void* r, const void* i, const void* lam, float* h, void* y, const GatedShape& s, cudaStream_t st) {
   const Rows a = rows(x, r, i, lam, nullptr, s);
-  return LA_GATED(step, a, h, y, s, st);
+  if (s.dtype == 0) return whole(a, 0, 8) ? step<float, true>(a, h, y, s, st) : step<float, false>(a, h, y, s, st);
+  return whole(a, 1, 4) ? step<bf16, true>(a, h, y, s, st) : step<bf16, false>(a, h, y, s, st);
 }
 #undef LA_GATED
 

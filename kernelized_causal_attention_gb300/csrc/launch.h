@@ -228,9 +228,9 @@ struct GatedShape {
 size_t gated_kept_bytes(const GatedShape& s);
 size_t gated_ws_bytes(const GatedShape& s, bool bwd);
 cudaError_t gated_fwd(const void* x, const void* r, const void* i, const void* lam, const int* lengths, float* h, float* kept, void* y,
-                      float* ws, const GatedShape& s, cudaStream_t st);
+                      void* ws, const GatedShape& s, cudaStream_t st);
 cudaError_t gated_bwd(const void* x, const void* r, const void* i, const void* lam, const int* lengths, const float* kept, const void* dy,
-                      void* dx, void* dr, void* di, void* dlam, float* ws, const GatedShape& s, cudaStream_t st);
+                      void* dx, void* dr, void* di, void* dlam, void* ws, const GatedShape& s, cudaStream_t st);
 cudaError_t gated_step(const void* x, const void* r, const void* i, const void* lam, float* h, void* y, const GatedShape& s, cudaStream_t st);
 
 // The layer norm (norm.cu): G groups of C / G columns; rows ldx and ldr elements apart.

@@ -3,8 +3,9 @@ each with the bound that the roundings of an fp32 computation stay under.
 
 Half steps of fp32 (F32 = 2^-24) are counted; a bf16 result is off by half a bf16 step more (``rounded``).  What the
 functions used are good for: exp, log1p, division, square root and their hardware approximations 4 half steps each
-(2^-22), a sum or product one.  sigmoid: the exponential of its argument (whose own rounding costs |x| steps), a sum
-and a quotient: 8 + 2 |x| half steps, relative; one minus it: as many of sigmoid, and one.
+(2^-22), a sum or product one.  sigmoid: the exponential (4, and 2 |x| at most for its argument x log2(e) in fp32), one
+plus it (1) and a quotient, which may be formed from the reciprocal of two sigmoids' product (1 + 4 + 1): 11 + 2 |x|
+half steps, relative; one minus it: as many of sigmoid, and one.
 """
 import math
 
@@ -18,7 +19,7 @@ def rounded(want, e, dtype):
 
 
 def _sig(x):
-    return 1 / (1 + torch.exp(-x)), (8 + 2 * x.abs()) * F32
+    return 1 / (1 + torch.exp(-x)), (11 + 2 * x.abs()) * F32
 
 
 def gated(x, r, i, lam, scale=8.0, h=None, lengths=None, dy=None):

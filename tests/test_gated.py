@@ -69,6 +69,20 @@ def test_backward(cuda, linattn, B, N, C, dtype, pad, lengths, span, from_state)
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,N,C,dtype,lengths", [(1, 9001, 8, "bf16", None), (2, 5000, 6, "f32", [5000, 4231]), (1, 4100, 72, "f32", None)])
+def test_states_over_many_tiles(cuda, linattn, B, N, C, dtype, lengths):
+    """More tiles than are looked up at once, in both directions."""
+    wide, lam, dy, h = inputs(B, N, C, dtype, 0, 10, -13, -7)
+    n, a, hd = number(lengths, cuda), cut(wide, C, cuda), h.to(cuda)
+    y, kept = linattn.gated_fwd(*a, lam.to(cuda), h=hd, lengths=n, keep=True)
+    got = linattn.gated_bwd(*a, lam.to(cuda), kept, dy.to(cuda), lengths=n)
+    want = around64.gated(*cut(wide, C), lam, 8.0, h, lengths, dy)
+    for name, t in zip(("y", "dx", "dr", "di", "dlam"), (y, *got)):
+        within(t, want[name][0], rounded(*want[name], dtype), name)
+    within(hd, *want["h"], "state")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("B,C,dtype,pad", [(1, 1, "f32", 0), (5, 33, "bf16", 7), (300, 64, "bf16", 16), (7, 1030, "f32", 4)])
 def test_steps_continue_a_prompt(cuda, linattn, B, C, dtype, pad):
     wide, lam, _, h = inputs(B, 90, C, dtype, pad, 2)
