@@ -31,6 +31,7 @@ constexpr int CH = 64;      // channels of a tile, two a lane
 constexpr int WARPS = 8;    // strips of a tile
 constexpr int KEEP = 64;    // rows of a gradient tile, and between the states kept for it
 constexpr int FWD_WINDOW = 16, BACK_WINDOW = 32;  // tiles looked up before one must have its state
+constexpr int BLOCKS = 2;   // on an SM; three of half the strips were slower: 107 us against 79 for 65536 x 512
 template <typename T>
 constexpr int FWD = sizeof(T) == 4 ? 8 : 16;  // rows of a strip, forward: 48 KB of rows a tile
 template <typename T>
@@ -91,24 +92,34 @@ __device__ __forceinline__ u64 near_one(u64 u) {
   return mul2(u, p);
 }
 __device__ __forceinline__ u64 minus_one(u64 w) { return fma2(w, two(-1.f), two(1.f)); }
-// beta = sqrt(w (1 + a)); zero where that is below 1e-36.
+// beta = sqrt(w (1 + a)), with 1e-36 under the root of its inverse: zero where w is.
 __device__ __forceinline__ u64 root(u64 w, u64 a) {
   const u64 om = fma2(w, a, w);
-  const float2 f = un(om);
-  return mul2(om, pk(rsqrt_fast(fmaxf(f.x, 1e-36f)), rsqrt_fast(fmaxf(f.y, 1e-36f))));
+  const float2 f = un(add2(om, two(1e-36f)));
+  return mul2(om, pk(rsqrt_fast(f.x), rsqrt_fast(f.y)));
+}
+// The larger of three, NaN if one is.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float v;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(v) : "f"(a), "f"(b), "f"(c));
+  return v;
 }
 
 // A row's gates: s, g, a and beta.  Both sigmoids, 1 / (1 + e) each, come from one
 // reciprocal of the product, unless that is near overflow or NaN (arguments below -69 in
-// sum); `quick` stays true where the short forms hold, and the full form gives a channel
-// for which they do the same bits.
-__device__ __forceinline__ void gates_quick(u64 r, u64 i, u64 k, u64& s, u64& g, u64& a, u64& beta, bool& quick) {
+// sum).  The short forms hold while the largest product stays below 1e30 and the largest
+// u below one; the full form gives a channel for which they do the same bits.
+struct Reach {
+  float p = 0.f, u = 0.f;
+  __device__ __forceinline__ bool quick() const { return (p < 1e30f) & (u < 1.f); }
+};
+__device__ __forceinline__ void gates_quick(u64 r, u64 i, u64 k, u64& s, u64& g, u64& a, u64& beta, Reach& reach) {
   const u64 scale = two(-1.4426950408889634f), one = two(1.f);
   const u64 d1 = add2(ex2_2(mul2(r, scale)), one), d2 = add2(ex2_2(mul2(i, scale)), one), p = mul2(d1, d2), q = rcp_2(p);
   s = mul2(q, d2), g = mul2(q, d1);
   const u64 u = mul2(k, s), w = near_one(u);
   const float2 pf = un(p), uf = un(u);
-  quick = quick & (pf.x < 1e30f) & (pf.y < 1e30f) & (uf.x < 1.f) & (uf.y < 1.f);
+  reach.p = max3(reach.p, pf.x, pf.y), reach.u = max3(reach.u, uf.x, uf.y);
   a = minus_one(w);
   beta = root(w, a);
 }
@@ -231,11 +242,19 @@ __device__ __forceinline__ void bring(T* to, const void* base, long ld, const Ro
     const bool wide = j.c0 + c < a.C;
     const T* q = from + r0 * ld + c;
     T* o = to + r0 * CH + c;
+    if (t0 + RW <= j.L && j.c0 + CH <= a.C) {
 #pragma unroll
-    for (int r = 0; r < RW; r += PER) {
-      const bool in = wide && t0 + r0 + r < j.L;
-      copy_async<16>(o + r * CH, in ? q : base, in ? 16 : 0);
-      q += PER * ld;
+      for (int r = 0; r < RW; r += PER) {
+        copy_async<16>(o + r * CH, q, 16);
+        q += PER * ld;
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < RW; r += PER) {
+        const bool in = wide && t0 + r0 + r < j.L;
+        copy_async<16>(o + r * CH, in ? q : base, in ? 16 : 0);
+        q += PER * ld;
+      }
     }
   } else if constexpr (UNIT == 4) {
     constexpr int E = 4 / sizeof(T);
@@ -265,11 +284,22 @@ __device__ __forceinline__ void leave(T* out, const T* from, const Rows& a, cons
   if constexpr (UNIT == 16) {
     constexpr int E = 16 / sizeof(T), LR = CH / E, PER = 32 / LR;
     const int c = (lane % LR) * E, r0 = lane / LR;
-    const bool wide = j.c0 + c < a.C;
+    T* q = to + (long)r0 * a.C + c;
+    const T* o = from + r0 * CH + c;
+    const bool wide = j.c0 + c < a.C, all = t0 + RW <= a.N && j.c0 + CH <= a.C;
+    if (all) {
 #pragma unroll
-    for (int r = 0; r < RW; r += PER)
-      if (wide && t0 + r0 + r < a.N)
-        *reinterpret_cast<uint4*>(to + (long)(r0 + r) * a.C + c) = *reinterpret_cast<const uint4*>(from + (r0 + r) * CH + c);
+      for (int r = 0; r < RW; r += PER) {
+        *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(o + r * CH);
+        q += (long)PER * a.C;
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < RW; r += PER) {
+        if (wide && t0 + r0 + r < a.N) *reinterpret_cast<uint4*>(q) = *reinterpret_cast<const uint4*>(o + r * CH);
+        q += (long)PER * a.C;
+      }
+    }
   } else {
     const int n = a.C - j.c0 - 2 * lane;
 #pragma unroll 4
@@ -358,7 +388,7 @@ __global__ void __launch_bounds__(256) k_gated_start(const Chain ch, long n, flo
 // ---------------------------------------------------------------------- forward
 
 template <typename T, int UNIT, bool CHAIN>
-__global__ void __launch_bounds__(32 * WARPS, 2)
+__global__ void __launch_bounds__(32 * WARPS, BLOCKS)
     k_gated_fwd(const Rows a, const Chain ch, float* h, float* __restrict__ kept, T* __restrict__ y, int total) {
   constexpr int RW = FWD<T>, ROWS = WARPS * RW;
   using R = typename Raw<T>::type;
@@ -392,17 +422,18 @@ __global__ void __launch_bounds__(32 * WARPS, 2)
     const R *pr = reinterpret_cast<const R*>(own(stage, 1)) + lane, *pi = reinterpret_cast<const R*>(own(stage, 2)) + lane;
     float* hp = h == nullptr ? nullptr : h + (long)job.b * a.C + c;
     u64 av[RW], bv[RW], A = two(1.f), H = 0ull;
+    const bool full = t0 + RW <= job.L;  // the same for a warp
     if (live) {
-      bool quick = t0 + RW <= job.L;
-      if (quick) {
+      Reach reach;
+      if (full) {
 #pragma unroll
         for (int j = 0; j < RW; ++j) {
           u64 s, g, beta;
-          gates_quick(open(pr[j * (CH / 2)]), open(pi[j * (CH / 2)]), k, s, g, av[j], beta, quick);
+          gates_quick(open(pr[j * (CH / 2)]), open(pi[j * (CH / 2)]), k, s, g, av[j], beta, reach);
           bv[j] = mul2(beta, mul2(g, open(px[j * (CH / 2)])));
         }
       }
-      if (!quick) {
+      if (!full || !reach.quick()) {
 #pragma unroll
         for (int j = 0; j < RW; ++j) {
           av[j] = two(1.f), bv[j] = 0ull;  // rows past the length keep the state
@@ -446,10 +477,18 @@ __global__ void __launch_bounds__(32 * WARPS, 2)
       for (int i = 0; i < w; ++i) s = fma2(sh.A[stage][i][lane], s, sh.H[stage][i][lane]);
       float* to = kept == nullptr ? nullptr : kept + ((long)job.b * ((a.N + KEEP - 1) / KEEP) + t0 / KEEP) * a.C + c;
       if (to != nullptr && t0 % KEEP == 0 && t0 < a.N) scatter(to, n, s);
+      if (full) {
 #pragma unroll
-      for (int j = 0; j < RW; ++j) {
-        s = fma2(av[j], s, bv[j]);
-        px[j * (CH / 2)] = t0 + j < job.L ? close<T>(s) : R{};
+        for (int j = 0; j < RW; ++j) {
+          s = fma2(av[j], s, bv[j]);
+          px[j * (CH / 2)] = close<T>(s);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < RW; ++j) {
+          s = fma2(av[j], s, bv[j]);
+          px[j * (CH / 2)] = t0 + j < job.L ? close<T>(s) : R{};
+        }
       }
       if (hp != nullptr && w == WARPS - 1 && last) {
         __threadfence();
@@ -473,7 +512,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2)
 // X_n = a_n (dy_n + X_{n+1}).  s, g, a and the states before the rows stay in registers,
 // beta goes where the row's r and i were.
 template <typename T, int UNIT, bool CHAIN>
-__global__ void __launch_bounds__(32 * WARPS, 2)
+__global__ void __launch_bounds__(32 * WARPS, BLOCKS)
     k_gated_bwd(const Rows a, const Chain ch, const T* __restrict__ dy, const float* __restrict__ kept, T* __restrict__ dx, T* __restrict__ dr,
                 T* __restrict__ di, float* __restrict__ sums, int total) {
   constexpr int RW = KEEP / WARPS, STAGES = CHAIN ? BACK_STAGES<T> : 1;
@@ -514,19 +553,20 @@ __global__ void __launch_bounds__(32 * WARPS, 2)
       *pi = reinterpret_cast<R*>(own(stage, 2)) + lane;
     const R* pd = reinterpret_cast<const R*>(own(stage, 3)) + lane;
     u64 sv[RW], gv[RW], av[RW], bv[RW], A = two(1.f), H = 0ull, Y = 0ull;
+    const bool full = t0 + RW <= job.L;  // the same for a warp
     if (live) {
-      bool quick = t0 + RW <= job.L;
+      Reach reach;
       float2 beta_of[RW];
-      if (quick) {
+      if (full) {
 #pragma unroll
         for (int j = 0; j < RW; ++j) {
           u64 beta;
-          gates_quick(open(pr[j * (CH / 2)]), open(pi[j * (CH / 2)]), k, sv[j], gv[j], av[j], beta, quick);
+          gates_quick(open(pr[j * (CH / 2)]), open(pi[j * (CH / 2)]), k, sv[j], gv[j], av[j], beta, reach);
           bv[j] = mul2(beta, mul2(gv[j], open(px[j * (CH / 2)])));
           beta_of[j] = un(beta);
         }
       }
-      if (!quick) {
+      if (!full || !reach.quick()) {
 #pragma unroll
         for (int j = 0; j < RW; ++j) {
           av[j] = two(1.f), sv[j] = gv[j] = bv[j] = 0ull, beta_of[j] = make_float2(0.f, 0.f);
@@ -548,8 +588,13 @@ __global__ void __launch_bounds__(32 * WARPS, 2)
         H = fma2(av[j], H, bv[j]);
         A = mul2(A, av[j]);
       }
+      if (full) {
 #pragma unroll
-      for (int j = RW - 1; j >= 0; --j) Y = mul2(av[j], add2(t0 + j < job.L ? open(pd[j * (CH / 2)]) : 0ull, Y));
+        for (int j = RW - 1; j >= 0; --j) Y = mul2(av[j], add2(open(pd[j * (CH / 2)]), Y));
+      } else {
+#pragma unroll
+        for (int j = RW - 1; j >= 0; --j) Y = mul2(av[j], add2(t0 + j < job.L ? open(pd[j * (CH / 2)]) : 0ull, Y));
+      }
       sh.A[half][w][lane] = A, sh.H[half][w][lane] = H, sY[half][w][lane] = Y;
     }
     __syncthreads();
@@ -578,30 +623,39 @@ __global__ void __launch_bounds__(32 * WARPS, 2)
         bv[j] = s;
         s = after;
       }
+      auto gradients = [&](int j, u64& ox, u64& orr, u64& oi) {
+        const u64 one = two(1.f), neg = two(-1.f);
+        u64 beta;
+        if constexpr (sizeof(T) == 4)
+          beta = pr[j * (CH / 2)];
+        else
+          beta = pk(__uint_as_float(pr[j * (CH / 2)]), __uint_as_float(pi[j * (CH / 2)]));
+        const u64 inverse = rcp_2(add2(beta, two(1e-18f)));  // u is zero where beta is
+        const u64 G = add2(open(pd[j * (CH / 2)]), X), gx = mul2(gv[j], open(px[j * (CH / 2)]));
+        X = mul2(av[j], G);
+        // Q = a G (a g x u / beta - u h)
+        const u64 u = mul2(k, sv[j]);
+        const u64 Q = mul2(X, fma2(mul2(u, neg), bv[j], mul2(mul2(av[j], gx), mul2(u, inverse))));
+        sum = add2(sum, Q);
+        const u64 Gb = mul2(G, beta);
+        ox = mul2(Gb, gv[j]);
+        orr = mul2(Q, fma2(sv[j], neg, one));
+        oi = mul2(mul2(Gb, gx), fma2(gv[j], neg, one));
+      };
+      if (full) {
 #pragma unroll
-      for (int j = RW - 1; j >= 0; --j) {
-        u64 ox = 0ull, orr = 0ull, oi = 0ull;
-        if (t0 + j < job.L) {
-          const u64 one = two(1.f), neg = two(-1.f);
-          u64 beta;
-          if constexpr (sizeof(T) == 4)
-            beta = pr[j * (CH / 2)];
-          else
-            beta = pk(__uint_as_float(pr[j * (CH / 2)]), __uint_as_float(pi[j * (CH / 2)]));
-          const float2 bf = un(beta);
-          const u64 inverse = pk(rcp_fast(fmaxf(bf.x, 1e-18f)), rcp_fast(fmaxf(bf.y, 1e-18f)));  // u is zero where beta is
-          const u64 G = add2(open(pd[j * (CH / 2)]), X), gx = mul2(gv[j], open(px[j * (CH / 2)]));
-          X = mul2(av[j], G);
-          // Q = a G (a g x u / beta - u h)
-          const u64 u = mul2(k, sv[j]);
-          const u64 Q = mul2(X, fma2(mul2(u, neg), bv[j], mul2(mul2(av[j], gx), mul2(u, inverse))));
-          sum = add2(sum, Q);
-          const u64 Gb = mul2(G, beta);
-          ox = mul2(Gb, gv[j]);
-          orr = mul2(Q, fma2(sv[j], neg, one));
-          oi = mul2(mul2(Gb, gx), fma2(gv[j], neg, one));
+        for (int j = RW - 1; j >= 0; --j) {
+          u64 ox, orr, oi;
+          gradients(j, ox, orr, oi);
+          px[j * (CH / 2)] = close<T>(ox), pr[j * (CH / 2)] = close<T>(orr), pi[j * (CH / 2)] = close<T>(oi);
         }
-        px[j * (CH / 2)] = close<T>(ox), pr[j * (CH / 2)] = close<T>(orr), pi[j * (CH / 2)] = close<T>(oi);
+      } else {
+#pragma unroll
+        for (int j = RW - 1; j >= 0; --j) {
+          u64 ox = 0ull, orr = 0ull, oi = 0ull;
+          if (t0 + j < job.L) gradients(j, ox, orr, oi);
+          px[j * (CH / 2)] = close<T>(ox), pr[j * (CH / 2)] = close<T>(orr), pi[j * (CH / 2)] = close<T>(oi);
+        }
       }
       total_of[w][lane] = sum;
     } else {
@@ -711,7 +765,7 @@ cudaError_t room(K kernel, size_t bytes) {
 template <typename... Exp, typename... Act>
 cudaError_t together(void (*kernel)(Exp...), size_t tiles, size_t smem, cudaStream_t st, Act&&... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<size_t>(tiles, 2 * sm_count())));
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<size_t>(tiles, BLOCKS * sm_count())));
   cfg.blockDim = dim3(32 * WARPS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
