@@ -10,6 +10,8 @@
 // Bound by HBM: every value is read and written once.  Sine and cosine cost about 25
 // instructions a row and pair; a thread forms those of its four pairs once and takes
 // its row's heads, of queries and keys alike, in turn.
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -90,11 +92,13 @@ __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float (
   }
 }
 
+constexpr int BATCH = 4;  // heads whose loads are on their way together
+
 // A thread's unit of a head's row is two runs of V neighbouring values, V pairs in
 // all (V = 4, aligned vectors) or, past R, values to copy; V = 1 takes any sizes and
 // strides, its units past R being one value.
 template <typename T, int V, bool INTER>
-__global__ void __launch_bounds__(1024) k_rotary(const Turn a, int units, int rb) {
+__global__ void __launch_bounds__(V == 1 ? 1024 : 256) k_rotary(const Turn a, int units, int rb) {
   const int u = threadIdx.x % units, rl = threadIdx.x / units;
   const long row = (long)blockIdx.x * rb + rl;
   if (rl >= rb || row >= a.rows) return;
@@ -108,12 +112,37 @@ __global__ void __launch_bounds__(1024) k_rotary(const Turn a, int units, int rb
   int o0, o1;
   if (copy) {
     o0 = V == 1 ? a.R + (u - turning) : a.R + (u - turning) * 2 * V;
-    o1 = V == 1 ? -1 : o0 + V;
+    o1 = V == 1 ? o0 : o0 + V;
   } else if (INTER) {
     o0 = u * 2 * V, o1 = o0 + V;
   } else {
     o0 = u * V, o1 = a.R / 2 + o0;
   }
+  const int all = a.t[0].heads + a.t[1].heads, first = blockIdx.y * a.per, last = min(first + a.per, all);
+  auto input = [&](int h) {
+    const bool second = h >= a.t[0].heads;
+    const Side& t = a.t[second];
+    return static_cast<const T*>(t.in) + b * t.ib + n * t.in_row + (second ? h - a.t[0].heads : h) * t.ih;
+  };
+  auto output = [&](int h) {
+    const bool second = h >= a.t[0].heads;
+    const Side& t = a.t[second];
+    return static_cast<T*>(t.out) + b * t.ob + n * t.o_row + (second ? h - a.t[0].heads : h) * t.oh;
+  };
+  using Raw = std::conditional_t<V == 4, typename Quad<T>::Raw, T>;
+  Raw r0[BATCH], r1[BATCH];
+  auto fetch = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      r0[i] = r1[i] = Raw{};
+      if (live && h0 + i < last) {
+        const T* x = input(h0 + i);
+        r0[i] = *reinterpret_cast<const Raw*>(x + o0);
+        r1[i] = *reinterpret_cast<const Raw*>(x + o1);
+      }
+    }
+  };
+  fetch(first);
   float c[V], s[V];
   if (!copy && live) {
     const long long p = a.positions == nullptr ? n : a.per_row ? a.positions[row] : (long long)a.positions[b] + n;
@@ -125,24 +154,17 @@ __global__ void __launch_bounds__(1024) k_rotary(const Turn a, int units, int rb
       s[i] *= a.inverse ? -a.gain : a.gain;
     }
   }
-  const int first = blockIdx.y * a.per, all = a.t[0].heads + a.t[1].heads;
-  const int last = min(first + a.per, all);
-  for (int h = first; h < last; ++h) {
-    const bool second = h >= a.t[0].heads;
-    const Side& t = a.t[second];
-    const int hh = second ? h - a.t[0].heads : h;
-    const T* x = static_cast<const T*>(t.in) + b * t.ib + n * t.in_row + hh * t.ih;
-    T* y = static_cast<T*>(t.out) + b * t.ob + n * t.o_row + hh * t.oh;
-    if constexpr (V == 4) {
-      using Raw = typename Quad<T>::Raw;
-      Raw r0 = Raw{}, r1 = Raw{};
-      if (live) {
-        r0 = *reinterpret_cast<const Raw*>(x + o0);
-        r1 = *reinterpret_cast<const Raw*>(x + o1);
-        if (!copy) {
+#pragma unroll 1
+  for (int h0 = first;;) {
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (h0 + i >= last) break;
+      T* y = output(h0 + i);
+      if constexpr (V == 4) {
+        if (!copy && live) {
           float f[4], g[4];
-          Quad<T>::open(r0, f);
-          Quad<T>::open(r1, g);
+          Quad<T>::open(r0[i], f);
+          Quad<T>::open(r1[i], g);
           if (INTER) {
             float p[4] = {f[0], f[2], g[0], g[2]}, q[4] = {f[1], f[3], g[1], g[3]};
             turn<4>(p, q, c, s);
@@ -151,22 +173,20 @@ __global__ void __launch_bounds__(1024) k_rotary(const Turn a, int units, int rb
           } else {
             turn<4>(f, g, c, s);
           }
-          r0 = Quad<T>::close(f);
-          r1 = Quad<T>::close(g);
+          r0[i] = Quad<T>::close(f);
+          r1[i] = Quad<T>::close(g);
         }
+      } else if (!copy && live) {
+        float f[1] = {to_f(r0[i])}, g[1] = {to_f(r1[i])};
+        turn<1>(f, g, c, s);
+        r0[i] = from_f<T>(f[0]), r1[i] = from_f<T>(g[0]);
       }
-      *reinterpret_cast<Raw*>(y + o0) = r0;
-      *reinterpret_cast<Raw*>(y + o1) = r1;
-    } else {
-      if (copy) {
-        y[o0] = live ? x[o0] : from_f<T>(0.f);
-      } else {
-        float f[1] = {live ? to_f(x[o0]) : 0.f}, g[1] = {live ? to_f(x[o1]) : 0.f};
-        if (live) turn<1>(f, g, c, s);
-        y[o0] = from_f<T>(f[0]);
-        y[o1] = from_f<T>(g[0]);
-      }
+      *reinterpret_cast<Raw*>(y + o0) = r0[i];
+      if (V == 4 || !copy) *reinterpret_cast<Raw*>(y + o1) = r1[i];
     }
+    h0 += BATCH;
+    if (h0 >= last) break;
+    fetch(h0);
   }
 }
 

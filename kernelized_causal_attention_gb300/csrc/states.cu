@@ -120,8 +120,10 @@ __global__ void __launch_bounds__(128)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const float f = __shfl_sync(0xffffffffu, wt[k * RS / 32], (r0 + k * RS) & 31);
-      const uint32_t x[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      uint32_t x[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
       float g[16];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) asm volatile("" : "+r"(x[j]));  // decoded here, not ahead of the loop into four times the registers
 #pragma unroll
       for (int j = 0; j < 4; ++j) decode4<E4M3>(x[j], g + 4 * j);
       if (D % RS == 0 || r0 + k * RS < D) {  // a lane without a row adds nothing
