@@ -19,13 +19,13 @@
 // theirs already, so results repeat bit for bit.
 #include <algorithm>
 
+#include "pair.cuh"
 #include "scan.cuh"
 
 namespace la {
 namespace {
 
 using bf16 = __nv_bfloat16;
-using u64 = unsigned long long;
 
 constexpr int CH = 64;      // channels of a tile, two a lane
 constexpr int WARPS = 8;    // strips of a tile
@@ -39,32 +39,6 @@ constexpr int BACK_STAGES = sizeof(T) == 4 ? 1 : 2;  // 64 and 32 KB of rows a g
 
 // ---------------------------------------------------------- two channels at once
 
-__device__ __forceinline__ u64 pk(float x, float y) {
-  u64 v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
-  return v;
-}
-__device__ __forceinline__ float2 un(u64 v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ u64 two(float x) { return pk(x, x); }
-__device__ __forceinline__ u64 mul2(u64 a, u64 b) {
-  u64 v;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-  return v;
-}
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-  u64 v;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(v) : "l"(a), "l"(b));
-  return v;
-}
-__device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
-  u64 v;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
-  return v;
-}
 __device__ __forceinline__ float rsqrt_fast(float x) {
   float y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

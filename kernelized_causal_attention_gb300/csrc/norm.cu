@@ -14,6 +14,7 @@
 #include <algorithm>
 #include <numeric>
 
+#include "pair.cuh"
 #include "scan.cuh"
 
 namespace la {
@@ -22,30 +23,38 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 // V neighbouring values as one vector of up to 16 bytes (V > 1: the caller has
-// checked the alignment), as it lies in memory and as fp32.
+// checked the alignment), as it lies in memory and as pairs of fp32 (V = 1: with zero).
 template <typename T, int V>
 struct Vec;
 template <typename T>
 struct Vec<T, 1> {
   using Raw = T;
-  __device__ __forceinline__ static void open(const Raw& u, float* f) { f[0] = to_f(u); }
-  __device__ __forceinline__ static Raw close(const float* f) { return from_f<T>(f[0]); }
+  __device__ __forceinline__ static void open(const Raw& u, u64* f) { f[0] = pk(to_f(u), 0.f); }
+  __device__ __forceinline__ static Raw close(const u64* f) { return from_f<T>(un(f[0]).x); }
 };
 template <>
 struct Vec<float, 4> {
   using Raw = float4;
-  __device__ __forceinline__ static void open(const Raw& u, float* f) { f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w; }
-  __device__ __forceinline__ static Raw close(const float* f) { return make_float4(f[0], f[1], f[2], f[3]); }
+  __device__ __forceinline__ static void open(const Raw& u, u64* f) { f[0] = pk(u.x, u.y), f[1] = pk(u.z, u.w); }
+  __device__ __forceinline__ static Raw close(const u64* f) {
+    const float2 a = un(f[0]), b = un(f[1]);
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
 };
 template <>
 struct Vec<bf16, 8> {
   using Raw = uint4;
-  __device__ __forceinline__ static void open(const Raw& u, float* f) { Vec16<bf16>::unpack(u, f); }
-  __device__ __forceinline__ static Raw close(const float* f) {
+  __device__ __forceinline__ static void open(const Raw& u, u64* f) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = pk(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+  __device__ __forceinline__ static Raw close(const u64* f) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      const float2 a = un(f[i]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a.x, a.y);
       w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -59,6 +68,13 @@ template <typename T, int V>
 __device__ __forceinline__ void set(T* p, const typename Vec<T, V>::Raw& v) {
   *reinterpret_cast<typename Vec<T, V>::Raw*>(p) = v;
 }
+
+// Values read again are opened again from their raw form, which takes fewer registers:
+// this keeps the compiler from holding the opened ones.
+__device__ __forceinline__ void again(uint4& v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
+__device__ __forceinline__ void again(float4& v) { asm volatile("" : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w)); }
+__device__ __forceinline__ void again(float& v) { asm volatile("" : "+f"(v)); }
+__device__ __forceinline__ void again(bf16& v) { asm volatile("" : "+h"(reinterpret_cast<unsigned short&>(v))); }
 
 // A group of more than a warp is a block of its own.
 template <int TPR>
@@ -126,28 +142,32 @@ struct NormArgs {
   void *y, *s;
   float *mean, *rstd;
   Place at;
-  long ldx, ldr;  // elements between rows
+  long ldx, ldr, slots;  // ldx, ldr: elements between rows
   int M;
-  float eps;
+  float inv, eps;  // inv: 1 / M
 };
 
-// Columns of a thread: k-th vector at (k TPR + lane) V.
+// Slot (block, group of threads) takes R items slot, slot + slots, ...; slots is a
+// multiple of G, so a thread's columns and their weights stay the same.  Its k-th vector
+// of columns is at (k TPR + lane) V.
 template <typename T, int V, int K, int TPR, int R>
 __global__ void __launch_bounds__(THREADS<TPR>) k_norm_fwd(const NormArgs a) {
   using Raw = typename Vec<T, V>::Raw;
-  constexpr int PER = THREADS<TPR> / TPR;
+  constexpr int PER = THREADS<TPR> / TPR, P = (V + 1) / 2;
   __shared__ float red[2][R][TPR > 32 ? TPR / 32 : 1];
   Sums<TPR, R> sum{red};
   const int lane = threadIdx.x % TPR;
-  const long first = (long)blockIdx.x * (R * PER) + threadIdx.x / TPR;
+  const long slot = (long)blockIdx.x * PER + threadIdx.x / TPR;
   bool in[R], live[R];  // every thread stays for the sums
-  uint32_t row[R], g[R];
+  uint32_t g = 0;
   Raw x[R][K], res[R][K];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    a.at.of(first + r * PER, in[r], live[r], row[r], g[r]);
-    const T* p = static_cast<const T*>(a.x) + row[r] * a.ldx + (long)g[r] * a.M;
-    const T* q = static_cast<const T*>(a.res) + row[r] * a.ldr + (long)g[r] * a.M;
+    uint32_t row, gr;
+    a.at.of(slot + r * a.slots, in[r], live[r], row, gr);
+    if (r == 0) g = gr;
+    const T* p = static_cast<const T*>(a.x) + row * a.ldx + gr * a.M;
+    const T* q = static_cast<const T*>(a.res) + row * a.ldr + gr * a.M;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (k * TPR + lane) * V;
@@ -158,68 +178,78 @@ __global__ void __launch_bounds__(THREADS<TPR>) k_norm_fwd(const NormArgs a) {
       }
     }
   }
-  float f[R][K][V], v[R];
+  u64 f[R][K][P];
+  float v[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    v[r] = 0.f;
+    u64 t = 0ull;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (k * TPR + lane) * V;
       Vec<T, V>::open(x[r][k], f[r][k]);
       if (a.res != nullptr) {
-        float e[V];
+        u64 e[P];
         Vec<T, V>::open(res[r][k], e);
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[r][k][i] += e[i];
+        for (int i = 0; i < P; ++i) f[r][k][i] = add2(f[r][k][i], e[i]);
         const Raw total = Vec<T, V>::close(f[r][k]);
         Vec<T, V>::open(total, f[r][k]);
-        if (in[r] && c < a.M) set<T, V>(static_cast<T*>(a.s) + (first + r * PER) * a.M + c, total);
+        if (in[r] && c < a.M) set<T, V>(static_cast<T*>(a.s) + (slot + r * a.slots) * a.M + c, total);
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[r] += f[r][k][i];
+      for (int i = 0; i < P; ++i) t = add2(t, f[r][k][i]);
     }
+    const float2 tf = un(t);
+    v[r] = tf.x + tf.y;
   }
   sum(v);
   float mean[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    mean[r] = v[r] / a.M;
-    v[r] = 0.f;
+    mean[r] = v[r] * a.inv;
+    const u64 off = pk(-mean[r], V == 1 ? 0.f : -mean[r]);
+    u64 t = 0ull;
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if ((k * TPR + lane) * V < a.M) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          f[r][k][i] -= mean[r];
-          v[r] = fmaf(f[r][k][i], f[r][k][i], v[r]);
+        for (int i = 0; i < P; ++i) {
+          f[r][k][i] = add2(f[r][k][i], off);
+          t = fma2(f[r][k][i], f[r][k][i], t);
         }
       }
+    const float2 tf = un(t);
+    v[r] = tf.x + tf.y;
   }
   sum(v);
 #pragma unroll
-  for (int r = 0; r < R; ++r) {
-    if (!in[r]) continue;
-    const long item = first + r * PER;
-    const float rstd = rsqrtf(v[r] / a.M + a.eps);
-    const T *w = static_cast<const T*>(a.w) + (long)g[r] * a.M, *b = static_cast<const T*>(a.b) + (long)g[r] * a.M;
+  for (int r = 0; r < R; ++r) v[r] = rsqrtf(fmaf(v[r], a.inv, a.eps));
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * TPR + lane) * V;
-      if (c < a.M) {
-        float o[V], wv[V], bv[V];
-        Vec<T, V>::open(get<T, V>(w + c), wv);
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * TPR + lane) * V;
+    if (c >= a.M) continue;
+    u64 w[P], b[P];
+    Vec<T, V>::open(get<T, V>(static_cast<const T*>(a.w) + g * a.M + c), w);
 #pragma unroll
-        for (int i = 0; i < V; ++i) bv[i] = 0.f;
-        if (a.b != nullptr) Vec<T, V>::open(get<T, V>(b + c), bv);
+    for (int i = 0; i < P; ++i) b[i] = 0ull;
+    if (a.b != nullptr) Vec<T, V>::open(get<T, V>(static_cast<const T*>(a.b) + g * a.M + c), b);
 #pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = live[r] ? fmaf(f[r][k][i] * rstd, wv[i], bv[i]) : 0.f;
-        set<T, V>(static_cast<T*>(a.y) + item * a.M + c, Vec<T, V>::close(o));
+    for (int r = 0; r < R; ++r) {
+      if (!in[r]) continue;
+      u64 o[P];
+      const u64 scale = two(v[r]);
+#pragma unroll
+      for (int i = 0; i < P; ++i) o[i] = live[r] ? fma2(mul2(f[r][k][i], scale), w[i], b[i]) : 0ull;
+      set<T, V>(static_cast<T*>(a.y) + (slot + r * a.slots) * a.M + c, Vec<T, V>::close(o));
+    }
+  }
+  if (lane == 0 && a.mean != nullptr) {
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (in[r]) {
+        a.mean[slot + r * a.slots] = live[r] ? mean[r] : 0.f;
+        a.rstd[slot + r * a.slots] = live[r] ? v[r] : 0.f;
       }
-    }
-    if (lane == 0 && a.mean != nullptr) {
-      a.mean[item] = live[r] ? mean[r] : 0.f;
-      a.rstd[item] = live[r] ? rstd : 0.f;
-    }
   }
 }
 
@@ -231,33 +261,33 @@ struct GradArgs {
   Place at;
   long lds, slots;
   int M;
+  float inv;  // 1 / M
 };
 
 // How many groups' sums of its own a block leaves: those of its slots, or, where G
 // divides them, of the G groups, added up over the slots that share one.
 inline __host__ __device__ int distinct(int per, int G) { return per % G == 0 ? G : per; }
 
-// Slot (block, group of threads) takes items slot, slot + slots, ...; slots is a
-// multiple of G, so a thread's columns, and their sums, stay the same.
+// Items as forward, R at a time until there are no more.
 template <typename T, int V, int K, int TPR, int R>
 __global__ void __launch_bounds__(THREADS<TPR>, (THREADS<TPR> < 512 ? 512 / THREADS<TPR> : 1)) k_norm_bwd(const GradArgs a) {
   using Raw = typename Vec<T, V>::Raw;
-  constexpr int PER = THREADS<TPR> / TPR;
+  constexpr int PER = THREADS<TPR> / TPR, P = (V + 1) / 2;
   __shared__ float red[2][2 * R][TPR > 32 ? TPR / 32 : 1];
   Sums<TPR, 2 * R> sum{red};
   const int lane = threadIdx.x % TPR;
   const long slot = (long)blockIdx.x * PER + threadIdx.x / TPR;
-  const uint32_t own = static_cast<uint32_t>(slot % a.at.groups.d);
-  const T* w = static_cast<const T*>(a.w) + (long)own * a.M;
-  float dw[K][V], db[K][V];
-  Raw wr[K];
+  const uint32_t own = static_cast<uint32_t>(slot) % a.at.groups.d;
+  const T* w = static_cast<const T*>(a.w) + own * a.M;
+  u64 dw[K][P], db[K][P], wv[K][P];
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     const int c = (k * TPR + lane) * V;
-    wr[k] = Raw{};
-    if (c < a.M) wr[k] = get<T, V>(w + c);
+    Raw wr = Raw{};
+    if (c < a.M) wr = get<T, V>(w + c);
+    Vec<T, V>::open(wr, wv[k]);
 #pragma unroll
-    for (int i = 0; i < V; ++i) dw[k][i] = db[k][i] = 0.f;
+    for (int i = 0; i < P; ++i) dw[k][i] = db[k][i] = 0ull;
   }
   for (long base = slot; base - slot < a.at.items; base += R * a.slots) {  // the same steps for all threads: they meet in the sums
     bool in[R], live[R];
@@ -268,7 +298,7 @@ __global__ void __launch_bounds__(THREADS<TPR>, (THREADS<TPR> < 512 ? 512 / THRE
       const long item = base + r * a.slots, at = item * a.M;
       uint32_t row, g;
       a.at.of(item, in[r], live[r], row, g);
-      const T* s = static_cast<const T*>(a.s) + row * a.lds + (long)g * a.M;
+      const T* s = static_cast<const T*>(a.s) + row * a.lds + own * a.M;
       mean[r] = live[r] ? a.mean[item] : 0.f, rstd[r] = live[r] ? a.rstd[item] : 0.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
@@ -281,52 +311,56 @@ __global__ void __launch_bounds__(THREADS<TPR>, (THREADS<TPR> < 512 ? 512 / THRE
         }
       }
     }
+    // rows that are not live hold zeros, and rstd zero: they add nothing, and dx is zero
     float v[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      v[2 * r] = v[2 * r + 1] = 0.f;
+      u64 t1 = 0ull, t2 = 0ull;
+      const u64 off = two(-mean[r]), scale = two(rstd[r]);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        if (!live[r] || (k * TPR + lane) * V >= a.M) continue;
-        float f[V], d[V], wv[V];
+        u64 f[P], d[P];
         Vec<T, V>::open(sr[r][k], f);
         Vec<T, V>::open(dr[r][k], d);
-        Vec<T, V>::open(wr[k], wv);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          f[i] = (f[i] - mean[r]) * rstd[r];
-          dw[k][i] = fmaf(d[i], f[i], dw[k][i]);
-          db[k][i] += d[i];
-          d[i] *= wv[i];
-          v[2 * r] += d[i];
-          v[2 * r + 1] = fmaf(d[i], f[i], v[2 * r + 1]);
+        for (int i = 0; i < P; ++i) {
+          f[i] = mul2(add2(f[i], off), scale);
+          dw[k][i] = fma2(d[i], f[i], dw[k][i]);
+          db[k][i] = add2(db[k][i], d[i]);
+          d[i] = mul2(d[i], wv[k][i]);
+          t1 = add2(t1, d[i]);
+          t2 = fma2(d[i], f[i], t2);
         }
       }
+      const float2 a1 = un(t1), a2 = un(t2);
+      v[2 * r] = a1.x + a1.y, v[2 * r + 1] = a2.x + a2.y;
     }
     sum(v);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const float s1 = v[2 * r] / a.M, s2 = v[2 * r + 1] / a.M;
+      if (!in[r]) continue;
+      const u64 s1 = two(-v[2 * r] * a.inv), s2 = two(-v[2 * r + 1] * a.inv), off = two(-mean[r]), scale = two(rstd[r]);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int c = (k * TPR + lane) * V;
-        if (!in[r] || c >= a.M) continue;
-        float f[V], d[V], wv[V], o[V];
+        if (c >= a.M) continue;
+        u64 f[P], d[P], e[P];
+        again(sr[r][k]), again(dr[r][k]);
         Vec<T, V>::open(sr[r][k], f);
         Vec<T, V>::open(dr[r][k], d);
-        Vec<T, V>::open(wr[k], wv);
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = (fmaf(d[i], wv[i], -s1) - (f[i] - mean[r]) * rstd[r] * s2) * rstd[r];
         if (a.ds != nullptr) {
-          float e[V];
           Vec<T, V>::open(er[r][k], e);
+        } else {
 #pragma unroll
-          for (int i = 0; i < V; ++i) o[i] += e[i];
+          for (int i = 0; i < P; ++i) e[i] = 0ull;
         }
-        if (!live[r])
 #pragma unroll
-          for (int i = 0; i < V; ++i) o[i] = 0.f;
-        set<T, V>(static_cast<T*>(a.dx) + (base + r * a.slots) * a.M + c, Vec<T, V>::close(o));
+        for (int i = 0; i < P; ++i) {
+          f[i] = mul2(add2(f[i], off), scale);
+          d[i] = fma2(f[i], s2, fma2(d[i], wv[k][i], s1));
+          d[i] = fma2(d[i], scale, e[i]);
+        }
+        set<T, V>(static_cast<T*>(a.dx) + (base + r * a.slots) * a.M + c, Vec<T, V>::close(d));
       }
     }
   }
@@ -334,13 +368,19 @@ __global__ void __launch_bounds__(THREADS<TPR>, (THREADS<TPR> < 512 ? 512 / THRE
   const int G = a.at.groups.d, keep = distinct(PER, G);
   float* part = a.part + (long)blockIdx.x * keep * a.M;
   const long plane = (long)gridDim.x * keep * a.M;
+  auto spread = [&](float* to, const u64* from) {
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const float2 t = un(from[i]);
+      to[2 * i] = t.x;
+      if (V > 1) to[2 * i + 1] = t.y;
+    }
+  };
   if constexpr (PER == 1) {
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int c = (k * TPR + lane) * V;
-      if (c < a.M)
-#pragma unroll
-        for (int i = 0; i < V; ++i) part[c + i] = dw[k][i], part[plane + c + i] = db[k][i];
+      if (c < a.M) spread(part + c, dw[k]), spread(part + plane + c, db[k]);
     }
   } else {
     __shared__ float all[PER * TPR * V * K];
@@ -351,9 +391,7 @@ __global__ void __launch_bounds__(THREADS<TPR>, (THREADS<TPR> < 512 ? 512 / THRE
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int c = (k * TPR + lane) * V;
-        if (c < a.M)
-#pragma unroll
-          for (int i = 0; i < V; ++i) all[mine * a.M + c + i] = which ? db[k][i] : dw[k][i];
+        if (c < a.M) spread(all + mine * a.M + c, which ? db[k] : dw[k]);
       }
       __syncthreads();
       for (int e = threadIdx.x; e < keep * a.M; e += THREADS<TPR>) {
@@ -387,23 +425,27 @@ __global__ void __launch_bounds__(1024) k_norm_join(const float* __restrict__ pa
   }
 }
 
-// How a group is held: f.run<V, K, TPR, R>() of the first shape that covers M.
+// How a group is held: f.run<V, K, TPR, R>() of the first shape that covers M.  Both
+// directions of 4 x 2048 x 2048 bf16 with a residual took 55 us with three groups at once
+// backward and four vectors a thread forward (67 with four groups, which spill, 60 with
+// two on more threads; 58 with one vector a thread forward); 32 groups of 64 took 38
+// (43 with four at once, 41 with two).
 #define LA_NORM_SHAPE(VV, KK, TT, RR) \
   if (M <= (VV) * (KK) * (TT)) return f.template run<VV, KK, TT, RR>();
 template <typename T, typename F>
 cudaError_t fwd_shape(int M, bool vec, F&& f) {
   constexpr int V = 16 / sizeof(T);
   if (vec) {
-    LA_NORM_SHAPE(V, 1, 4, 4)
-    LA_NORM_SHAPE(V, 1, 8, 4)
-    LA_NORM_SHAPE(V, 1, 16, 4)
-    LA_NORM_SHAPE(V, 1, 32, 4)
+    LA_NORM_SHAPE(V, 1, 4, 3)
+    LA_NORM_SHAPE(V, 1, 8, 3)
+    LA_NORM_SHAPE(V, 1, 16, 3)
+    LA_NORM_SHAPE(V, 1, 32, 3)
     LA_NORM_SHAPE(V, 2, 32, 2)
     LA_NORM_SHAPE(V, 4, 32, 1)
-    LA_NORM_SHAPE(V, 8, 32, 1)
+    LA_NORM_SHAPE(V, 2, 128, 2)
     LA_NORM_SHAPE(V, 2, 256, 2)
     LA_NORM_SHAPE(V, 4, 256, 1)
-    LA_NORM_SHAPE(V, 4, 512, 1)
+    if constexpr (V == 4) LA_NORM_SHAPE(V, 4, 512, 1)
   } else {
     LA_NORM_SHAPE(1, 1, 8, 4)
     LA_NORM_SHAPE(1, 1, 32, 4)
@@ -418,16 +460,16 @@ template <typename T, typename F>
 cudaError_t bwd_shape(int M, bool vec, F&& f) {
   constexpr int V = 16 / sizeof(T);
   if (vec) {
-    LA_NORM_SHAPE(V, 1, 4, 4)
-    LA_NORM_SHAPE(V, 1, 8, 4)
-    LA_NORM_SHAPE(V, 1, 16, 4)
-    LA_NORM_SHAPE(V, 1, 32, 4)
-    LA_NORM_SHAPE(V, 2, 32, 2)
-    LA_NORM_SHAPE(V, 1, 128, 4)
-    LA_NORM_SHAPE(V, 1, 256, 4)
+    LA_NORM_SHAPE(V, 1, 4, 3)
+    LA_NORM_SHAPE(V, 1, 8, 3)
+    LA_NORM_SHAPE(V, 1, 16, 3)
+    LA_NORM_SHAPE(V, 1, 32, 3)
+    LA_NORM_SHAPE(V, 1, 64, 3)
+    LA_NORM_SHAPE(V, 1, 128, 3)
+    LA_NORM_SHAPE(V, 1, 256, 3)
     LA_NORM_SHAPE(V, 2, 256, 2)
     LA_NORM_SHAPE(V, 2, 512, 1)
-    LA_NORM_SHAPE(V, 4, 512, 1)
+    if constexpr (V == 4) LA_NORM_SHAPE(V, 4, 512, 1)
   } else {
     LA_NORM_SHAPE(1, 1, 8, 4)
     LA_NORM_SHAPE(1, 1, 32, 4)
@@ -440,24 +482,29 @@ cudaError_t bwd_shape(int M, bool vec, F&& f) {
 }
 #undef LA_NORM_SHAPE
 
+// At least `want` blocks, and a multiple of what keeps slots a multiple of G.
+long in_units(long want, int G, int per) {
+  const long unit = G / std::gcd(G, per);
+  return (want + unit - 1) / unit * unit;
+}
+
 template <typename T>
 struct Forward {
-  const NormArgs& a;
+  NormArgs& a;
   cudaStream_t st;
   template <int V, int K, int TPR, int R>
   cudaError_t run() {
-    constexpr int ITEMS = THREADS<TPR> / TPR * R;
-    k_norm_fwd<T, V, K, TPR, R><<<static_cast<unsigned>((a.at.items + ITEMS - 1) / ITEMS), THREADS<TPR>, 0, st>>>(a);
+    constexpr int PER = THREADS<TPR> / TPR;
+    const long blocks = in_units((a.at.items + R * PER - 1) / (R * PER), a.at.groups.d, PER);
+    a.slots = blocks * PER;
+    k_norm_fwd<T, V, K, TPR, R><<<static_cast<unsigned>(blocks), THREADS<TPR>, 0, st>>>(a);
     return cudaGetLastError();
   }
 };
 
-// As many blocks as run at once (512 threads on an SM), and a multiple of what keeps
-// slots a multiple of G.
+// As many blocks as run at once: 512 threads on an SM.
 long blocks_of(long items, int G, int per, int threads) {
-  const long unit = G / std::gcd(G, per);
-  const long most = (items + per - 1) / per, want = std::min<long>(most, (long)sm_count() * std::max(1, 512 / threads));
-  return (want + unit - 1) / unit * unit;
+  return in_units(std::min<long>((items + per - 1) / per, (long)sm_count() * std::max(1, 512 / threads)), G, per);
 }
 
 template <typename T>
@@ -518,7 +565,8 @@ size_t norm_bwd_ws_bytes(const NormShape& s) {
 
 cudaError_t norm_fwd(const void* x, const void* res, const void* w, const void* b, const int* lengths, void* y, void* s, float* mean,
                      float* rstd, float eps, const NormShape& sh, cudaStream_t st) {
-  const NormArgs a{x, res, w, b, y, s, mean, rstd, place(lengths, sh), sh.ldx, sh.ldr, sh.C / sh.G, eps};
+  const int M = sh.C / sh.G;
+  NormArgs a{x, res, w, b, y, s, mean, rstd, place(lengths, sh), sh.ldx, sh.ldr, 0, M, 1.f / M, eps};
   const bool vec = vectors(sh, sh.ldx, {x, res}) && (res == nullptr || sh.ldr % (sh.dtype == 0 ? 4 : 8) == 0);
   if (sh.dtype == 0) return fwd_shape<float>(a.M, vec, Forward<float>{a, st});
   return fwd_shape<bf16>(a.M, vec, Forward<bf16>{a, st});
@@ -526,7 +574,8 @@ cudaError_t norm_fwd(const void* x, const void* res, const void* w, const void* 
 
 cudaError_t norm_bwd(const void* s, const void* w, const float* mean, const float* rstd, const int* lengths, const void* dy, const void* ds,
                      void* dx, void* dw, void* db, float* ws, const NormShape& sh, cudaStream_t st) {
-  GradArgs a{s, w, dy, ds, mean, rstd, dx, ws, place(lengths, sh), sh.ldx, 0, sh.C / sh.G};
+  const int M = sh.C / sh.G;
+  GradArgs a{s, w, dy, ds, mean, rstd, dx, ws, place(lengths, sh), sh.ldx, 0, M, 1.f / M};
   const bool vec = vectors(sh, sh.ldx, {s});
   if (sh.dtype == 0) return bwd_shape<float>(a.M, vec, Backward<float>{a, dw, db, st});
   return bwd_shape<bf16>(a.M, vec, Backward<bf16>{a, dw, db, st});
