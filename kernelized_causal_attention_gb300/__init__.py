@@ -877,6 +877,18 @@ def cross_step(q, S, Z):
 
 # ----------------------------- around the recurrent layer: gated recurrence, norm, positions, packed states
 
+@functools.lru_cache(maxsize=256)
+def _gated_bytes(B, N, C, code):
+    """Bytes of the forward's workspace, of what it keeps, of the gradients' workspace."""
+    L = lib()
+    return L.la_gated_workspace_bytes(0, B, N, C, code), L.la_gated_kept_bytes(B, N, C, code), L.la_gated_workspace_bytes(1, B, N, C, code)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_bytes(device, B, N, C, groups, code):  # as many blocks' sums as the device runs at once
+    return lib().la_norm_workspace_bytes(B, N, C, groups, code)
+
+
 def _gated_args(x, r, i, lam, lengths, scale, lead):
     """(pointers up to lengths, row strides, rows' shape, type code, type, device)"""
     if x.dim() != lead + 1:
@@ -904,8 +916,9 @@ def gated_fwd(x, r, i, lam, h=None, scale=8.0, lengths=None, keep=False):
     ph = _take_opt(h, "h", (B, C), torch.float32, dev)
     _need_cuda(x)
     y = torch.empty((B, N, C), dtype=dtype, device=dev)
-    kept = torch.empty((lib().la_gated_kept_bytes(B, N, C, code) // 4,), dtype=torch.float32, device=dev) if keep else None
-    ws, pws, nws = _scratch(lib().la_gated_workspace_bytes(0, B, N, C, code), x)
+    fwd, keeps, _ = _gated_bytes(B, N, C, code)
+    kept = torch.empty((keeps // 4,), dtype=torch.float32, device=dev) if keep else None
+    ws, pws, nws = _scratch(fwd, x)
     _check(lib().la_gated_fwd(*ptrs, ph, None if kept is None else kept.data_ptr(), y.data_ptr(), pws, nws, B, N, C, *ld, scale,
                               code, _stream(None)), "la_gated_fwd")
     return (y, kept) if keep else y
@@ -916,11 +929,12 @@ def gated_bwd(x, r, i, lam, kept, dy, scale=8.0, lengths=None):
     """(dx, dr, di, dlam) of sum(dy * y); kept from gated_fwd(..., keep=True)."""
     ptrs, ld, (B, N, C), code, dtype, dev = _gated_args(x, r, i, lam, lengths, scale, 2)
     _need_cuda(x)
-    pk = _take(kept, "kept", (lib().la_gated_kept_bytes(B, N, C, code) // 4,), torch.float32, dev)
+    _, keeps, bwd = _gated_bytes(B, N, C, code)
+    pk = _take(kept, "kept", (keeps // 4,), torch.float32, dev)
     pg = _take(dy, "dy", x.shape, dtype, dev)
     new = functools.partial(torch.empty, dtype=dtype, device=dev)
     d = (new((B, N, C)), new((B, N, C)), new((B, N, C)), new((C,)))
-    ws, pws, nws = _scratch(lib().la_gated_workspace_bytes(1, B, N, C, code), x)
+    ws, pws, nws = _scratch(bwd, x)
     _check(lib().la_gated_bwd(*ptrs, pk, pg, *[t.data_ptr() for t in d], pws, nws, B, N, C, *ld, scale, code, _stream(None)),
            "la_gated_bwd")
     return d
@@ -980,7 +994,7 @@ def norm_bwd(s, w, mean, rstd, dy, ds=None, groups=1, bias=True, lengths=None):
     _need_cuda(s)
     dx, dw = torch.empty(s.shape, dtype=dtype, device=dev), torch.empty_like(w)
     db = torch.empty_like(w) if bias else None
-    ws, pws, nws = _scratch(lib().la_norm_workspace_bytes(B, N, C, groups, code), s)
+    ws, pws, nws = _scratch(_norm_bytes(dev.index, B, N, C, groups, code), s)
     _check(lib().la_norm_bwd(ps, *ptrs, dx.data_ptr(), dw.data_ptr(), db.data_ptr() if bias else None, pws, nws, B, N, C, groups, ld, code,
                              _stream(None)), "la_norm_bwd")
     return dx, dw, db
@@ -1027,6 +1041,8 @@ def _rotary(q, k, turns, positions, gain, interleaved, head_major, lengths, inpl
     per_row = positions is not None and positions.dim() == 2
     pp = _take_opt(positions, "positions", (B, N) if per_row else (B,), torch.int32, dev)
     pn = _take_opt(lengths, "lengths", (B,), torch.int32, dev)
+    if inplace and pq == pk:
+        raise ValueError("inplace: q and k must be different tensors")
     _need_cuda(q)
     oq = q if inplace else torch.empty(q.shape, dtype=dtype, device=dev)
     ok = k if inplace or k is None else torch.empty(kshape, dtype=dtype, device=dev)

@@ -18,6 +18,7 @@
 // The state passed on is the same sequence of fused multiply-adds whichever tiles had
 // theirs already, so results repeat bit for bit.
 #include <algorithm>
+#include <atomic>
 
 #include "pair.cuh"
 #include "scan.cuh"
@@ -730,16 +731,33 @@ cudaError_t chain(Chain& ch, Rows& a, char* ws, size_t n, const GatedShape& s, c
   return cudaGetLastError();
 }
 
-template <typename K>
-cudaError_t room(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+// A kernel's dynamic shared memory, said once a device, and how many of its blocks an SM
+// holds (no less than BLOCKS here; asked, because a cooperative launch of more is refused).
+template <auto kernel>
+cudaError_t room(size_t bytes, int* per_sm) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int n = dev < 64 ? known[dev].load(std::memory_order_acquire) : 0;
+  if (n == 0) {
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes))) != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, 32 * WARPS, bytes)) != cudaSuccess) return e;
+    if (n < 1) return cudaErrorCooperativeLaunchTooLarge;
+    if (dev < 64) known[dev].store(n, std::memory_order_release);
+  }
+  *per_sm = n;
+  return cudaSuccess;
 }
 
 // A cooperative launch: all blocks run at once, or the launch fails.
-template <typename... Exp, typename... Act>
-cudaError_t together(void (*kernel)(Exp...), size_t tiles, size_t smem, cudaStream_t st, Act&&... args) {
+template <auto kernel, typename... Act>
+cudaError_t together(size_t tiles, size_t smem, cudaStream_t st, Act&&... args) {
+  int per_sm = 0;
+  const cudaError_t e = room<kernel>(smem, &per_sm);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<size_t>(tiles, BLOCKS * sm_count())));
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<size_t>(tiles, (size_t)per_sm * sm_count())));
   cfg.blockDim = dim3(32 * WARPS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -757,17 +775,16 @@ cudaError_t fwd(Rows a, float* h, float* kept, void* y, void* ws, const GatedSha
   constexpr size_t stage = 3 * ROWS * CH * sizeof(T);
   a.tiles = (s.N + ROWS - 1) / ROWS;
   const size_t n = entries(s, ROWS);
-  const dim3 block(32 * WARPS);
   Chain ch{};
   cudaError_t e;
   if (a.tiles == 1) {
-    if ((e = room(k_gated_fwd<T, UNIT, false>, stage)) != cudaSuccess) return e;
-    k_gated_fwd<T, UNIT, false><<<static_cast<unsigned>(n), block, stage, st>>>(a, ch, h, kept, (T*)y, static_cast<int>(n));
+    int per_sm;
+    if ((e = room<k_gated_fwd<T, UNIT, false>>(stage, &per_sm)) != cudaSuccess) return e;
+    k_gated_fwd<T, UNIT, false><<<static_cast<unsigned>(n), 32 * WARPS, stage, st>>>(a, ch, h, kept, (T*)y, static_cast<int>(n));
     return cudaGetLastError();
   }
-  if ((e = room(k_gated_fwd<T, UNIT, true>, 2 * stage)) != cudaSuccess) return e;
   if ((e = chain<T>(ch, a, static_cast<char*>(ws), n, s, st)) != cudaSuccess) return e;
-  return together(k_gated_fwd<T, UNIT, true>, n, 2 * stage, st, a, ch, h, kept, (T*)y, static_cast<int>(n));
+  return together<k_gated_fwd<T, UNIT, true>>(n, 2 * stage, st, a, ch, h, kept, (T*)y, static_cast<int>(n));
 }
 
 template <typename T, int UNIT>
@@ -776,18 +793,17 @@ cudaError_t bwd(Rows a, const float* kept, const void* dy, void* dx, void* dr, v
   constexpr size_t stage = 4 * KEEP * CH * sizeof(T);
   a.tiles = (s.N + KEEP - 1) / KEEP;
   const size_t n = entries(s, KEEP);
-  const dim3 block(32 * WARPS);
   float* sums = static_cast<float*>(ws);
   Chain ch{};
   cudaError_t e;
   if (a.tiles == 1) {
-    if ((e = room(k_gated_bwd<T, UNIT, false>, stage)) != cudaSuccess) return e;
-    k_gated_bwd<T, UNIT, false><<<static_cast<unsigned>(n), block, stage, st>>>(a, ch, (const T*)dy, kept, (T*)dx, (T*)dr, (T*)di, sums, static_cast<int>(n));
+    int per_sm;
+    if ((e = room<k_gated_bwd<T, UNIT, false>>(stage, &per_sm)) != cudaSuccess) return e;
+    k_gated_bwd<T, UNIT, false><<<static_cast<unsigned>(n), 32 * WARPS, stage, st>>>(a, ch, (const T*)dy, kept, (T*)dx, (T*)dr, (T*)di, sums, static_cast<int>(n));
     e = cudaGetLastError();
   } else {
-    if ((e = room(k_gated_bwd<T, UNIT, true>, BACK_STAGES<T> * stage)) != cudaSuccess) return e;
     if ((e = chain<T>(ch, a, static_cast<char*>(ws) + align16(4 * records(s)), n, s, st)) != cudaSuccess) return e;
-    e = together(k_gated_bwd<T, UNIT, true>, n, BACK_STAGES<T> * stage, st, a, ch, (const T*)dy, kept, (T*)dx, (T*)dr, (T*)di, sums,
+    e = together<k_gated_bwd<T, UNIT, true>>(n, BACK_STAGES<T> * stage, st, a, ch, (const T*)dy, kept, (T*)dx, (T*)dr, (T*)di, sums,
                  static_cast<int>(n));
   }
   if (e != cudaSuccess) return e;

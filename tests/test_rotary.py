@@ -231,3 +231,5 @@ def test_binding_refuses(linattn):
         linattn.rotary_fwd(q.transpose(1, 2), None, t, head_major=True)
     with pytest.raises(ValueError, match="dense"):
         linattn.rotary_fwd(q.transpose(1, 2), None, t)
+    with pytest.raises(ValueError, match="different tensors"):
+        linattn.rotary_fwd(q, q, t, inplace=True)
