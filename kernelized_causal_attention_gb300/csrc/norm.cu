@@ -108,17 +108,6 @@ struct Sums {
   }
 };
 
-// Whole numbers below 2^31 divided by d: one product.
-struct Divide {
-  uint32_t d, m;
-  int s;
-  explicit Divide(uint32_t d_ = 1) : d(d_), s(0) {
-    while ((1ull << s) < d) ++s;
-    m = static_cast<uint32_t>((((1ull << s) - d) << 32) / d + 1);
-  }
-  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
-};
-
 // Where an item (a group of a row) is.
 struct Place {
   Divide groups, rows;  // by the groups of a row, by the rows of a sequence

@@ -1,7 +1,9 @@
-// Two fp32 values in one 64-bit register pair, and the instructions that take both.
+// Two fp32 values in one 64-bit register pair, and the instructions that take both; a
+// division by a number known at the launch.
 #pragma once
 
 #include <cuda_runtime.h>
+#include <stdint.h>
 
 namespace la {
 
@@ -33,5 +35,16 @@ __device__ __forceinline__ u64 fma2(u64 a, u64 b, u64 c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(v) : "l"(a), "l"(b), "l"(c));
   return v;
 }
+
+// Whole numbers below 2^31 divided by d: one product.
+struct Divide {
+  uint32_t d, m;
+  int s;
+  explicit Divide(uint32_t d_ = 1) : d(d_), s(0) {
+    while ((1ull << s) < d) ++s;
+    m = static_cast<uint32_t>((((1ull << s) - d) << 32) / d + 1);
+  }
+  __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(m, n) + n) >> s; }
+};
 
 }  // namespace la
