@@ -32,6 +32,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import inspect
 import math
 import os
@@ -100,7 +101,7 @@ _SIGS = {
 EXPORTED = tuple(_SIGS)
 
 _lock = threading.Lock()
-_lib = None
+_lib = _front = None
 
 
 class LinAttnError(RuntimeError):
@@ -133,6 +134,23 @@ def lib():
                 fn.restype = res
             _lib = h
     return _lib
+
+
+def _load_front():
+    """The compiled allocating calls (_front.so, built with the library); raises if they have not been built."""
+    global _front
+    with _lock:
+        if _front is None:
+            path = os.path.join(_HERE, "_lib", "_front.so")
+            if not os.path.exists(path):
+                raise RuntimeError(f"not built: {path} is missing. Build it with `python -m kernelized_causal_attention_gb300._build`.")
+            name = __name__ + "._front"
+            spec = importlib.util.spec_from_file_location(name, path)
+            front = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(front)
+            front.setup(LinAttnError)
+            _front = front
+    return _front
 
 
 def status_string(code: int) -> str:
@@ -877,127 +895,36 @@ def cross_step(q, S, Z):
 
 # ----------------------------- around the recurrent layer: gated recurrence, norm, positions, packed states
 
-@functools.lru_cache(maxsize=256)
-def _gated_bytes(B, N, C, code):
-    """Bytes of the forward's workspace, of what it keeps, of the gradients' workspace."""
-    L = lib()
-    return L.la_gated_workspace_bytes(0, B, N, C, code), L.la_gated_kept_bytes(B, N, C, code), L.la_gated_workspace_bytes(1, B, N, C, code)
-
-
-@functools.lru_cache(maxsize=256)
-def _norm_bytes(device, B, N, C, groups, code):  # as many blocks' sums as the device runs at once
-    return lib().la_norm_workspace_bytes(B, N, C, groups, code)
-
-
-def _gated_args(x, r, i, lam, lengths, scale, lead):
-    """(pointers up to lengths, row strides, rows' shape, type code, type, device)"""
-    if x.dim() != lead + 1:
-        raise ValueError(f"x: {lead + 1} dimensions")
-    shape, dtype, dev = x.shape, x.dtype, x.device
-    _need_ints(x)
-    if not 0 < scale < float("inf"):
-        raise ValueError("scale: a positive number is needed")
-    code = _dtype_code(x)
-    px, lx = _take_rows(x, "x", shape, dtype, dev, lead)
-    pr, lr = _take_rows(r, "r", shape, dtype, dev, lead)
-    pi, li = _take_rows(i, "i", shape, dtype, dev, lead)
-    ptrs = (px, pr, pi, _take(lam, "lam", shape[-1:], dtype, dev), _take_opt(lengths, "lengths", shape[:1], torch.int32, dev))
-    return ptrs, (lx, lr, li), shape, code, dtype, dev
-
-
-@_on_device
 def gated_fwd(x, r, i, lam, h=None, scale=8.0, lengths=None, keep=False):
     """y [B,N,C] of the gated recurrence h_n = a_n h_{n-1} + sqrt(1 - a_n^2) sigmoid(i_n) x_n,
     a_n = exp(-scale softplus(lam) sigmoid(r_n)).  x, r, i [B,N,C] (rows may be slices of wider ones),
     lam [C].  h [B,C] (float32) is the state before row 0 (zeros if None), updated in place to the state
     after each sequence's last valid row; gated_step continues from it.  keep: (y, kept), where kept is
     what gated_bwd needs of this call."""
-    ptrs, ld, (B, N, C), code, dtype, dev = _gated_args(x, r, i, lam, lengths, scale, 2)
-    ph = _take_opt(h, "h", (B, C), torch.float32, dev)
-    _need_cuda(x)
-    y = torch.empty((B, N, C), dtype=dtype, device=dev)
-    fwd, keeps, _ = _gated_bytes(B, N, C, code)
-    kept = torch.empty((keeps // 4,), dtype=torch.float32, device=dev) if keep else None
-    ws, pws, nws = _scratch(fwd, x)
-    _check(lib().la_gated_fwd(*ptrs, ph, None if kept is None else kept.data_ptr(), y.data_ptr(), pws, nws, B, N, C, *ld, scale,
-                              code, _stream(None)), "la_gated_fwd")
-    return (y, kept) if keep else y
+    return (_front or _load_front()).gated_fwd(x, r, i, lam, h, scale, lengths, keep)
 
 
-@_on_device
 def gated_bwd(x, r, i, lam, kept, dy, scale=8.0, lengths=None):
     """(dx, dr, di, dlam) of sum(dy * y); kept from gated_fwd(..., keep=True)."""
-    ptrs, ld, (B, N, C), code, dtype, dev = _gated_args(x, r, i, lam, lengths, scale, 2)
-    _need_cuda(x)
-    _, keeps, bwd = _gated_bytes(B, N, C, code)
-    pk = _take(kept, "kept", (keeps // 4,), torch.float32, dev)
-    pg = _take(dy, "dy", x.shape, dtype, dev)
-    new = functools.partial(torch.empty, dtype=dtype, device=dev)
-    d = (new((B, N, C)), new((B, N, C)), new((B, N, C)), new((C,)))
-    ws, pws, nws = _scratch(bwd, x)
-    _check(lib().la_gated_bwd(*ptrs, pk, pg, *[t.data_ptr() for t in d], pws, nws, B, N, C, *ld, scale, code, _stream(None)),
-           "la_gated_bwd")
-    return d
+    return (_front or _load_front()).gated_bwd(x, r, i, lam, kept, dy, scale, lengths)
 
 
-@_on_device
 def gated_step(x, r, i, lam, h, scale=8.0):
     """y [B,C] for one row of each stream: x, r, i [B,C]; h [B,C] (float32) is updated in place."""
-    ptrs, ld, (B, C), code, dtype, dev = _gated_args(x, r, i, lam, None, scale, 1)
-    ph = _take(h, "h", (B, C), torch.float32, dev)
-    _need_cuda(x)
-    y = torch.empty((B, C), dtype=dtype, device=dev)
-    _check(lib().la_gated_step(*ptrs[:4], ph, y.data_ptr(), B, C, *ld, scale, code, _stream(None)), "la_gated_step")
-    return y
+    return (_front or _load_front()).gated_step(x, r, i, lam, h, scale)
 
 
-def _norm_rows(x, name, groups, lengths):
-    """(address, row stride, (B, N, C), type code, type, device, address of the lengths) of rows [N,C] or [B,N,C]."""
-    if x.dim() not in (2, 3):
-        raise ValueError(f"{name}: 2 or 3 dimensions")
-    lead, shape, dtype, dev = x.dim() - 1, x.shape, x.dtype, x.device
-    if lengths is not None and lead != 2:
-        raise ValueError(f"lengths: {name} must have 3 dimensions")
-    if groups < 1 or shape[-1] % groups:
-        raise ValueError(f"groups: {groups} does not divide {shape[-1]} columns")
-    _need_ints(x)
-    code = _dtype_code(x)
-    p, ld = _take_rows(x, name, shape, dtype, dev, lead)
-    return p, ld, (shape if lead == 2 else (1, *shape)), code, dtype, dev, _take_opt(lengths, "lengths", shape[:1], torch.int32, dev)
-
-
-@_on_device
 def norm_fwd(x, w, b=None, residual=None, groups=1, eps=1e-5, lengths=None):
     """(y, s, mean, rstd) of the layer norm of s = x + residual (x itself without one) over each of `groups`
     groups of neighbouring columns: y = (s - mean) rstd w + b.  x, residual [N,C] or [B,N,C] (rows may be
     slices of wider ones), w, b [C]; mean, rstd [...,groups] (float32); lengths: int32 [B] of valid rows."""
-    px, ld, (B, N, C), code, dtype, dev, pn = _norm_rows(x, "x", groups, lengths)
-    pr, lr = (None, C) if residual is None else _take_rows(residual, "residual", x.shape, dtype, dev, x.dim() - 1)
-    pw, pb = _take(w, "w", (C,), dtype, dev), _take_opt(b, "b", (C,), dtype, dev)
-    _need_cuda(x)
-    y = torch.empty(x.shape, dtype=dtype, device=dev)
-    s = x if residual is None else torch.empty(x.shape, dtype=dtype, device=dev)
-    mean, rstd = (torch.empty((*x.shape[:-1], groups), dtype=torch.float32, device=dev) for _ in range(2))
-    _check(lib().la_norm_fwd(px, pr, pw, pb, pn, y.data_ptr(), None if residual is None else s.data_ptr(), mean.data_ptr(),
-                             rstd.data_ptr(), eps, B, N, C, groups, ld, lr, code, _stream(None)), "la_norm_fwd")
-    return y, s, mean, rstd
+    return (_front or _load_front()).norm_fwd(x, w, b, residual, groups, eps, lengths)
 
 
-@_on_device
 def norm_bwd(s, w, mean, rstd, dy, ds=None, groups=1, bias=True, lengths=None):
     """(dx, dw, db) of sum(dy * y) + sum(ds * s) for norm_fwd's s, mean and rstd; dx is the gradient of x and of
     the residual alike; db is None with bias=False."""
-    ps, ld, (B, N, C), code, dtype, dev, pn = _norm_rows(s, "s", groups, lengths)
-    stat = (*s.shape[:-1], groups)
-    ptrs = (_take(w, "w", (C,), dtype, dev), _take(mean, "mean", stat, torch.float32, dev), _take(rstd, "rstd", stat, torch.float32, dev),
-            pn, _take(dy, "dy", s.shape, dtype, dev), _take_opt(ds, "ds", s.shape, dtype, dev))
-    _need_cuda(s)
-    dx, dw = torch.empty(s.shape, dtype=dtype, device=dev), torch.empty_like(w)
-    db = torch.empty_like(w) if bias else None
-    ws, pws, nws = _scratch(_norm_bytes(dev.index, B, N, C, groups, code), s)
-    _check(lib().la_norm_bwd(ps, *ptrs, dx.data_ptr(), dw.data_ptr(), db.data_ptr() if bias else None, pws, nws, B, N, C, groups, ld, code,
-                             _stream(None)), "la_norm_bwd")
-    return dx, dw, db
+    return (_front or _load_front()).norm_bwd(s, w, mean, rstd, dy, ds, groups, bias, lengths)
 
 
 def rotary_turns(dim, base=10000.0, factor=1.0, original=None, fast=32.0, slow=1.0, device="cuda"):
@@ -1016,56 +943,18 @@ def rotary_turns(dim, base=10000.0, factor=1.0, original=None, fast=32.0, slow=1
     return torch.tensor(signed, dtype=torch.int64, device=device), 0.1 * math.log(factor) + 1 if original is not None else 1.0
 
 
-def _rotary(q, k, turns, positions, gain, interleaved, head_major, lengths, inplace, inverse):
-    step = q.dim() == 3
-    if q.dim() not in (3, 4) or (step and (head_major or lengths is not None)):
-        raise ValueError("q: 4 dimensions, or 3 (one row a stream, token-major, without lengths)")
-    dtype, dev, code = q.dtype, q.device, _dtype_code(q)
-    _need_ints(q)
-    lead = q.dim() - 2
-    if head_major:
-        B, H, N, D = q.shape
-        kshape = None if k is None else (B, k.shape[1], N, D)
-        pq, lq = _take(q, "q", q.shape, dtype, dev), 0
-        pk, lk = (None, 0) if k is None else (_take(k, "k", kshape, dtype, dev), 0)
-    else:
-        B, H, D = q.shape[0], q.shape[-2], q.shape[-1]
-        N = 1 if step else q.shape[1]
-        kshape = None if k is None else (*q.shape[:lead], k.shape[-2], D)
-        pq, lq = _take_rows(q, "q", q.shape, dtype, dev, lead)
-        pk, lk = (None, 0) if k is None else _take_rows(k, "k", kshape, dtype, dev, lead)
-    Hk = 0 if k is None else kshape[1 if head_major else -2]
-    if turns.dim() != 1:
-        raise ValueError("turns: 1 dimension")
-    pt = _take(turns, "turns", turns.shape, torch.int64, dev)
-    per_row = positions is not None and positions.dim() == 2
-    pp = _take_opt(positions, "positions", (B, N) if per_row else (B,), torch.int32, dev)
-    pn = _take_opt(lengths, "lengths", (B,), torch.int32, dev)
-    if inplace and pq == pk:
-        raise ValueError("inplace: q and k must be different tensors")
-    _need_cuda(q)
-    oq = q if inplace else torch.empty(q.shape, dtype=dtype, device=dev)
-    ok = k if inplace or k is None else torch.empty(kshape, dtype=dtype, device=dev)
-    _check(lib().la_rotary(pq, pk, oq.data_ptr(), None if k is None else ok.data_ptr(), pt, pp, pn, gain, B, N, H, Hk, D,
-                           2 * turns.shape[0], lq, lk, per_row, bool(interleaved), bool(head_major), inverse, code, _stream(None)),
-           "la_rotary")
-    return oq, ok
-
-
-@_on_device
 def rotary_fwd(q, k, turns, positions=None, gain=1.0, interleaved=False, head_major=False, lengths=None, inplace=False):
     """(q', k') with the first 2 len(turns) columns of every head turned by its row's position (rotary_turns gives turns
     and gain).  q [B,N,H,D] and k [B,N,Hk,D] or None (rows may be slices of wider ones), dense [B,H,N,D] with head_major,
     or [B,H,D] for one row a stream; positions: int32 [B] (of each sequence's row 0) or [B,N], None: rows at 0, 1, ...
     Pairs are halves (j, j + R/2), or neighbours with interleaved.  inplace: q and k themselves, rows past a
     sequence's length left as they were."""
-    return _rotary(q, k, turns, positions, gain, interleaved, head_major, lengths, inplace, False)
+    return (_front or _load_front()).rotary(q, k, turns, positions, gain, interleaved, head_major, lengths, inplace, False)
 
 
-@_on_device
 def rotary_bwd(dq, dk, turns, positions=None, gain=1.0, interleaved=False, head_major=False, lengths=None, inplace=False):
     """The gradients of rotary_fwd's inputs from those of its outputs."""
-    return _rotary(dq, dk, turns, positions, gain, interleaved, head_major, lengths, inplace, True)
+    return (_front or _load_front()).rotary(dq, dk, turns, positions, gain, interleaved, head_major, lengths, inplace, True)
 
 
 _CODES = {torch.int8: LA_CODE_I8, torch.float8_e4m3fn: LA_CODE_E4M3}
@@ -1077,49 +966,19 @@ def _code_of(dtype):
     return _CODES[dtype]
 
 
-@_on_device
 def state_pack(S, code=torch.int8):
     """(codes, scale): a state S [B,H,D,M] (float32) in 8 bits (int8 or float8_e4m3fn) with one fp32 scale [B,H,D] a row."""
-    if S.dim() != 4:
-        raise ValueError("S: 4 dimensions")
-    B, H, D, M = S.shape
-    fmt, dev = _code_of(code), S.device
-    p = _take(S, "S", S.shape, torch.float32, dev)
-    _need_cuda(S)
-    codes, scale = torch.empty((B, H, D, M), dtype=code, device=dev), torch.empty((B, H, D), dtype=torch.float32, device=dev)
-    _check(lib().la_state_pack(p, codes.data_ptr(), scale.data_ptr(), B, H, D, M, fmt, _stream(None)), "la_state_pack")
-    return codes, scale
+    return (_front or _load_front()).state_pack(S, _code_of(code))
 
 
-@_on_device
 def state_unpack(codes, scale):
     """The state [B,H,D,M] (float32) that state_pack's codes and scale stand for."""
-    if codes.dim() != 4:
-        raise ValueError("codes: 4 dimensions")
-    B, H, D, M = codes.shape
-    fmt, dev = _code_of(codes.dtype), codes.device
-    ptrs = _take(codes, "codes", codes.shape, codes.dtype, dev), _take(scale, "scale", (B, H, D), torch.float32, dev)
-    _need_cuda(codes)
-    S = torch.empty((B, H, D, M), dtype=torch.float32, device=dev)
-    _check(lib().la_state_unpack(*ptrs, S.data_ptr(), B, H, D, M, fmt, _stream(None)), "la_state_unpack")
-    return S
+    return (_front or _load_front()).state_unpack(codes, scale)
 
 
-@_on_device
 def cross_step_packed(q, codes, scale, Z):
     """cross_step from an S that state_pack has put into 8 bits: q [B,H,D], codes [B,Hk,D,M], scale and Z [B,Hk,D]."""
-    if q.dim() != 3 or codes.dim() != 4:
-        raise ValueError("q: 3 dimensions, codes: 4")
-    B, H, D = q.shape
-    Hk, M = codes.shape[1], codes.shape[3]
-    _need_ints(q, codes)
-    code, fmt, dtype, dev = _dtype_code(q), _code_of(codes.dtype), q.dtype, q.device
-    ptrs = (_take(q, "q", q.shape, dtype, dev), _take(codes, "codes", (B, Hk, D, M), codes.dtype, dev),
-            _take(scale, "scale", (B, Hk, D), torch.float32, dev), _take(Z, "Z", (B, Hk, D), torch.float32, dev))
-    _need_cuda(q)
-    y = torch.empty((B, H, M), dtype=dtype, device=dev)
-    _check(lib().la_cross_step_packed(*ptrs, y.data_ptr(), B, H, Hk, D, M, fmt, code, _stream(None)), "la_cross_step_packed")
-    return y
+    return (_front or _load_front()).cross_step_packed(q, codes, scale, Z)
 
 
 class _Causal(torch.autograd.Function):

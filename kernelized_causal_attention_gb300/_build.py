@@ -1,7 +1,9 @@
-"""Builds the CUDA library in-tree: kernelized_causal_attention_gb300/_lib/liblinattn.so.
+"""Builds the CUDA library in-tree: kernelized_causal_attention_gb300/_lib/liblinattn.so, and
+beside it _front.so, the compiled calls from torch tensors to it.
 
 Every translation unit is compiled for sm_103a only (GB300), in parallel, then
-linked into one shared library with the static CUDA runtime.  Run directly
+linked into one shared library with the static CUDA runtime; _front.so is host
+code against the headers of Python and torch.  Run directly
 (python -m kernelized_causal_attention_gb300._build) or through
 __graft_entry__.build().
 """
@@ -12,15 +14,18 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "_lib")
 LIB = os.path.join(LIBDIR, "liblinattn.so")
+FRONT = os.path.join(LIBDIR, "_front.so")
+INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
-              "-I", os.path.join(os.path.dirname(HERE), "include")]
+              "-I", INCLUDE]
 
 
 def nvcc() -> str:
@@ -36,26 +41,56 @@ def sources():
 
 def _deps():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
-        + [os.path.join(os.path.dirname(HERE), "include", "linattn.h"), __file__]
+        + [os.path.join(CSRC, "front.cpp"), os.path.join(os.path.dirname(HERE), "include", "linattn.h"), __file__]
 
 
 MANIFEST = os.path.join(LIBDIR, "sources.txt")
 
 
 def _manifest() -> str:
-    return "\n".join(os.path.basename(f) for f in sources())
+    import torch
+    return "\n".join([*(os.path.basename(f) for f in sources()), f"torch {torch.__version__}"])
 
 
 def up_to_date() -> bool:
-    """The library exists, was built from the current set of sources (an
-    added or removed file forces a rebuild) and is newer than every input."""
-    if not os.path.exists(LIB) or not os.path.exists(MANIFEST):
+    """Both libraries exist, were built from the current set of sources (an
+    added or removed file, or another torch, forces a rebuild) and are newer
+    than every input."""
+    if not all(os.path.exists(f) for f in (LIB, FRONT, MANIFEST)):
         return False
     with open(MANIFEST) as f:
         if f.read() != _manifest():
             return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(FRONT))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _front_obj(cuda_home: str) -> str:
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(LIBDIR, "front.o")
+    dirs = [INCLUDE, root, os.path.join(root, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
+            os.path.join(cuda_home, "include")]
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in dirs), "-c",
+          os.path.join(CSRC, "front.cpp"), "-o", obj], "front.cpp")
+    return obj
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed on {what}:\n{r.stderr}")
+    return r.stderr
+
+
+def _link_front(obj: str) -> None:
+    import torch
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = FRONT + f".tmp{os.getpid()}"
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{LIBDIR}", "-l:liblinattn.so", "-Wl,-rpath,$ORIGIN",
+          f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], "_front.so")
+    os.replace(tmp, FRONT)
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
@@ -67,22 +102,19 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
 
     def compile_one(src):
         obj = os.path.join(LIBDIR, os.path.basename(src)[:-3] + ".o")
-        cmd = [cc, *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stderr}")
-        if verbose and r.stderr:
-            sys.stderr.write(r.stderr)
+        err = _run([cc, *ARCH, *NVCC_FLAGS, *extra, "-c", src, "-o", obj], src)
+        if verbose and err:
+            sys.stderr.write(err)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(sources()), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(sources()) + 1, os.cpu_count() or 1))) as ex:
+        front = ex.submit(_front_obj, os.path.dirname(os.path.dirname(os.path.realpath(cc))))
         objs = list(ex.map(compile_one, sources()))
+        front = front.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stderr}")
+    _run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], "the library")
     os.replace(tmp, LIB)
+    _link_front(front)
     with open(MANIFEST, "w") as f:
         f.write(_manifest())
     return LIB
