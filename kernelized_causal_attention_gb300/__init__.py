@@ -22,7 +22,8 @@ Convenience wrappers that allocate outputs with torch: ``causal_fwd``,
 ``causal_fwd_poly``, ``causal_bwd_poly``, ``short_conv_fwd``, ``short_conv_bwd``, ``short_conv_step``,
 ``scan_fwd``, ``scan_bwd``, ``scan_step``, ``cross_fwd``, ``cross_bwd``, ``cross_step``, ``gated_fwd``, ``gated_bwd``,
 ``gated_step``, ``norm_fwd``, ``norm_bwd``, ``rotary_turns``, ``rotary_fwd``, ``rotary_bwd``, ``state_pack``, ``state_unpack``,
-``cross_step_packed`` and the autograd functions ``causal_linear_attention`` / ``noncausal_linear_attention`` /
+``cross_step_packed`` (the calls from ``gated_fwd`` on through ``_lib/_front.so``, which does in C++ what the others
+do here) and the autograd functions ``causal_linear_attention`` / ``noncausal_linear_attention`` /
 ``short_conv`` / ``selective_scan`` / ``cross_linear_attention`` / ``gated_recurrence`` / ``layer_norm`` / ``rotary``.
 
 The method is Katharopoulos et al., "Transformers are RNNs" (part 2/3):
@@ -894,6 +895,8 @@ def cross_step(q, S, Z):
 
 
 # ----------------------------- around the recurrent layer: gated recurrence, norm, positions, packed states
+#
+# Shapes, types and devices are checked and outputs allocated in csrc/front.cpp, every argument by its place.
 
 def gated_fwd(x, r, i, lam, h=None, scale=8.0, lengths=None, keep=False):
     """y [B,N,C] of the gated recurrence h_n = a_n h_{n-1} + sqrt(1 - a_n^2) sigmoid(i_n) x_n,
