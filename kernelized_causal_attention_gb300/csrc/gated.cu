@@ -363,7 +363,8 @@ __device__ __forceinline__ u64 look_up(Shared<WINDOW>& sh, const Chain& ch, long
 
 // A call's words to EMPTY, and the channels' rates.
 template <typename T>
-__global__ void __launch_bounds__(256) k_gated_start(const Chain ch, long n, float* rate, const T* __restrict__ lam, float scale, int C, int padded) {
+__global__ void __launch_bounds__(256) k_gated_start(const Chain ch, long n, float* rate, const T* lam, float scale, int C, int padded) {
+  tcc::grid_dep_wait();  // before letting the next kernel start: that one asks for its rows before it waits for this
   tcc::grid_dep_launch();
   const long e = (long)blockIdx.x * 256 + threadIdx.x, step = (long)gridDim.x * 256;
   for (long i = e; i < n * 48; i += step) reinterpret_cast<ulonglong2*>(ch.word)[i] = make_ulonglong2(EMPTY, EMPTY);
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS)
 
 // dlam from the [n][C] sums of Q: 32 channels a block, 32 rows at a time, in a fixed order.
 template <typename T>
-__global__ void __launch_bounds__(1024) k_gated_lam(const float* __restrict__ sums, const T* __restrict__ lam, T* __restrict__ dlam, long n, int C) {
+__global__ void __launch_bounds__(1024) k_gated_lam(const float* sums, const T* lam, T* dlam, long n, int C) {
   __shared__ float red[32][33];
   grid_dep_enter();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
@@ -689,7 +690,8 @@ __global__ void __launch_bounds__(1024) k_gated_lam(const float* __restrict__ su
 
 // One row a stream: h <- a h + beta g x, y = h.
 template <typename T, bool PAIR>
-__global__ void __launch_bounds__(256) k_gated_step(const Rows a, float* __restrict__ h, T* __restrict__ y) {
+__global__ void __launch_bounds__(256) k_gated_step(const Rows a, float* h, T* y) {
+  grid_dep_enter();
   using R = typename Raw<T>::type;
   const long b = blockIdx.x / a.groups;  // groups of 512 channels here
   const int c = 2 * ((blockIdx.x % a.groups) * 256 + threadIdx.x), n = a.C - c;
@@ -739,8 +741,8 @@ cudaError_t chain(Chain& ch, Rows& a, char* ws, size_t n, const GatedShape& s, c
   ch.err = status_word();
   const size_t most = std::max(48 * n, padded(s));
   const unsigned grid = static_cast<unsigned>(std::min<size_t>((most + 255) / 256, 8 * sm_count()));
-  k_gated_start<T><<<grid, 256, 0, st>>>(ch, static_cast<long>(n), rate, (const T*)a.lam, s.scale, s.C, static_cast<int>(padded(s)));
-  return cudaGetLastError();
+  return launch_pdl(k_gated_start<T>, dim3(grid), dim3(256), 0, st, ch, static_cast<long>(n), rate, (const T*)a.lam, s.scale, s.C,
+                    static_cast<int>(padded(s)));
 }
 
 // A kernel's dynamic shared memory, said once a device, and how many of its blocks an SM
@@ -830,8 +832,7 @@ cudaError_t bwd(Rows a, const float* kept, const void* dy, void* dx, void* dr, v
 template <typename T, bool PAIR>
 cudaError_t step(Rows a, float* h, void* y, const GatedShape& s, cudaStream_t st) {
   a.groups = (s.C + 511) / 512;
-  k_gated_step<T, PAIR><<<a.groups * s.B, 256, 0, st>>>(a, h, (T*)y);
-  return cudaGetLastError();
+  return launch_pdl(k_gated_step<T, PAIR>, dim3(a.groups * s.B), dim3(256), 0, st, a, h, (T*)y);
 }
 
 }  // namespace

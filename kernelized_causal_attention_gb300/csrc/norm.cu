@@ -144,6 +144,7 @@ struct NormArgs {
 // of columns is at (k TPR + lane) V.
 template <typename T, int V, int K, int TPR, int R>
 __global__ void __launch_bounds__(THREADS<TPR>) k_norm_fwd(const NormArgs a) {
+  grid_dep_enter();
   using Raw = typename Vec<T, V>::Raw;
   constexpr int PER = THREADS<TPR> / TPR, P = (V + 1) / 2;
   __shared__ float red[2][R][TPR > 32 ? TPR / 32 : 1];
@@ -263,6 +264,7 @@ inline __host__ __device__ int distinct(int per, int G) { return per % G == 0 ? 
 // Items as forward, R at a time until there are no more.
 template <typename T, int V, int K, int TPR, int R>
 __global__ void __launch_bounds__(THREADS<TPR>, (THREADS<TPR> < 512 ? 512 / THREADS<TPR> : 1)) k_norm_bwd(const GradArgs a) {
+  grid_dep_enter();
   using Raw = typename Vec<T, V>::Raw;
   constexpr int PER = THREADS<TPR> / TPR, P = (V + 1) / 2;
   __shared__ float red[2][2 * R][TPR > 32 ? TPR / 32 : 1];
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(THREADS<TPR>, (THREADS<TPR> < 512 ? 512 / THRE
 
 // dw and db: column c of the [P][C] partial sums, 32 columns a block, 32 rows at a time.
 template <typename T>
-__global__ void __launch_bounds__(1024) k_norm_join(const float* __restrict__ part, T* __restrict__ dw, T* __restrict__ db, long P, int C) {
+__global__ void __launch_bounds__(1024) k_norm_join(const float* part, T* dw, T* db, long P, int C) {
   __shared__ float red[32][33];
   grid_dep_enter();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + tx;
@@ -489,8 +491,7 @@ struct Forward {
     constexpr int PER = THREADS<TPR> / TPR;
     const long blocks = in_units((a.at.items + R * PER - 1) / (R * PER), a.at.groups.d, PER);
     a.slots = blocks * PER;
-    k_norm_fwd<T, V, K, TPR, R><<<static_cast<unsigned>(blocks), THREADS<TPR>, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(k_norm_fwd<T, V, K, TPR, R>, dim3(static_cast<unsigned>(blocks)), dim3(THREADS<TPR>), 0, st, a);
   }
 };
 
@@ -510,7 +511,8 @@ struct Backward {
     const int G = a.at.groups.d, C = G * a.M;
     const long blocks = blocks_of(a.at.items, G, PER, NT);
     a.slots = blocks * PER;
-    k_norm_bwd<T, V, K, TPR, R><<<static_cast<unsigned>(blocks), NT, 0, st>>>(a);
+    const cudaError_t e = launch_pdl(k_norm_bwd<T, V, K, TPR, R>, dim3(static_cast<unsigned>(blocks)), dim3(NT), 0, st, a);
+    if (e != cudaSuccess) return e;
     return launch_pdl(k_norm_join<T>, dim3((C + 31) / 32, 2), dim3(1024), 0, st, (const float*)a.part, (T*)dw, (T*)db,
                       blocks * distinct(PER, G) / G, C);
   }

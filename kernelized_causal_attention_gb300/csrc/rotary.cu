@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "launch.h"
 #include "pair.cuh"
+#include "scan.cuh"
 
 namespace la {
 namespace {
@@ -107,6 +108,7 @@ constexpr int BATCH = 4;  // heads whose loads are on their way together
 // sizes and strides, its units past R being one value.
 template <typename T, int V, bool INTER>
 __global__ void __launch_bounds__(V == 1 ? 1024 : 256) k_rotary(const Turn a, int units, int rb) {
+  grid_dep_enter();
   const int u = threadIdx.x % units, rl = threadIdx.x / units;
   const long row = (long)blockIdx.x * rb + rl;
   if (rl >= rb || row >= a.rows) return;
@@ -230,8 +232,7 @@ cudaError_t launch(Turn& a, bool inter, cudaStream_t st) {
   const long groups = std::max(1l, std::min<long>(all, 3l * sm_count() / blocks));
   a.per = std::min(8, static_cast<int>((all + groups - 1) / groups));
   const dim3 grid(static_cast<unsigned>(blocks), (all + a.per - 1) / a.per);
-  inter ? k_rotary<T, V, true><<<grid, threads, 0, st>>>(a, units, rb) : k_rotary<T, V, false><<<grid, threads, 0, st>>>(a, units, rb);
-  return cudaGetLastError();
+  return launch_pdl(inter ? k_rotary<T, V, true> : k_rotary<T, V, false>, grid, dim3(threads), 0, st, a, units, rb);
 }
 
 // Rows, heads and strides in whole runs of V values, aligned.

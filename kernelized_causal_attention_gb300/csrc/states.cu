@@ -12,6 +12,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "scan.cuh"
 
 namespace la {
 namespace {
@@ -58,7 +59,8 @@ __device__ __forceinline__ void decode4(uint32_t u, float* f) {
 // ordered as unsigned numbers with NaN above infinity, so their maximum also says
 // whether the row is finite: if not, its scale is NaN.
 template <int M, bool E4M3>
-__global__ void __launch_bounds__(256) k_pack(const float4* __restrict__ S, uint32_t* __restrict__ code, float* __restrict__ scale, long n) {
+__global__ void __launch_bounds__(256) k_pack(const float4* S, uint32_t* code, float* scale, long n) {
+  grid_dep_enter();
   constexpr int L = M / 4;
   const long e = (long)blockIdx.x * 256 + threadIdx.x;
   const float4 v = e < n ? S[e] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -73,7 +75,8 @@ __global__ void __launch_bounds__(256) k_pack(const float4* __restrict__ S, uint
 }
 
 template <int M, bool E4M3>
-__global__ void __launch_bounds__(256) k_unpack(const uint32_t* __restrict__ code, const float* __restrict__ scale, float4* __restrict__ S, long n) {
+__global__ void __launch_bounds__(256) k_unpack(const uint32_t* code, const float* scale, float4* S, long n) {
+  grid_dep_enter();
   const long e = (long)blockIdx.x * 256 + threadIdx.x;
   if (e >= n) return;
   float f[4];
@@ -87,8 +90,8 @@ __global__ void __launch_bounds__(256) k_unpack(const uint32_t* __restrict__ cod
 // joined by halving: each exchange adds the half of the columns that the partner keeps.
 template <int D, int M, bool E4M3, typename T>
 __global__ void __launch_bounds__(128)
-    k_step_packed(const T* __restrict__ q, const uint4* __restrict__ code, const float* __restrict__ scale, const float* __restrict__ Z,
-                  T* __restrict__ y, int per, long heads) {
+    k_step_packed(const T* q, const uint4* code, const float* scale, const float* Z, T* y, int per, long heads) {
+  grid_dep_enter();
   constexpr int L = M / 16, RS = 32 / L, K = (D + RS - 1) / RS, W = (D + 31) / 32;
   const int lane = threadIdx.x & 31, c = lane % L, r0 = lane / L;
   const long bhk = (long)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -161,30 +164,23 @@ __global__ void __launch_bounds__(128)
 
 template <int M>
 cudaError_t pack(const float* S, void* code, float* scale, long n, int fmt, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>((n + 255) / 256);
-  if (fmt == 0)
-    k_pack<M, false><<<grid, 256, 0, st>>>((const float4*)S, (uint32_t*)code, scale, n);
-  else
-    k_pack<M, true><<<grid, 256, 0, st>>>((const float4*)S, (uint32_t*)code, scale, n);
-  return cudaGetLastError();
+  return launch_pdl(fmt == 0 ? k_pack<M, false> : k_pack<M, true>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, st,
+                    (const float4*)S, (uint32_t*)code, scale, n);
 }
 
 template <int M>
 cudaError_t unpack(const void* code, const float* scale, float* S, long n, int fmt, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>((n + 255) / 256);
-  if (fmt == 0)
-    k_unpack<M, false><<<grid, 256, 0, st>>>((const uint32_t*)code, scale, (float4*)S, n);
-  else
-    k_unpack<M, true><<<grid, 256, 0, st>>>((const uint32_t*)code, scale, (float4*)S, n);
-  return cudaGetLastError();
+  return launch_pdl(fmt == 0 ? k_unpack<M, false> : k_unpack<M, true>, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, st,
+                    (const uint32_t*)code, scale, (float4*)S, n);
 }
 
 template <bool E4M3, typename T>
 cudaError_t step(const void* q, const void* code, const float* scale, const float* Z, void* y, const CrossShape& s, cudaStream_t st) {
   const long heads = (long)s.B * s.Hk;
-  LA_DISPATCH_DM(s.D, s.M, (k_step_packed<D_, M_, E4M3, T><<<static_cast<unsigned>((heads + 3) / 4), 128, 0, st>>>(
-                               (const T*)q, (const uint4*)code, scale, Z, (T*)y, s.H / s.Hk, heads)));
-  return cudaGetLastError();
+  cudaError_t e = cudaErrorInvalidValue;
+  LA_DISPATCH_DM(s.D, s.M, (e = launch_pdl(k_step_packed<D_, M_, E4M3, T>, dim3(static_cast<unsigned>((heads + 3) / 4)), dim3(128), 0, st,
+                                           (const T*)q, (const uint4*)code, scale, Z, (T*)y, s.H / s.Hk, heads)));
+  return e;
 }
 
 }  // namespace
