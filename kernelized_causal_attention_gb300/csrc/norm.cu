@@ -72,12 +72,17 @@ __device__ __forceinline__ void set(T* p, const typename Vec<T, V>::Raw& v) {
   *reinterpret_cast<typename Vec<T, V>::Raw*>(p) = v;
 }
 
-// Values read again are opened again from their raw form, which takes fewer registers:
-// this keeps the compiler from holding the opened ones.
-__device__ __forceinline__ void again(uint4& v) { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
-__device__ __forceinline__ void again(float4& v) { asm volatile("" : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w)); }
-__device__ __forceinline__ void again(float& v) { asm volatile("" : "+f"(v)); }
-__device__ __forceinline__ void again(bf16& v) { asm volatile("" : "+h"(reinterpret_cast<unsigned short&>(v))); }
+// A vector (V = 1: a value) into a thread's own place in shared memory, zero without `some`:
+// an asynchronous copy of 16 or 4 bytes, or a load and a store.
+template <typename Raw, typename T>
+__device__ __forceinline__ void fetch(Raw& to, const T* from, bool some) {
+  if constexpr (sizeof(Raw) == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(&to)), "l"(from), "r"(some ? 16 : 0) : "memory");
+  else if constexpr (sizeof(Raw) == 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(tc::smem_u32(&to)), "l"(from), "r"(some ? 4 : 0) : "memory");
+  else
+    to = some ? *from : Raw{};
+}
 
 // A group of more than a warp is a block of its own.
 template <int TPR>
@@ -261,7 +266,11 @@ struct GradArgs {
 // divides them, of the G groups, added up over the slots that share one.
 inline __host__ __device__ int distinct(int per, int G) { return per % G == 0 ? G : per; }
 
-// Items as forward, R at a time until there are no more.
+// Items as forward, R at a time until there are no more.  The next ones are on their way
+// into shared memory (a thread's own places, so it waits for its own copies only) while R
+// are worked on, and are read from there twice: 48.3 us both ways for 4 x 2048 x 2048 bf16
+// with a residual, 54.5 with registers for them and loads that wait, 34.9 and 38.3 for 32
+// groups of 64.  Two items at once 50.1 and 37.1, four spill.
 template <typename T, int V, int K, int TPR, int R>
 __global__ void __launch_bounds__(THREADS<TPR>, (THREADS<TPR> < 512 ? 512 / THREADS<TPR> : 1)) k_norm_bwd(const GradArgs a) {
   grid_dep_enter();
@@ -283,39 +292,54 @@ __global__ void __launch_bounds__(THREADS<TPR>, (THREADS<TPR> < 512 ? 512 / THRE
 #pragma unroll
     for (int i = 0; i < P; ++i) dw[k][i] = db[k][i] = 0ull;
   }
-  for (long base = slot; base - slot < a.at.items; base += R * a.slots) {  // the same steps for all threads: they meet in the sums
-    bool in[R], live[R];
-    float mean[R], rstd[R];
-    Raw sr[R][K], dr[R][K], er[R][K];
+  extern __shared__ __align__(16) unsigned char room[];
+  auto own_slot = [&](int stage, int t, int r, int k) -> Raw& {
+    return reinterpret_cast<Raw*>(room)[(((stage * 3 + t) * R + r) * K + k) * THREADS<TPR> + threadIdx.x];
+  };
+  bool in[R];
+  float mean[R], rstd[R];
+  auto request = [&](long base, int stage) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const long item = base + r * a.slots, at = item * a.M;
+      bool live;
       uint32_t row, g;
-      a.at.of(item, in[r], live[r], row, g);
-      const T* s = static_cast<const T*>(a.s) + row * a.lds + own * a.M;
-      mean[r] = live[r] ? a.mean[item] : 0.f, rstd[r] = live[r] ? a.rstd[item] : 0.f;
+      a.at.of(base + r * a.slots, in[r], live, row, g);
+      const long item = in[r] ? base + r * a.slots : 0;
+      const T *p[3] = {static_cast<const T*>(a.s) + row * a.lds + own * a.M, static_cast<const T*>(a.dy) + item * a.M,
+                       static_cast<const T*>(a.ds) + item * a.M};
+      mean[r] = live ? a.mean[item] : 0.f, rstd[r] = live ? a.rstd[item] : 0.f;
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int c = (k * TPR + lane) * V;
-        sr[r][k] = dr[r][k] = er[r][k] = Raw{};
-        if (live[r] && c < a.M) {
-          sr[r][k] = get<T, V>(s + c);
-          dr[r][k] = get<T, V>(static_cast<const T*>(a.dy) + at + c);
-          if (a.ds != nullptr) er[r][k] = get<T, V>(static_cast<const T*>(a.ds) + at + c);
-        }
+        const bool some = live && c < a.M;
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+          if (t < 2 || a.ds != nullptr) fetch(own_slot(stage, t, r, k), some ? p[t] + c : p[t], some);
       }
     }
+  };
+  request(slot, 0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  int stage = 0;
+  for (long base = slot; base - slot < a.at.items; base += R * a.slots, stage ^= 1) {  // the same steps for all threads: they meet in the sums
+    bool now[R];
+    float off_[R], scale_[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) now[r] = in[r], off_[r] = -mean[r], scale_[r] = rstd[r];
+    if (base + R * a.slots - slot < a.at.items) request(base + R * a.slots, stage ^ 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");  // all but the group just made
     // rows that are not live hold zeros, and rstd zero: they add nothing, and dx is zero
     float v[2 * R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       u64 t1 = 0ull, t2 = 0ull;
-      const u64 off = two(-mean[r]), scale = two(rstd[r]);
+      const u64 off = two(off_[r]), scale = two(scale_[r]);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         u64 f[P], d[P];
-        Vec<T, V>::open(sr[r][k], f);
-        Vec<T, V>::open(dr[r][k], d);
+        Vec<T, V>::open(own_slot(stage, 0, r, k), f);
+        Vec<T, V>::open(own_slot(stage, 1, r, k), d);
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           f[i] = mul2(add2(f[i], off), scale);
@@ -332,18 +356,17 @@ __global__ void __launch_bounds__(THREADS<TPR>, (THREADS<TPR> < 512 ? 512 / THRE
     sum(v);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (!in[r]) continue;
-      const u64 s1 = two(-v[2 * r] * a.inv), s2 = two(-v[2 * r + 1] * a.inv), off = two(-mean[r]), scale = two(rstd[r]);
+      if (!now[r]) continue;
+      const u64 s1 = two(-v[2 * r] * a.inv), s2 = two(-v[2 * r + 1] * a.inv), off = two(off_[r]), scale = two(scale_[r]);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int c = (k * TPR + lane) * V;
         if (c >= a.M) continue;
         u64 f[P], d[P], e[P];
-        again(sr[r][k]), again(dr[r][k]);
-        Vec<T, V>::open(sr[r][k], f);
-        Vec<T, V>::open(dr[r][k], d);
+        Vec<T, V>::open(own_slot(stage, 0, r, k), f);
+        Vec<T, V>::open(own_slot(stage, 1, r, k), d);
         if (a.ds != nullptr) {
-          Vec<T, V>::open(er[r][k], e);
+          Vec<T, V>::open(own_slot(stage, 2, r, k), e);
         } else {
 #pragma unroll
           for (int i = 0; i < P; ++i) e[i] = 0ull;
@@ -419,11 +442,10 @@ __global__ void __launch_bounds__(1024) k_norm_join(const float* part, T* dw, T*
   }
 }
 
-// How a group is held: f.run<V, K, TPR, R>() of the first shape that covers M.  Both
-// directions of 4 x 2048 x 2048 bf16 with a residual took 55 us with three groups at once
-// backward and four vectors a thread forward (67 with four groups, which spill, 60 with
-// two on more threads; 58 with one vector a thread forward); 32 groups of 64 took 38
-// (43 with four at once, 41 with two).
+// How a group is held: f.run<V, K, TPR, R>() of the first shape that covers M.  Forward,
+// both directions of 4 x 2048 x 2048 bf16 with a residual took 3 us more with one vector a
+// thread than with two; 32 groups of 64 took 3 to 5 us more with two or four at once than
+// with three.
 #define LA_NORM_SHAPE(VV, KK, TT, RR) \
   if (M <= (VV) * (KK) * (TT)) return f.template run<VV, KK, TT, RR>();
 template <typename T, typename F>
@@ -511,8 +533,10 @@ struct Backward {
     const int G = a.at.groups.d, C = G * a.M;
     const long blocks = blocks_of(a.at.items, G, PER, NT);
     a.slots = blocks * PER;
-    const cudaError_t e = launch_pdl(k_norm_bwd<T, V, K, TPR, R>, dim3(static_cast<unsigned>(blocks)), dim3(NT), 0, st, a);
+    constexpr int room = 2 * 3 * R * K * NT * V * static_cast<int>(sizeof(T));
+    cudaError_t e = cudaFuncSetAttribute(k_norm_bwd<T, V, K, TPR, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, room);
     if (e != cudaSuccess) return e;
+    if ((e = launch_pdl(k_norm_bwd<T, V, K, TPR, R>, dim3(static_cast<unsigned>(blocks)), dim3(NT), room, st, a)) != cudaSuccess) return e;
     return launch_pdl(k_norm_join<T>, dim3((C + 31) / 32, 2), dim3(1024), 0, st, (const float*)a.part, (T*)dw, (T*)db,
                       blocks * distinct(PER, G) / G, C);
   }
