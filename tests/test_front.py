@@ -1,6 +1,8 @@
 """The compiled allocating calls: what they refuse before a device is touched, that they hold no
 references, and calls from several threads at once."""
 import gc
+import os
+import subprocess
 import sys
 import threading
 
@@ -170,3 +172,111 @@ def test_threads(cuda, linattn):
     for a, b in zip(want, got):
         assert all(torch.equal(p, q) for p, q in zip(a, b))
     linattn.check_device_status()
+
+
+def around(la, x, w, turns, h, Z):
+    """Every kind of call behind x, a tensor that another stream writes."""
+    y, s, mean, rstd = la.norm_fwd(x, w, w, x)
+    z, kept = la.gated_fwd(x, y, s, w, keep=True)
+    state = h.clone()
+    codes, scale = la.state_pack(x[:, :64, :64].reshape(2, 1, 64, 64).contiguous())
+    q = x[:, 0].reshape(2, 10, 64).contiguous()
+    return [y, *la.norm_bwd(x, w, mean, rstd, y), z, *la.gated_bwd(x, y, s, w, kept, x), la.gated_step(x[:, 1], y[:, 1], s[:, 1], w, state), state,
+            la.rotary_fwd(x.view(2, 300, 10, 64), None, turns)[0], la.state_unpack(codes, scale), la.cross_step_packed(q, codes, scale, Z)]
+
+
+def late(x, y):
+    """y into x at the end of some hundred microseconds of work."""
+    t = torch.randn(2048, 2048, device=x.device)
+    for _ in range(20):
+        t = t @ t * 1e-3
+    x.copy_(y + 0 * t.nan_to_num().clamp(-1, 1)[0, 0])
+
+
+@pytest.fixture(scope="module")
+def behind(cuda, linattn):
+    g = torch.Generator().manual_seed(6)
+    y = [torch.randn(2, 300, 640, generator=g).to(cuda) for _ in range(3)]
+    turns, _ = linattn.rotary_turns(32, device=cuda)
+    rest = torch.randn(640, generator=g).to(cuda), turns, torch.randn(2, 640, generator=g).to(cuda), torch.rand(2, 1, 64, generator=g).to(cuda)
+    want = [around(linattn, t, *rest) for t in y]
+    torch.cuda.synchronize()
+    return y, rest, want
+
+
+@pytest.mark.gpu
+def test_behind_another_stream(cuda, linattn, behind):
+    """Calls that wait for another stream's event read what it wrote, not what was there."""
+    y, rest, want = behind
+    x, side = torch.zeros_like(y[0]), torch.cuda.Stream()
+    for t, expect in zip(y, want):
+        for first in range(5):
+            x.zero_()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                late(x, t)
+            linattn.norm_fwd(y[0], rest[0])  # a kernel of the same stream just before the wait
+            torch.cuda.current_stream().wait_stream(side)
+            calls_ = [lambda: linattn.rotary_fwd(x.view(2, 300, 10, 64), None, rest[1])[0], lambda: linattn.norm_fwd(x, rest[0], rest[0], x)[0],
+                      lambda: linattn.gated_fwd(x, x, x, rest[0]), lambda: linattn.gated_step(x[:, 1], x[:, 1], x[:, 1], rest[0], rest[2].clone()),
+                      lambda: linattn.state_pack(x.view(1, 375, 16, 64))[0]]
+            got = calls_[first]()  # each as the first behind the wait
+            rest_of = around(linattn, x, *rest)
+            torch.cuda.synchronize()
+            assert torch.equal(got, calls_[first]())
+            assert all(torch.equal(a, b) for a, b in zip(rest_of, expect))
+
+
+@pytest.mark.gpu
+def test_captured_behind_another_stream(cuda, linattn, behind):
+    """The same in a graph that forks and joins."""
+    y, rest, want = behind
+    x, source, side, main = torch.zeros_like(y[0]), y[0].clone(), torch.cuda.Stream(), torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        late(x, source)
+        around(linattn, x, *rest)
+    main.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            late(x, source)
+        linattn.norm_fwd(y[0], rest[0])
+        main.wait_stream(side)
+        got = around(linattn, x, *rest)
+    for _ in range(3):
+        for t, expect in zip(y, want):
+            x.zero_()
+            source.copy_(t)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, expect))
+    linattn.check_device_status()
+
+
+FIRST = """
+import torch
+import kernelized_causal_attention_gb300 as la
+g = torch.Generator().manual_seed(1)
+x, w = torch.randn(2, 300, 640, generator=g).cuda(), torch.randn(640, generator=g).cuda()
+def run():
+    y, s, mean, rstd = la.norm_fwd(x, w, w)
+    z, kept = la.gated_fwd(x, y, x, w, keep=True)
+    return [y, z, *la.gated_bwd(x, y, x, w, kept, x), *la.norm_bwd(x, w, mean, rstd, y)]
+graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(graph, stream=s):
+    got = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, run()))
+la.check_device_status()
+"""
+
+
+@pytest.mark.gpu
+def test_first_call_is_captured(cuda, linattn):
+    """A process whose first calls are captured."""
+    r = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr
