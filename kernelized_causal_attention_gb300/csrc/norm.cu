@@ -11,9 +11,9 @@
 // and all sums are fp32.  Backward, blocks walk rows at a stride that keeps a thread on
 // the same columns, whose sums dw and db it holds in registers; a second kernel adds the
 // blocks' sums up in a fixed order.  4 x 2048 x 2048 bf16 behind a residual sum: forward
-// 19 us (134 MB, the copy rate), gradients 33 and 3 for the join (134 MB, 0.55); 32 groups
-// of 64: 13.8 (67 MB, 0.72) and 22.6 (101 MB, 0.66): issue at 70 and 50 %, with 24 to 44 %
-// of the warps for the registers that hold the groups.
+// 20 us (134 MB, the copy rate), gradients 28 with cold caches (134 MB, 0.71) and 3 for the
+// join; 32 groups of 64: 13.8 (67 MB, 0.72) and 20 (101 MB, 0.74): issue at 69 and 57 %,
+// with 22 to 44 % of the warps for the registers that hold the groups.
 #include <algorithm>
 #include <numeric>
 
