@@ -461,7 +461,9 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS)
           put(word + 64, fma2(A, s, H));
         }
       }
-      for (int i = 0; i < w; ++i) s = fma2(sh.A[stage][i][lane], s, sh.H[stage][i][lane]);
+#pragma unroll  // as many loads at once for every warp: 1 % of both directions
+      for (int i = 0; i < WARPS - 1; ++i)
+        if (i < w) s = fma2(sh.A[stage][i][lane], s, sh.H[stage][i][lane]);
       float* to = kept == nullptr ? nullptr : kept + ((long)job.b * ((a.N + KEEP - 1) / KEEP) + t0 / KEEP) * a.C + c;
       if (to != nullptr && t0 % KEEP == 0 && t0 < a.N) scatter(to, n, s);
       if (full) {
@@ -603,8 +605,11 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS)
         if (job.tile < last) X = look_up(sh, ch, entry + cols, cols, last - job.tile, 92);
         if (w == WARPS - 1 && job.tile > 0) put(word + 64, fma2(A, X, Y));
       }
-      for (int i = 0; i < w; ++i) s = fma2(sh.A[half][i][lane], s, sh.H[half][i][lane]);
-      for (int i = WARPS - 1; i > w; --i) X = fma2(sh.A[half][i][lane], X, sY[half][i][lane]);
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) {
+        if (i < w) s = fma2(sh.A[half][i][lane], s, sh.H[half][i][lane]);
+        if (WARPS - 1 - i > w) X = fma2(sh.A[half][WARPS - 1 - i][lane], X, sY[half][WARPS - 1 - i][lane]);
+      }
 #pragma unroll
       for (int j = 0; j < RW; ++j) {  // bv becomes the state before the row
         const u64 after = fma2(av[j], s, bv[j]);
