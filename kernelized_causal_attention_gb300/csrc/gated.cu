@@ -18,9 +18,9 @@
 // The state passed on is the same sequence of fused multiply-adds whichever tiles had
 // theirs already, so results repeat bit for bit.
 //
-// 4 x 2048 x 2048 bf16: forward 35 us (134 MB, 0.56 of the copy rate), gradients 66 (235
-// MB, 0.52), clearing the words and joining dlam 2 to 3 each; 65536 x 512 bf16: forward
-// 79 (268 MB, 0.50).  About 79 and 167 instructions for a warp's row (64 channels), issued
+// 4 x 2048 x 2048 bf16: forward 34 us (134 MB, 0.57 of the copy rate), gradients 64 (235
+// MB, 0.54), clearing the words and joining dlam 2 each; 65536 x 512 bf16: forward
+// 76 (268 MB, 0.52).  About 79 and 167 instructions for a warp's row (64 channels), issued
 // at 55 % of the rate: a tile's phases (rows in, gates, the states before it, replay, rows
 // out: 1300, 3700, 1800, 900, 300 cycles forward) follow one another on two blocks an SM;
 // without the gates' arithmetic it is still 89 us for 103.  One block a column that walks
@@ -313,19 +313,19 @@ struct Shared {
   int kind[WINDOW];
 };
 
-// What the n tiles before this one (the j-th is entry at + j step of the chain) pass on:
+// What the n tiles before this one (the j-th is at entry + j step of the chain) pass on:
 // the nearest state, moved on by the tiles since.  All threads call it; warp w looks
 // up the tiles w, w + WARPS, ...  The tile that is WINDOW back must have its state.
 // A wait of two seconds gives up: zero, and the code in the status word.
 template <int WINDOW>
-__device__ __forceinline__ u64 look_up(Shared<WINDOW>& sh, const Chain& ch, long at, long step, int n, int code) {
+__device__ __forceinline__ u64 look_up(Shared<WINDOW>& sh, const Chain& ch, long entry, long step, int n, int code) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int found = -1;
 #pragma unroll 1
   for (int base = 0; base < WINDOW && found < 0; base += WARPS) {
     const int j = base + w;
     if (j < n) {
-      const u64* p = ch.word + (at + j * step) * 96 + lane;
+      const u64* p = ch.word + (entry + j * step) * 96 + lane;
       u64 A, H, t0 = 0;
       int kind = 0;
       for (int tries = 0; kind == 0; ++tries) {
@@ -349,12 +349,9 @@ __device__ __forceinline__ u64 look_up(Shared<WINDOW>& sh, const Chain& ch, long
       if (lane == 0) sh.kind[j] = kind;
     }
     __syncthreads();
-    const int top = min(base + WARPS, n);
-    for (int i = base; i < top; ++i)
-      if (sh.kind[i] == 2) {
-        found = i;
-        break;
-      }
+    const int i = base + lane % WARPS;  // one load for all of them: 76 us for 79 where 38 tiles of a column are under way
+    const unsigned states = __ballot_sync(0xffffffffu, sh.kind[i] == 2 && i < n);
+    if (states != 0) found = base + __ffs(states) - 1;
   }
   u64 s = sh.wH[found][lane];
   for (int i = found - 1; i >= 0; --i) s = fma2(sh.wA[i][lane], s, sh.wH[i][lane]);
