@@ -6,7 +6,8 @@
 //
 // All three kernels are bound by HBM: packing reads 4 and writes 1 byte a value, the
 // token's read takes D (M + 8) bytes a head instead of D (4 M + 4).  2048 streams of 8
-// heads, 64 x 64, int8: 13.1 us (79.7 MB, 0.89 of the copy rate; 42.9 from fp32 states);
+// heads, 64 x 64, int8: 14.5 us from HBM (79.7 MB, 0.81 of the copy rate), 12.4 again from
+// what L2 holds of them (42.9 from fp32 states);
 // 600 heads of 32 x 64 in e4m3, from L2: 2.4 us to pack, 2.0 to unpack.
 #include <cuda_fp8.h>
 
@@ -88,8 +89,12 @@ __global__ void __launch_bounds__(256) k_unpack(const uint32_t* code, const floa
 // One warp a key head: a lane holds 16 columns of every RS-th row.  The weights
 // phi(q_d) scale_d live two to a lane and are passed by shuffles; the lanes' sums are
 // joined by halving: each exchange adds the half of the columns that the partner keeps.
+// Seven blocks an SM, whose loads fill more of the time in which others compute, and codes
+// marked as read once: 14.5 us for the 2048 x 8 heads above where they come from HBM, 16.1
+// without the mark, 15.8 with the six blocks that 79 registers allow, 16.9 with neither;
+// eight blocks spill (19.8).
 template <int D, int M, bool E4M3, typename T>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 7)
     k_step_packed(const T* q, const uint4* code, const float* scale, const float* Z, T* y, int per, long heads) {
   grid_dep_enter();
   constexpr int L = M / 16, RS = 32 / L, K = (D + RS - 1) / RS, W = (D + 31) / 32;
@@ -99,7 +104,7 @@ __global__ void __launch_bounds__(128)
   const uint4* p = code + bhk * (D * L);
   uint4 u[K];
 #pragma unroll
-  for (int k = 0; k < K; ++k) u[k] = r0 + k * RS < D ? p[k * 32 + lane] : make_uint4(0, 0, 0, 0);
+  for (int k = 0; k < K; ++k) u[k] = r0 + k * RS < D ? __ldcs(p + k * 32 + lane) : make_uint4(0, 0, 0, 0);
   float z[W], sc[W];
 #pragma unroll
   for (int w = 0; w < W; ++w) {
