@@ -2,10 +2,12 @@
 beside it _front.so, the compiled calls from torch tensors to it.
 
 Every translation unit is compiled for sm_103a only (GB300), in parallel, then
-linked into one shared library with the static CUDA runtime; _front.so is host
-code against the headers of Python and torch.  Run directly
-(python -m kernelized_causal_attention_gb300._build) or through
-__graft_entry__.build().
+linked into one shared library with the static CUDA runtime: library(), which needs
+nvcc and its host compiler only.  _front.so is host code against the headers of
+Python and torch, and linked to that library; where it cannot be built, build() says
+so with the library in place.  Run directly
+(python -m kernelized_causal_attention_gb300._build, with --library for the library
+alone) or through __graft_entry__.build().
 """
 from __future__ import annotations
 
@@ -41,32 +43,52 @@ def sources():
 
 def _deps():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) \
-        + [os.path.join(CSRC, "front.cpp"), os.path.join(os.path.dirname(HERE), "include", "linattn.h"), __file__]
+        + [os.path.join(INCLUDE, "linattn.h"), __file__]
+
+
+def _front_deps():
+    return [os.path.join(CSRC, "front.cpp"), os.path.join(INCLUDE, "linattn.h"), __file__]
 
 
 MANIFEST = os.path.join(LIBDIR, "sources.txt")
+FRONT_MANIFEST = os.path.join(LIBDIR, "front.txt")
 
 
 def _manifest() -> str:
+    return "\n".join(os.path.basename(f) for f in sources())
+
+
+def front_manifest() -> str:
+    """What _front.so is good for: the torch and the Python whose headers it was compiled against."""
     import torch
-    return "\n".join([*(os.path.basename(f) for f in sources()), f"torch {torch.__version__}"])
+    return f"torch {torch.__version__}\npython {sys.version_info.major}.{sys.version_info.minor}"
+
+
+def _current(lib, manifest, said, deps) -> bool:
+    """lib exists, was built from what the manifest says and is newer than every input."""
+    if not (os.path.exists(lib) and os.path.exists(manifest)):
+        return False
+    with open(manifest) as f:
+        if f.read() != said:
+            return False
+    t = os.path.getmtime(lib)
+    return all(os.path.getmtime(d) <= t for d in deps)
 
 
 def up_to_date() -> bool:
-    """Both libraries exist, were built from the current set of sources (an
-    added or removed file, or another torch, forces a rebuild) and are newer
-    than every input."""
-    if not all(os.path.exists(f) for f in (LIB, FRONT, MANIFEST)):
-        return False
-    with open(MANIFEST) as f:
-        if f.read() != _manifest():
-            return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(FRONT))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    """The library exists, was built from the current set of sources (an
+    added or removed file forces a rebuild) and is newer than every input."""
+    return _current(LIB, MANIFEST, _manifest(), _deps())
 
 
-def _front_obj(cuda_home: str) -> str:
+def front_up_to_date() -> bool:
+    """The same of _front.so, which another torch or Python makes out of date."""
+    return _current(FRONT, FRONT_MANIFEST, front_manifest(), _front_deps())
+
+
+def _front_obj() -> str:
     import torch
+    cuda_home = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     root = os.path.join(os.path.dirname(torch.__file__), "include")
     obj = os.path.join(LIBDIR, "front.o")
     dirs = [INCLUDE, root, os.path.join(root, "torch", "csrc", "api", "include"), sysconfig.get_paths()["include"],
@@ -91,14 +113,24 @@ def _link_front(obj: str) -> None:
     _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{LIBDIR}", "-l:liblinattn.so", "-Wl,-rpath,$ORIGIN",
           f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], "_front.so")
     os.replace(tmp, FRONT)
+    with open(FRONT_MANIFEST, "w") as f:
+        f.write(front_manifest())
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+def _link(cc, objs) -> None:
+    tmp = LIB + f".tmp{os.getpid()}"
+    _run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], "the library")
+    os.replace(tmp, LIB)
+    with open(MANIFEST, "w") as f:
+        f.write(_manifest())
+
+
+def _build(ex, force, verbose, extra) -> None:
+    """The library, its units compiled by the executor."""
     if not force and up_to_date():
-        return LIB
+        return
     os.makedirs(LIBDIR, exist_ok=True)
     cc = nvcc()
-    objs = []
 
     def compile_one(src):
         obj = os.path.join(LIBDIR, os.path.basename(src)[:-3] + ".o")
@@ -107,22 +139,40 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
             sys.stderr.write(err)
         return obj
 
-    with ThreadPoolExecutor(max_workers=max(1, min(len(sources()) + 1, os.cpu_count() or 1))) as ex:
-        front = ex.submit(_front_obj, os.path.dirname(os.path.dirname(os.path.realpath(cc))))
-        objs = list(ex.map(compile_one, sources()))
-        front = front.result()
-    tmp = LIB + f".tmp{os.getpid()}"
-    _run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], "the library")
-    os.replace(tmp, LIB)
-    _link_front(front)
-    with open(MANIFEST, "w") as f:
-        f.write(_manifest())
+    _link(cc, list(ex.map(compile_one, sources())))
+
+
+def _executor():
+    return ThreadPoolExecutor(max_workers=max(1, min(len(sources()) + 1, os.cpu_count() or 1)))
+
+
+def library(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """The CUDA library alone."""
+    with _executor() as ex:
+        _build(ex, force, verbose, extra)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """The CUDA library, and _front.so beside it; the library's path."""
+    if not force and up_to_date() and front_up_to_date():
+        return LIB
+    os.makedirs(LIBDIR, exist_ok=True)
+    with _executor() as ex:
+        # compiled beside the library's units, waited for (and refused) once the library is linked
+        front = ex.submit(_front_obj) if force or not front_up_to_date() else None
+        _build(ex, force, verbose, extra)
+        if front is not None:
+            try:
+                _link_front(front.result())
+            except Exception as e:
+                raise RuntimeError(f"{LIB} is built; _front.so, which the calls from gated_fwd on go through, is not: {e}") from e
     return LIB
 
 
 if __name__ == "__main__":
     import time
     t0 = time.time()
-    print(build(force="--force" in sys.argv, verbose="-v" in sys.argv,
-                extra=["-Xptxas", "-v"] if "--ptxas" in sys.argv else []))
+    print((library if "--library" in sys.argv else build)(force="--force" in sys.argv, verbose="-v" in sys.argv,
+                                                          extra=["-Xptxas", "-v"] if "--ptxas" in sys.argv else []))
     print(f"built in {time.time() - t0:.1f}s")
