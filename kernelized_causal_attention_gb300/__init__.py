@@ -138,13 +138,20 @@ def lib():
 
 
 def _load_front():
-    """The compiled allocating calls (_front.so, built with the library); raises if they have not been built."""
+    """The compiled allocating calls (_front.so, built beside the library); raises if they have not been built, or were
+    built against another torch or Python."""
     global _front
     with _lock:
         if _front is None:
-            path = os.path.join(_HERE, "_lib", "_front.so")
-            if not os.path.exists(path):
-                raise RuntimeError(f"not built: {path} is missing. Build it with `python -m kernelized_causal_attention_gb300._build`.")
+            from . import _build
+            path, how = _build.FRONT, "Build it with `python -m kernelized_causal_attention_gb300._build`."
+            if not (os.path.exists(path) and os.path.exists(_build.FRONT_MANIFEST)):
+                raise RuntimeError(f"not built: {path} is missing. {how}")
+            with open(_build.FRONT_MANIFEST) as f:
+                built = f.read()
+            if built != _build.front_manifest():
+                said = [s.replace("\n", ", ") for s in (built, _build.front_manifest())]
+                raise RuntimeError(f"{path} was built for {said[0]}, this is {said[1]}. {how}")
             name = __name__ + "._front"
             spec = importlib.util.spec_from_file_location(name, path)
             front = importlib.util.module_from_spec(spec)

@@ -1,10 +1,11 @@
-"""The build of the compiled calls beside the library (no GPU, no compiler): when _front.so is out of date and that a front
-which cannot be built leaves the library built."""
+"""The build of the compiled calls beside the library (no GPU, no compiler): when _front.so is out of date, that a front
+which cannot be built leaves the library built, and what loading one that does not fit says."""
 import os
 import time
 
 import pytest
 
+import kernelized_causal_attention_gb300 as la
 from kernelized_causal_attention_gb300 import _build as b
 
 
@@ -66,6 +67,17 @@ def test_another_torch_or_python(tmp_path, monkeypatch, said):
     _, lib = _tree(tmp_path, monkeypatch)
     (lib / "front.txt").write_text(said)
     assert b.up_to_date() and not b.front_up_to_date()
+    monkeypatch.setattr(la, "_front", None)
+    with pytest.raises(RuntimeError, match="torch 2.0.0.*this is torch"):
+        la._load_front()
+
+
+def test_a_front_that_is_not_there(tmp_path, monkeypatch):
+    _, lib = _tree(tmp_path, monkeypatch)
+    (lib / "_front.so").unlink()
+    monkeypatch.setattr(la, "_front", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        la._load_front()
 
 
 def _compilers(monkeypatch, ran, front_fails):
