@@ -76,10 +76,11 @@ __device__ __forceinline__ u64 near_one(u64 u) {
   return mul2(u, p);
 }
 __device__ __forceinline__ u64 minus_one(u64 w) { return fma2(w, two(-1.f), two(1.f)); }
-// beta = sqrt(w (1 + a)), with 1e-36 under the root of its inverse: zero where w is.
+// beta = sqrt(w (1 + a)), with the smallest normal number under the root of its inverse: zero
+// where w is, and half a step off from w = 5e-32 on.
 __device__ __forceinline__ u64 root(u64 w, u64 a) {
   const u64 om = fma2(w, a, w);
-  const float2 f = un(add2(om, two(1e-36f)));
+  const float2 f = un(add2(om, two(1.2e-38f)));
   return mul2(om, pk(rsqrt_fast(f.x), rsqrt_fast(f.y)));
 }
 // The larger of three, NaN if one is.
@@ -621,7 +622,7 @@ __global__ void __launch_bounds__(32 * WARPS, BLOCKS)
           beta = pr[j * (CH / 2)];
         else
           beta = pk(__uint_as_float(pr[j * (CH / 2)]), __uint_as_float(pi[j * (CH / 2)]));
-        const u64 inverse = rcp_2(add2(beta, two(1e-18f)));  // u is zero where beta is
+        const u64 inverse = rcp_2(add2(beta, two(1e-27f)));  // u is zero where beta is; any other beta is 1e-26 at least
         const u64 G = add2(open(pd[j * (CH / 2)]), X), gx = mul2(gv[j], open(px[j * (CH / 2)]));
         X = mul2(av[j], G);
         // Q = a G (a g x u / beta - u h)

@@ -1,5 +1,6 @@
-"""The gated recurrence where its decay is strong (u = k sigmoid(r) of one to many: a row forgets): every value against 64
-bits within bounds that follow the decay a in relative terms, so that a small a has to hold as many bits as a large one."""
+"""The gated recurrence at the ends of its decay's range, where it is strong (u = k sigmoid(r) of one to many: a row forgets)
+and where a gate is all but closed (u down to 1e-33): every value against 64 bits within bounds that follow the decay a and
+beta = sqrt(1 - a^2) in relative terms, so that small ones have to hold as many bits as large ones."""
 import pytest
 import torch
 
@@ -32,7 +33,8 @@ def gates(r, i, lam, scale):
     """s, g, u, a and beta as Near.  u: k 16 half steps and sigmoid's and a product.  Below one, w = 1 - a is off by as much as u
     and 4 half steps for its polynomial, and a = 1 - w by as much in absolute terms and a rounding.  From one on a is an
     exponential: u's relative error u times, two half steps of the argument u log2(e), and the exponential's 4; w = 1 - a.
-    beta = om / sqrt(om), om = w (1 + a): half of om's error, 4 half steps of the root, 3 for sums and products."""
+    beta = om / sqrt(om + 1.2e-38), om = w (1 + a): half of om's error, 4 half steps of the root, 3 for sums and products, and
+    half of what the floor under the root is of om."""
     s, es = _sig(r)
     g, eg = _sig(i)
     soft = torch.logaddexp(lam, torch.zeros_like(lam))
@@ -44,7 +46,7 @@ def gates(r, i, lam, scale):
     ew = torch.where(low, w * (eu + 4 * F32), a * (u * (eu + 2 * F32) + 4 * F32) + F32 * w)
     ea = torch.where(low, ew + F32 * a, a * (u * (eu + 2 * F32) + 4 * F32))
     om = -torch.expm1(-2 * u)
-    rel = (ew / w + ea / (1 + a) + 2 * F32) / 2 + 7 * F32
+    rel = (ew / w + ea / (1 + a) + 2 * F32) / 2 + 7 * F32 + 0.6e-38 / om
     return Near(s, s * es), Near(g, g * eg), Near(u, u * eu), Near(a, ea), Near(torch.sqrt(om), torch.sqrt(om) * rel)
 
 
@@ -137,3 +139,19 @@ def test_strong_decays(cuda, linattn, B, N, C, dtype, span, from_state):
         within(t, want[name][0], rounded(*want[name], dtype), name)
     if from_state:
         within(hd, *want["h"], "state")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_all_but_closed_gates(cuda, linattn, dtype):
+    """Every row's u between 1e-33 and 1e-9: y, dx, di and with u / beta dr and dlam go by beta, of 1e-16 to 1e-5."""
+    x, r, i, lam, dy, _ = inputs(2, 30, 48, dtype, -60, -24, 2)
+    r = (3 * r.float() - 8).clamp(-18, 2).to(r.dtype)
+    u = gates(*d64(r, i, lam), 8.0)[2].v
+    assert 1e-33 < float(u.min()) < 1e-31 and float(u.max()) < 1e-9
+    a = [t.to(cuda) for t in (x, r, i, lam)]
+    y, kept = linattn.gated_fwd(*a, keep=True)
+    got = linattn.gated_bwd(*a, kept, dy.to(cuda))
+    want = bounds(x, r, i, lam, dy=dy)
+    for name, t in zip(("y", "dx", "dr", "di", "dlam"), (y, *got)):
+        within(t, want[name][0], rounded(*want[name], dtype), name)
