@@ -146,7 +146,7 @@ def _load_front():
             from . import _build
             path, how = _build.FRONT, "Build it with `python -m kernelized_causal_attention_gb300._build`."
             if not (os.path.exists(path) and os.path.exists(_build.FRONT_MANIFEST)):
-                raise RuntimeError(f"not built: {path} is missing. {how}")
+                raise RuntimeError(f"not built: {path} or what it was built against is missing. {how}")
             with open(_build.FRONT_MANIFEST) as f:
                 built = f.read()
             if built != _build.front_manifest():

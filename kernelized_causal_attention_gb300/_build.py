@@ -64,15 +64,17 @@ def front_manifest() -> str:
     return f"torch {torch.__version__}\npython {sys.version_info.major}.{sys.version_info.minor}"
 
 
+def _newest(lib, deps) -> bool:
+    t = os.path.getmtime(lib)
+    return all(os.path.getmtime(d) <= t for d in deps)
+
+
 def _current(lib, manifest, said, deps) -> bool:
     """lib exists, was built from what the manifest says and is newer than every input."""
     if not (os.path.exists(lib) and os.path.exists(manifest)):
         return False
     with open(manifest) as f:
-        if f.read() != said:
-            return False
-    t = os.path.getmtime(lib)
-    return all(os.path.getmtime(d) <= t for d in deps)
+        return f.read() == said and _newest(lib, deps)
 
 
 def up_to_date() -> bool:
@@ -118,6 +120,8 @@ def _link_front(obj: str) -> None:
 
 
 def _link(cc, objs) -> None:
+    if os.path.exists(FRONT_MANIFEST) and not (os.path.exists(FRONT) and _newest(FRONT, _front_deps())):
+        os.remove(FRONT_MANIFEST)  # a front of another header than the library's is not to be loaded
     tmp = LIB + f".tmp{os.getpid()}"
     _run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], "the library")
     os.replace(tmp, LIB)

@@ -118,6 +118,27 @@ def test_the_library_alone(tmp_path, monkeypatch):
     assert "front.cpp" not in ran and "_front.so" not in ran and b.up_to_date()
 
 
+@pytest.mark.parametrize("alone", [False, True])
+def test_a_front_of_another_header_is_not_loaded(tmp_path, monkeypatch, alone):
+    """The ABI's header changes and only the library can be built, or is asked for: the older _front.so would call it by the
+    header before."""
+    _, lib = _tree(tmp_path, monkeypatch)
+    ran = []
+    _compilers(monkeypatch, ran, True)
+    for n in ("liblinattn.so", "_front.so"):
+        os.utime(lib / n, (time.time() - 50,) * 2)
+    os.utime(tmp_path / "linattn.h", (time.time() - 20,) * 2)
+    if alone:
+        b.library()
+    else:
+        with pytest.raises(RuntimeError, match="Python.h"):
+            b.build()
+    assert b.up_to_date() and not b.front_up_to_date()
+    monkeypatch.setattr(la, "_front", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        la._load_front()
+
+
 def test_everything_again(tmp_path, monkeypatch):
     _, lib = _tree(tmp_path, monkeypatch)
     ran = []
