@@ -422,7 +422,8 @@ la_status la_cross_step(const void* q, const float* S, const float* Z, void* y, 
  * own.  With s = sigmoid(r), g = sigmoid(i), a = exp(-scale softplus(lam) s),
  *   h_n = a_n h_{n-1} + sqrt(1 - a_n^2) g_n x_n,  y_n = h_n.
  * x, r, i [B][N][C] (row strides ldx, ldr, ldi >= C; aligned to their elements),
- * lam [C] of the call's dtype, scale > 0; y [B][N][C].  h [B][C] float, read as
+ * lam [C] of the call's dtype (bf16 around -6 is spaced 2^-5, which moves 1 - a by up
+ * to 1.6 %), scale > 0; y [B][N][C].  h [B][C] float, read as
  * the state before row 0 and replaced by the state after each sequence's last
  * valid row, or NULL (from zero, not returned).  kept: NULL, or
  * la_gated_kept_bytes(...) bytes that receive what la_gated_bwd needs of this

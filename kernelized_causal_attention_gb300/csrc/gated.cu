@@ -23,9 +23,16 @@
 // 76 (268 MB, 0.52).  About 79 and 167 instructions for a warp's row (64 channels), issued
 // at 55 % of the rate: a tile's phases (rows in, gates, the states before it, replay, rows
 // out: 1300, 3700, 1800, 900, 300 cycles forward) follow one another on two blocks an SM;
-// without the gates' arithmetic it is still 89 us for 103.  One block a column that walks
-// the rows would leave most SMs idle at these widths; three passes that read the rows
-// twice took 216; three blocks an SM without rows ahead 113.
+// with the gates' arithmetic taken out a training pass took 89 us where it took 103 (102 now).
+// One block a column that walks the rows would leave most SMs idle at these widths; three
+// passes that read the rows twice took 216; three blocks an SM without rows ahead 113.
+//
+// These are decays of u < 1.  A warp whose strip has one u above that computes the strip's
+// gates a second time, in the full form: with lam spread over -9 to 2 (scale 8) training takes
+// 152 us for 102 and the prompt 120 for 77; over 0 to 2 149 and 117.
+//
+// 128 registers a thread; the bf16 gradients spill 4 bytes, the bf16 forward of rows off
+// sixteen bytes 36 (multiples of four) and 68.
 #include <algorithm>
 #include <atomic>
 
@@ -768,7 +775,9 @@ cudaError_t room(size_t bytes, int* per_sm) {
   return cudaSuccess;
 }
 
-// A cooperative launch: all blocks run at once, or the launch fails.  Blocks may start and
+// A cooperative launch: all blocks run at once, or the launch fails.  A full grid takes every
+// register of every SM: it starts once no other kernel is resident, and kernels of another
+// stream run before or after it.  Blocks may start and
 // ask for their first rows while k_gated_start, itself behind all that was queued before,
 // still runs (27.5 us for 29.4 where tiles are few: fp32, 3 x 784 x 645, both directions).
 template <auto kernel, typename... Act>
@@ -799,7 +808,7 @@ cudaError_t fwd(Rows a, float* h, float* kept, void* y, void* ws, const GatedSha
   const size_t n = entries(s, ROWS);
   Chain ch{};
   cudaError_t e;
-  if (a.tiles == 1) {
+  if (a.tiles == 1) {  // an ordinary launch: nothing in this form of the kernel waits for the one before
     int per_sm;
     if ((e = room<k_gated_fwd<T, UNIT, false>>(stage, &per_sm)) != cudaSuccess) return e;
     k_gated_fwd<T, UNIT, false><<<static_cast<unsigned>(n), 32 * WARPS, stage, st>>>(a, ch, h, kept, (T*)y, static_cast<int>(n));
@@ -818,7 +827,7 @@ cudaError_t bwd(Rows a, const float* kept, const void* dy, void* dx, void* dr, v
   float* sums = static_cast<float*>(ws);
   Chain ch{};
   cudaError_t e;
-  if (a.tiles == 1) {
+  if (a.tiles == 1) {  // as forward
     int per_sm;
     if ((e = room<k_gated_bwd<T, UNIT, false>>(stage, &per_sm)) != cudaSuccess) return e;
     k_gated_bwd<T, UNIT, false><<<static_cast<unsigned>(n), 32 * WARPS, stage, st>>>(a, ch, (const T*)dy, kept, (T*)dx, (T*)dr, (T*)di, sums, static_cast<int>(n));

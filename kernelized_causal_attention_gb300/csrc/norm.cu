@@ -270,7 +270,8 @@ inline __host__ __device__ int distinct(int per, int G) { return per % G == 0 ? 
 // into shared memory (a thread's own places, so it waits for its own copies only) while R
 // are worked on, and are read from there twice: 48.3 us both ways for 4 x 2048 x 2048 bf16
 // with a residual, 54.5 with registers for them and loads that wait, 34.9 and 38.3 for 32
-// groups of 64.  Two items at once 50.1 and 37.1, four spill.
+// groups of 64.  Two items at once 50.1 and 37.1; four spill (of three, the form of 128 threads
+// does: 4 bytes).
 template <typename T, int V, int K, int TPR, int R>
 __global__ void __launch_bounds__(THREADS<TPR>, (THREADS<TPR> < 512 ? 512 / THREADS<TPR> : 1)) k_norm_bwd(const GradArgs a) {
   grid_dep_enter();
