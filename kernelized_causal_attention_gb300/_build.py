@@ -11,6 +11,7 @@ alone) or through __graft_entry__.build().
 """
 from __future__ import annotations
 
+import contextlib
 import glob
 import os
 import shutil
@@ -108,6 +109,14 @@ def _run(cmd, what):
     return r.stderr
 
 
+def _say(manifest, text) -> None:
+    """Whole or not at all, for a process that reads it meanwhile."""
+    tmp = manifest + f".tmp{os.getpid()}"
+    with open(tmp, "w") as f:
+        f.write(text)
+    os.replace(tmp, manifest)
+
+
 def _link_front(obj: str) -> None:
     import torch
     libs = os.path.join(os.path.dirname(torch.__file__), "lib")
@@ -115,18 +124,17 @@ def _link_front(obj: str) -> None:
     _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, f"-L{LIBDIR}", "-l:liblinattn.so", "-Wl,-rpath,$ORIGIN",
           f"-L{libs}", "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10"], "_front.so")
     os.replace(tmp, FRONT)
-    with open(FRONT_MANIFEST, "w") as f:
-        f.write(front_manifest())
+    _say(FRONT_MANIFEST, front_manifest())
 
 
 def _link(cc, objs) -> None:
     if os.path.exists(FRONT_MANIFEST) and not (os.path.exists(FRONT) and _newest(FRONT, _front_deps())):
-        os.remove(FRONT_MANIFEST)  # a front of another header than the library's is not to be loaded
+        with contextlib.suppress(FileNotFoundError):  # another process that builds
+            os.remove(FRONT_MANIFEST)  # a front of another header than the library's is not to be loaded
     tmp = LIB + f".tmp{os.getpid()}"
     _run([cc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs], "the library")
     os.replace(tmp, LIB)
-    with open(MANIFEST, "w") as f:
-        f.write(_manifest())
+    _say(MANIFEST, _manifest())
 
 
 def _build(ex, force, verbose, extra) -> None:

@@ -146,3 +146,17 @@ def test_everything_again(tmp_path, monkeypatch):
     b.build(force=True)
     assert sorted(ran) == sorted([str(tmp_path / "csrc" / "a.cu"), "front.cpp", "the library", "_front.so"])
     assert b.up_to_date() and b.front_up_to_date()
+
+
+def test_a_manifest_is_whole_or_not_there(tmp_path, monkeypatch):
+    """What a process that loads meanwhile reads: the text before until the text after is complete."""
+    _, lib = _tree(tmp_path, monkeypatch)
+    real, seen = os.replace, []
+
+    def replace(a, c):
+        seen.append((lib / "front.txt").read_text())
+        real(a, c)
+    monkeypatch.setattr(os, "replace", replace)
+    b._say(b.FRONT_MANIFEST, "torch 9\npython 9")
+    assert seen == [b.front_manifest()] and (lib / "front.txt").read_text() == "torch 9\npython 9"
+    assert [f.name for f in lib.iterdir() if "tmp" in f.name] == []
